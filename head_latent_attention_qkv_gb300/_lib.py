@@ -17,6 +17,7 @@ MLA_BF16, MLA_FP32 = 0, 1
 MLA_ROPE_NEOX, MLA_ROPE_INTERLEAVED = 0, 1
 MLA_DEV_BAD_SLOT, MLA_DEV_BAD_POSITION, MLA_DEV_BAD_PAGE, MLA_DEV_TIMEOUT, MLA_DEV_BAD_LENGTH = 1, 2, 4, 8, 16
 MLA_DEV_BAD_WINDOW = 32
+MLA_DEV_BAD_TREE, MLA_DEV_BAD_KEEP = 64, 128
 MLA_WS_Q_ABS, MLA_WS_O_LAT, MLA_WS_O = 0, 1, 2
 
 
@@ -90,6 +91,17 @@ def _load():
         "mla_check_wait_timeout": (I32, [P, C.c_uint32, P, P]),
         "mla_latent_attention_backward": (I32, [P, P, P, P, I32, C.POINTER(mla_attn_desc_t), P, P,
                                                 P, P, P, P]),
+        "mla_tree_attention_workspace_bytes": (SZ, [P, C.POINTER(mla_attn_desc_t)]),
+        "mla_tree_attention": (I32, [P, P, P, P, I32, C.POINTER(mla_attn_desc_t), P, P, P, P, SZ, P]),
+        "mla_forward_tree_workspace_bytes": (SZ, [P, C.POINTER(mla_attn_desc_t)]),
+        "mla_draft_forward_tree": (I32, [P, P, P, P, P, I32, C.POINTER(mla_attn_desc_t), P, P, P, SZ,
+                                         P]),
+        "mla_key_weights": (I32, [P, P, P, P, I32, C.POINTER(mla_attn_desc_t), P, P, C.c_float, P, P,
+                                  C.c_int64, P]),
+        "mla_cache_select": (I32, [P, P, C.c_int64, P, I32, I32, I32, I32, P, P, P]),
+        "mla_cache_compact_workspace_bytes": (SZ, [P, I32, C.c_int64]),
+        "mla_cache_compact": (I32, [P, P, I32, P, I32, P, I32, P, C.c_int64, P, P, P, I32, P, P,
+                                    C.c_int64, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

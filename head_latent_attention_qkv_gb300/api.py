@@ -52,6 +52,9 @@ class Handle:
 
     def __init__(self, dims, weights: dict, page_size: int, device="cuda", stream=None):
         self.dims, self.page_size, self.device = dims, page_size, torch.device(device)
+        # the device as tensors name it (an index in place of "the current one")
+        self.tensor_device = self.device if self.device.index is not None or self.device.type != "cuda" \
+            else torch.device("cuda", torch.cuda.current_device())
         self.cfg = make_config(dims, page_size)
         self.arena = _buf(lib.mla_weight_arena_bytes(C.byref(self.cfg)), self.device)
         w = _lib.mla_weights_t(**{k: (weights[k].data_ptr() if weights.get(k) is not None else None)
@@ -215,6 +218,174 @@ def mla_latent_attention_backward(h: Handle, q_abs, positions, cache, desc, o_la
                                             cache.shape[0], C.byref(desc), _ptr(o_lat), _ptr(lse),
                                             _ptr(d_o_lat), _ptr(d_q_abs), _ptr(d_cache),
                                             _stream(stream)), "mla_latent_attention_backward")
+
+
+class _on:
+    """Allocations under `stream` (the stream the call runs on), so that the
+    caching allocator reuses a buffer only behind the work that reads it."""
+
+    def __init__(self, stream):
+        self.ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _take(name, t, dtype, shape, device):
+    """The pointer of `t`, checked: on the handle's device, contiguous, of this
+    type and shape (a dimension given as None is free)."""
+    if t.device != device or t.dtype != dtype or not t.is_contiguous() or t.dim() != len(shape) or any(
+            w is not None and s != w for s, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _opt(name, t, dtype, shape, device):
+    return None if t is None else _take(name, t, dtype, shape, device)
+
+
+def _tree_args(h: Handle, q_abs, positions, cache, desc, parent):
+    d, dev, dt = h.dims, h.tensor_device, torch_dtype(h.dims)
+    tokens = desc.num_blocks * desc.block_len
+    if q_abs.numel() != tokens * d.num_heads * d.cache_dim:
+        raise ValueError(f"q_abs: expected {tokens * d.num_heads} rows of {d.cache_dim}, got {tuple(q_abs.shape)}")
+    return (_take("q_abs", q_abs, dt, (None,) * q_abs.dim(), dev),
+            _take("positions", positions, torch.int32, (tokens,), dev),
+            _take("cache", cache, dt, (None, h.page_size, d.cache_dim), dev),
+            _opt("parent", parent, torch.int32, (tokens,), dev))
+
+
+def mla_tree_attention(h: Handle, q_abs, positions, cache, desc, parent, o_lat=None, lse=None,
+                       stream=None, workspace=None):
+    """Latent attention of trees of drafted tokens: ``parent`` int32 [blocks *
+    nodes] (-1: a child of the context, -2: padding, else an earlier node), the
+    nodes' own keys the last ``block_len`` of each sequence.  ``o_lat`` [rows,
+    kv_lora_rank] (fp16 for bf16 layers) and, when ``lse`` is given, its fp32
+    [rows] log-sum-exp."""
+    q, pos, c, par = _tree_args(h, q_abs, positions, cache, desc, parent)
+    rows = desc.num_blocks * desc.block_len * h.dims.num_heads
+    dt = torch.float16 if h.dims.dtype == "bf16" else torch.float32
+    lse_p = _opt("lse", lse, torch.float32, (rows,), h.tensor_device)
+    with _on(stream):
+        if o_lat is None:
+            o_lat = torch.empty(rows, h.dims.kv_lora_rank, dtype=dt, device=h.tensor_device)
+        need = lib.mla_tree_attention_workspace_bytes(h.h, C.byref(desc))
+        ws = workspace if workspace is not None else (_buf(need, h.tensor_device) if need else None)
+        out = _take("o_lat", o_lat, dt, (rows, h.dims.kv_lora_rank), h.tensor_device)
+        check(lib.mla_tree_attention(h.h, q, pos, c, cache.shape[0], C.byref(desc), par, out, lse_p,
+                                     None if ws is None else ws.data_ptr(),
+                                     0 if ws is None else ws.numel(), _stream(stream)),
+              "mla_tree_attention")
+    return o_lat
+
+
+def mla_tree_attention_workspace_bytes(h: Handle, desc) -> int:
+    return int(lib.mla_tree_attention_workspace_bytes(h.h, C.byref(desc)))
+
+
+def mla_draft_forward_tree(h: Handle, hidden, positions, block_slot_mapping, cache, desc, parent,
+                           out=None, stream=None, workspace=None):
+    """mla_draft_forward over trees of drafted tokens (``parent`` as in
+    mla_tree_attention)."""
+    d, dev, dt = h.dims, h.tensor_device, torch_dtype(h.dims)
+    M = desc.num_blocks * desc.block_len
+    args = (_take("hidden", hidden, dt, (M, d.hidden_size), dev),
+            _take("positions", positions, torch.int32, (M,), dev),
+            _opt("block_slot_mapping", block_slot_mapping, torch.int64, (M,), dev),
+            _take("cache", cache, dt, (None, h.page_size, d.cache_dim), dev))
+    par = _take("parent", parent, torch.int32, (M,), dev)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(M, d.hidden_size, dtype=dt, device=dev)
+        need = lib.mla_forward_tree_workspace_bytes(h.h, C.byref(desc))
+        ws = workspace if workspace is not None else _buf(need, dev)
+        check(lib.mla_draft_forward_tree(h.h, *args, cache.shape[0], C.byref(desc), par,
+                                         _take("out", out, dt, (M, d.hidden_size), dev), ws.data_ptr(),
+                                         ws.numel(), _stream(stream)), "mla_draft_forward_tree")
+    return out
+
+
+def mla_forward_tree_workspace_bytes(h: Handle, desc) -> int:
+    return int(lib.mla_forward_tree_workspace_bytes(h.h, C.byref(desc)))
+
+
+def mla_key_weights(h: Handle, q_abs, positions, cache, desc, lse, weights_out, prior=None, decay=1.0,
+                    parent=None, stream=None):
+    """``weights_out[b, j] = decay * prior[b, j] + `` the attention weight key j
+    of block b received from the block's rows, whose log-sum-exp is ``lse``
+    (mla_tree_attention's with ``parent``, mla_latent_attention's without);
+    ``prior`` may be ``weights_out`` itself, fp32 [blocks, keys or more]."""
+    q, pos, c, par = _tree_args(h, q_abs, positions, cache, desc, parent)
+    dev, nb = h.tensor_device, desc.num_blocks
+    rows = nb * desc.block_len * h.dims.num_heads
+    out = _take("weights_out", weights_out, torch.float32, (nb, None), dev)
+    ldw = weights_out.shape[1]
+    check(lib.mla_key_weights(h.h, q, pos, c, cache.shape[0], C.byref(desc), par,
+                              _take("lse", lse, torch.float32, (rows,), dev), decay,
+                              _opt("prior", prior, torch.float32, (nb, ldw), dev), out, ldw,
+                              _stream(stream)), "mla_key_weights")
+    return weights_out
+
+
+def mla_cache_select(h: Handle, weights, kv_len, budget: int, sink: int = 0, recent: int = 0,
+                     keep=None, keep_len=None, stream=None):
+    """``(keep, keep_len)``: per sequence the ascending indices of the keys that
+    stay under ``budget`` (the first ``sink``, the last ``recent``, then the
+    heaviest; -1 behind the last) and how many they are."""
+    dev, n = h.tensor_device, kv_len.shape[0]
+    w = _take("weights", weights, torch.float32, (n, None), dev)
+    with _on(stream):
+        if keep is None:
+            keep = torch.empty(n, max(budget, 0), dtype=torch.int32, device=dev)
+        if keep_len is None:
+            keep_len = torch.empty(n, dtype=torch.int32, device=dev)
+        check(lib.mla_cache_select(h.h, w, weights.shape[1], _take("kv_len", kv_len, torch.int32, (n,), dev),
+                                   n, budget, sink, recent,
+                                   _take("keep", keep, torch.int32, (n, max(budget, 0)), dev),
+                                   _take("keep_len", keep_len, torch.int32, (n,), dev),
+                                   _stream(stream)), "mla_cache_select")
+    return keep, keep_len
+
+
+def mla_cache_compact(h: Handle, cache, block_table, kv_len, keep, keep_len, first=None,
+                      dst_block_table=None, weights=None, weights_out=None, stream=None,
+                      workspace=None):
+    """Moves the kept entries of every sequence together (see the header): in
+    place, ``weights`` with them, or into the pages of ``dst_block_table``,
+    the weights into ``weights_out``.  The new lengths are ``keep_len`` (+
+    ``first``)."""
+    dev, n, d = h.tensor_device, kv_len.shape[0], h.dims
+    if weights is not None and weights_out is None and dst_block_table is None:
+        weights_out = weights
+    args = (_take("cache", cache, torch_dtype(d), (None, h.page_size, d.cache_dim), dev), cache.shape[0],
+            _take("block_table", block_table, torch.int32, (n, None), dev), block_table.shape[1],
+            _take("kv_len", kv_len, torch.int32, (n,), dev), n,
+            _take("keep", keep, torch.int32, (n, None), dev), keep.shape[1],
+            _take("keep_len", keep_len, torch.int32, (n,), dev),
+            _opt("first", first, torch.int32, (n,), dev),
+            _opt("dst_block_table", dst_block_table, torch.int32, (n, None), dev),
+            0 if dst_block_table is None else dst_block_table.shape[1],
+            _opt("weights", weights, torch.float32, (n, None), dev),
+            _opt("weights_out", weights_out, torch.float32,
+                 (n, None) if weights is None else tuple(weights.shape), dev),
+            0 if weights is None else weights.shape[1])
+    with _on(stream):
+        ws = workspace
+        if ws is None and dst_block_table is None:
+            ws = _buf(lib.mla_cache_compact_workspace_bytes(h.h, n, keep.shape[1]), dev)
+        check(lib.mla_cache_compact(h.h, *args, None if ws is None else ws.data_ptr(),
+                                    0 if ws is None else ws.numel(), _stream(stream)),
+              "mla_cache_compact")
+
+
+def mla_cache_compact_workspace_bytes(h: Handle, num_seqs: int, ldk: int) -> int:
+    return int(lib.mla_cache_compact_workspace_bytes(h.h, num_seqs, ldk))
 
 
 def mla_check_wait_timeout(h: Handle, max_rounds: int, gave_up, stream=None):

@@ -14,6 +14,7 @@
 #include "expand_tc.cuh"
 #include "gemm_tc.cuh"
 #include "simt.cuh"
+#include "tree.cuh"
 
 namespace mla {
 
@@ -453,10 +454,29 @@ extern "C" mla_status_t mla_latent_cache_append(mla_handle_t* h, const void* hid
 namespace mla {
 namespace {
 
+tree::Rule tree_rule(const mla_handle* h, const int32_t* positions, int num_pages,
+                     const mla_attn_desc_t& d, const int32_t* parent) {
+  return tree::Rule{d.block_table, d.kv_len, d.window, d.q_visible, positions, parent, num_pages,
+                    h->cfg.page_size, d.max_pages, d.block_len, h->lay.H, h->status};
+}
+
+// The attention of trees (mla_draft.h); `ws`: tree_ws() bytes.
+size_t tree_ws(const mla_handle*, const mla_attn_desc_t&) { return 0; }
+
+mla_status_t tree_attention(mla_handle_t* h, cudaStream_t st, const void* q_abs,
+                            const int32_t* pos, const void* cache, int num_pages,
+                            const mla_attn_desc_t& d, const int32_t* parent, void* o_lat, float* lse,
+                            void* ws) {
+  simt::tree_attention(st, h, tree_rule(h, pos, num_pages, d, parent), d.num_blocks, q_abs, cache,
+                       o_lat, lse, d.vis_stats);
+  return MLA_OK;
+}
+
 template <typename TX, typename TI>
 mla_status_t forward_impl(mla_handle_t* h, const void* hidden, const int32_t* pos, const int64_t* bslots,
                   void* cache, int num_pages, const mla_attn_desc_t& d, void* out, char* ws,
-                  cudaStream_t st, cudaEvent_t kv_ready, const mla_shared_ctx_t* ctx = nullptr) {
+                  cudaStream_t st, cudaEvent_t kv_ready, const mla_shared_ctx_t* ctx = nullptr,
+                  const int32_t* parent = nullptr) {
   const Layout& l = h->lay;
   const int M = d.num_blocks * d.block_len;
   const FwdWs w = forward_ws(h, M);
@@ -559,7 +579,10 @@ mla_status_t forward_impl(mla_handle_t* h, const void* hidden, const int32_t* po
   // the cache writes of another stream the attention depends on (a plain
   // launch after the wait: no programmatic edge crosses it)
   if (kv_ready) MLA_CUDA_TRY(cudaStreamWaitEvent(st, kv_ready, 0));
-  if constexpr (std::is_same<TX, float>::value) {
+  if (parent) {
+    s = tree_attention(h, st, q_abs, pos, cache, num_pages, d, parent, o_lat, nullptr, ws + w.total);
+    if (s != MLA_OK) return s;
+  } else if constexpr (std::is_same<TX, float>::value) {
     simt::latent_attention<TI, TX>(st, h, q_abs, (const TX*)cache, num_pages, d, pos, o_lat);
   } else if (tc::decode_applies(h, d.block_len)) {
     // few query rows per block: keys in the MMA's M dimension, splits merged after
@@ -711,6 +734,108 @@ extern "C" mla_status_t mla_draft_forward(mla_handle_t* h, const void* hidden,
                                           void* stream) {
   return mla_draft_forward_after(h, hidden, positions, block_slot_mapping, cache, num_pages, desc,
                                  out, workspace, workspace_bytes, stream, nullptr);
+}
+
+// What every entry point over trees asks of its descriptor (`who` opens the message).
+static mla_status_t check_tree_desc(const mla_handle_t* h, const mla_attn_desc_t* d, const char* who) {
+  const std::string w(who);
+  if (!h || !d) return fail(MLA_ERR_INVALID_ARG, w + ": null handle or descriptor");
+  if (d->num_blocks < 0 || d->block_len <= 0 || d->max_pages <= 0)
+    return fail(MLA_ERR_INVALID_ARG, w + ": num_blocks >= 0, block_len > 0, max_pages > 0");
+  if ((long)d->max_pages * h->cfg.page_size > 0x3fffffffL)
+    return fail(MLA_ERR_INVALID_ARG, w + ": max_pages * page_size < 2^30");
+  if ((double)d->num_blocks * d->block_len * h->lay.H > 2147483647.0)
+    return fail(MLA_ERR_INVALID_ARG, w + ": too many rows");
+  return MLA_OK;
+}
+
+extern "C" size_t mla_tree_attention_workspace_bytes(const mla_handle_t* h, const mla_attn_desc_t* desc) {
+  if (!h || !desc || desc->num_blocks <= 0 || desc->block_len <= 0 || desc->max_pages <= 0) return 0;
+  return tree_ws(h, *desc);
+}
+
+extern "C" mla_status_t mla_tree_attention(mla_handle_t* h, const void* q_abs,
+                                           const int32_t* positions, const void* cache,
+                                           int32_t num_pages, const mla_attn_desc_t* desc,
+                                           const int32_t* parent, void* o_lat, float* lse,
+                                           void* workspace, size_t workspace_bytes, void* stream) {
+  mla_status_t s = check_tree_desc(h, desc, "tree attention");
+  if (s != MLA_OK || desc->num_blocks == 0) return s;
+  const mla_attn_desc_t& d = *desc;
+  if (d.block_len > tree::MAX_NODES)
+    return fail(MLA_ERR_UNSUPPORTED, "tree attention: at most 1024 nodes a block");
+  if (!q_abs || !positions || !cache || !parent || !o_lat || !d.block_table || !d.kv_len)
+    return fail(MLA_ERR_INVALID_ARG, "tree attention: null pointer");
+  if (num_pages <= 0) return fail(MLA_ERR_INVALID_ARG, "tree attention: num_pages <= 0");
+  if ((uintptr_t)q_abs % 16 || (uintptr_t)o_lat % 16 || (uintptr_t)cache % 16)
+    return fail(MLA_ERR_INVALID_ARG, "tree attention: q_abs, cache and o_lat must be 16-byte aligned");
+  const size_t need = tree_ws(h, d);
+  if (need && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 256))
+    return fail(MLA_ERR_INVALID_ARG, "tree attention: workspace smaller than "
+                                     "mla_tree_attention_workspace_bytes() or not 256-byte aligned");
+  h->launches += 1;
+  s = tree_attention(h, (cudaStream_t)stream, q_abs, positions, cache, num_pages, d, parent, o_lat,
+                     lse, workspace);
+  if (s != MLA_OK) return s;
+  MLA_CUDA_TRY(cudaGetLastError());
+  return MLA_OK;
+}
+
+extern "C" size_t mla_forward_tree_workspace_bytes(const mla_handle_t* h, const mla_attn_desc_t* desc) {
+  if (!h || !desc || desc->num_blocks <= 0 || desc->block_len <= 0 || desc->max_pages <= 0) return 0;
+  return forward_ws(h, (long)desc->num_blocks * desc->block_len).total + tree_ws(h, *desc);
+}
+
+extern "C" mla_status_t mla_draft_forward_tree(mla_handle_t* h, const void* hidden,
+                                               const int32_t* positions,
+                                               const int64_t* block_slot_mapping, void* cache,
+                                               int32_t num_pages, const mla_attn_desc_t* desc,
+                                               const int32_t* parent, void* out, void* workspace,
+                                               size_t workspace_bytes, void* stream) {
+  mla_status_t s = check_tree_desc(h, desc, "forward_tree");
+  if (s != MLA_OK || desc->num_blocks == 0) return s;
+  const mla_attn_desc_t& d = *desc;
+  if (d.block_len > tree::MAX_NODES)
+    return fail(MLA_ERR_UNSUPPORTED, "forward_tree: at most 1024 nodes a block");
+  if (!hidden || !positions || !cache || !parent || !out || !workspace || !d.block_table || !d.kv_len)
+    return fail(MLA_ERR_INVALID_ARG, "forward_tree: null pointer");
+  if (num_pages <= 0) return fail(MLA_ERR_INVALID_ARG, "forward_tree: num_pages <= 0");
+  if (workspace_bytes < mla_forward_tree_workspace_bytes(h, desc) || (uintptr_t)workspace % 256)
+    return fail(MLA_ERR_INVALID_ARG, "forward_tree: workspace smaller than "
+                                     "mla_forward_tree_workspace_bytes() or not 256-byte aligned");
+  cudaStream_t st = (cudaStream_t)stream;
+  s = h->cfg.dtype == MLA_BF16
+          ? forward_impl<__nv_bfloat16, __half>(h, hidden, positions, block_slot_mapping, cache, num_pages,
+                                                d, out, (char*)workspace, st, nullptr, nullptr, parent)
+          : forward_impl<float, float>(h, hidden, positions, block_slot_mapping, cache, num_pages, d,
+                                       out, (char*)workspace, st, nullptr, nullptr, parent);
+  if (s != MLA_OK) return s;
+  MLA_CUDA_TRY(cudaGetLastError());
+  return MLA_OK;
+}
+
+extern "C" mla_status_t mla_key_weights(mla_handle_t* h, const void* q_abs, const int32_t* positions,
+                                        const void* cache, int32_t num_pages,
+                                        const mla_attn_desc_t* desc, const int32_t* parent,
+                                        const float* lse, float decay, const float* prior,
+                                        float* weights_out, int64_t ldw, void* stream) {
+  const mla_status_t s = check_tree_desc(h, desc, "key weights");
+  if (s != MLA_OK || desc->num_blocks == 0) return s;
+  const mla_attn_desc_t& d = *desc;
+  if (parent && d.block_len > tree::MAX_NODES)
+    return fail(MLA_ERR_UNSUPPORTED, "key weights: at most 1024 nodes a block");
+  if (!q_abs || !positions || !cache || !lse || !weights_out || !d.block_table || !d.kv_len)
+    return fail(MLA_ERR_INVALID_ARG, "key weights: null pointer");
+  if (num_pages <= 0 || ldw <= 0) return fail(MLA_ERR_INVALID_ARG, "key weights: num_pages and ldw > 0");
+  if ((double)d.num_blocks * d.max_pages * h->cfg.page_size > 34359738367.0)
+    return fail(MLA_ERR_INVALID_ARG, "key weights: num_blocks * max_pages * page_size < 2^35");
+  if ((uintptr_t)q_abs % 16 || (uintptr_t)cache % 16)
+    return fail(MLA_ERR_INVALID_ARG, "key weights: q_abs and cache must be 16-byte aligned");
+  simt::key_weights((cudaStream_t)stream, h, tree_rule(h, positions, num_pages, d, parent), d.num_blocks,
+                    q_abs, cache, lse, decay, prior, weights_out, (long)ldw);
+  h->launches += 1;
+  MLA_CUDA_TRY(cudaGetLastError());
+  return MLA_OK;
 }
 
 extern "C" size_t mla_forward_workspace_offset(const mla_handle_t* h, int32_t num_tokens,

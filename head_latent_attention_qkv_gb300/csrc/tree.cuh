@@ -1,0 +1,107 @@
+// Which keys a query sees when its block's own keys form a tree, and the
+// launchers of the kernels built on it (tree attention, key weights).
+//
+// A block of T nodes over a context: logical keys 0 .. kv_len - T - 1 are the
+// context, key kv_len - T + k is node k's own.  parent[i] is -1 (a child of
+// the context) or an earlier node; any other value takes the node, and the
+// nodes below it, out of the tree: their rows see nothing and nobody sees
+// their keys.  Node i sees the context and the nodes on its path from the
+// root, itself among them; a window W > 0 keeps the keys less than W positions
+// before it (a context key's position is its index, a node's its own
+// positions[] entry).  Without parents the rule of mla_attn_desc_t applies.
+#pragma once
+
+#include "common.cuh"
+
+namespace mla {
+namespace tree {
+
+constexpr int MAX_NODES = 1024;
+
+struct Rule {
+  const int32_t* block_table; const int32_t* kv_len; const int32_t* window;
+  const uint8_t* q_visible; const int32_t* positions;
+  const int32_t* parent;        // NULL: the block rule
+  int num_pages, page_size, max_pages, T, H;
+  uint32_t* status;
+};
+
+// Keys of block b (0 when its length or window is rejected), its window and,
+// with a tree, the context length.
+__device__ __forceinline__ int block_keys(const Rule& a, int b, int* W, int* ctx, bool report) {
+  int n = a.kv_len[b];
+  const int cap = a.max_pages * a.page_size;
+  if (n < 0 || n > cap || (a.parent && n < a.T)) {
+    if (report) set_status(a.status, MLA_DEV_BAD_LENGTH);
+    n = a.parent ? 0 : max(0, min(n, cap));
+  }
+  *W = a.window ? a.window[b] : 0;
+  if (*W < 0) {
+    if (report) set_status(a.status, MLA_DEV_BAD_WINDOW);
+    n = 0;
+  }
+  *ctx = a.parent ? max(0, n - a.T) : n;
+  return n;
+}
+
+// Whether node i's path to the context is sound (its ancestors and itself in
+// the tree).  `parent` points at the block's T entries; every step goes to an
+// earlier node, so the walk ends.
+__device__ __forceinline__ bool in_tree(const Rule& a, const int32_t* parent, int i, bool report) {
+  while (true) {
+    const int p = parent[i];
+    if (p == -1) return true;
+    if (p < -1) return false;
+    if (p >= i) {
+      if (report) set_status(a.status, MLA_DEV_BAD_TREE);
+      return false;
+    }
+    i = p;
+  }
+}
+
+// Bits of the nodes k0 .. k0 + 63 (k0 >= 0) that node i sees (i in the tree).
+__device__ __forceinline__ unsigned long long path_bits(const int32_t* parent, const int32_t* pos,
+                                                        int W, int i, int k0) {
+  unsigned long long m = 0;
+  const int pi = pos[i];
+  for (int k = i; k >= k0; k = parent[k]) {
+    const bool near = W == 0 || pi - pos[k] < W;
+    if (near && k < k0 + 64) m |= 1ull << (k - k0);
+  }
+  return m;
+}
+
+// Bits of keys j0 .. j0 + 63 that query i of block b sees.  n, W and ctx are
+// block_keys()'s; `ok`: the row sees anything at all (visible, in the tree).
+__device__ __forceinline__ unsigned long long key_bits(const Rule& a, long b, int i, bool ok, int n,
+                                                       int W, int ctx, int j0) {
+  if (!ok || j0 >= n) return 0ull;
+  const int32_t* pos = a.positions + b * a.T;
+  // [lo, hi): what the window and the context (or the whole block) leave
+  const int lo = W > 0 ? max(0, min(n, pos[i] - W + 1) - j0) : 0, hi = min(ctx - j0, 64);
+  unsigned long long m = 0;
+  if (hi > lo) {
+    m = hi >= 64 ? ~0ull : (1ull << hi) - 1ull;
+    m &= ~0ull << lo;
+  }
+  if (a.parent && j0 + 64 > ctx) {
+    const int k0 = j0 - ctx;                          // node of bit 0 (negative: still context)
+    const unsigned long long t = path_bits(a.parent + b * a.T, pos, W, i, max(k0, 0));
+    m |= k0 >= 0 ? t : t << (-k0);
+  }
+  return m;
+}
+
+}  // namespace tree
+
+namespace simt {
+// Tree attention and key weights of any layer, fp32 arithmetic on the CUDA
+// cores (the fp32 layers' path).
+void tree_attention(cudaStream_t st, const mla_handle* h, const tree::Rule& r, int num_blocks,
+                    const void* q_abs, const void* cache, void* o_lat, float* lse, int32_t* vis_stats);
+void key_weights(cudaStream_t st, const mla_handle* h, const tree::Rule& r, int num_blocks,
+                 const void* q_abs, const void* cache, const float* lse, float decay,
+                 const float* prior, float* out, long ldw);
+}  // namespace simt
+}  // namespace mla

@@ -73,7 +73,10 @@ enum {
   MLA_DEV_BAD_PAGE = 4,      /* block_table entry outside [0, num_pages)      */
   MLA_DEV_TIMEOUT = 8,       /* a bounded mbarrier wait gave up               */
   MLA_DEV_BAD_LENGTH = 16,   /* kv_len < 0 or > max_pages * page_size         */
-  MLA_DEV_BAD_WINDOW = 32    /* window < 0 (the block's rows are zeroed)      */
+  MLA_DEV_BAD_WINDOW = 32,   /* window < 0 (the block's rows are zeroed)      */
+  MLA_DEV_BAD_TREE = 64,     /* a node's parent is not an earlier node        */
+  MLA_DEV_BAD_KEEP = 128     /* a list of kept keys that is not ascending in
+                                [0, kv_len), or longer than its sequence      */
 };
 
 /* Intermediate tensors the forward leaves in its workspace
@@ -381,6 +384,117 @@ mla_status_t mla_latent_attention_backward(mla_handle_t *h, const void *q_abs,
                                            const void *o_lat, const float *lse,
                                            const float *d_o_lat, float *d_q_abs,
                                            float *d_cache, void *stream);
+
+/* ---- trees of drafted tokens, and a cache of bounded length --------------
+ * One verification step of speculative decoding over the latent cache: the
+ * drafted tree attends the cache, the weight that every cached key received
+ * is accumulated, and from time to time the keys with little weight leave the
+ * cache.  The accepted path of a tree is kept by the same compaction.
+ *
+ * A block of T = block_len nodes is the tail of its sequence: logical keys
+ * 0 .. kv_len - T - 1 are the context and key kv_len - T + k is node k's own.
+ * parent: device int32 [num_blocks * block_len], per block: -1 for a child of
+ * the context, else the index of an earlier node of the block (parent < node).
+ * A node whose parent is below -1 (padding), and every node under it, is not
+ * in the tree: its row sees no key and no row sees its key, whose entry may
+ * hold anything.  A parent >= the node is reported as MLA_DEV_BAD_TREE and
+ * treated the same.  Node i sees, with q_visible and window as in
+ * mla_attn_desc_t, the context keys j with window == 0 or positions[i] - j <
+ * window, and of the own keys those of the nodes a on its path from the
+ * context, itself included, with window == 0 or positions[i] - positions[a] <
+ * window.  positions are token positions: siblings share one.  A kv_len below
+ * T or behind the page table is reported as MLA_DEV_BAD_LENGTH and the block's
+ * rows see no key.  A chain (parent[i] = i - 1) is causal attention inside the
+ * block; T = 1 is the one-token decode.  At most 1024 nodes a block
+ * (MLA_ERR_UNSUPPORTED beyond).  Entries of the context that a window leaves
+ * to some rows only, and of the tree's nodes, must be finite; entries that no
+ * row sees may hold anything. */
+
+/* Latent attention of trees: mla_latent_attention with the visibility above
+ * (same q_abs, cache, desc, o_lat, lse; vis_stats counts what a node sees).
+ *   s_j = scale * <q_abs[m], entry_j>,  o_lat = sum_j softmax(s)_j entry_j[:r],
+ *   lse = log sum_j exp(s_j)
+ * workspace: mla_tree_attention_workspace_bytes() bytes, 256-byte aligned
+ * (NULL when that is 0). */
+size_t mla_tree_attention_workspace_bytes(const mla_handle_t *h, const mla_attn_desc_t *desc);
+mla_status_t mla_tree_attention(mla_handle_t *h, const void *q_abs, const int32_t *positions,
+                                const void *cache, int32_t num_pages,
+                                const mla_attn_desc_t *desc, const int32_t *parent,
+                                void *o_lat, float *lse, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* The whole layer over trees: mla_draft_forward with the tree's visibility in
+ * its attention (same arguments, results and errors; block_slot_mapping
+ * writes the nodes' own entries first, padding nodes take a free slot of
+ * their own). */
+size_t mla_forward_tree_workspace_bytes(const mla_handle_t *h, const mla_attn_desc_t *desc);
+mla_status_t mla_draft_forward_tree(mla_handle_t *h, const void *hidden,
+                                    const int32_t *positions,
+                                    const int64_t *block_slot_mapping, void *cache,
+                                    int32_t num_pages, const mla_attn_desc_t *desc,
+                                    const int32_t *parent, void *out, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/* The attention weight that every key of a block received from the block's
+ * rows, added to what it had:
+ *   weights_out[b, j] = decay * prior[b, j] + sum_m exp(scale <q_abs[m], entry_j> - lse[m])
+ * over the rows m = (query, head) of block b that see key j, for j < kv_len[b]
+ * (other elements are left as they are).  parent: the tree's (NULL: the rule
+ * of mla_attn_desc_t).  lse: device fp32 [nb*T, H], mla_tree_attention's or
+ * mla_latent_attention's for the same rows; a row with lse = -inf adds
+ * nothing.  prior, weights_out: device fp32 [num_blocks, ldw], the same
+ * pointer or disjoint; prior may be NULL (nothing before).  ldw < kv_len is
+ * reported as MLA_DEV_BAD_LENGTH and the keys behind it are left out.  Each
+ * key's sum is taken in one fixed order: equal calls give equal bits.
+ * vis_stats of desc is not written.  q_abs and cache 16-byte aligned. */
+mla_status_t mla_key_weights(mla_handle_t *h, const void *q_abs, const int32_t *positions,
+                             const void *cache, int32_t num_pages, const mla_attn_desc_t *desc,
+                             const int32_t *parent, const float *lse, float decay,
+                             const float *prior, float *weights_out, int64_t ldw, void *stream);
+
+/* Which keys of a sequence stay when it may hold `budget` of them: all when
+ * kv_len <= budget, else the first `sink`, the last `recent` and, of the
+ * others, the budget - sink - recent with the largest weights (equal weights:
+ * the lower index; NaN counts as less than -inf).  weights: device fp32
+ * [num_seqs, ldw]; keep: device int32 [num_seqs, budget], ascending indices,
+ * -1 behind the last; keep_len: device int32 [num_seqs].  kv_len > ldw is
+ * reported as MLA_DEV_BAD_LENGTH and taken as ldw. */
+mla_status_t mla_cache_select(mla_handle_t *h, const float *weights, int64_t ldw,
+                              const int32_t *kv_len, int32_t num_seqs, int32_t budget,
+                              int32_t sink, int32_t recent, int32_t *keep, int32_t *keep_len,
+                              void *stream);
+
+/* Moves the kept entries of every sequence together.  Row d of sequence b
+ * becomes its row src(d): d for d < first[b], keep[b, d - first[b]] for the
+ * keep_len[b] rows from first[b] on; keep (device int32 [num_seqs, ldk]) is
+ * ascending, every index in [first[b], kv_len[b]).  first: device int32
+ * [num_seqs], NULL = 0.  Eviction takes mla_cache_select's lists; an accepted
+ * path takes first = context length and keep = the accepted nodes' keys.
+ * The new length is first[b] + keep_len[b]; rows behind it are left as they
+ * are.  Entries are moved as they are: their rotation stays that of their old
+ * position, so positions go on counting tokens while logical indices move
+ * up.  A sliding window counts logical indices of the context: after an
+ * eviction use window 0.
+ *   dst_block_table NULL: in place.  No page may belong to two sequences of
+ * the call (or twice to one).  Else the rows go to the pages of
+ * dst_block_table [num_seqs, dst_max_pages], none of which is read by the call
+ * and none named twice.
+ *   weights, weights_out: NULL, or device fp32 [num_seqs, ldw], moved the same
+ * way (weights_out == weights exactly in place); elements first + keep_len ..
+ * kv_len - 1 of weights_out become 0.
+ * Reported on the device, the row or sequence left alone: an index that is not
+ * ascending or outside its sequence, keep_len > ldk or > kv_len - first
+ * (MLA_DEV_BAD_KEEP), a bad page, a kv_len beyond the table or ldw.
+ * workspace: mla_cache_compact_workspace_bytes() bytes, 256-byte aligned,
+ * needed in place only; two calls that may overlap on the GPU need two. */
+size_t mla_cache_compact_workspace_bytes(const mla_handle_t *h, int32_t num_seqs, int64_t ldk);
+mla_status_t mla_cache_compact(mla_handle_t *h, void *cache, int32_t num_pages,
+                               const int32_t *block_table, int32_t max_pages,
+                               const int32_t *kv_len, int32_t num_seqs, const int32_t *keep,
+                               int64_t ldk, const int32_t *keep_len, const int32_t *first,
+                               const int32_t *dst_block_table, int32_t dst_max_pages,
+                               const float *weights, float *weights_out, int64_t ldw,
+                               void *workspace, size_t workspace_bytes, void *stream);
 
 /* Synchronise `stream`, read and clear the device status word.  Returns
  * MLA_OK, MLA_ERR_TIMEOUT (MLA_DEV_TIMEOUT set) or MLA_ERR_DEVICE_CHECK; the
