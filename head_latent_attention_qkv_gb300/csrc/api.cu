@@ -15,6 +15,7 @@
 #include "gemm_tc.cuh"
 #include "simt.cuh"
 #include "tree.cuh"
+#include "tree_tc.cuh"
 
 namespace mla {
 
@@ -461,14 +462,20 @@ tree::Rule tree_rule(const mla_handle* h, const int32_t* positions, int num_page
 }
 
 // The attention of trees (mla_draft.h); `ws`: tree_ws() bytes.
-size_t tree_ws(const mla_handle*, const mla_attn_desc_t&) { return 0; }
+size_t tree_ws(const mla_handle* h, const mla_attn_desc_t& d) {
+  return h->cfg.dtype == MLA_BF16 ? tc::tree_attention_ws(h, d) : 0;
+}
 
 mla_status_t tree_attention(mla_handle_t* h, cudaStream_t st, const void* q_abs,
                             const int32_t* pos, const void* cache, int num_pages,
                             const mla_attn_desc_t& d, const int32_t* parent, void* o_lat, float* lse,
-                            void* ws) {
-  simt::tree_attention(st, h, tree_rule(h, pos, num_pages, d, parent), d.num_blocks, q_abs, cache,
-                       o_lat, lse, d.vis_stats);
+                            void* ws, bool pdl) {
+  const tree::Rule r = tree_rule(h, pos, num_pages, d, parent);
+  if (h->cfg.dtype == MLA_BF16)
+    return tc::tree_attention(st, h, r, d, (const __nv_bfloat16*)q_abs, (const __nv_bfloat16*)cache,
+                              (__half*)o_lat, lse, ws, pdl);
+  simt::tree_attention(st, h, r, d.num_blocks, q_abs, cache, o_lat, lse, d.vis_stats);
+  h->launches += 1;
   return MLA_OK;
 }
 
@@ -580,8 +587,9 @@ mla_status_t forward_impl(mla_handle_t* h, const void* hidden, const int32_t* po
   // launch after the wait: no programmatic edge crosses it)
   if (kv_ready) MLA_CUDA_TRY(cudaStreamWaitEvent(st, kv_ready, 0));
   if (parent) {
-    s = tree_attention(h, st, q_abs, pos, cache, num_pages, d, parent, o_lat, nullptr, ws + w.total);
+    s = tree_attention(h, st, q_abs, pos, cache, num_pages, d, parent, o_lat, nullptr, ws + w.total, pdl);
     if (s != MLA_OK) return s;
+    h->launches -= 1;     // counted with the other non-GEMM kernels below
   } else if constexpr (std::is_same<TX, float>::value) {
     simt::latent_attention<TI, TX>(st, h, q_abs, (const TX*)cache, num_pages, d, pos, o_lat);
   } else if (tc::decode_applies(h, d.block_len)) {
@@ -773,9 +781,8 @@ extern "C" mla_status_t mla_tree_attention(mla_handle_t* h, const void* q_abs,
   if (need && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 256))
     return fail(MLA_ERR_INVALID_ARG, "tree attention: workspace smaller than "
                                      "mla_tree_attention_workspace_bytes() or not 256-byte aligned");
-  h->launches += 1;
   s = tree_attention(h, (cudaStream_t)stream, q_abs, positions, cache, num_pages, d, parent, o_lat,
-                     lse, workspace);
+                     lse, workspace, false);
   if (s != MLA_OK) return s;
   MLA_CUDA_TRY(cudaGetLastError());
   return MLA_OK;

@@ -1,0 +1,33 @@
+// Launchers of the tensor-core kernels over trees (tree_attn_tc.cu).
+#pragma once
+
+#include <cuda.h>
+
+#include "tree.cuh"
+
+namespace mla {
+namespace tc {
+
+struct TreeParams {
+  CUtensorMap tmQ;    // Q_abs bf16 [rows, 576], chunked view, box 128 rows x 7 chunks
+  CUtensorMap tmC;    // the cache, chunked view, box 128 rows x 2 chunks
+  CUtensorMap tmK;    // the cache, box 64 dims x seg_rows
+  tree::Rule rule;
+  const __nv_bfloat16* q_abs;
+  __half* o_lat;      // [rows, 512]
+  float* lse;         // [rows] or NULL
+  int32_t* vis_stats;
+  float* part;        // [splits, rows, 512] when splits > 1
+  float* part_lse;    // [splits, rows] log2-sum-exp
+  long rows;
+  int splits, seg_rows, tiles_per_block;
+  float scale_log2;
+};
+
+size_t tree_attention_ws(const mla_handle* h, const mla_attn_desc_t& d);
+mla_status_t tree_attention(cudaStream_t st, mla_handle* h, const tree::Rule& r,
+                            const mla_attn_desc_t& d, const __nv_bfloat16* q_abs,
+                            const __nv_bfloat16* cache, __half* o_lat, float* lse, void* ws, bool pdl);
+
+}  // namespace tc
+}  // namespace mla
