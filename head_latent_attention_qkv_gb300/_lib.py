@@ -97,7 +97,8 @@ def _load():
         "mla_draft_forward_tree": (I32, [P, P, P, P, P, I32, C.POINTER(mla_attn_desc_t), P, P, P, SZ,
                                          P]),
         "mla_key_weights": (I32, [P, P, P, P, I32, C.POINTER(mla_attn_desc_t), P, P, C.c_float, P, P,
-                                  C.c_int64, P]),
+                                  C.c_int64, P, SZ, P]),
+        "mla_key_weights_workspace_bytes": (SZ, [P, C.POINTER(mla_attn_desc_t), C.c_int64]),
         "mla_cache_select": (I32, [P, P, C.c_int64, P, I32, I32, I32, I32, P, P, P]),
         "mla_cache_compact_workspace_bytes": (SZ, [P, I32, C.c_int64]),
         "mla_cache_compact": (I32, [P, P, I32, P, I32, P, I32, P, C.c_int64, P, P, P, I32, P, P,

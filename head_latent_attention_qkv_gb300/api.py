@@ -316,7 +316,7 @@ def mla_forward_tree_workspace_bytes(h: Handle, desc) -> int:
 
 
 def mla_key_weights(h: Handle, q_abs, positions, cache, desc, lse, weights_out, prior=None, decay=1.0,
-                    parent=None, stream=None):
+                    parent=None, stream=None, workspace=None):
     """``weights_out[b, j] = decay * prior[b, j] + `` the attention weight key j
     of block b received from the block's rows, whose log-sum-exp is ``lse``
     (mla_tree_attention's with ``parent``, mla_latent_attention's without);
@@ -326,11 +326,19 @@ def mla_key_weights(h: Handle, q_abs, positions, cache, desc, lse, weights_out, 
     rows = nb * desc.block_len * h.dims.num_heads
     out = _take("weights_out", weights_out, torch.float32, (nb, None), dev)
     ldw = weights_out.shape[1]
-    check(lib.mla_key_weights(h.h, q, pos, c, cache.shape[0], C.byref(desc), par,
-                              _take("lse", lse, torch.float32, (rows,), dev), decay,
-                              _opt("prior", prior, torch.float32, (nb, ldw), dev), out, ldw,
-                              _stream(stream)), "mla_key_weights")
+    with _on(stream):
+        need = lib.mla_key_weights_workspace_bytes(h.h, C.byref(desc), ldw)
+        ws = workspace if workspace is not None else (_buf(need, dev) if need else None)
+        check(lib.mla_key_weights(h.h, q, pos, c, cache.shape[0], C.byref(desc), par,
+                                  _take("lse", lse, torch.float32, (rows,), dev), decay,
+                                  _opt("prior", prior, torch.float32, (nb, ldw), dev), out, ldw,
+                                  None if ws is None else ws.data_ptr(),
+                                  0 if ws is None else ws.numel(), _stream(stream)), "mla_key_weights")
     return weights_out
+
+
+def mla_key_weights_workspace_bytes(h: Handle, desc, ldw: int) -> int:
+    return int(lib.mla_key_weights_workspace_bytes(h.h, C.byref(desc), ldw))
 
 
 def mla_cache_select(h: Handle, weights, kv_len, budget: int, sink: int = 0, recent: int = 0,

@@ -821,12 +821,19 @@ extern "C" mla_status_t mla_draft_forward_tree(mla_handle_t* h, const void* hidd
   return MLA_OK;
 }
 
+extern "C" size_t mla_key_weights_workspace_bytes(const mla_handle_t* h, const mla_attn_desc_t* desc,
+                                                  int64_t ldw) {
+  if (!h || !desc || desc->num_blocks <= 0 || desc->block_len <= 0 || desc->max_pages <= 0 || ldw <= 0) return 0;
+  return h->cfg.dtype == MLA_BF16 ? tc::key_weights_ws(h, *desc, (long)ldw) : 0;
+}
+
 extern "C" mla_status_t mla_key_weights(mla_handle_t* h, const void* q_abs, const int32_t* positions,
                                         const void* cache, int32_t num_pages,
                                         const mla_attn_desc_t* desc, const int32_t* parent,
                                         const float* lse, float decay, const float* prior,
-                                        float* weights_out, int64_t ldw, void* stream) {
-  const mla_status_t s = check_tree_desc(h, desc, "key weights");
+                                        float* weights_out, int64_t ldw, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  mla_status_t s = check_tree_desc(h, desc, "key weights");
   if (s != MLA_OK || desc->num_blocks == 0) return s;
   const mla_attn_desc_t& d = *desc;
   if (parent && d.block_len > tree::MAX_NODES)
@@ -838,9 +845,20 @@ extern "C" mla_status_t mla_key_weights(mla_handle_t* h, const void* q_abs, cons
     return fail(MLA_ERR_INVALID_ARG, "key weights: num_blocks * max_pages * page_size < 2^35");
   if ((uintptr_t)q_abs % 16 || (uintptr_t)cache % 16)
     return fail(MLA_ERR_INVALID_ARG, "key weights: q_abs and cache must be 16-byte aligned");
-  simt::key_weights((cudaStream_t)stream, h, tree_rule(h, positions, num_pages, d, parent), d.num_blocks,
-                    q_abs, cache, lse, decay, prior, weights_out, (long)ldw);
-  h->launches += 1;
+  const size_t need = mla_key_weights_workspace_bytes(h, desc, ldw);
+  if (need && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 256))
+    return fail(MLA_ERR_INVALID_ARG, "key weights: workspace smaller than "
+                                     "mla_key_weights_workspace_bytes() or not 256-byte aligned");
+  const tree::Rule r = tree_rule(h, positions, num_pages, d, parent);
+  if (h->cfg.dtype == MLA_BF16) {
+    s = tc::key_weights((cudaStream_t)stream, h, r, d, (const __nv_bfloat16*)q_abs,
+                        (const __nv_bfloat16*)cache, lse, decay, prior, weights_out, (long)ldw, workspace);
+    if (s != MLA_OK) return s;
+  } else {
+    simt::key_weights((cudaStream_t)stream, h, r, d.num_blocks, q_abs, cache, lse, decay, prior, weights_out,
+                      (long)ldw);
+    h->launches += 1;
+  }
   MLA_CUDA_TRY(cudaGetLastError());
   return MLA_OK;
 }

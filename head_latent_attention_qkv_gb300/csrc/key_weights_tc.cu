@@ -1,0 +1,450 @@
+// tcgen05 key weights (mla_draft.h has the formula, tree.cuh the rule of
+// visibility; bf16 layers, entries 512 + 64): per cached key the sum over the
+// block's rows of exp(scale <q, e> - lse).
+//
+// The keys are the MMA's M: S^T = E Q^T puts a key on a tensor-memory lane and
+// its rows on the columns, so a key's sum over the rows stays in the registers
+// of its two threads and nothing crosses lanes.  Two CTAs work on one MMA
+// (cta_group::2): each holds 128 keys (nine 64-dim chunks, 144 KB, all of its
+// shared memory's worth) and half of the rows of Q, which streams past in
+// 16 KB chunks of 128 rows; a pair's MMA of 256 keys x 256 rows x 64 dims takes
+// 512 cycles, in which each SM has 16 KB of Q to fetch (64 dims of 128 keys
+// alone would need 32 KB).  The keys are read from HBM once; a chunk trio is
+// refilled for the next key tile as soon as the last rows are done with it, so
+// for few rows (decode) the kernel is a stream over the cache.
+//
+// Persistent: the (block, 256-key tile, row part) items are dealt out to the
+// pairs in turn.  The scores of one row tile are summed while the next are
+// computed (two accumulators of 256 columns).  exp2 by the hardware
+// approximation (2^-22), the arguments in fp32.  Keys wholly inside the context
+// of rows without a window need no mask; otherwise every lane works out the 32
+// keys of its warp for four columns (tree::key_bits) and the words are
+// broadcast.  When the key tiles alone do not fill the GPU the rows are cut in
+// parts whose sums a second kernel adds in order.
+#include <math.h>
+
+#include <mutex>
+
+#include "gemm_tc.cuh"
+#include "pair_ptx.cuh"
+#include "tree_tc.cuh"
+
+namespace mla {
+namespace tc {
+namespace {
+
+constexpr int KT = 128, PAIR_KT = 2 * KT, NCH = 9, TRIO = 3, NMAX = 256;
+constexpr int CH_BYTES = 128 * 64 * 2, QSLOTS = 5;
+constexpr int THREADS = 384;                              // sums x4, MMA, keys, Q x2, sums x4
+constexpr int W_MMA = 4, W_KEYS = 5, W_Q = 6;
+constexpr int OFF_K = 0, OFF_Q = OFF_K + NCH * CH_BYTES, OFF_BAR = OFF_Q + QSLOTS * CH_BYTES;
+constexpr int OFF_LSE = OFF_BAR + 256, SMEM_BYTES = 1024 + OFF_LSE + NMAX * 4;
+static_assert(SMEM_BYTES <= 232448, "shared memory");
+constexpr uint32_t TMEM_COLS = 512;
+
+struct Bars {
+  uint64_t k_full[TRIO], k_empty[TRIO];
+  uint64_t q_full[QSLOTS], q_empty[QSLOTS];
+  uint64_t s_full[2], s_free[2];
+  uint64_t drain;
+  uint32_t tmem_slot;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+__device__ __forceinline__ bool wait_bar(Bars* B, uint64_t* bar, uint32_t parity, uint32_t* st) {
+  if (*(volatile int*)&B->abort) return false;
+  if (mbar_test_wait_cluster(bar, parity)) return true;
+  for (uint32_t i = 0; i < kWaitBudget; ++i)
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+  set_status(st, MLA_DEV_TIMEOUT);
+  B->abort = 1;
+  return false;
+}
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void sum_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// One (block, 256-key tile, row part) item; every role of both CTAs walks the
+// same items.  Called by whole warps.
+struct Items {
+  const WeightParams& P;
+  long id, step;
+  int b0 = 0;                 // blocks before b0 hold `before` key tiles
+  long before = 0;
+  // the item at hand
+  int b, n, n0, W, ctx, kt, sp, qt0, qt1;
+  bool skip;                  // no row of the block reaches the tile (windows)
+
+  __device__ Items(const WeightParams& p) : P(p), id(blockIdx.x >> 1), step(gridDim.x >> 1) {}
+
+  __device__ bool next() {
+    const tree::Rule& R = P.rule;
+    const int lane = threadIdx.x % 32;
+    const long tile = id / P.splits;
+    sp = (int)(id - tile * P.splits);
+    id += step;
+    while (b0 < P.num_blocks) {
+      int t = 0;
+      if (b0 + lane < P.num_blocks) {
+        int w, c;
+        const long keys = min((long)tree::block_keys(R, b0 + lane, &w, &c, false), P.ldw);
+        t = (int)((keys + PAIR_KT - 1) / PAIR_KT);
+      }
+      int x = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const long total = __shfl_sync(0xffffffffu, x, 31);
+      if (tile < before + total) {
+        const uint32_t m = __ballot_sync(0xffffffffu, tile < before + x);
+        const int l = __ffs(m) - 1;
+        b = b0 + l;
+        kt = (int)(tile - before) - (__shfl_sync(0xffffffffu, x, l) - __shfl_sync(0xffffffffu, t, l));
+        n0 = tree::block_keys(R, b, &W, &ctx, false);
+        n = (int)min((long)n0, P.ldw);
+        const int tiles = (R.T * R.H + NMAX - 1) / NMAX;
+        qt0 = (int)((long)sp * tiles / P.splits);
+        qt1 = (int)((long)(sp + 1) * tiles / P.splits);
+        skip = qt0 == qt1;
+        if (W > 0 && (kt + 1) * PAIR_KT <= ctx) {
+          int pmin = 0x7fffffff;
+          for (int i = lane; i < R.T; i += 32) pmin = min(pmin, R.positions[(long)b * R.T + i]);
+          pmin = __reduce_min_sync(0xffffffffu, pmin);
+          skip |= (kt + 1) * PAIR_KT <= pmin - W + 1;
+        }
+        return true;
+      }
+      before += total;
+      b0 += 32;
+    }
+    return false;
+  }
+  __device__ int rows(int qt) const { return min(NMAX, P.rule.T * P.rule.H - qt * NMAX); }
+  // columns of row tile qt's MMA (each CTA holds half of them)
+  __device__ int cols(int qt) const { return (rows(qt) + 31) & ~31; }
+};
+
+__device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t* smem, uint32_t tmem,
+                                         int rank) {
+  const tree::Rule& R = P.rule;
+  const int key = threadIdx.x & (KT - 1), half = threadIdx.x >= 256 ? 1 : 0;
+  const int w = key / 32, lane = threadIdx.x % 32, col_id = half * 128 + key;
+  const uint32_t lane_base = (uint32_t)(w * 32) << 16;
+  float* lse2 = (float*)(smem + OFF_LSE);
+  const uint32_t s_free0 = mapa(smem_u32(&B->s_free[0]), 0), s_free1 = mapa(smem_u32(&B->s_free[1]), 0);
+  constexpr float kLog2e = 1.4426950408889634f;
+  uint32_t tile = 0;                                      // row tiles so far, over all items
+  Items it(P);
+  while (it.next()) {
+    const int j = it.kt * PAIR_KT + rank * KT + key;
+    const int jw = j - lane;                              // the warp's first key
+    float sum = 0.f;
+    if (!it.skip) {
+      for (int qt = it.qt0; qt < it.qt1; ++qt, ++tile) {
+        const int rows = it.rows(qt), cols = it.cols(qt);
+        const long row0 = (long)it.b * R.T * R.H + (long)qt * NMAX;
+        // each thread's own column: its row's log-sum-exp, and whether the row counts
+        sum_sync();                                       // the last tile's values have been read
+        {
+          float l = -INFINITY;
+          if (col_id < rows) l = P.lse[row0 + col_id];
+          lse2[col_id] = l * kLog2e;
+        }
+        // the warp's 32 keys as this lane's four columns see them
+        uint32_t word[4];
+        bool all = true;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = half * 128 + 32 * q + lane;
+          word[q] = 0;
+          if (c < rows) {
+            const int node = (qt * NMAX + c) / R.H;
+            const long m = (long)it.b * R.T + node;
+            bool ok = (R.q_visible ? R.q_visible[m] != 0 : true) && P.lse[row0 + c] != -INFINITY;
+            if (ok && R.parent)
+              ok = tree::in_tree(R, R.parent + (long)it.b * R.T, node, jw == 0);
+            word[q] = (uint32_t)tree::key_bits(R, it.b, node, ok, it.n0, it.W, it.ctx, jw);
+          }
+          all = all && (word[q] == 0xffffffffu || c >= cols);
+        }
+        all = __all_sync(0xffffffffu, all);
+        sum_sync();
+        const int buf = tile & 1;
+        wait_bar(B, &B->s_full[buf], (tile >> 1) & 1, R.status);
+        tc_fence_after();
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c0 = half * 128 + 32 * q;
+          if (c0 < cols) {
+            float s[32];
+            tmem_ld32(tmem + buf * NMAX + c0 + lane_base, s);
+            if (all) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(lse2 + c0 + i);
+                part[0] += fast_exp2(fmaf(s[i], P.scale_log2, -l.x));
+                part[1] += fast_exp2(fmaf(s[i + 1], P.scale_log2, -l.y));
+                part[2] += fast_exp2(fmaf(s[i + 2], P.scale_log2, -l.z));
+                part[3] += fast_exp2(fmaf(s[i + 3], P.scale_log2, -l.w));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const uint32_t m = __shfl_sync(0xffffffffu, word[q], i);
+                const float p = fast_exp2(fmaf(s[i], P.scale_log2, -lse2[c0 + i]));
+                part[i & 3] += ((m >> lane) & 1u) ? p : 0.f;
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(buf ? s_free1 : s_free0);
+        sum += (part[0] + part[1]) + (part[2] + part[3]);
+      }
+    }
+    // the key's two halves; half 0 writes
+    sum_sync();
+    if (half) lse2[key] = sum;
+    sum_sync();
+    if (!half && j < it.n) {
+      const float t = sum + lse2[key];
+      if (P.splits > 1) {
+        P.part[((long)it.sp * P.num_blocks + it.b) * P.ldp + j] = t;
+      } else {
+        const long at = (long)it.b * P.ldw + j;
+        P.out[at] = P.prior ? fmaf(P.decay, P.prior[at], t) : t;
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid_constant__ WeightParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  Bars* B = (Bars*)(smem + OFF_BAR);
+  const tree::Rule& R = P.rule;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int rank = (int)cluster_ctarank();
+  if (tid == 0) {
+    for (int i = 0; i < TRIO; ++i) { mbar_init(&B->k_full[i], 1); mbar_init(&B->k_empty[i], 1); }
+    for (int i = 0; i < QSLOTS; ++i) { mbar_init(&B->q_full[i], 1); mbar_init(&B->q_empty[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&B->s_full[i], 1); mbar_init(&B->s_free[i], 16); }
+    mbar_init(&B->drain, 1);
+    B->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == W_MMA) tmem_alloc_pair(&B->tmem_slot, TMEM_COLS);
+  if (blockIdx.x == 0)
+    for (int b = tid; b < P.num_blocks; b += THREADS) {
+      int w, c;
+      if (tree::block_keys(R, b, &w, &c, true) > P.ldw) set_status(R.status, MLA_DEV_BAD_LENGTH);
+    }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();          // both CTAs' barriers are up
+  tc_fence_after();
+  const uint32_t tmem = B->tmem_slot;
+
+  if (warp == W_KEYS) {
+    // ---- the CTA's 128 keys of every item, in three trios of chunks ----
+    const int ps = R.page_size, past_end = R.num_pages * ps, seg = P.seg_rows, nseg = KT / seg;
+    if (lane == 0) prefetch_tmap(&P.tmC);
+    uint32_t use = 0;
+    bool ok = true;
+    Items it(P);
+    while (ok && it.next()) {
+      if (it.skip) continue;
+      int y = past_end;
+      const int j = it.kt * PAIR_KT + rank * KT + lane * seg;
+      if (lane < nseg && j < it.n) {
+        const int pg = R.block_table[(long)it.b * R.max_pages + j / ps];
+        if (pg >= 0 && pg < R.num_pages) y = pg * ps + j % ps;
+        else set_status(R.status, MLA_DEV_BAD_PAGE);
+      }
+      for (int c3 = 0; c3 < TRIO && ok; ++c3) {
+        ok = wait_bar(B, &B->k_empty[c3], (use & 1) ^ 1, R.status);
+        if (!ok) break;
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&B->k_full[c3], 2 * 3 * CH_BYTES);
+        __syncwarp();
+        const uint32_t bar = mapa(smem_u32(&B->k_full[c3]), 0);
+        uint8_t* dst = smem + OFF_K + 3 * c3 * CH_BYTES;
+        if (nseg == 1) {
+          if (lane == 0) tma_load_3d_pair(dst, &P.tmC, bar, 0, y, 3 * c3);
+        } else if (lane < nseg) {
+          for (int c = 0; c < 3; ++c)
+            tma_load_3d_pair(dst + c * CH_BYTES + lane * seg * 128, &P.tmK, bar, (3 * c3 + c) * 64, y, 0);
+        }
+        __syncwarp();
+      }
+      ++use;
+    }
+    // every copy has landed before the pair may exit (its barriers are the even CTA's)
+    if (rank == 0 && use > 0)
+      for (int i = 0; i < TRIO; ++i) mbar_wait_cluster(&B->k_full[i], (use - 1) & 1, R.status);
+  } else if (warp == W_Q || warp == W_Q + 1) {
+    // ---- this CTA's half of the rows, chunk by chunk; the two warps take turns ----
+    if (lane == 0) prefetch_tmap(&P.tmQ);
+    uint32_t u = 0;                                       // chunks so far
+    int last = -1;
+    bool ok = true;
+    Items it(P);
+    while (ok && it.next()) {
+      if (it.skip) continue;
+      for (int qt = it.qt0; qt < it.qt1 && ok; ++qt) {
+        const int y = (int)((long)it.b * R.T * R.H + (long)qt * NMAX + rank * (it.cols(qt) / 2));
+        for (int c = 0; c < NCH; ++c, ++u) {
+          if ((u & 1) != (uint32_t)(warp - W_Q)) continue;
+          const int s = u % QSLOTS;
+          ok = wait_bar(B, &B->q_empty[s], ((u / QSLOTS) & 1) ^ 1, R.status);
+          if (!ok) break;
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(&B->q_full[s], 2 * P.q_box_rows * 128);
+            tma_load_3d_pair(smem + OFF_Q + s * CH_BYTES, &P.tmQ, mapa(smem_u32(&B->q_full[s]), 0), c * 64, y, 0);
+          }
+          __syncwarp();
+          last = (int)u;
+        }
+      }
+    }
+    if (rank == 0 && last >= 0)
+      mbar_wait_cluster(&B->q_full[last % QSLOTS], (last / QSLOTS) & 1, R.status);
+  } else if (warp == W_MMA && rank == 0) {
+    // ---- MMA issue for the pair (the even CTA) ----
+    constexpr uint64_t U_CH = CH_BYTES / 16;
+    const uint64_t dK = smem_desc_sw128(smem + OFF_K), dQ = smem_desc_sw128(smem + OFF_Q);
+    uint32_t use = 0, tile = 0;
+    int s = 0;
+    uint32_t qpar = 0;
+    bool ok = true;
+    Items it(P);
+    while (ok && it.next()) {
+      if (it.skip) continue;
+      if (lane == 0) {
+        for (int qt = it.qt0; qt < it.qt1 && ok; ++qt, ++tile) {
+          const int buf = tile & 1;
+          const uint32_t d = tmem + buf * NMAX, idesc = idesc_f16(256, it.cols(qt), false);
+          if (!(ok = wait_bar(B, &B->s_free[buf], ((tile >> 1) & 1) ^ 1, R.status))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < NCH; ++c) {
+            if (qt == it.qt0 && c % 3 == 0 && ok) ok = wait_bar(B, &B->k_full[c / 3], use & 1, R.status);
+            if (!ok || !(ok = wait_bar(B, &B->q_full[s], qpar, R.status))) break;
+            tc_fence_after();
+            const uint64_t db = dQ + s * U_CH;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16_pair(d, dK + c * U_CH + 2 * k, db + 2 * k, idesc, (c | k) ? 1u : 0u);
+            mma_commit_pair(&B->q_empty[s]);
+            if (qt == it.qt1 - 1 && c % 3 == 2) mma_commit_pair(&B->k_empty[c / 3]);
+            if (++s == QSLOTS) { s = 0; qpar ^= 1; }
+          }
+          mma_commit_pair(&B->s_full[buf]);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+      ++use;
+    }
+    if (lane == 0) {
+      mma_commit_pair(&B->drain);
+      mbar_wait_cluster(&B->drain, 0, R.status);
+    }
+  } else if (warp != W_MMA) {
+    sum_role(P, B, smem, tmem, rank);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();          // the pair's MMAs and copies are done in both CTAs
+  tc_fence_after();
+  if (warp == W_MMA) tmem_dealloc_pair(tmem, TMEM_COLS);
+}
+
+// out = decay * prior + the row parts' sums, in order.
+__global__ void __launch_bounds__(256) weights_finish_kernel(const WeightParams P) {
+  const long t = blockIdx.x * 256L + threadIdx.x;
+  const int b = (int)(t / P.ldp);
+  const long j = t % P.ldp;
+  if (b >= P.num_blocks) return;
+  int W, ctx;
+  const long n = min((long)tree::block_keys(P.rule, b, &W, &ctx, false), P.ldw);
+  if (j >= n) return;
+  float sum = 0.f;
+  for (int s = 0; s < P.splits; ++s) sum += P.part[((long)s * P.num_blocks + b) * P.ldp + j];
+  const long at = (long)b * P.ldw + j;
+  P.out[at] = P.prior ? fmaf(P.decay, P.prior[at], sum) : sum;
+}
+
+long key_tiles(const mla_handle* h, const mla_attn_desc_t& d, long ldw) {
+  const long cap = (long)d.max_pages * h->cfg.page_size;
+  return ((ldw < cap ? ldw : cap) + PAIR_KT - 1) / PAIR_KT;
+}
+
+// Parts of a block's rows: as many as give every pair of SMs two items, by the
+// page table's bound on the keys.
+int weight_splits(const mla_handle* h, const mla_attn_desc_t& d, long ldw) {
+  const long rows = (long)d.block_len * h->lay.H, row_tiles = (rows + NMAX - 1) / NMAX;
+  const long items = (long)d.num_blocks * key_tiles(h, d, ldw), pairs = h->num_sms / 2;
+  if (items >= 2 * pairs) return 1;
+  const long s = (2 * pairs + items - 1) / items;
+  return (int)(s < row_tiles ? s : row_tiles);
+}
+
+}  // namespace
+
+size_t key_weights_ws(const mla_handle* h, const mla_attn_desc_t& d, long ldw) {
+  const int s = weight_splits(h, d, ldw);
+  return s == 1 ? 0 : align256((size_t)s * d.num_blocks * key_tiles(h, d, ldw) * PAIR_KT * 4);
+}
+
+mla_status_t key_weights(cudaStream_t st, mla_handle* h, const tree::Rule& r, const mla_attn_desc_t& d,
+                         const __nv_bfloat16* q_abs, const __nv_bfloat16* cache, const float* lse,
+                         float decay, const float* prior, float* out, long ldw, void* ws) {
+  const Layout& l = h->lay;
+  const long rows = (long)d.num_blocks * r.T * r.H, slots = (long)r.num_pages * r.page_size;
+  if (slots > 0x7fffffffL) return fail(MLA_ERR_UNSUPPORTED, "key weights: num_pages * page_size < 2^31");
+  WeightParams P;
+  const long block_rows = (long)r.T * r.H;
+  P.q_box_rows = (int)((block_rows < NMAX ? (block_rows + 31) & ~31L : NMAX) / 2);
+  P.seg_rows = r.page_size < KT ? r.page_size : KT;
+  if (!make_tmap_2d(&P.tmQ, false, q_abs, rows, l.L, l.L, P.q_box_rows) ||
+      !make_tmap_chunked(&P.tmC, false, cache, slots, l.L, l.L, KT, 3) ||
+      !make_tmap_2d(&P.tmK, false, cache, slots, l.L, l.L, P.seg_rows))
+    return fail(MLA_ERR_CUDA, "key weights: cuTensorMapEncodeTiled failed");
+  P.rule = r;
+  P.lse = lse;
+  P.prior = prior;
+  P.out = out;
+  P.part = (float*)ws;
+  P.ldw = ldw;
+  P.ldp = key_tiles(h, d, ldw) * PAIR_KT;
+  P.num_blocks = d.num_blocks;
+  P.splits = weight_splits(h, d, ldw);
+  P.decay = decay;
+  P.scale_log2 = h->scale * 1.4426950408889634f;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    cudaFuncSetAttribute(key_weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  });
+  const long items = (long)d.num_blocks * key_tiles(h, d, ldw) * P.splits, pairs = h->num_sms / 2;
+  Launch L(dim3((unsigned)(2 * (items < pairs ? items : pairs))), dim3(THREADS), SMEM_BYTES, st, false,
+           dim3(2, 1, 1));
+  cudaError_t e = cudaLaunchKernelEx(&L.cfg, key_weights_tc_kernel, P);
+  if (e != cudaSuccess) return cuda_fail(e, "key weights launch");
+  h->launches += 1;
+  if (P.splits > 1) {
+    weights_finish_kernel<<<(unsigned)((d.num_blocks * P.ldp + 255) / 256), 256, 0, st>>>(P);
+    h->launches += 1;
+  }
+  return MLA_OK;
+}
+
+}  // namespace tc
+}  // namespace mla

@@ -1,4 +1,4 @@
-// Launchers of the tensor-core kernels over trees (tree_attn_tc.cu).
+// Launchers of the tensor-core kernels over trees (tree_attn_tc.cu, key_weights_tc.cu).
 #pragma once
 
 #include <cuda.h>
@@ -24,10 +24,30 @@ struct TreeParams {
   float scale_log2;
 };
 
+struct WeightParams {
+  CUtensorMap tmQ;    // Q_abs, box 64 dims x q_box_rows
+  CUtensorMap tmC;    // the cache, chunked view, box 128 rows x 3 chunks
+  CUtensorMap tmK;    // the cache, box 64 dims x seg_rows
+  tree::Rule rule;
+  const float* lse;
+  const float* prior; // may be NULL
+  float* out;         // [num_blocks, ldw]
+  float* part;        // [splits, num_blocks, ldp] when splits > 1
+  long ldw, ldp;
+  int num_blocks, splits, seg_rows, q_box_rows;
+  float decay, scale_log2;
+};
+
 size_t tree_attention_ws(const mla_handle* h, const mla_attn_desc_t& d);
 mla_status_t tree_attention(cudaStream_t st, mla_handle* h, const tree::Rule& r,
                             const mla_attn_desc_t& d, const __nv_bfloat16* q_abs,
                             const __nv_bfloat16* cache, __half* o_lat, float* lse, void* ws, bool pdl);
+
+
+size_t key_weights_ws(const mla_handle* h, const mla_attn_desc_t& d, long ldw);
+mla_status_t key_weights(cudaStream_t st, mla_handle* h, const tree::Rule& r, const mla_attn_desc_t& d,
+                         const __nv_bfloat16* q_abs, const __nv_bfloat16* cache, const float* lse,
+                         float decay, const float* prior, float* out, long ldw, void* ws);
 
 }  // namespace tc
 }  // namespace mla

@@ -446,11 +446,16 @@ mla_status_t mla_draft_forward_tree(mla_handle_t *h, const void *hidden,
  * pointer or disjoint; prior may be NULL (nothing before).  ldw < kv_len is
  * reported as MLA_DEV_BAD_LENGTH and the keys behind it are left out.  Each
  * key's sum is taken in one fixed order: equal calls give equal bits.
- * vis_stats of desc is not written.  q_abs and cache 16-byte aligned. */
+ * vis_stats of desc is not written.  q_abs and cache 16-byte aligned.
+ * workspace: mla_key_weights_workspace_bytes() bytes, 256-byte aligned (NULL
+ * when that is 0). */
+size_t mla_key_weights_workspace_bytes(const mla_handle_t *h, const mla_attn_desc_t *desc,
+                                       int64_t ldw);
 mla_status_t mla_key_weights(mla_handle_t *h, const void *q_abs, const int32_t *positions,
                              const void *cache, int32_t num_pages, const mla_attn_desc_t *desc,
                              const int32_t *parent, const float *lse, float decay,
-                             const float *prior, float *weights_out, int64_t ldw, void *stream);
+                             const float *prior, float *weights_out, int64_t ldw,
+                             void *workspace, size_t workspace_bytes, void *stream);
 
 /* Which keys of a sequence stay when it may hold `budget` of them: all when
  * kv_len <= budget, else the first `sink`, the last `recent` and, of the
