@@ -17,7 +17,10 @@
 // L2.  The stream of a CTA is, per tile, four pairs of 64-dim key chunks and two
 // pairs of value chunks, through a ring of three 32 KB slots, each refilled by
 // a warp of its own (a copy holds its thread for about 550 cycles), and the
-// 16 KB rope chunk in a slot of its own, read last.
+// 16 KB rope chunk in a slot of its own, read last.  The scores and P V are issued by
+// two threads, and each looks at its next barrier before it issues the MMAs of
+// the one at hand: a look at a barrier takes about 340 cycles, the eight MMAs
+// of a pair 512 (one issuer that waited in turn: 7.3 k cycles a tile).
 //
 // Softmax: warps 0-3 and 8-11, two threads a row (64 keys and 128 value
 // columns each) that exchange their half maxima; fp32, exp2 domain, O rescaled
@@ -48,28 +51,37 @@ constexpr int QROWS = 128, KT = 128, NCH = 9;
 constexpr int CH_BYTES = 128 * 64 * 2;                    // a 64-dim chunk of 128 rows
 constexpr int NQT = 2, NQS = NCH - NQT;                   // Q chunks in tensor / shared memory
 constexpr int SLOTS = 3, SLOT_BYTES = 2 * CH_BYTES;
-constexpr int THREADS = 416;                              // softmax x4, MMA, ring x3, softmax x4, Q and rope
-constexpr int W_MMA = 4, W_RING = 5, W_ROPE = 12;
+constexpr int THREADS = 448;                              // softmax x4, S, ring x3, softmax x4, PV, Q and rope
+constexpr int W_S = 4, W_RING = 5, W_PV = 12, W_ROPE = 13;
 constexpr int OFF_Q = 0, OFF_RING = OFF_Q + NQS * CH_BYTES, OFF_ROPE = OFF_RING + SLOTS * SLOT_BYTES;
 constexpr int OFF_BAR = OFF_ROPE + CH_BYTES, OFF_SEEN = OFF_BAR + 256, OFF_XM = OFF_SEEN + tree::MAX_NODES / 8;
 constexpr int SMEM_BYTES = 1024 + OFF_XM + 2 * QROWS * 4;
+// the epilogue's rows, over Q and the ring: fp32, 256 dims, padded against bank conflicts
+constexpr int STG_PITCH = 260;
+static_assert(QROWS * STG_PITCH * 4 <= OFF_BAR, "staging");
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 constexpr uint32_t TMEM_COLS = 512, TM_O = 0, TM_S = 256, TM_P = 384, TM_Q = 448;
+constexpr int MAX_SPLITS = 64;
 constexpr float RESCALE_LOG2 = 8.f, kLn2 = 0.6931471805599453f;
 
 struct Bars {
   uint64_t q_full, q_tmem;            // Q in shared memory (TMA) / in tensor memory
-  uint64_t full[SLOTS], empty[SLOTS], clean[SLOTS];
+  // a slot's keys and its values land on barriers of their own: each has one
+  // consumer, which never falls two phases behind (a parity tells only two apart)
+  uint64_t k_full[SLOTS], v_full[SLOTS], empty[SLOTS], clean[SLOTS];
   uint64_t rope_full, rope_empty;
   uint64_t s_full, s_free;            // S(t) complete / read
   uint64_t p_full, o_done;            // P(t) written / P(t) V(t) complete
-  uint64_t drain;
+  uint64_t seen_full;                 // z_lo and the nodes' bits are known
+  uint64_t drain[2];
   uint32_t tmem_slot;
-  int abort, z_lo, any;
+  int abort, z_lo;
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
-__device__ __forceinline__ bool wait_bar(Bars* B, uint64_t* bar, uint32_t parity, uint32_t* st) {
+__device__ __forceinline__ bool wait_bar(Bars* B, uint64_t* bar, uint32_t parity, uint32_t* st,
+                                         bool ready = false) {
+  if (ready) return true;
   if (*(volatile int*)&B->abort) return false;
   if (mbar_wait(bar, parity, st)) return true;
   B->abort = 1;
@@ -84,7 +96,8 @@ __device__ __forceinline__ float fast_exp2(float x) {
 // The 64 threads of a row group (warps w and w + 8).
 __device__ __forceinline__ void pair_sync(int w) { asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory"); }
 
-// What use u of the ring holds: keys (pair 0..3) or values (pair 0..1) of a tile.
+// What use u of the ring holds: keys (pair 0..3) or values (pair 0..1) of a
+// tile.  The order is that of the tensor pipe: S(0), S(1), PV(0), S(2), ...
 struct Item {
   int tile, pair;
   bool value;
@@ -95,17 +108,19 @@ __device__ __forceinline__ Item item_of(int u, int nt) {
   if (g < nt - 1) return i < 4 ? Item{g + 1, i, false} : Item{g, i - 4, true};
   return Item{nt - 1, i, true};
 }
+__device__ __forceinline__ int first_key_use(int t) { return t == 0 ? 0 : 6 * t - 2; }
+__device__ __forceinline__ int first_value_use(int t, int nt) { return 6 * t + (t < nt - 1 ? 8 : 4); }
 
 struct Unit {
-  int b, qt, half, n, W, ctx, j_lo, nt, z_lo;
+  int b, qt, half, n, W, ctx, j_lo, nt;
   long row0;
 };
 
 // Tiles whose value rows need clearing: those that reach the block's own keys
 // or the end, and those that reach below the first key that a row sees.
-__device__ __forceinline__ bool dirty_tile(const Unit& U, int t) {
+__device__ __forceinline__ bool dirty_tile(const Unit& U, int z_lo, int t) {
   const int j0 = U.j_lo + t * KT;
-  return j0 + KT > U.ctx || j0 < U.z_lo;
+  return j0 + KT > U.ctx || j0 < z_lo;
 }
 
 __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8_t* smem, uint32_t tmem,
@@ -121,11 +136,21 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   const long m = (long)U.b * R.T + node;
   const int32_t* parent = R.parent + (long)U.b * R.T;
   const bool ok = live && U.n > 0 && (R.q_visible ? R.q_visible[m] != 0 : true) &&
-                  tree::in_tree(R, parent, node, false);
+                  tree::in_tree(R, parent, node, U.half == 0 && kh == 0);
   // rows that see nothing are computed like their neighbours and written as
   // zeros, so that they do not take a warp off the unmasked path
   const int lo = U.W > 0 ? max(0, R.positions[m] - U.W + 1) : 0;
   float mrun = -INFINITY, lsum = 0.f;
+  // what the unit's rows see: the first context key and the nodes on their
+  // paths (one row of a node stands for all)
+  if (ok && !kh && (row_in_block % R.H == 0 || r == 0)) {
+    uint32_t* seen = (uint32_t*)(smem + OFF_SEEN);
+    const int32_t* pos = R.positions + (long)U.b * R.T;
+    atomicMin(&B->z_lo, min(lo, U.ctx));
+    for (int k = node; k >= 0; k = parent[k])
+      if (U.W == 0 || pos[node] - pos[k] < U.W) atomicOr(&seen[k >> 5], 1u << (k & 31));
+  }
+  mbar_arrive(&B->seen_full);
   if (U.nt > 0) {
     // Q dims 0..127 of this row -> tensor memory (bf16 pairs), 64 dims a thread
     const uint4* src = reinterpret_cast<const uint4*>(P.q_abs + (U.row0 + r) * 576 + 64 * kh);
@@ -215,29 +240,17 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   tc_fence_after();
   const bool any = ok && U.nt > 0 && lsum > 0.f;
   const float inv = any ? 1.f / lsum : 0.f;
-  const int col = U.half * 256 + 128 * kh;
   const long row = U.row0 + r;
+  float* prow = (float*)smem + r * STG_PITCH + 128 * kh;
 #pragma unroll 1
   for (int c = 0; c < 128; c += 32) {
     float o[32];
     if (U.nt > 0) tmem_ld32(tmem + TM_O + lane_base + 128 * kh + c, o);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = any ? o[i] * inv : 0.f;
-    if (!live) continue;
-    if (P.splits == 1) {
-      uint4* dst = reinterpret_cast<uint4*>(P.o_lat + row * 512 + col + c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        __half2 h2[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) h2[k] = __floats2half2_rn(o[8 * i + 2 * k], o[8 * i + 2 * k + 1]);
-        dst[i] = *reinterpret_cast<uint4*>(h2);
-      }
-    } else if (any) {
-      float4* dst = reinterpret_cast<float4*>(P.part + ((long)blockIdx.y * P.rows + row) * 512 + col + c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-    }
+    for (int i = 0; i < 32; i += 4)
+      *reinterpret_cast<float4*>(prow + c + i) =
+          any ? make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv)
+              : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   if (!live || U.half || kh) return;
   const float l2 = any ? mrun + log2f(lsum) : -INFINITY;
@@ -269,6 +282,26 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   }
 }
 
+// The staged rows, whole: a warp per row, 16 or 32 bytes a lane.
+__device__ __forceinline__ void store_rows(const TreeParams& P, const uint8_t* smem, const Unit& U) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rows = min(QROWS, P.rule.T * P.rule.H - U.qt * QROWS);
+  for (int r = warp; r < rows; r += THREADS / 32) {
+    const float4* src = (const float4*)((const float*)smem + r * STG_PITCH);
+    const long row = U.row0 + r;
+    if (P.splits == 1) {
+      const float4 a = src[2 * lane], c = src[2 * lane + 1];
+      __half2 h2[4] = {__floats2half2_rn(a.x, a.y), __floats2half2_rn(a.z, a.w), __floats2half2_rn(c.x, c.y),
+                       __floats2half2_rn(c.z, c.w)};
+      *reinterpret_cast<uint4*>(P.o_lat + row * 512 + U.half * 256 + 8 * lane) = *reinterpret_cast<uint4*>(h2);
+    } else {
+      float4* dst = reinterpret_cast<float4*>(P.part + ((long)blockIdx.y * P.rows + row) * 512 + U.half * 256);
+      dst[lane] = src[lane];
+      dst[lane + 32] = src[lane + 32];
+    }
+  }
+}
+
 __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_constant__ TreeParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -287,7 +320,8 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
     mbar_init(&B->q_full, 1);
     mbar_init(&B->q_tmem, 2 * QROWS);
     for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(&B->full[i], 1);
+      mbar_init(&B->k_full[i], 1);
+      mbar_init(&B->v_full[i], 1);
       mbar_init(&B->empty[i], 1);
       mbar_init(&B->clean[i], 1);
     }
@@ -297,54 +331,57 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
     mbar_init(&B->s_free, 2 * QROWS);
     mbar_init(&B->p_full, 2 * QROWS);
     mbar_init(&B->o_done, 1);
-    mbar_init(&B->drain, 1);
+    mbar_init(&B->seen_full, 2 * QROWS);
+    mbar_init(&B->drain[0], 1);
+    mbar_init(&B->drain[1], 1);
     B->abort = 0;
     B->z_lo = 0x7fffffff;
-    B->any = 0;
     fence_mbar_init();
+    pdl_trigger();
   }
-  if (warp == W_MMA) tmem_alloc(&B->tmem_slot, TMEM_COLS);
+  if (warp == W_S) tmem_alloc(&B->tmem_slot, TMEM_COLS);
   for (int i = tid; i < tree::MAX_NODES / 32; i += THREADS) seen[i] = 0;
-  if (tid == 0) pdl_trigger();
   pdl_wait();                  // Q_abs and the nodes' own entries come from the kernels before
   U.n = tree::block_keys(R, U.b, &U.W, &U.ctx, tid == 0 && U.half == 0 && U.qt == 0 && blockIdx.y == 0);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = B->tmem_slot;
-  // what the unit's rows see: the first context key and the nodes on their paths
+  // whether a row may see anything (padding and masked rows left out), and the
+  // first tile that a row's window reaches; every warp works it out
+  bool any = false;
   {
     const int t0 = U.qt * QROWS / R.H, t1 = min(R.T - 1, (U.qt * QROWS + QROWS - 1) / R.H);
-    const int32_t* parent = R.parent + (long)U.b * R.T;
-    const int32_t* pos = R.positions + (long)U.b * R.T;
-    for (int i = t0 + tid; i <= t1; i += THREADS) {
-      if (U.n <= 0 || (R.q_visible && !R.q_visible[(long)U.b * R.T + i])) continue;
-      if (!tree::in_tree(R, parent, i, U.half == 0 && blockIdx.y == 0)) continue;
-      B->any = 1;
-      atomicMin(&B->z_lo, U.W > 0 ? max(0, min(pos[i] - U.W + 1, U.ctx)) : 0);
-      for (int k = i; k >= 0; k = parent[k])
-        if (U.W == 0 || pos[i] - pos[k] < U.W) atomicOr(&seen[k >> 5], 1u << (k & 31));
+    int pmin = 0x7fffffff;
+    for (int i = t0 + lane; i <= t1; i += 32) {
+      const long m = (long)U.b * R.T + i;
+      if (R.parent[m] < -1 || (R.q_visible && !R.q_visible[m])) continue;
+      any = true;
+      if (U.W > 0) pmin = min(pmin, R.positions[m]);
     }
-    __syncthreads();
-    U.z_lo = B->any ? B->z_lo : 0;
-    U.j_lo = U.z_lo / KT * KT;
-    const int all = B->any ? (U.n - U.j_lo + KT - 1) / KT : 0;
+    any = __any_sync(0xffffffffu, any);
+    pmin = __reduce_min_sync(0xffffffffu, pmin);
+    U.j_lo = U.W > 0 ? max(0, min(pmin - U.W + 1, U.ctx)) / KT * KT : 0;
+  }
+  {  // this part's share of the tiles
+    const int all = any && U.n > 0 ? (U.n - U.j_lo + KT - 1) / KT : 0;
     const int tb = (int)((long)blockIdx.y * all / P.splits), te = (int)((long)(blockIdx.y + 1) * all / P.splits);
     U.j_lo += tb * KT;
     U.nt = te - tb;
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem_slot;
 
   if (warp >= W_RING && warp < W_RING + SLOTS) {
     // ---- ring slot `s`: uses s, s + 3, ... ----
     const int s = warp - W_RING;
     const int ps = R.page_size, past_end = R.num_pages * ps, seg = P.seg_rows, nseg = KT / seg;
     uint8_t* slot = smem + OFF_RING + s * SLOT_BYTES;
-    if (lane == 0) { prefetch_tmap(&P.tmC); prefetch_tmap(&P.tmK); }
-    int k = 0;
-    for (int u = s; u < 6 * U.nt; u += SLOTS, ++k) {
+    int nk = 0, nv = 0;                                   // key and value uses issued
+    int z_lo = -1;                                        // known from seen_full on
+    for (int u = s; u < 6 * U.nt; u += SLOTS) {
       const Item it = item_of(u, U.nt);
       const int j0 = U.j_lo + it.tile * KT;
       const int ch = it.value ? 4 * U.half + 2 * it.pair : 2 * it.pair;
+      uint64_t* full = it.value ? &B->v_full[s] : &B->k_full[s];
       // cache row of this lane's page segment (past the end: the copy fills zeros)
       int y = past_end;
       if (lane < nseg && j0 + lane * seg < U.n) {
@@ -353,27 +390,31 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
         if (pg >= 0 && pg < R.num_pages) y = pg * ps + j % ps;
         else set_status(R.status, MLA_DEV_BAD_PAGE);
       }
-      if (!wait_bar(B, &B->empty[s], (k & 1) ^ 1, R.status)) break;
+      if (!wait_bar(B, &B->empty[s], ((u / SLOTS) & 1) ^ 1, R.status)) break;
+      if (lane == 0) mbar_arrive_expect_tx(full, SLOT_BYTES);
+      __syncwarp();
       if (nseg == 1) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&B->full[s], SLOT_BYTES);
-          tma_load_3d(slot, &P.tmC, &B->full[s], 0, y, ch);
-        }
-      } else {
-        if (lane == 0) mbar_arrive_expect_tx(&B->full[s], SLOT_BYTES);
-        __syncwarp();
-        if (lane < nseg) {
-          tma_load_3d(slot + lane * seg * 128, &P.tmK, &B->full[s], ch * 64, y, 0);
-          tma_load_3d(slot + CH_BYTES + lane * seg * 128, &P.tmK, &B->full[s], ch * 64 + 64, y, 0);
-        }
+        if (lane == 0) tma_load_3d(slot, &P.tmC, full, 0, y, ch);
+      } else if (lane < nseg) {
+        tma_load_3d(slot + lane * seg * 128, &P.tmK, full, ch * 64, y, 0);
+        tma_load_3d(slot + CH_BYTES + lane * seg * 128, &P.tmK, full, ch * 64 + 64, y, 0);
       }
       __syncwarp();
-      if (it.value && dirty_tile(U, it.tile)) {
+      if (!it.value) {
+        ++nk;
+        continue;
+      }
+      ++nv;
+      if (z_lo < 0) {
+        if (!wait_bar(B, &B->seen_full, 0, R.status)) break;
+        z_lo = B->z_lo;
+      }
+      if (dirty_tile(U, z_lo, it.tile)) {
         // rows nobody sees become zeros: 0 x NaN is not 0
-        if (!wait_bar(B, &B->full[s], k & 1, R.status)) { ++k; break; }
+        if (!wait_bar(B, full, (nv - 1) & 1, R.status)) break;
         for (int key = lane; key < KT; key += 32) {
           const int j = j0 + key, node = j - U.ctx;
-          const bool need = j < U.n && j >= U.z_lo && (node < 0 || ((seen[node >> 5] >> (node & 31)) & 1u));
+          const bool need = j < U.n && j >= z_lo && (node < 0 || ((seen[node >> 5] >> (node & 31)) & 1u));
           if (!need) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -387,14 +428,14 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
         if (lane == 0) mbar_arrive(&B->clean[s]);
       }
     }
-    // every copy into this CTA has landed before it may exit
-    if (k > 0) mbar_wait(&B->full[s], (k - 1) & 1, R.status);
+    // every copy into this CTA has landed before its shared memory is used again
+    if (nk > 0) mbar_wait(&B->k_full[s], (nk - 1) & 1, R.status);
+    if (nv > 0) mbar_wait(&B->v_full[s], (nv - 1) & 1, R.status);
   } else if (warp == W_ROPE) {
     // ---- Q once, then the rope chunk of every tile ----
+    const int ps = R.page_size, past_end = R.num_pages * ps, seg = P.seg_rows, nseg = KT / seg;
     if (U.nt > 0) {
-      const int ps = R.page_size, past_end = R.num_pages * ps, seg = P.seg_rows, nseg = KT / seg;
       if (lane == 0) {
-        prefetch_tmap(&P.tmQ);
         mbar_arrive_expect_tx(&B->q_full, NQS * CH_BYTES);
         tma_load_3d(smem + OFF_Q, &P.tmQ, &B->q_full, 0, (int)U.row0, NQT);
       }
@@ -410,80 +451,94 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
         if (!wait_bar(B, &B->rope_empty, (t & 1) ^ 1, R.status)) break;
         if (lane == 0) mbar_arrive_expect_tx(&B->rope_full, CH_BYTES);
         __syncwarp();
-        if (lane < nseg)
-          tma_load_3d(smem + OFF_ROPE + lane * seg * 128, &P.tmK, &B->rope_full, 512, y, 0);
+        if (lane < nseg) tma_load_3d(smem + OFF_ROPE + lane * seg * 128, &P.tmK, &B->rope_full, 512, y, 0);
         __syncwarp();
       }
       mbar_wait(&B->q_full, 0, R.status);
       if (t > 0) mbar_wait(&B->rope_full, (t - 1) & 1, R.status);
     }
-  } else if (warp == W_MMA) {
+  } else if (warp == W_S) {
     if (lane == 0 && U.nt > 0) {
-      const uint32_t idesc_qk = idesc_f16(QROWS, KT, false), idesc_pv = idesc_f16_bmn(QROWS, 128, false);
-      constexpr uint64_t U_CH = CH_BYTES / 16, U_SLOT = SLOT_BYTES / 16, U_KSTEP = 16 * 128 / 16;
+      // ---- S(t) = Q K(t)^T ----
+      const uint32_t idesc = idesc_f16(QROWS, KT, false), tS = tmem + TM_S, tQ = tmem + TM_Q;
+      constexpr uint64_t U_CH = CH_BYTES / 16, U_SLOT = SLOT_BYTES / 16;
       const uint64_t dQ = smem_desc_sw128(smem + OFF_Q), dR = smem_desc_sw128(smem + OFF_RING);
       const uint64_t dRope = smem_desc_sw128(smem + OFF_ROPE);
-      const uint64_t dV = smem_desc_sw128_mn(smem + OFF_RING, CH_BYTES);
-      const uint32_t tS = tmem + TM_S, tQ = tmem + TM_Q, tO = tmem + TM_O, tP = tmem + TM_P;
-      int s = 0;                                          // slot of the next use of the ring
-      uint32_t par = 0, cpar = 0;                         // its parity; bit i: parity of clean[i]
       bool ok = wait_bar(B, &B->q_full, 0, R.status) && wait_bar(B, &B->q_tmem, 0, R.status);
-      auto next = [&]() { if (++s == SLOTS) { s = 0; par ^= 1; } };
-      auto scores = [&](int t) {
+      tc_fence_after();
+      uint32_t par = 0;                                   // bit i: parity of k_full[i]
+      for (int t = 0; t < U.nt && ok; ++t) {
+        int s = first_key_use(t) % SLOTS;
+        bool ready = mbar_test_wait(&B->k_full[s], (par >> s) & 1);
+        if (t > 0) {
+          if (!(ok = wait_bar(B, &B->s_free, (t - 1) & 1, R.status))) break;
+          tc_fence_after();
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (!ok || !(ok = wait_bar(B, &B->full[s], par, R.status))) return;
-          tc_fence_after();
+          if (!(ok = ok && wait_bar(B, &B->k_full[s], (par >> s) & 1, R.status, ready))) break;
+          par ^= 1u << s;
+          const int s1 = s + 1 < SLOTS ? s + 1 : 0;
+          // a look at the next barrier, its answer used after these MMAs
+          ready = i < 3 ? mbar_test_wait(&B->k_full[s1], (par >> s1) & 1) : mbar_test_wait(&B->rope_full, t & 1);
           const uint64_t db = dR + s * U_SLOT;
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
               if (i == 0)
-                mma_f16_ts(tS, tQ + 32 * c + 8 * d, db + c * U_CH + 2 * d, idesc_qk, (c | d) ? 1u : 0u);
+                mma_f16_ts(tS, tQ + 32 * c + 8 * d, db + c * U_CH + 2 * d, idesc, (c | d) ? 1u : 0u);
               else
-                mma_f16(tS, dQ + (2 * i - 2 + c) * U_CH + 2 * d, db + c * U_CH + 2 * d, idesc_qk, 1u);
+                mma_f16(tS, dQ + (2 * i - 2 + c) * U_CH + 2 * d, db + c * U_CH + 2 * d, idesc, 1u);
             }
           mma_commit(&B->empty[s]);
-          next();
+          s = s1;
         }
-        if (!(ok = wait_bar(B, &B->rope_full, t & 1, R.status))) return;
-        tc_fence_after();
+        if (!(ok = ok && wait_bar(B, &B->rope_full, t & 1, R.status, ready))) break;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) mma_f16(tS, dQ + (NQS - 1) * U_CH + 2 * d, dRope + 2 * d, idesc_qk, 1u);
+        for (int d = 0; d < 4; ++d) mma_f16(tS, dQ + (NQS - 1) * U_CH + 2 * d, dRope + 2 * d, idesc, 1u);
         mma_commit(&B->rope_empty);
         mma_commit(&B->s_full);
-      };
-      scores(0);
+      }
+      mma_commit(&B->drain[0]);
+      mbar_wait(&B->drain[0], 0, R.status);
+    }
+  } else if (warp == W_PV) {
+    if (lane == 0 && U.nt > 0) {
+      // ---- O += P(t) V(t) ----
+      const uint32_t idesc = idesc_f16_bmn(QROWS, 128, false), tO = tmem + TM_O, tP = tmem + TM_P;
+      constexpr uint64_t U_SLOT = SLOT_BYTES / 16, U_KSTEP = 16 * 128 / 16;
+      const uint64_t dV = smem_desc_sw128_mn(smem + OFF_RING, CH_BYTES);
+      uint32_t par = 0, cpar = 0;                         // bit i: parity of v_full[i], clean[i]
+      bool ok = wait_bar(B, &B->seen_full, 0, R.status);
+      const int z_lo = B->z_lo;
       for (int t = 0; t < U.nt && ok; ++t) {
-        if (t + 1 < U.nt) {
-          if (!(ok = wait_bar(B, &B->s_free, t & 1, R.status))) break;
-          tc_fence_after();
-          scores(t + 1);
-          if (!ok) break;
-        }
+        int s = first_value_use(t, U.nt) % SLOTS;
+        const bool dirty = dirty_tile(U, z_lo, t);
         if (!(ok = wait_bar(B, &B->p_full, t & 1, R.status))) break;
         tc_fence_after();
-        const bool dirty = dirty_tile(U, t);
+        bool ready = false;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           if (dirty) {
             ok = ok && wait_bar(B, &B->clean[s], (cpar >> s) & 1, R.status);
             cpar ^= 1u << s;
           }
-          if (!ok || !(ok = wait_bar(B, &B->full[s], par, R.status))) break;
-          tc_fence_after();
+          if (!(ok = ok && wait_bar(B, &B->v_full[s], (par >> s) & 1, R.status, ready))) break;
+          par ^= 1u << s;
+          const int s1 = s + 1 < SLOTS ? s + 1 : 0;
+          if (p == 0) ready = mbar_test_wait(&B->v_full[s1], (par >> s1) & 1);
           const uint64_t db = dV + s * U_SLOT;
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
-            mma_f16_ts(tO + 128 * p, tP + 8 * k, db + U_KSTEP * k, idesc_pv, (t | k) ? 1u : 0u);
+            mma_f16_ts(tO + 128 * p, tP + 8 * k, db + U_KSTEP * k, idesc, (t | k) ? 1u : 0u);
           mma_commit(&B->empty[s]);
-          next();
+          s = s1;
         }
         mma_commit(&B->o_done);
       }
-      mma_commit(&B->drain);
-      mbar_wait(&B->drain, 0, R.status);
+      mma_commit(&B->drain[1]);
+      mbar_wait(&B->drain[1], 0, R.status);
     }
   } else {
     softmax_role(P, B, smem, tmem, U);
@@ -492,47 +547,43 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == W_MMA) tmem_dealloc(tmem, TMEM_COLS);
+  if (warp == W_S) tmem_dealloc(tmem, TMEM_COLS);
+  store_rows(P, smem, U);
 }
 
-// One warp per row: sum_s w_s o_s / sum_s w_s with w_s = 2^(lse_s - max), in
-// split order; a row that no split saw is zero.
+// One warp per row and quarter of its dims: sum_s w_s o_s / sum_s w_s with w_s =
+// 2^(lse_s - max), in split order; a row that no split saw is zero.  The lanes
+// hold the splits' log-sum-exps (at most MAX_SPLITS), eight loads are in flight.
 __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict__ part,
                                                          const float* __restrict__ part_lse, long rows,
                                                          int splits, __half* __restrict__ o_lat,
                                                          float* __restrict__ lse) {
-  pdl_wait();
-  const long row = (long)blockIdx.x * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
+  const long item = (long)blockIdx.x * 8 + threadIdx.x / 32;
+  const long row = item >> 2;
+  const int quarter = (int)(item & 3), lane = threadIdx.x % 32;
   if (row >= rows) return;
-  float mx = -INFINITY;
-  for (int s = 0; s < splits; ++s) mx = fmaxf(mx, part_lse[s * rows + row]);
-  float acc[16], den = 0.f;
+  const float l0 = lane < splits ? part_lse[lane * rows + row] : -INFINITY;
+  const float l1 = lane + 32 < splits ? part_lse[(lane + 32) * rows + row] : -INFINITY;
+  float mx = fmaxf(l0, l1);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  if (mx != -INFINITY) {
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const float l = part_lse[s * rows + row];
-      if (l == -INFINITY) continue;                      // nothing was written for it
-      const float w = exp2f(l - mx);
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float w0 = mx == -INFINITY ? 0.f : exp2f(l0 - mx), w1 = mx == -INFINITY ? 0.f : exp2f(l1 - mx);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.f;
+  const float4* src = reinterpret_cast<const float4*>(part + row * 512) + quarter * 32 + lane;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float w = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31);
+    if (w != 0.f) {                                      // else nothing may have been written
+      const float4 v = src[(long)s * rows * 128];
       den += w;
-      const float4* src = reinterpret_cast<const float4*>(part + (s * rows + row) * 512) + lane;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = src[32 * i];
-        acc[4 * i] += w * v.x; acc[4 * i + 1] += w * v.y; acc[4 * i + 2] += w * v.z; acc[4 * i + 3] += w * v.w;
-      }
+      acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
     }
   }
   const float inv = den > 0.f ? 1.f / den : 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __half2 h2[2] = {__floats2half2_rn(acc[4 * i] * inv, acc[4 * i + 1] * inv),
-                     __floats2half2_rn(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv)};
-    *reinterpret_cast<uint2*>(o_lat + row * 512 + 128 * i + 4 * lane) = *reinterpret_cast<uint2*>(h2);
-  }
-  if (lse && lane == 0) lse[row] = den > 0.f ? (mx + log2f(den)) * kLn2 : -INFINITY;
+  __half2 h2[2] = {__floats2half2_rn(acc.x * inv, acc.y * inv), __floats2half2_rn(acc.z * inv, acc.w * inv)};
+  *reinterpret_cast<uint2*>(o_lat + row * 512 + quarter * 128 + 4 * lane) = *reinterpret_cast<uint2*>(h2);
+  if (lse && lane == 0 && quarter == 0) lse[row] = den > 0.f ? (mx + log2f(den)) * kLn2 : -INFINITY;
 }
 
 }  // namespace
@@ -547,7 +598,7 @@ int tree_splits(const mla_handle* h, const mla_attn_desc_t& d) {
   const long tiles = ((long)d.max_pages * h->cfg.page_size + KT - 1) / KT, pairs = h->num_sms / 2;
   int best = 1;
   double cost = 1e300;
-  for (int s = 1; s <= 64 && s <= tiles; ++s) {
+  for (int s = 1; s <= MAX_SPLITS && s <= tiles; ++s) {
     const double waves = (double)((units * s + pairs - 1) / pairs);
     const double c = waves * (FIXED + (double)((tiles + s - 1) / s)) +
                      (s > 1 ? MERGE + MERGE_PART * units * s : 0.0);
@@ -598,7 +649,7 @@ mla_status_t tree_attention(cudaStream_t st, mla_handle* h, const tree::Rule& r,
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   h->launches += 1;
   if (P.splits > 1) {
-    Launch M(dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, false);
+    Launch M(dim3((unsigned)((rows + 1) / 2)), dim3(256), 0, st, false);
     e = cudaLaunchKernelEx(&M.cfg, tree_merge_kernel, (const float*)P.part, (const float*)P.part_lse, rows,
                            P.splits, o_lat, lse);
     if (e != cudaSuccess) return cuda_fail(e, "tree attention merge launch");
