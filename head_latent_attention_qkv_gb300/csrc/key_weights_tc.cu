@@ -54,10 +54,7 @@ static_assert(sizeof(Bars) <= 256, "barrier block");
 
 __device__ __forceinline__ bool wait_bar(Bars* B, uint64_t* bar, uint32_t parity, uint32_t* st) {
   if (*(volatile int*)&B->abort) return false;
-  if (mbar_test_wait_cluster(bar, parity)) return true;
-  for (uint32_t i = 0; i < kWaitBudget; ++i)
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-  set_status(st, MLA_DEV_TIMEOUT);
+  if (mbar_wait(bar, parity, st)) return true;
   B->abort = 1;
   return false;
 }
@@ -206,7 +203,7 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(buf ? s_free1 : s_free0);
+        if (lane == 0) mbar_arrive_tmem(buf ? s_free1 : s_free0);
         sum += (part[0] + part[1]) + (part[2] + part[3]);
       }
     }
@@ -288,7 +285,7 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid
     }
     // every copy has landed before the pair may exit (its barriers are the even CTA's)
     if (rank == 0 && use > 0)
-      for (int i = 0; i < TRIO; ++i) mbar_wait_cluster(&B->k_full[i], (use - 1) & 1, R.status);
+      for (int i = 0; i < TRIO; ++i) mbar_wait(&B->k_full[i], (use - 1) & 1, R.status);
   } else if (warp == W_Q || warp == W_Q + 1) {
     // ---- this CTA's half of the rows, chunk by chunk; the two warps take turns ----
     if (lane == 0) prefetch_tmap(&P.tmQ);
@@ -315,7 +312,7 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid
       }
     }
     if (rank == 0 && last >= 0)
-      mbar_wait_cluster(&B->q_full[last % QSLOTS], (last / QSLOTS) & 1, R.status);
+      mbar_wait(&B->q_full[last % QSLOTS], (last / QSLOTS) & 1, R.status);
   } else if (warp == W_MMA && rank == 0) {
     // ---- MMA issue for the pair (the even CTA) ----
     constexpr uint64_t U_CH = CH_BYTES / 16;
@@ -354,7 +351,7 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid
     }
     if (lane == 0) {
       mma_commit_pair(&B->drain);
-      mbar_wait_cluster(&B->drain, 0, R.status);
+      mbar_wait(&B->drain, 0, R.status);
     }
   } else if (warp != W_MMA) {
     sum_role(P, B, smem, tmem, rank);

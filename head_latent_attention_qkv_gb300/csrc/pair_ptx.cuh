@@ -32,12 +32,19 @@ __device__ __forceinline__ void mma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem
       " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
       ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
-// Arrive on this barrier of both CTAs once the pair's MMAs issued so far have
-// completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+// Arrive on this barrier of both CTAs (`mask`: their bits by rank in the
+// cluster) once the pair's MMAs issued so far have completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t mask = 3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-      ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+      ::"r"(smem_u32(bar)), "h"((uint16_t)mask) : "memory");
+}
+// Arrive on a barrier of the cluster for tensor memory alone (no shared or
+// global data handed over): release at CTA scope, which does not wait for the
+// thread's writes to reach the cluster (at cluster scope the arrive held the
+// softmax threads for about 1700 cycles).
+__device__ __forceinline__ void mbar_arrive_tmem(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 // A copy into this CTA's shared memory that completes on a barrier of the pair
 // (a shared::cluster address, e.g. of the even CTA).

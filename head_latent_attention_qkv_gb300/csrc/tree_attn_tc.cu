@@ -1,12 +1,17 @@
 // tcgen05 latent attention of trees of drafted tokens (tree.cuh has the rule
 // of visibility, mla_draft.h the formulas; bf16 layers, entries 512 + 64).
 //
-// Work unit: 128 consecutive rows (node, head) of a block, over a range of its
-// keys in tiles of 128, by a cluster of two CTAs, one per half of the 512 value
-// dims: a 128 x 512 fp32 accumulator alone would fill an SM's tensor memory,
-// so each CTA keeps O for 256 dims and computes the 576-wide scores itself
-// (3328 tensor cycles a tile instead of 2176: at most 65% of the peak on the
-// algorithm's flops).
+// A 128 x 512 fp32 accumulator alone would fill an SM's tensor memory, so a
+// CTA keeps O for 128 rows (node, head) and 256 of the value dims and computes
+// the 576-wide scores of its rows itself: 3328 tensor cycles per tile of 128
+// keys instead of 2176, at most 65% of the peak on the algorithm's flops.  A
+// cluster works on one range of a block's keys:
+//  - tree_attn_pair_kernel, blocks of more than 128 rows: two row tiles and one
+//    value half; their MMAs run as one over the pair (cta_group::2), so each
+//    CTA fetches and reads half of the keys' and values' bytes (2560 cycles of
+//    shared-memory traffic a tile against 3328 of MMAs);
+//  - tree_attn_tc_kernel, blocks of at most 128 rows: one row tile, a CTA per
+//    value half (4224 cycles of shared-memory traffic a tile, the bound).
 //
 // What a tile costs beyond its MMAs is hidden by running the scores one tile
 // ahead: the tensor pipe executes S(0), S(1), PV(0), S(2), PV(1), ..., and
@@ -14,13 +19,10 @@
 // soon as the softmax has read it, so P has tensor memory of its own (O 256
 // columns, S 128, P 64, two of the nine Q chunks 64) and every operand streams:
 // the cache chunks that a CTA reads as values come a second time for PV, from
-// L2.  The stream of a CTA is, per tile, four pairs of 64-dim key chunks and two
-// pairs of value chunks, through a ring of three 32 KB slots, each refilled by
-// a warp of its own (a copy holds its thread for about 550 cycles), and the
-// 16 KB rope chunk in a slot of its own, read last.  The scores and P V are issued by
-// two threads, and each looks at its next barrier before it issues the MMAs of
-// the one at hand: a look at a barrier takes about 340 cycles, the eight MMAs
-// of a pair 512 (one issuer that waited in turn: 7.3 k cycles a tile).
+// L2.  Per tile the stream has four pairs of 64-dim key chunks, two pairs of
+// value chunks and the rope chunk.  Scores and P V are issued by two threads,
+// and each looks at its next barrier before it issues the MMAs of the one at
+// hand (a look takes about 340 cycles, the eight MMAs of a pair 512).
 //
 // Softmax: warps 0-3 and 8-11, two threads a row (64 keys and 128 value
 // columns each) that exchange their half maxima; fp32, exp2 domain, O rescaled
@@ -28,12 +30,13 @@
 // as it meets the bf16 values (one kind::f16 MMA takes one type; its sum keeps
 // the unrounded weights).  Tiles wholly inside the context need no mask without
 // a window; the others test 64 bits a thread (tree::key_bits).  Entries that
-// no row of the unit sees may hold anything: their scores are masked, and the
-// refilling warp clears their rows of the value chunks before PV reads them.
+// no row of the cluster sees may hold anything: their scores are masked, and
+// the refilling warps clear their rows of the value chunks before PV reads them.
 //
-// When the units do not fill the GPU their key range is cut in `splits` parts
-// (grid y); a part writes its normalised rows in fp32 and their log2-sum-exp to
-// the workspace and tree_merge_kernel joins them in split order.
+// When the units do not fill the GPU their key range is cut in parts (grid y).
+// Up to four neighbouring parts share a cluster and are joined through its
+// shared memory; what is left of them writes its rows in fp32 and their
+// log2-sum-exp to the workspace, and tree_merge_kernel joins them in order.
 #include "tree_tc.cuh"
 
 #include <math.h>
@@ -41,7 +44,7 @@
 #include <mutex>
 
 #include "gemm_tc.cuh"
-#include "tc_ptx.cuh"
+#include "pair_ptx.cuh"
 
 namespace mla {
 namespace tc {
@@ -51,24 +54,28 @@ constexpr int QROWS = 128, KT = 128, NCH = 9;
 constexpr int CH_BYTES = 128 * 64 * 2;                    // a 64-dim chunk of 128 rows
 constexpr int NQT = 2, NQS = NCH - NQT;                   // Q chunks in tensor / shared memory
 constexpr int SLOTS = 3, SLOT_BYTES = 2 * CH_BYTES;
-constexpr int THREADS = 448;                              // softmax x4, S, ring x3, softmax x4, PV, Q and rope
+constexpr int THREADS = 448;                              // softmax x4, S, loads x3, softmax x4, PV, Q and rope
 constexpr int W_S = 4, W_RING = 5, W_PV = 12, W_ROPE = 13;
 constexpr int OFF_Q = 0, OFF_RING = OFF_Q + NQS * CH_BYTES, OFF_ROPE = OFF_RING + SLOTS * SLOT_BYTES;
 constexpr int OFF_BAR = OFF_ROPE + CH_BYTES, OFF_SEEN = OFF_BAR + 256, OFF_XM = OFF_SEEN + tree::MAX_NODES / 8;
 constexpr int SMEM_BYTES = 1024 + OFF_XM + 2 * QROWS * 4;
-// the epilogue's rows, over Q and the ring: fp32, 256 dims, padded against bank conflicts
-constexpr int STG_PITCH = 260;
-static_assert(QROWS * STG_PITCH * 4 <= OFF_BAR, "staging");
+// the pair kernel's slots (a CTA's halves): four key pairs and two value pairs of 16 KB
+constexpr int PK = 4, PV = 2, PSLOT_BYTES = CH_BYTES, OFF_PK = OFF_RING, OFF_PV = OFF_PK + PK * PSLOT_BYTES;
+static_assert(OFF_PV + PV * PSLOT_BYTES <= OFF_ROPE, "slots");
+// the epilogue's rows, over Q and the slots: fp32, 256 dims, padded against bank
+// conflicts, then their log2-sum-exps
+constexpr int STG_PITCH = 260, OFF_STG_LSE = QROWS * STG_PITCH * 4;
+static_assert(OFF_STG_LSE + QROWS * 4 <= OFF_BAR, "staging");
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 constexpr uint32_t TMEM_COLS = 512, TM_O = 0, TM_S = 256, TM_P = 384, TM_Q = 448;
-constexpr int MAX_SPLITS = 64;
+constexpr int MAX_PARTS = 64;                             // partials of a row that the merge joins
 constexpr float RESCALE_LOG2 = 8.f, kLn2 = 0.6931471805599453f;
 
 struct Bars {
   uint64_t q_full, q_tmem;            // Q in shared memory (TMA) / in tensor memory
-  // a slot's keys and its values land on barriers of their own: each has one
-  // consumer, which never falls two phases behind (a parity tells only two apart)
-  uint64_t k_full[SLOTS], v_full[SLOTS], empty[SLOTS], clean[SLOTS];
+  // keys and values land on barriers of their own: each has one consumer, which
+  // never falls two phases behind (a parity tells only two apart)
+  uint64_t k_full[4], k_empty[4], v_full[SLOTS], v_empty[2], clean[SLOTS], land[2];
   uint64_t rope_full, rope_empty;
   uint64_t s_full, s_free;            // S(t) complete / read
   uint64_t p_full, o_done;            // P(t) written / P(t) V(t) complete
@@ -113,6 +120,9 @@ __device__ __forceinline__ int first_value_use(int t, int nt) { return 6 * t + (
 
 struct Unit {
   int b, qt, half, n, W, ctx, j_lo, nt;
+  int tiles;             // row tiles of the cluster: 1, or 2 (this CTA's and its peer's)
+  uint32_t lead;         // rank of the CTA whose barriers the issuing threads wait on
+  bool first;            // reports and statistics of the block's rows are this CTA's
   long row0;
 };
 
@@ -125,7 +135,7 @@ __device__ __forceinline__ bool dirty_tile(const Unit& U, int z_lo, int t) {
 
 __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8_t* smem, uint32_t tmem,
                                              const Unit& U) {
-  const int r = threadIdx.x & (QROWS - 1), kh = threadIdx.x >= 256 ? 1 : 0, w = r / 32;
+  const int r = threadIdx.x & (QROWS - 1), kh = threadIdx.x >= 256 ? 1 : 0, w = r / 32, lane = r % 32;
   constexpr int KH = KT / 2;
   const uint32_t lane_base = (uint32_t)(w * 32) << 16;
   float* xm = (float*)(smem + OFF_XM);                    // [2][128]
@@ -135,20 +145,27 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   const int node = live ? row_in_block / R.H : 0;
   const long m = (long)U.b * R.T + node;
   const int32_t* parent = R.parent + (long)U.b * R.T;
-  const bool ok = live && U.n > 0 && (R.q_visible ? R.q_visible[m] != 0 : true) &&
-                  tree::in_tree(R, parent, node, U.half == 0 && kh == 0);
+  auto row_ok = [&](int nd, bool report) {
+    return U.n > 0 && (R.q_visible ? R.q_visible[(long)U.b * R.T + nd] != 0 : true) &&
+           tree::in_tree(R, parent, nd, report);
+  };
+  const bool ok = live && row_ok(node, U.first && kh == 0);
   // rows that see nothing are computed like their neighbours and written as
   // zeros, so that they do not take a warp off the unmasked path
   const int lo = U.W > 0 ? max(0, R.positions[m] - U.W + 1) : 0;
   float mrun = -INFINITY, lsum = 0.f;
-  // what the unit's rows see: the first context key and the nodes on their
-  // paths (one row of a node stands for all)
-  if (ok && !kh && (row_in_block % R.H == 0 || r == 0)) {
-    uint32_t* seen = (uint32_t*)(smem + OFF_SEEN);
-    const int32_t* pos = R.positions + (long)U.b * R.T;
-    atomicMin(&B->z_lo, min(lo, U.ctx));
-    for (int k = node; k >= 0; k = parent[k])
-      if (U.W == 0 || pos[node] - pos[k] < U.W) atomicOr(&seen[k >> 5], 1u << (k & 31));
+  // what the cluster's rows see: the first context key and the nodes on their
+  // paths (one row of a node stands for all; the second threads take the peer's)
+  const uint32_t s_free = mapa(smem_u32(&B->s_free), U.lead), p_full = mapa(smem_u32(&B->p_full), U.lead);
+  if (kh < U.tiles) {
+    const int other = (kh ? U.qt ^ 1 : U.qt) * QROWS + r, nd = other / R.H;
+    if (other < R.T * R.H && (other % R.H == 0 || r == 0) && row_ok(nd, false)) {
+      uint32_t* seen = (uint32_t*)(smem + OFF_SEEN);
+      const int32_t* pos = R.positions + (long)U.b * R.T;
+      atomicMin(&B->z_lo, U.W > 0 ? max(0, min(pos[nd] - U.W + 1, U.ctx)) : 0);
+      for (int k = nd; k >= 0; k = parent[k])
+        if (U.W == 0 || pos[nd] - pos[k] < U.W) atomicOr(&seen[k >> 5], 1u << (k & 31));
+    }
   }
   mbar_arrive(&B->seen_full);
   if (U.nt > 0) {
@@ -162,7 +179,8 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
     }
     tmem_st32_u(tmem + TM_Q + 32 * kh + lane_base, q);
     tc_fence_before();
-    mbar_arrive(&B->q_tmem);
+    __syncwarp();
+    if (lane == 0) mbar_arrive_tmem(mapa(smem_u32(&B->q_tmem), U.lead));
   }
   for (int t = 0; t < U.nt; ++t) {
     const int jh = U.j_lo + t * KT + KH * kh;             // first key of this thread's half
@@ -175,7 +193,8 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
 #pragma unroll
     for (int c = 0; c < KH; c += 32) tmem_reg_fence32(s + c);
     tc_fence_before();
-    mbar_arrive(&B->s_free);                              // S(t + 1) may overwrite it
+    __syncwarp();
+    if (lane == 0) mbar_arrive_tmem(s_free);              // S(t + 1) may overwrite it
     float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     if (__all_sync(0xffffffffu, !ok || (jh >= lo && jh + KH <= U.ctx))) {
 #pragma unroll
@@ -230,7 +249,8 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
     }
     tmem_st32_u(tmem + TM_P + 32 * kh + lane_base, pw);
     tc_fence_before();
-    mbar_arrive(&B->p_full);
+    __syncwarp();
+    if (lane == 0) mbar_arrive_tmem(p_full);
   }
   // the row sum from both halves
   xm[kh * QROWS + r] = lsum;
@@ -240,7 +260,6 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   tc_fence_after();
   const bool any = ok && U.nt > 0 && lsum > 0.f;
   const float inv = any ? 1.f / lsum : 0.f;
-  const long row = U.row0 + r;
   float* prow = (float*)smem + r * STG_PITCH + 128 * kh;
 #pragma unroll 1
   for (int c = 0; c < 128; c += 32) {
@@ -252,14 +271,9 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
           any ? make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv)
               : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  if (!live || U.half || kh) return;
-  const float l2 = any ? mrun + log2f(lsum) : -INFINITY;
-  if (P.splits == 1) {
-    if (P.lse) P.lse[row] = any ? l2 * kLn2 : -INFINITY;
-  } else {
-    P.part_lse[(long)blockIdx.y * P.rows + row] = l2;
-  }
-  if (P.vis_stats && blockIdx.y == 0 && row_in_block % R.H == 0) {
+  if (kh) return;
+  ((float*)(smem + OFF_STG_LSE))[r] = any ? mrun + log2f(lsum) : -INFINITY;
+  if (live && P.vis_stats && U.first && row_in_block % R.H == 0) {
     int cnt = 0, first = -1, last = -1;
     if (ok) {
       if (lo < U.ctx) { cnt = U.ctx - lo; first = lo; last = U.ctx - 1; }
@@ -282,54 +296,97 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   }
 }
 
-// The staged rows, whole: a warp per row, 16 or 32 bytes a lane.
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// The staged rows of the cluster's parts, joined and written whole: part y of
+// the cluster takes rows [128 y / CS, 128 (y + 1) / CS), a warp per row, 8 dims
+// a lane, parts in order; a row that no part saw is zero.
+template <int CS>
 __device__ __forceinline__ void store_rows(const TreeParams& P, const uint8_t* smem, const Unit& U) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rows = min(QROWS, P.rule.T * P.rule.H - U.qt * QROWS);
-  for (int r = warp; r < rows; r += THREADS / 32) {
-    const float4* src = (const float4*)((const float*)smem + r * STG_PITCH);
+  const int y = CS > 1 ? (int)(blockIdx.y % CS) : 0, x = (int)(blockIdx.x & 1);
+  const uint32_t stg = smem_u32(smem), lse_a = stg + OFF_STG_LSE;
+  for (int r = y * (QROWS / CS) + warp; r < min(rows, (y + 1) * (QROWS / CS)); r += THREADS / 32) {
+    float l[CS];
+    float4 a[CS], c[CS];
+#pragma unroll
+    for (int s = 0; s < CS; ++s) {
+      const uint32_t rank = (uint32_t)(x + 2 * s), at = stg + (uint32_t)(r * STG_PITCH + 8 * lane) * 4;
+      if (CS == 1) {
+        l[s] = ((const float*)(smem + OFF_STG_LSE))[r];
+        a[s] = *(const float4*)((const float*)smem + r * STG_PITCH + 8 * lane);
+        c[s] = *(const float4*)((const float*)smem + r * STG_PITCH + 8 * lane + 4);
+      } else {
+        l[s] = ld_cluster_f32(mapa(lse_a + 4 * r, rank));
+        a[s] = ld_cluster_v4(mapa(at, rank));
+        c[s] = ld_cluster_v4(mapa(at + 16, rank));
+      }
+    }
+    float mx = l[0];
+#pragma unroll
+    for (int s = 1; s < CS; ++s) mx = fmaxf(mx, l[s]);
+    float v[8] = {a[0].x, a[0].y, a[0].z, a[0].w, c[0].x, c[0].y, c[0].z, c[0].w}, l2 = l[0];
+    if (CS > 1) {
+      float den = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll
+      for (int s = 0; s < CS; ++s) {
+        const float w = mx == -INFINITY ? 0.f : exp2f(l[s] - mx);
+        den += w;
+        v[0] += w * a[s].x; v[1] += w * a[s].y; v[2] += w * a[s].z; v[3] += w * a[s].w;
+        v[4] += w * c[s].x; v[5] += w * c[s].y; v[6] += w * c[s].z; v[7] += w * c[s].w;
+      }
+      const float inv = den > 0.f ? 1.f / den : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= inv;
+      l2 = den > 0.f ? mx + log2f(den) : -INFINITY;
+    }
     const long row = U.row0 + r;
-    if (P.splits == 1) {
-      const float4 a = src[2 * lane], c = src[2 * lane + 1];
-      __half2 h2[4] = {__floats2half2_rn(a.x, a.y), __floats2half2_rn(a.z, a.w), __floats2half2_rn(c.x, c.y),
-                       __floats2half2_rn(c.z, c.w)};
+    const int parts = gridDim.y / CS;
+    if (parts == 1) {
+      __half2 h2[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h2[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
       *reinterpret_cast<uint4*>(P.o_lat + row * 512 + U.half * 256 + 8 * lane) = *reinterpret_cast<uint4*>(h2);
+      if (P.lse && U.half == 0 && lane == 0) P.lse[row] = l2 == -INFINITY ? l2 : l2 * kLn2;
     } else {
-      float4* dst = reinterpret_cast<float4*>(P.part + ((long)blockIdx.y * P.rows + row) * 512 + U.half * 256);
-      dst[lane] = src[lane];
-      dst[lane + 32] = src[lane + 32];
+      const long at = (long)(blockIdx.y / CS) * P.rows + row;
+      float4* dst = reinterpret_cast<float4*>(P.part + at * 512 + U.half * 256 + 8 * lane);
+      dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+      dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+      if (U.half == 0 && lane == 0) P.part_lse[at] = l2;
     }
   }
 }
+__device__ __forceinline__ void join_and_store(const TreeParams& P, const uint8_t* smem, const Unit& U) {
+  if (P.cluster_parts == 1) store_rows<1>(P, smem, U);
+  else if (P.cluster_parts == 2) store_rows<2>(P, smem, U);
+  else store_rows<4>(P, smem, U);
+}
 
-__global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_constant__ TreeParams P) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  Bars* B = (Bars*)(smem + OFF_BAR);
-  uint32_t* seen = (uint32_t*)(smem + OFF_SEEN);         // nodes that a row of this unit sees
+// Barriers, the unit's keys and this part's share of their tiles; every warp.
+__device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* smem, Unit& U) {
   const tree::Rule& R = P.rule;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int unit = blockIdx.x >> 1;
-  Unit U;
-  U.half = blockIdx.x & 1;
-  U.b = unit / P.tiles_per_block;
-  U.qt = unit % P.tiles_per_block;
-  U.row0 = ((long)U.b * R.T) * R.H + (long)U.qt * QROWS;
-
+  const int tid = threadIdx.x, lane = tid % 32;
+  uint32_t* seen = (uint32_t*)(smem + OFF_SEEN);          // nodes that a row of the cluster sees
   if (tid == 0) {
     mbar_init(&B->q_full, 1);
-    mbar_init(&B->q_tmem, 2 * QROWS);
-    for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(&B->k_full[i], 1);
-      mbar_init(&B->v_full[i], 1);
-      mbar_init(&B->empty[i], 1);
-      mbar_init(&B->clean[i], 1);
-    }
+    mbar_init(&B->q_tmem, 8 * U.tiles);
+    for (int i = 0; i < 4; ++i) { mbar_init(&B->k_full[i], 1); mbar_init(&B->k_empty[i], 1); }
+    for (int i = 0; i < SLOTS; ++i) { mbar_init(&B->v_full[i], 1); mbar_init(&B->clean[i], U.tiles); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&B->v_empty[i], 1); mbar_init(&B->land[i], 1); }
     mbar_init(&B->rope_full, 1);
     mbar_init(&B->rope_empty, 1);
     mbar_init(&B->s_full, 1);
-    mbar_init(&B->s_free, 2 * QROWS);
-    mbar_init(&B->p_full, 2 * QROWS);
+    mbar_init(&B->s_free, 8 * U.tiles);
+    mbar_init(&B->p_full, 8 * U.tiles);
     mbar_init(&B->o_done, 1);
     mbar_init(&B->seen_full, 2 * QROWS);
     mbar_init(&B->drain[0], 1);
@@ -339,41 +396,84 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
     fence_mbar_init();
     pdl_trigger();
   }
-  if (warp == W_S) tmem_alloc(&B->tmem_slot, TMEM_COLS);
   for (int i = tid; i < tree::MAX_NODES / 32; i += THREADS) seen[i] = 0;
   pdl_wait();                  // Q_abs and the nodes' own entries come from the kernels before
-  U.n = tree::block_keys(R, U.b, &U.W, &U.ctx, tid == 0 && U.half == 0 && U.qt == 0 && blockIdx.y == 0);
+  U.n = tree::block_keys(R, U.b, &U.W, &U.ctx, tid == 0 && U.first && U.qt == 0);
   // whether a row may see anything (padding and masked rows left out), and the
-  // first tile that a row's window reaches; every warp works it out
+  // first tile that a row's window reaches
+  const int q0 = U.tiles == 2 ? U.qt & ~1 : U.qt;
+  const int t0 = q0 * QROWS / R.H, t1 = min(R.T - 1, ((q0 + U.tiles) * QROWS - 1) / R.H);
   bool any = false;
-  {
-    const int t0 = U.qt * QROWS / R.H, t1 = min(R.T - 1, (U.qt * QROWS + QROWS - 1) / R.H);
-    int pmin = 0x7fffffff;
-    for (int i = t0 + lane; i <= t1; i += 32) {
-      const long m = (long)U.b * R.T + i;
-      if (R.parent[m] < -1 || (R.q_visible && !R.q_visible[m])) continue;
-      any = true;
-      if (U.W > 0) pmin = min(pmin, R.positions[m]);
-    }
-    any = __any_sync(0xffffffffu, any);
-    pmin = __reduce_min_sync(0xffffffffu, pmin);
-    U.j_lo = U.W > 0 ? max(0, min(pmin - U.W + 1, U.ctx)) / KT * KT : 0;
+  int pmin = 0x7fffffff;
+  for (int i = t0 + lane; i <= t1; i += 32) {
+    const long m = (long)U.b * R.T + i;
+    if (R.parent[m] < -1 || (R.q_visible && !R.q_visible[m])) continue;
+    any = true;
+    if (U.W > 0) pmin = min(pmin, R.positions[m]);
   }
-  {  // this part's share of the tiles
-    const int all = any && U.n > 0 ? (U.n - U.j_lo + KT - 1) / KT : 0;
-    const int tb = (int)((long)blockIdx.y * all / P.splits), te = (int)((long)(blockIdx.y + 1) * all / P.splits);
-    U.j_lo += tb * KT;
-    U.nt = te - tb;
+  any = __any_sync(0xffffffffu, any);
+  pmin = __reduce_min_sync(0xffffffffu, pmin);
+  U.j_lo = U.W > 0 ? max(0, min(pmin - U.W + 1, U.ctx)) / KT * KT : 0;
+  const int all = any && U.n > 0 ? (U.n - U.j_lo + KT - 1) / KT : 0;
+  const int tb = (int)((long)blockIdx.y * all / gridDim.y), te = (int)((long)(blockIdx.y + 1) * all / gridDim.y);
+  U.j_lo += tb * KT;
+  U.nt = te - tb;
+}
+
+// Cache row of logical key j (past the end of the keys or on a bad page: past
+// the cache, where a copy reads zeros).
+__device__ __forceinline__ int cache_row(const tree::Rule& R, const Unit& U, int j, bool report) {
+  const int past_end = R.num_pages * R.page_size;
+  if (j >= U.n) return past_end;
+  const int pg = R.block_table[(long)U.b * R.max_pages + j / R.page_size];
+  if (pg >= 0 && pg < R.num_pages) return pg * R.page_size + j % R.page_size;
+  if (report) set_status(R.status, MLA_DEV_BAD_PAGE);
+  return past_end;
+}
+
+// Clears the rows of `nch` value chunks whose keys nobody sees (0 x NaN is not
+// 0); a warp.
+__device__ __forceinline__ void clear_unseen(const Unit& U, const uint8_t* smem, uint8_t* chunks, int nch,
+                                             int j0, int z_lo) {
+  const uint32_t* seen = (const uint32_t*)(smem + OFF_SEEN);
+  for (int key = threadIdx.x % 32; key < KT; key += 32) {
+    const int j = j0 + key, node = j - U.ctx;
+    if (j < U.n && j >= z_lo && (node < 0 || ((seen[node >> 5] >> (node & 31)) & 1u))) continue;
+    for (int c = 0; c < nch; ++c)
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<uint4*>(chunks + c * CH_BYTES + key * 128 + q * 16) = make_uint4(0, 0, 0, 0);
   }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+__global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_constant__ TreeParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  Bars* B = (Bars*)(smem + OFF_BAR);
+  const tree::Rule& R = P.rule;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int unit = blockIdx.x >> 1;
+  Unit U;
+  U.half = blockIdx.x & 1;
+  U.tiles = 1;
+  U.lead = cluster_ctarank();
+  U.first = U.half == 0 && blockIdx.y == 0;
+  U.b = unit / P.tiles_per_block;
+  U.qt = unit % P.tiles_per_block;
+  U.row0 = ((long)U.b * R.T) * R.H + (long)U.qt * QROWS;
+  if (warp == W_S) tmem_alloc(&B->tmem_slot, TMEM_COLS);
+  set_up(P, B, smem, U);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem_slot;
+  const int seg = P.seg_rows, nseg = KT / seg;
 
   if (warp >= W_RING && warp < W_RING + SLOTS) {
     // ---- ring slot `s`: uses s, s + 3, ... ----
     const int s = warp - W_RING;
-    const int ps = R.page_size, past_end = R.num_pages * ps, seg = P.seg_rows, nseg = KT / seg;
     uint8_t* slot = smem + OFF_RING + s * SLOT_BYTES;
     int nk = 0, nv = 0;                                   // key and value uses issued
     int z_lo = -1;                                        // known from seen_full on
@@ -382,15 +482,8 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
       const int j0 = U.j_lo + it.tile * KT;
       const int ch = it.value ? 4 * U.half + 2 * it.pair : 2 * it.pair;
       uint64_t* full = it.value ? &B->v_full[s] : &B->k_full[s];
-      // cache row of this lane's page segment (past the end: the copy fills zeros)
-      int y = past_end;
-      if (lane < nseg && j0 + lane * seg < U.n) {
-        const int j = j0 + lane * seg;
-        const int pg = R.block_table[(long)U.b * R.max_pages + j / ps];
-        if (pg >= 0 && pg < R.num_pages) y = pg * ps + j % ps;
-        else set_status(R.status, MLA_DEV_BAD_PAGE);
-      }
-      if (!wait_bar(B, &B->empty[s], ((u / SLOTS) & 1) ^ 1, R.status)) break;
+      const int y = lane < nseg ? cache_row(R, U, j0 + lane * seg, true) : 0;
+      if (!wait_bar(B, &B->k_empty[s], ((u / SLOTS) & 1) ^ 1, R.status)) break;
       if (lane == 0) mbar_arrive_expect_tx(full, SLOT_BYTES);
       __syncwarp();
       if (nseg == 1) {
@@ -410,21 +503,8 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
         z_lo = B->z_lo;
       }
       if (dirty_tile(U, z_lo, it.tile)) {
-        // rows nobody sees become zeros: 0 x NaN is not 0
         if (!wait_bar(B, full, (nv - 1) & 1, R.status)) break;
-        for (int key = lane; key < KT; key += 32) {
-          const int j = j0 + key, node = j - U.ctx;
-          const bool need = j < U.n && j >= z_lo && (node < 0 || ((seen[node >> 5] >> (node & 31)) & 1u));
-          if (!need) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              *reinterpret_cast<uint4*>(slot + key * 128 + q * 16) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(slot + CH_BYTES + key * 128 + q * 16) = make_uint4(0, 0, 0, 0);
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
+        clear_unseen(U, smem, slot, 2, j0, z_lo);
         if (lane == 0) mbar_arrive(&B->clean[s]);
       }
     }
@@ -433,7 +513,6 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
     if (nv > 0) mbar_wait(&B->v_full[s], (nv - 1) & 1, R.status);
   } else if (warp == W_ROPE) {
     // ---- Q once, then the rope chunk of every tile ----
-    const int ps = R.page_size, past_end = R.num_pages * ps, seg = P.seg_rows, nseg = KT / seg;
     if (U.nt > 0) {
       if (lane == 0) {
         mbar_arrive_expect_tx(&B->q_full, NQS * CH_BYTES);
@@ -442,12 +521,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
       __syncwarp();
       int t = 0;
       for (; t < U.nt; ++t) {
-        int y = past_end;
-        const int j = U.j_lo + t * KT + lane * seg;
-        if (lane < nseg && j < U.n) {
-          const int pg = R.block_table[(long)U.b * R.max_pages + j / ps];
-          if (pg >= 0 && pg < R.num_pages) y = pg * ps + j % ps;
-        }
+        const int y = lane < nseg ? cache_row(R, U, U.j_lo + t * KT + lane * seg, false) : 0;
         if (!wait_bar(B, &B->rope_empty, (t & 1) ^ 1, R.status)) break;
         if (lane == 0) mbar_arrive_expect_tx(&B->rope_full, CH_BYTES);
         __syncwarp();
@@ -491,7 +565,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
               else
                 mma_f16(tS, dQ + (2 * i - 2 + c) * U_CH + 2 * d, db + c * U_CH + 2 * d, idesc, 1u);
             }
-          mma_commit(&B->empty[s]);
+          mma_commit(&B->k_empty[s]);
           s = s1;
         }
         if (!(ok = ok && wait_bar(B, &B->rope_full, t & 1, R.status, ready))) break;
@@ -532,7 +606,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
             mma_f16_ts(tO + 128 * p, tP + 8 * k, db + U_KSTEP * k, idesc, (t | k) ? 1u : 0u);
-          mma_commit(&B->empty[s]);
+          mma_commit(&B->k_empty[s]);
           s = s1;
         }
         mma_commit(&B->o_done);
@@ -546,14 +620,205 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (P.cluster_parts > 1) cluster_sync_all();            // every part has staged its rows
   tc_fence_after();
   if (warp == W_S) tmem_dealloc(tmem, TMEM_COLS);
-  store_rows(P, smem, U);
+  join_and_store(P, smem, U);
+  if (P.cluster_parts > 1) cluster_sync_all();            // nobody leaves while its rows may be read
+}
+
+__global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid_constant__ TreeParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  Bars* B = (Bars*)(smem + OFF_BAR);
+  const tree::Rule& R = P.rule;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int unit = blockIdx.x >> 2, p = blockIdx.x & 1, units = (P.tiles_per_block + 1) / 2;
+  const uint32_t rank = cluster_ctarank();
+  Unit U;
+  U.half = (blockIdx.x >> 1) & 1;
+  U.tiles = 2;
+  U.lead = rank & ~1u;
+  U.first = U.half == 0 && blockIdx.y == 0;
+  U.b = unit / units;
+  U.qt = 2 * (unit % units) + p;
+  U.row0 = ((long)U.b * R.T) * R.H + (long)U.qt * QROWS;
+  if (warp == W_S) tmem_alloc_pair(&B->tmem_slot, TMEM_COLS);
+  set_up(P, B, smem, U);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();          // the peer's barriers are up
+  tc_fence_after();
+  const uint32_t tmem = B->tmem_slot, both = 3u << U.lead;
+  // segments: rows of a page, at most this CTA's 64 keys of a tile
+  const int seg = P.seg_rows, nkseg = 64 / seg, nvseg = KT / seg;
+
+  if (warp == W_RING || warp == W_RING + 1) {
+    // ---- keys: this CTA's 64 of every tile, chunk pairs 2 w and 2 w + 1 ----
+    const int i0 = 2 * (warp - W_RING), c = lane / nkseg, sg = lane % nkseg;
+    int t = 0;
+    bool ok = true;
+    for (; t < U.nt && ok; ++t) {
+      const int y = lane < 2 * nkseg ? cache_row(R, U, U.j_lo + t * KT + 64 * p + sg * seg, true) : 0;
+      for (int i = i0; i < i0 + 2; ++i) {
+        if (!(ok = wait_bar(B, &B->k_empty[i], (t & 1) ^ 1, R.status))) break;
+        if (p == 0 && lane == 0) mbar_arrive_expect_tx(&B->k_full[i], 2 * PSLOT_BYTES);
+        __syncwarp();
+        if (lane < 2 * nkseg)
+          tma_load_3d_pair(smem + OFF_PK + i * PSLOT_BYTES + c * (CH_BYTES / 2) + sg * seg * 128, &P.tmK,
+                           mapa(smem_u32(&B->k_full[i]), U.lead), (2 * i + c) * 64, y, 0);
+        __syncwarp();
+      }
+    }
+    // every copy of the pair has landed before its shared memory is used again
+    if (p == 0 && ok && t > 0)
+      for (int i = i0; i < i0 + 2; ++i) mbar_wait(&B->k_full[i], (t - 1) & 1, R.status);
+  } else if (warp == W_RING + 2) {
+    // ---- values: chunk 2 i + p of this half for both pairs ----
+    bool ok = U.nt > 0 && wait_bar(B, &B->seen_full, 0, R.status);
+    const int z_lo = ok ? B->z_lo : 0;
+    uint32_t nd = 0;                                      // tiles cleared so far
+    for (int t = 0; t < U.nt && ok; ++t) {
+      const int j0 = U.j_lo + t * KT;
+      const int y = lane < nvseg ? cache_row(R, U, j0 + lane * seg, true) : 0;
+      const bool dirty = dirty_tile(U, z_lo, t);
+      for (int i = 0; i < PV; ++i) {
+        if (!(ok = wait_bar(B, &B->v_empty[i], (t & 1) ^ 1, R.status))) break;
+        uint8_t* slot = smem + OFF_PV + i * PSLOT_BYTES;
+        // a tile to be cleared lands on a barrier of this CTA's own
+        const uint32_t bar = dirty ? smem_u32(&B->land[i]) : mapa(smem_u32(&B->v_full[i]), U.lead);
+        if (lane == 0) {
+          if (dirty) mbar_arrive_expect_tx(&B->land[i], PSLOT_BYTES);
+          else if (p == 0) mbar_arrive_expect_tx(&B->v_full[i], 2 * PSLOT_BYTES);
+        }
+        __syncwarp();
+        if (lane < nvseg)
+          tma_load_3d_pair(slot + lane * seg * 128, &P.tmK, bar, (4 * U.half + 2 * i + p) * 64, y, 0);
+        __syncwarp();
+        if (dirty) {
+          if (!(ok = wait_bar(B, &B->land[i], nd & 1, R.status))) break;
+          clear_unseen(U, smem, slot, 1, j0, z_lo);
+          if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&B->clean[i]), U.lead));
+        }
+      }
+      nd += dirty;
+    }
+  } else if (warp == W_ROPE) {
+    // ---- Q once, then the rope chunk of this CTA's 64 keys of every tile ----
+    if (U.nt > 0) {
+      if (lane == 0) {
+        if (p == 0) mbar_arrive_expect_tx(&B->q_full, 2 * NQS * CH_BYTES);
+        tma_load_3d_pair(smem + OFF_Q, &P.tmQ, mapa(smem_u32(&B->q_full), U.lead), 0, (int)U.row0, NQT);
+      }
+      __syncwarp();
+      int t = 0;
+      for (; t < U.nt; ++t) {
+        const int y = lane < nkseg ? cache_row(R, U, U.j_lo + t * KT + 64 * p + lane * seg, false) : 0;
+        if (!wait_bar(B, &B->rope_empty, (t & 1) ^ 1, R.status)) break;
+        if (p == 0 && lane == 0) mbar_arrive_expect_tx(&B->rope_full, CH_BYTES);
+        __syncwarp();
+        if (lane < nkseg)
+          tma_load_3d_pair(smem + OFF_ROPE + lane * seg * 128, &P.tmK, mapa(smem_u32(&B->rope_full), U.lead), 512,
+                           y, 0);
+        __syncwarp();
+      }
+      if (p == 0) {
+        mbar_wait(&B->q_full, 0, R.status);
+        if (t > 0) mbar_wait(&B->rope_full, (t - 1) & 1, R.status);
+      }
+    }
+  } else if (warp == W_S) {
+    if (p == 0 && lane == 0 && U.nt > 0) {
+      // ---- S(t) = Q K(t)^T of both row tiles ----
+      const uint32_t idesc = idesc_f16(2 * QROWS, KT, false), tS = tmem + TM_S, tQ = tmem + TM_Q;
+      constexpr uint64_t U_CH = CH_BYTES / 16, U_SLOT = PSLOT_BYTES / 16;
+      const uint64_t dQ = smem_desc_sw128(smem + OFF_Q), dK = smem_desc_sw128(smem + OFF_PK);
+      const uint64_t dRope = smem_desc_sw128(smem + OFF_ROPE);
+      bool ok = wait_bar(B, &B->q_full, 0, R.status) && wait_bar(B, &B->q_tmem, 0, R.status);
+      tc_fence_after();
+      for (int t = 0; t < U.nt && ok; ++t) {
+        const uint32_t par = t & 1;
+        bool ready = mbar_test_wait(&B->k_full[0], par);
+        if (t > 0) {
+          if (!(ok = wait_bar(B, &B->s_free, par ^ 1, R.status))) break;
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int i = 0; i < PK; ++i) {
+          if (!(ok = ok && wait_bar(B, &B->k_full[i], par, R.status, ready))) break;
+          // a look at the next barrier, its answer used after these MMAs
+          ready = mbar_test_wait(i < PK - 1 ? &B->k_full[i + 1] : &B->rope_full, par);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              const uint64_t db = dK + i * U_SLOT + c * (U_CH / 2) + 2 * d;
+              if (i == 0)
+                mma_f16_ts_pair(tS, tQ + 32 * c + 8 * d, db, idesc, (c | d) ? 1u : 0u);
+              else
+                mma_f16_pair(tS, dQ + (2 * i - 2 + c) * U_CH + 2 * d, db, idesc, 1u);
+            }
+          mma_commit_pair(&B->k_empty[i], both);
+        }
+        if (!(ok = ok && wait_bar(B, &B->rope_full, par, R.status, ready))) break;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) mma_f16_pair(tS, dQ + (NQS - 1) * U_CH + 2 * d, dRope + 2 * d, idesc, 1u);
+        mma_commit_pair(&B->rope_empty, both);
+        mma_commit_pair(&B->s_full, both);
+      }
+      mma_commit_pair(&B->drain[0], both);
+      mbar_wait(&B->drain[0], 0, R.status);
+    }
+  } else if (warp == W_PV) {
+    if (p == 0 && lane == 0 && U.nt > 0) {
+      // ---- O += P(t) V(t) of both row tiles ----
+      const uint32_t idesc = idesc_f16_bmn(2 * QROWS, 128, false), tO = tmem + TM_O, tP = tmem + TM_P;
+      constexpr uint64_t U_SLOT = PSLOT_BYTES / 16, U_KSTEP = 16 * 128 / 16;
+      const uint64_t dV = smem_desc_sw128_mn(smem + OFF_PV, CH_BYTES);
+      uint32_t nd = 0, nf = 0;                            // tiles cleared / not cleared so far
+      bool ok = wait_bar(B, &B->seen_full, 0, R.status);
+      const int z_lo = B->z_lo;
+      for (int t = 0; t < U.nt && ok; ++t) {
+        const bool dirty = dirty_tile(U, z_lo, t);
+        if (!(ok = wait_bar(B, &B->p_full, t & 1, R.status))) break;
+        tc_fence_after();
+        bool ready = false;
+#pragma unroll
+        for (int i = 0; i < PV; ++i) {
+          if (dirty) {           // both CTAs have cleared their halves (shared memory: cluster scope)
+            ok = ok && !*(volatile int*)&B->abort && mbar_wait_cluster(&B->clean[i], nd & 1, R.status);
+            if (!ok) break;
+          } else {
+            if (!(ok = ok && wait_bar(B, &B->v_full[i], nf & 1, R.status, ready))) break;
+            if (i == 0) ready = mbar_test_wait(&B->v_full[1], nf & 1);
+          }
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k)
+            mma_f16_ts_pair(tO + 128 * i, tP + 8 * k, dV + i * U_SLOT + U_KSTEP * k, idesc, (t | k) ? 1u : 0u);
+          mma_commit_pair(&B->v_empty[i], both);
+        }
+        mma_commit_pair(&B->o_done, both);
+        if (dirty) ++nd; else ++nf;
+      }
+      mma_commit_pair(&B->drain[1], both);
+      mbar_wait(&B->drain[1], 0, R.status);
+    }
+  } else {
+    softmax_role(P, B, smem, tmem, U);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();          // the pair's MMAs are done, every part has staged its rows
+  tc_fence_after();
+  if (warp == W_S) tmem_dealloc_pair(tmem, TMEM_COLS);
+  join_and_store(P, smem, U);
+  if (P.cluster_parts > 1) cluster_sync_all();            // nobody leaves while its rows may be read
 }
 
 // One warp per row and quarter of its dims: sum_s w_s o_s / sum_s w_s with w_s =
 // 2^(lse_s - max), in split order; a row that no split saw is zero.  The lanes
-// hold the splits' log-sum-exps (at most MAX_SPLITS), eight loads are in flight.
+// hold the splits' log-sum-exps (at most MAX_PARTS), eight loads are in flight.
 __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict__ part,
                                                          const float* __restrict__ part_lse, long rows,
                                                          int splits, __half* __restrict__ o_lat,
@@ -588,31 +853,42 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict
 
 }  // namespace
 
-// Parts of a unit's key range.  Cost in tiles: the waves of CTA pairs that one
-// split count needs, each of FIXED tiles' time beyond its share of the keys, and
-// the merge.  Keys are bounded by the page table; shorter sequences only split
-// finer than they need.
-int tree_splits(const mla_handle* h, const mla_attn_desc_t& d) {
-  constexpr double FIXED = 5.0, MERGE = 4.0, MERGE_PART = 0.02;
-  const long units = (long)d.num_blocks * (((long)d.block_len * h->lay.H + QROWS - 1) / QROWS);
-  const long tiles = ((long)d.max_pages * h->cfg.page_size + KT - 1) / KT, pairs = h->num_sms / 2;
-  int best = 1;
+// Row tiles in pairs, parts of a unit's key range (a multiple of the parts of a
+// cluster).  Cost in tiles of the waves of CTAs that a choice needs: FIXED
+// beyond a part's share of the keys, JOIN for a cluster's join, MERGE and
+// MERGE_PART for the second kernel.  Keys are bounded by the page table; shorter
+// sequences only split finer than they need.
+struct Plan {
+  bool pair;
+  int parts, cluster_parts;
+};
+Plan tree_plan(const mla_handle* h, const mla_attn_desc_t& d) {
+  constexpr double FIXED = 5.0, JOIN = 0.5, MERGE = 3.0, MERGE_PART = 0.02;
+  const long rows = (long)d.block_len * h->lay.H, tpb = (rows + QROWS - 1) / QROWS;
+  const long tiles = ((long)d.max_pages * h->cfg.page_size + KT - 1) / KT;
+  Plan best{tpb > 1, 1, 1};
+  const long groups = (long)d.num_blocks * (best.pair ? 2 * ((tpb + 1) / 2) : tpb);   // clusters of one part
   double cost = 1e300;
-  for (int s = 1; s <= MAX_SPLITS && s <= tiles; ++s) {
-    const double waves = (double)((units * s + pairs - 1) / pairs);
-    const double c = waves * (FIXED + (double)((tiles + s - 1) / s)) +
-                     (s > 1 ? MERGE + MERGE_PART * units * s : 0.0);
-    if (c < cost) { cost = c; best = s; }
-    if (units * s > 8 * pairs) break;
+  for (int cs = 1; cs <= 4; cs *= 2) {
+    // clusters of 2 cs CTAs that the GPU holds at once (GPCs are not a multiple of 8)
+    const long hold = cs == 1 ? h->num_sms / 2 : cs == 2 ? h->num_sms / 4 - 2 : h->num_sms / 8 - 4;
+    for (int g = 1; g <= MAX_PARTS && (long)g * cs <= (tiles > cs ? tiles : cs); ++g) {
+      const double waves = (double)((groups * g + hold - 1) / (hold > 0 ? hold : 1));
+      const double c = waves * (FIXED + (cs > 1 ? JOIN : 0.0) + (double)((tiles + g * cs - 1) / (g * cs))) +
+                       (g > 1 ? MERGE + MERGE_PART * groups * g : 0.0);
+      if (c < cost) { cost = c; best.parts = g * cs; best.cluster_parts = cs; }
+      if (groups * g > 8 * hold) break;
+    }
   }
   return best;
 }
 
 size_t tree_attention_ws(const mla_handle* h, const mla_attn_desc_t& d) {
-  const int s = tree_splits(h, d);
-  if (s == 1) return 0;
+  const Plan p = tree_plan(h, d);
+  const int parts = p.parts / p.cluster_parts;
+  if (parts == 1) return 0;
   const long rows = (long)d.num_blocks * d.block_len * h->lay.H;
-  return align256((size_t)s * rows * 512 * 4) + align256((size_t)s * rows * 4);
+  return align256((size_t)parts * rows * 512 * 4) + align256((size_t)parts * rows * 4);
 }
 
 mla_status_t tree_attention(cudaStream_t st, mla_handle* h, const tree::Rule& r,
@@ -620,9 +896,13 @@ mla_status_t tree_attention(cudaStream_t st, mla_handle* h, const tree::Rule& r,
                             const __nv_bfloat16* cache, __half* o_lat, float* lse, void* ws, bool pdl) {
   const Layout& l = h->lay;
   const long rows = (long)d.num_blocks * d.block_len * l.H, slots = (long)r.num_pages * r.page_size;
-  if (slots > 0x7fffffffL) return fail(MLA_ERR_UNSUPPORTED, "tree attention: num_pages * page_size < 2^31");
+  if (slots > 0x7fffffffL || rows > 0x7ffffc00L)
+    return fail(MLA_ERR_UNSUPPORTED, "tree attention: num_pages * page_size and rows below 2^31 - 1023");
+  const Plan plan = tree_plan(h, d);
+  const int parts = plan.parts / plan.cluster_parts;      // that reach the workspace when more than one
   TreeParams P;
-  P.seg_rows = r.page_size < KT ? r.page_size : KT;
+  const int max_seg = plan.pair ? KT / 2 : KT;
+  P.seg_rows = r.page_size < max_seg ? r.page_size : max_seg;
   if (!make_tmap_chunked(&P.tmQ, false, q_abs, rows, l.L, l.L, QROWS, NQS) ||
       !make_tmap_chunked(&P.tmC, false, cache, slots, l.L, l.L, KT, 2) ||
       !make_tmap_2d(&P.tmK, false, cache, slots, l.L, l.L, P.seg_rows))
@@ -633,25 +913,27 @@ mla_status_t tree_attention(cudaStream_t st, mla_handle* h, const tree::Rule& r,
   P.lse = lse;
   P.vis_stats = d.vis_stats;
   P.rows = rows;
-  P.splits = tree_splits(h, d);
+  P.cluster_parts = plan.cluster_parts;
   P.part = (float*)ws;
-  P.part_lse = P.splits > 1 ? (float*)((char*)ws + align256((size_t)P.splits * rows * 512 * 4)) : nullptr;
+  P.part_lse = parts > 1 ? (float*)((char*)ws + align256((size_t)parts * rows * 512 * 4)) : nullptr;
   P.tiles_per_block = (int)(((long)d.block_len * l.H + QROWS - 1) / QROWS);
   P.scale_log2 = h->scale * 1.4426950408889634f;
-  const long units = (long)d.num_blocks * P.tiles_per_block;
-  if (units > 0x3fffffffL) return fail(MLA_ERR_INVALID_ARG, "tree attention: too many rows");
+  const long ctas = 2L * d.num_blocks * (plan.pair ? 2 * ((P.tiles_per_block + 1) / 2) : P.tiles_per_block);
+  if (ctas > 0x7fffffffL) return fail(MLA_ERR_INVALID_ARG, "tree attention: too many rows");
   static std::once_flag once;
   std::call_once(once, [] {
     cudaFuncSetAttribute(tree_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    cudaFuncSetAttribute(tree_attn_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   });
-  Launch L(dim3((unsigned)(2 * units), (unsigned)P.splits), dim3(THREADS), SMEM_BYTES, st, pdl, dim3(2, 1, 1));
-  cudaError_t e = cudaLaunchKernelEx(&L.cfg, tree_attn_tc_kernel, P);
+  Launch L(dim3((unsigned)ctas, (unsigned)plan.parts), dim3(THREADS), SMEM_BYTES, st, pdl,
+           dim3(2, (unsigned)plan.cluster_parts, 1));
+  cudaError_t e = cudaLaunchKernelEx(&L.cfg, plan.pair ? tree_attn_pair_kernel : tree_attn_tc_kernel, P);
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   h->launches += 1;
-  if (P.splits > 1) {
+  if (parts > 1) {
     Launch M(dim3((unsigned)((rows + 1) / 2)), dim3(256), 0, st, false);
     e = cudaLaunchKernelEx(&M.cfg, tree_merge_kernel, (const float*)P.part, (const float*)P.part_lse, rows,
-                           P.splits, o_lat, lse);
+                           parts, o_lat, lse);
     if (e != cudaSuccess) return cuda_fail(e, "tree attention merge launch");
     h->launches += 1;
   }

@@ -17,10 +17,11 @@ struct TreeParams {
   __half* o_lat;      // [rows, 512]
   float* lse;         // [rows] or NULL
   int32_t* vis_stats;
-  float* part;        // [splits, rows, 512] when splits > 1
-  float* part_lse;    // [splits, rows] log2-sum-exp
+  float* part;        // [parts, rows, 512] when the parts do not all meet in a cluster
+  float* part_lse;    // [parts, rows] log2-sum-exp
   long rows;
-  int splits, seg_rows, tiles_per_block;
+  int cluster_parts;  // parts of a key range that share a cluster: 1, 2, 4
+  int seg_rows, tiles_per_block;
   float scale_log2;
 };
 
