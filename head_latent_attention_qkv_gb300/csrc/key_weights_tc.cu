@@ -203,7 +203,7 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_tmem(buf ? s_free1 : s_free0);
+        if (lane == 0) mbar_arrive_pair(buf ? s_free1 : s_free0);
         sum += (part[0] + part[1]) + (part[2] + part[3]);
       }
     }

@@ -39,11 +39,12 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t mask = 3
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
       ::"r"(smem_u32(bar)), "h"((uint16_t)mask) : "memory");
 }
-// Arrive on a barrier of the cluster for tensor memory alone (no shared or
-// global data handed over): release at CTA scope, which does not wait for the
-// thread's writes to reach the cluster (at cluster scope the arrive held the
-// softmax threads for about 1700 cycles).
-__device__ __forceinline__ void mbar_arrive_tmem(uint32_t cluster_bar) {
+// Arrive on a barrier of the cluster for what the pair's MMAs read next: tensor
+// memory (behind tcgen05.fence::before_thread_sync) or this CTA's own shared
+// memory (behind fence.proxy.async).  Nothing that a thread of the other CTA
+// reads is handed over, so the arrive releases at CTA scope: at cluster scope
+// it held the softmax threads for about 1700 cycles.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 // A copy into this CTA's shared memory that completes on a barrier of the pair

@@ -75,14 +75,15 @@ struct Bars {
   uint64_t q_full, q_tmem;            // Q in shared memory (TMA) / in tensor memory
   // keys and values land on barriers of their own: each has one consumer, which
   // never falls two phases behind (a parity tells only two apart)
-  uint64_t k_full[4], k_empty[4], v_full[SLOTS], v_empty[2], clean[SLOTS], land[2];
-  uint64_t rope_full, rope_empty;
-  uint64_t s_full, s_free;            // S(t) complete / read
+  uint64_t k_full[4], k_empty[SLOTS], v_full[SLOTS], clean[SLOTS], land[2];
+  uint64_t rope_full;
+  uint64_t s_full, s_free;            // S(t) complete (the rope chunk is free) / read
   uint64_t p_full, o_done;            // P(t) written / P(t) V(t) complete
   uint64_t seen_full;                 // z_lo and the nodes' bits are known
   uint64_t drain[2];
   uint32_t tmem_slot;
   int abort, z_lo;
+  int issued;                         // tiles whose scores are in the tensor pipe
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
@@ -118,6 +119,13 @@ __device__ __forceinline__ Item item_of(int u, int nt) {
 __device__ __forceinline__ int first_key_use(int t) { return t == 0 ? 0 : 6 * t - 2; }
 __device__ __forceinline__ int first_value_use(int t, int nt) { return 6 * t + (t < nt - 1 ? 8 : 4); }
 
+// Lets the scores of `tiles` tiles into the tensor pipe first: P V then fills
+// the gap until the softmax has read them, instead of delaying them.  Only an
+// order is at stake, so it gives up early.
+__device__ __forceinline__ void behind_scores(Bars* B, int tiles) {
+  for (int i = 0; i < 1024 && *(volatile int*)&B->issued < tiles; ++i) {}
+}
+
 struct Unit {
   int b, qt, half, n, W, ctx, j_lo, nt;
   int tiles;             // row tiles of the cluster: 1, or 2 (this CTA's and its peer's)
@@ -126,10 +134,15 @@ struct Unit {
   long row0;
 };
 
+// First key of the t-th tile.  The tiles run from the end of the range down:
+// the ones whose value rows need clearing (the block's own keys) come first,
+// while the pipeline fills.
+__device__ __forceinline__ int tile_key(const Unit& U, int t) { return U.j_lo + (U.nt - 1 - t) * KT; }
+
 // Tiles whose value rows need clearing: those that reach the block's own keys
 // or the end, and those that reach below the first key that a row sees.
 __device__ __forceinline__ bool dirty_tile(const Unit& U, int z_lo, int t) {
-  const int j0 = U.j_lo + t * KT;
+  const int j0 = tile_key(U, t);
   return j0 + KT > U.ctx || j0 < z_lo;
 }
 
@@ -180,10 +193,10 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
     tmem_st32_u(tmem + TM_Q + 32 * kh + lane_base, q);
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_tmem(mapa(smem_u32(&B->q_tmem), U.lead));
+    if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&B->q_tmem), U.lead));
   }
   for (int t = 0; t < U.nt; ++t) {
-    const int jh = U.j_lo + t * KT + KH * kh;             // first key of this thread's half
+    const int jh = tile_key(U, t) + KH * kh;              // first key of this thread's half
     float s[KH];
     wait_bar(B, &B->s_full, t & 1, P.rule.status);
     tc_fence_after();
@@ -194,7 +207,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
     for (int c = 0; c < KH; c += 32) tmem_reg_fence32(s + c);
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_tmem(s_free);              // S(t + 1) may overwrite it
+    if (lane == 0) mbar_arrive_pair(s_free);              // S(t + 1) may overwrite it
     float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     if (__all_sync(0xffffffffu, !ok || (jh >= lo && jh + KH <= U.ctx))) {
 #pragma unroll
@@ -250,7 +263,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
     tmem_st32_u(tmem + TM_P + 32 * kh + lane_base, pw);
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_tmem(p_full);
+    if (lane == 0) mbar_arrive_pair(p_full);
   }
   // the row sum from both halves
   xm[kh * QROWS + r] = lsum;
@@ -312,6 +325,7 @@ __device__ __forceinline__ void store_rows(const TreeParams& P, const uint8_t* s
   const int rows = min(QROWS, P.rule.T * P.rule.H - U.qt * QROWS);
   const int y = CS > 1 ? (int)(blockIdx.y % CS) : 0, x = (int)(blockIdx.x & 1);
   const uint32_t stg = smem_u32(smem), lse_a = stg + OFF_STG_LSE;
+#pragma unroll 2
   for (int r = y * (QROWS / CS) + warp; r < min(rows, (y + 1) * (QROWS / CS)); r += THREADS / 32) {
     float l[CS];
     float4 a[CS], c[CS];
@@ -379,11 +393,14 @@ __device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* sm
   if (tid == 0) {
     mbar_init(&B->q_full, 1);
     mbar_init(&B->q_tmem, 8 * U.tiles);
-    for (int i = 0; i < 4; ++i) { mbar_init(&B->k_full[i], 1); mbar_init(&B->k_empty[i], 1); }
-    for (int i = 0; i < SLOTS; ++i) { mbar_init(&B->v_full[i], 1); mbar_init(&B->clean[i], U.tiles); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&B->v_empty[i], 1); mbar_init(&B->land[i], 1); }
+    for (int i = 0; i < 4; ++i) mbar_init(&B->k_full[i], 1);
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(&B->k_empty[i], 1);
+      mbar_init(&B->v_full[i], 1);
+      mbar_init(&B->clean[i], U.tiles);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&B->land[i], 1);
     mbar_init(&B->rope_full, 1);
-    mbar_init(&B->rope_empty, 1);
     mbar_init(&B->s_full, 1);
     mbar_init(&B->s_free, 8 * U.tiles);
     mbar_init(&B->p_full, 8 * U.tiles);
@@ -392,6 +409,7 @@ __device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* sm
     mbar_init(&B->drain[0], 1);
     mbar_init(&B->drain[1], 1);
     B->abort = 0;
+    B->issued = 0;
     B->z_lo = 0x7fffffff;
     fence_mbar_init();
     pdl_trigger();
@@ -463,6 +481,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
   U.b = unit / P.tiles_per_block;
   U.qt = unit % P.tiles_per_block;
   U.row0 = ((long)U.b * R.T) * R.H + (long)U.qt * QROWS;
+  if (warp == W_ROPE && lane == 0) { prefetch_tmap(&P.tmK); prefetch_tmap(&P.tmC); prefetch_tmap(&P.tmQ); }
   if (warp == W_S) tmem_alloc(&B->tmem_slot, TMEM_COLS);
   set_up(P, B, smem, U);
   tc_fence_before();
@@ -479,7 +498,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
     int z_lo = -1;                                        // known from seen_full on
     for (int u = s; u < 6 * U.nt; u += SLOTS) {
       const Item it = item_of(u, U.nt);
-      const int j0 = U.j_lo + it.tile * KT;
+      const int j0 = tile_key(U, it.tile);
       const int ch = it.value ? 4 * U.half + 2 * it.pair : 2 * it.pair;
       uint64_t* full = it.value ? &B->v_full[s] : &B->k_full[s];
       const int y = lane < nseg ? cache_row(R, U, j0 + lane * seg, true) : 0;
@@ -521,8 +540,8 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
       __syncwarp();
       int t = 0;
       for (; t < U.nt; ++t) {
-        const int y = lane < nseg ? cache_row(R, U, U.j_lo + t * KT + lane * seg, false) : 0;
-        if (!wait_bar(B, &B->rope_empty, (t & 1) ^ 1, R.status)) break;
+        const int y = lane < nseg ? cache_row(R, U, tile_key(U, t) + lane * seg, false) : 0;
+        if (!wait_bar(B, &B->s_full, (t & 1) ^ 1, R.status)) break;
         if (lane == 0) mbar_arrive_expect_tx(&B->rope_full, CH_BYTES);
         __syncwarp();
         if (lane < nseg) tma_load_3d(smem + OFF_ROPE + lane * seg * 128, &P.tmK, &B->rope_full, 512, y, 0);
@@ -571,8 +590,8 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
         if (!(ok = ok && wait_bar(B, &B->rope_full, t & 1, R.status, ready))) break;
 #pragma unroll
         for (int d = 0; d < 4; ++d) mma_f16(tS, dQ + (NQS - 1) * U_CH + 2 * d, dRope + 2 * d, idesc, 1u);
-        mma_commit(&B->rope_empty);
         mma_commit(&B->s_full);
+        *(volatile int*)&B->issued = t + 1;
       }
       mma_commit(&B->drain[0]);
       mbar_wait(&B->drain[0], 0, R.status);
@@ -589,6 +608,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
       for (int t = 0; t < U.nt && ok; ++t) {
         int s = first_value_use(t, U.nt) % SLOTS;
         const bool dirty = dirty_tile(U, z_lo, t);
+        behind_scores(B, min(t + 2, U.nt));
         if (!(ok = wait_bar(B, &B->p_full, t & 1, R.status))) break;
         tc_fence_after();
         bool ready = false;
@@ -643,6 +663,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
   U.b = unit / units;
   U.qt = 2 * (unit % units) + p;
   U.row0 = ((long)U.b * R.T) * R.H + (long)U.qt * QROWS;
+  if (warp == W_ROPE && lane == 0) { prefetch_tmap(&P.tmK); prefetch_tmap(&P.tmQ); }
   if (warp == W_S) tmem_alloc_pair(&B->tmem_slot, TMEM_COLS);
   set_up(P, B, smem, U);
   tc_fence_before();
@@ -659,9 +680,11 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
     int t = 0;
     bool ok = true;
     for (; t < U.nt && ok; ++t) {
-      const int y = lane < 2 * nkseg ? cache_row(R, U, U.j_lo + t * KT + 64 * p + sg * seg, true) : 0;
+      const int y = lane < 2 * nkseg ? cache_row(R, U, tile_key(U, t) + 64 * p + sg * seg, true) : 0;
+      // a commit costs the issuing thread 125 cycles: one frees pairs 0 and 1, that
+      // of the finished scores pairs 2 and 3
+      if (!(ok = wait_bar(B, i0 == 0 ? &B->k_empty[0] : &B->s_full, (t & 1) ^ 1, R.status))) break;
       for (int i = i0; i < i0 + 2; ++i) {
-        if (!(ok = wait_bar(B, &B->k_empty[i], (t & 1) ^ 1, R.status))) break;
         if (p == 0 && lane == 0) mbar_arrive_expect_tx(&B->k_full[i], 2 * PSLOT_BYTES);
         __syncwarp();
         if (lane < 2 * nkseg)
@@ -679,11 +702,11 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
     const int z_lo = ok ? B->z_lo : 0;
     uint32_t nd = 0;                                      // tiles cleared so far
     for (int t = 0; t < U.nt && ok; ++t) {
-      const int j0 = U.j_lo + t * KT;
+      const int j0 = tile_key(U, t);
       const int y = lane < nvseg ? cache_row(R, U, j0 + lane * seg, true) : 0;
       const bool dirty = dirty_tile(U, z_lo, t);
+      if (!(ok = wait_bar(B, &B->o_done, (t & 1) ^ 1, R.status))) break;
       for (int i = 0; i < PV; ++i) {
-        if (!(ok = wait_bar(B, &B->v_empty[i], (t & 1) ^ 1, R.status))) break;
         uint8_t* slot = smem + OFF_PV + i * PSLOT_BYTES;
         // a tile to be cleared lands on a barrier of this CTA's own
         const uint32_t bar = dirty ? smem_u32(&B->land[i]) : mapa(smem_u32(&B->v_full[i]), U.lead);
@@ -698,7 +721,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
         if (dirty) {
           if (!(ok = wait_bar(B, &B->land[i], nd & 1, R.status))) break;
           clear_unseen(U, smem, slot, 1, j0, z_lo);
-          if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&B->clean[i]), U.lead));
+          if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&B->clean[i]), U.lead));
         }
       }
       nd += dirty;
@@ -713,8 +736,8 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
       __syncwarp();
       int t = 0;
       for (; t < U.nt; ++t) {
-        const int y = lane < nkseg ? cache_row(R, U, U.j_lo + t * KT + 64 * p + lane * seg, false) : 0;
-        if (!wait_bar(B, &B->rope_empty, (t & 1) ^ 1, R.status)) break;
+        const int y = lane < nkseg ? cache_row(R, U, tile_key(U, t) + 64 * p + lane * seg, false) : 0;
+        if (!wait_bar(B, &B->s_full, (t & 1) ^ 1, R.status)) break;
         if (p == 0 && lane == 0) mbar_arrive_expect_tx(&B->rope_full, CH_BYTES);
         __syncwarp();
         if (lane < nkseg)
@@ -758,13 +781,13 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
               else
                 mma_f16_pair(tS, dQ + (2 * i - 2 + c) * U_CH + 2 * d, db, idesc, 1u);
             }
-          mma_commit_pair(&B->k_empty[i], both);
+          if (i == 1) mma_commit_pair(&B->k_empty[0], both);
         }
         if (!(ok = ok && wait_bar(B, &B->rope_full, par, R.status, ready))) break;
 #pragma unroll
         for (int d = 0; d < 4; ++d) mma_f16_pair(tS, dQ + (NQS - 1) * U_CH + 2 * d, dRope + 2 * d, idesc, 1u);
-        mma_commit_pair(&B->rope_empty, both);
-        mma_commit_pair(&B->s_full, both);
+        mma_commit_pair(&B->s_full, both);          // keys 2 and 3 and the rope chunk are free, too
+        *(volatile int*)&B->issued = t + 1;
       }
       mma_commit_pair(&B->drain[0], both);
       mbar_wait(&B->drain[0], 0, R.status);
@@ -780,22 +803,18 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
       const int z_lo = B->z_lo;
       for (int t = 0; t < U.nt && ok; ++t) {
         const bool dirty = dirty_tile(U, z_lo, t);
+        behind_scores(B, min(t + 2, U.nt));
         if (!(ok = wait_bar(B, &B->p_full, t & 1, R.status))) break;
         tc_fence_after();
         bool ready = false;
 #pragma unroll
         for (int i = 0; i < PV; ++i) {
-          if (dirty) {           // both CTAs have cleared their halves (shared memory: cluster scope)
-            ok = ok && !*(volatile int*)&B->abort && mbar_wait_cluster(&B->clean[i], nd & 1, R.status);
-            if (!ok) break;
-          } else {
-            if (!(ok = ok && wait_bar(B, &B->v_full[i], nf & 1, R.status, ready))) break;
-            if (i == 0) ready = mbar_test_wait(&B->v_full[1], nf & 1);
-          }
+          uint64_t* bar = dirty ? &B->clean[i] : &B->v_full[i];   // (both CTAs have cleared their halves)
+          if (!(ok = ok && wait_bar(B, bar, (dirty ? nd : nf) & 1, R.status, ready))) break;
+          if (i == 0) ready = mbar_test_wait(bar + 1, (dirty ? nd : nf) & 1);
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
             mma_f16_ts_pair(tO + 128 * i, tP + 8 * k, dV + i * U_SLOT + U_KSTEP * k, idesc, (t | k) ? 1u : 0u);
-          mma_commit_pair(&B->v_empty[i], both);
         }
         mma_commit_pair(&B->o_done, both);
         if (dirty) ++nd; else ++nf;
