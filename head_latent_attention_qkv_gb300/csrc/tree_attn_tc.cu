@@ -162,25 +162,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
     return U.n > 0 && (R.q_visible ? R.q_visible[(long)U.b * R.T + nd] != 0 : true) &&
            tree::in_tree(R, parent, nd, report);
   };
-  const bool ok = live && row_ok(node, U.first && kh == 0);
-  // rows that see nothing are computed like their neighbours and written as
-  // zeros, so that they do not take a warp off the unmasked path
-  const int lo = U.W > 0 ? max(0, R.positions[m] - U.W + 1) : 0;
-  float mrun = -INFINITY, lsum = 0.f;
-  // what the cluster's rows see: the first context key and the nodes on their
-  // paths (one row of a node stands for all; the second threads take the peer's)
   const uint32_t s_free = mapa(smem_u32(&B->s_free), U.lead), p_full = mapa(smem_u32(&B->p_full), U.lead);
-  if (kh < U.tiles) {
-    const int other = (kh ? U.qt ^ 1 : U.qt) * QROWS + r, nd = other / R.H;
-    if (other < R.T * R.H && (other % R.H == 0 || r == 0) && row_ok(nd, false)) {
-      uint32_t* seen = (uint32_t*)(smem + OFF_SEEN);
-      const int32_t* pos = R.positions + (long)U.b * R.T;
-      atomicMin(&B->z_lo, U.W > 0 ? max(0, min(pos[nd] - U.W + 1, U.ctx)) : 0);
-      for (int k = nd; k >= 0; k = parent[k])
-        if (U.W == 0 || pos[nd] - pos[k] < U.W) atomicOr(&seen[k >> 5], 1u << (k & 31));
-    }
-  }
-  mbar_arrive(&B->seen_full);
   if (U.nt > 0) {
     // Q dims 0..127 of this row -> tensor memory (bf16 pairs), 64 dims a thread
     const uint4* src = reinterpret_cast<const uint4*>(P.q_abs + (U.row0 + r) * 576 + 64 * kh);
@@ -195,6 +177,25 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
     __syncwarp();
     if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&B->q_tmem), U.lead));
   }
+  // the walks over the tree run while the first scores are on their way
+  const bool ok = live && row_ok(node, U.first && kh == 0);
+  // rows that see nothing are computed like their neighbours and written as
+  // zeros, so that they do not take a warp off the unmasked path
+  const int lo = U.W > 0 ? max(0, R.positions[m] - U.W + 1) : 0;
+  float mrun = -INFINITY, lsum = 0.f;
+  // what the cluster's rows see: the first context key and the nodes on their
+  // paths (one row of a node stands for all; the second threads take the peer's)
+  if (kh < U.tiles) {
+    const int other = (kh ? U.qt ^ 1 : U.qt) * QROWS + r, nd = other / R.H;
+    if (other < R.T * R.H && (other % R.H == 0 || r == 0) && row_ok(nd, false)) {
+      uint32_t* seen = (uint32_t*)(smem + OFF_SEEN);
+      const int32_t* pos = R.positions + (long)U.b * R.T;
+      atomicMin(&B->z_lo, U.W > 0 ? max(0, min(pos[nd] - U.W + 1, U.ctx)) : 0);
+      for (int k = nd; k >= 0; k = parent[k])
+        if (U.W == 0 || pos[nd] - pos[k] < U.W) atomicOr(&seen[k >> 5], 1u << (k & 31));
+    }
+  }
+  mbar_arrive(&B->seen_full);
   for (int t = 0; t < U.nt; ++t) {
     const int jh = tile_key(U, t) + KH * kh;              // first key of this thread's half
     float s[KH];
@@ -385,7 +386,8 @@ __device__ __forceinline__ void join_and_store(const TreeParams& P, const uint8_
   else store_rows<4>(P, smem, U);
 }
 
-// Barriers, the unit's keys and this part's share of their tiles; every warp.
+// Barriers and, while the cluster meets, the unit's keys and this part's share
+// of their tiles; every warp.
 __device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* smem, Unit& U) {
   const tree::Rule& R = P.rule;
   const int tid = threadIdx.x, lane = tid % 32;
@@ -415,6 +417,8 @@ __device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* sm
     pdl_trigger();
   }
   for (int i = tid; i < tree::MAX_NODES / 32; i += THREADS) seen[i] = 0;
+  tc_fence_before();           // (the tensor memory's address)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();                  // Q_abs and the nodes' own entries come from the kernels before
   U.n = tree::block_keys(R, U.b, &U.W, &U.ctx, tid == 0 && U.first && U.qt == 0);
   // whether a row may see anything (padding and masked rows left out), and the
@@ -436,6 +440,8 @@ __device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* sm
   const int tb = (int)((long)blockIdx.y * all / gridDim.y), te = (int)((long)(blockIdx.y + 1) * all / gridDim.y);
   U.j_lo += tb * KT;
   U.nt = te - tb;
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  tc_fence_after();
 }
 
 // Cache row of logical key j (past the end of the keys or on a bad page: past
@@ -484,9 +490,6 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
   if (warp == W_ROPE && lane == 0) { prefetch_tmap(&P.tmK); prefetch_tmap(&P.tmC); prefetch_tmap(&P.tmQ); }
   if (warp == W_S) tmem_alloc(&B->tmem_slot, TMEM_COLS);
   set_up(P, B, smem, U);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = B->tmem_slot;
   const int seg = P.seg_rows, nseg = KT / seg;
 
@@ -666,10 +669,6 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
   if (warp == W_ROPE && lane == 0) { prefetch_tmap(&P.tmK); prefetch_tmap(&P.tmQ); }
   if (warp == W_S) tmem_alloc_pair(&B->tmem_slot, TMEM_COLS);
   set_up(P, B, smem, U);
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync_all();          // the peer's barriers are up
-  tc_fence_after();
   const uint32_t tmem = B->tmem_slot, both = 3u << U.lead;
   // segments: rows of a page, at most this CTA's 64 keys of a tile
   const int seg = P.seg_rows, nkseg = 64 / seg, nvseg = KT / seg;
@@ -835,35 +834,56 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
   if (P.cluster_parts > 1) cluster_sync_all();            // nobody leaves while its rows may be read
 }
 
-// One warp per row and quarter of its dims: sum_s w_s o_s / sum_s w_s with w_s =
-// 2^(lse_s - max), in split order; a row that no split saw is zero.  The lanes
-// hold the splits' log-sum-exps (at most MAX_PARTS), eight loads are in flight.
+// A row and quarter of its dims: sum_s w_s o_s / sum_s w_s with w_s = 2^(lse_s -
+// max); a row that no part saw is zero.  WPI warps share the parts (w, w + WPI,
+// ...; up to eight loads in flight each) and their sums are added in warp
+// order: one warp for few parts, eight for many, whose chain of loads would
+// otherwise be the kernel's time (52 parts of 128 rows: 32 us with one warp a
+// whole row).  The lanes hold the parts' log-sum-exps (at most MAX_PARTS).
+template <int WPI>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict__ part,
                                                          const float* __restrict__ part_lse, long rows,
-                                                         int splits, __half* __restrict__ o_lat,
+                                                         int parts, __half* __restrict__ o_lat,
                                                          float* __restrict__ lse) {
-  const long item = (long)blockIdx.x * 8 + threadIdx.x / 32;
+  __shared__ float4 sums[8][32];
+  pdl_wait();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const long item = ((long)blockIdx.x * 8 + warp) / WPI;
   const long row = item >> 2;
-  const int quarter = (int)(item & 3), lane = threadIdx.x % 32;
-  if (row >= rows) return;
-  const float l0 = lane < splits ? part_lse[lane * rows + row] : -INFINITY;
-  const float l1 = lane + 32 < splits ? part_lse[(lane + 32) * rows + row] : -INFINITY;
-  float mx = fmaxf(l0, l1);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const float w0 = mx == -INFINITY ? 0.f : exp2f(l0 - mx), w1 = mx == -INFINITY ? 0.f : exp2f(l1 - mx);
+  const int quarter = (int)(item & 3), w = warp % WPI;
+  const bool live = row < rows;
+  float w0 = 0.f, w1 = 0.f, den = 0.f, mx = -INFINITY;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float den = 0.f;
-  const float4* src = reinterpret_cast<const float4*>(part + row * 512) + quarter * 32 + lane;
+  if (live) {
+    const float l0 = lane < parts ? part_lse[lane * rows + row] : -INFINITY;
+    const float l1 = lane + 32 < parts ? part_lse[(lane + 32) * rows + row] : -INFINITY;
+    mx = fmaxf(l0, l1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    w0 = mx == -INFINITY ? 0.f : exp2f(l0 - mx);
+    w1 = mx == -INFINITY ? 0.f : exp2f(l1 - mx);
+    den = w0 + w1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    const float4* src = reinterpret_cast<const float4*>(part + row * 512) + quarter * 32 + lane;
 #pragma unroll 8
-  for (int s = 0; s < splits; ++s) {
-    const float w = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31);
-    if (w != 0.f) {                                      // else nothing may have been written
-      const float4 v = src[(long)s * rows * 128];
-      den += w;
-      acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
+    for (int s = w; s < parts; s += WPI) {
+      const float x = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31);
+      const float4 v = src[(long)s * rows * 128];         // (rows of parts that saw nothing are zero)
+      acc.x += x * v.x; acc.y += x * v.y; acc.z += x * v.z; acc.w += x * v.w;
     }
   }
+  if (WPI > 1) {
+    sums[warp][lane] = acc;
+    __syncthreads();
+    if (w) return;
+#pragma unroll
+    for (int k = 1; k < WPI; ++k) {
+      const float4 v = sums[warp + k][lane];
+      acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    }
+  }
+  if (!live) return;
   const float inv = den > 0.f ? 1.f / den : 0.f;
   __half2 h2[2] = {__floats2half2_rn(acc.x * inv, acc.y * inv), __floats2half2_rn(acc.z * inv, acc.w * inv)};
   *reinterpret_cast<uint2*>(o_lat + row * 512 + quarter * 128 + 4 * lane) = *reinterpret_cast<uint2*>(h2);
@@ -873,18 +893,24 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict
 }  // namespace
 
 // Row tiles in pairs, parts of a unit's key range (a multiple of the parts of a
-// cluster).  Cost in tiles of the waves of CTAs that a choice needs: FIXED
-// beyond a part's share of the keys, JOIN for a cluster's join, MERGE and
-// MERGE_PART for the second kernel.  Keys are bounded by the page table; shorter
-// sequences only split finer than they need.
+// cluster).  Cost in tiles (2.6 us) of the waves of CTAs that a choice needs:
+// FIXED beyond a part's share of the keys, JOIN for a cluster's join, MERGE and
+// MERGE_PART for the second kernel.  Measured, us: 512 rows x 2064 keys x 8
+// sequences 51 whole, 43 in two parts merged, 41 in two joined; 8192 rows x
+// 6-8 k keys x 4 sequences 544, 605, 607; 128 rows x 32 k keys 70 in 16 parts, 41
+// in 48, 39 in 64.  Keys are bounded by the page table (shorter sequences only
+// split finer than they need) and, when windows are given, taken as at most 16
+// tiles, since the windows are on the device: 800 rows x 5 sequences with a
+// window of 512 keys 31 us whole, 45 in three parts.
 struct Plan {
   bool pair;
   int parts, cluster_parts;
 };
 Plan tree_plan(const mla_handle* h, const mla_attn_desc_t& d) {
-  constexpr double FIXED = 5.0, JOIN = 0.5, MERGE = 3.0, MERGE_PART = 0.02;
+  constexpr double FIXED = 4.0, JOIN = 2.8, MERGE = 3.5, MERGE_PART = 0.05;
   const long rows = (long)d.block_len * h->lay.H, tpb = (rows + QROWS - 1) / QROWS;
-  const long tiles = ((long)d.max_pages * h->cfg.page_size + KT - 1) / KT;
+  long tiles = ((long)d.max_pages * h->cfg.page_size + KT - 1) / KT;
+  if (d.window && tiles > 16) tiles = 16;
   Plan best{tpb > 1, 1, 1};
   const long groups = (long)d.num_blocks * (best.pair ? 2 * ((tpb + 1) / 2) : tpb);   // clusters of one part
   double cost = 1e300;
@@ -950,9 +976,12 @@ mla_status_t tree_attention(cudaStream_t st, mla_handle* h, const tree::Rule& r,
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   h->launches += 1;
   if (parts > 1) {
-    Launch M(dim3((unsigned)((rows + 1) / 2)), dim3(256), 0, st, false);
-    e = cudaLaunchKernelEx(&M.cfg, tree_merge_kernel, (const float*)P.part, (const float*)P.part_lse, rows,
-                           parts, o_lat, lse);
+    const int wpi = parts > 8 ? 8 : 1;
+    const long blocks = (rows * 4 * wpi + 7) / 8;
+    if (blocks > 0x7fffffffL) return fail(MLA_ERR_INVALID_ARG, "tree attention: too many rows");
+    Launch M(dim3((unsigned)blocks), dim3(256), 0, st, true);
+    e = cudaLaunchKernelEx(&M.cfg, wpi == 8 ? tree_merge_kernel<8> : tree_merge_kernel<1>, (const float*)P.part,
+                           (const float*)P.part_lse, rows, parts, o_lat, lse);
     if (e != cudaSuccess) return cuda_fail(e, "tree attention merge launch");
     h->launches += 1;
   }
