@@ -52,9 +52,7 @@ class Handle:
 
     def __init__(self, dims, weights: dict, page_size: int, device="cuda", stream=None):
         self.dims, self.page_size, self.device = dims, page_size, torch.device(device)
-        # the device as tensors name it (an index in place of "the current one")
-        self.tensor_device = self.device if self.device.index is not None or self.device.type != "cuda" \
-            else torch.device("cuda", torch.cuda.current_device())
+        self.device_index = torch.cuda.current_device() if self.device.index is None else self.device.index
         self.cfg = make_config(dims, page_size)
         self.arena = _buf(lib.mla_weight_arena_bytes(C.byref(self.cfg)), self.device)
         w = _lib.mla_weights_t(**{k: (weights[k].data_ptr() if weights.get(k) is not None else None)
@@ -220,45 +218,39 @@ def mla_latent_attention_backward(h: Handle, q_abs, positions, cache, desc, o_la
                                             _stream(stream)), "mla_latent_attention_backward")
 
 
-class _on:
-    """Allocations under `stream` (the stream the call runs on), so that the
-    caching allocator reuses a buffer only behind the work that reads it."""
-
-    def __init__(self, stream):
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-
-
-def _take(name, t, dtype, shape, device):
+def _take(name, t, dtype, shape, h):
     """The pointer of `t`, checked: on the handle's device, contiguous, of this
-    type and shape (a dimension given as None is free)."""
-    if t.device != device or t.dtype != dtype or not t.is_contiguous() or t.dim() != len(shape) or any(
-            w is not None and s != w for s, w in zip(t.shape, shape)):
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    type and shape."""
+    if t.dtype is not dtype or t.get_device() != h.device_index or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:"
+                         f"{h.device_index}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
     return t.data_ptr()
 
 
-def _opt(name, t, dtype, shape, device):
-    return None if t is None else _take(name, t, dtype, shape, device)
+def _take_cache(h: Handle, cache):
+    return _take("cache", cache, torch_dtype(h.dims), (cache.shape[0], h.page_size, h.dims.cache_dim), h)
+
+
+def _take_rows(name, t, dtype, n, h):
+    """A matrix of n rows: its pointer and row length."""
+    return _take(name, t, dtype, (n, t.shape[-1]), h), t.shape[-1]
+
+
+def _run(fn, h: Handle, *args):
+    """The entry point `fn` on the current stream (a caller's stream argument is
+    made the current one, so that what the call allocates belongs to it)."""
+    check(fn(h.h, *args, torch._C._cuda_getCurrentRawStream(h.device_index)), fn.__name__)
 
 
 def _tree_args(h: Handle, q_abs, positions, cache, desc, parent):
-    d, dev, dt = h.dims, h.tensor_device, torch_dtype(h.dims)
+    d = h.dims
     tokens = desc.num_blocks * desc.block_len
     if q_abs.numel() != tokens * d.num_heads * d.cache_dim:
         raise ValueError(f"q_abs: expected {tokens * d.num_heads} rows of {d.cache_dim}, got {tuple(q_abs.shape)}")
-    return (_take("q_abs", q_abs, dt, (None,) * q_abs.dim(), dev),
-            _take("positions", positions, torch.int32, (tokens,), dev),
-            _take("cache", cache, dt, (None, h.page_size, d.cache_dim), dev),
-            _opt("parent", parent, torch.int32, (tokens,), dev))
+    return (_take("q_abs", q_abs, torch_dtype(d), q_abs.shape, h),
+            _take("positions", positions, torch.int32, (tokens,), h), _take_cache(h, cache),
+            None if parent is None else _take("parent", parent, torch.int32, (tokens,), h))
 
 
 def mla_tree_attention(h: Handle, q_abs, positions, cache, desc, parent, o_lat=None, lse=None,
@@ -268,20 +260,22 @@ def mla_tree_attention(h: Handle, q_abs, positions, cache, desc, parent, o_lat=N
     nodes' own keys the last ``block_len`` of each sequence.  ``o_lat`` [rows,
     kv_lora_rank] (fp16 for bf16 layers) and, when ``lse`` is given, its fp32
     [rows] log-sum-exp."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mla_tree_attention(h, q_abs, positions, cache, desc, parent, o_lat, lse, None, workspace)
     q, pos, c, par = _tree_args(h, q_abs, positions, cache, desc, parent)
-    rows = desc.num_blocks * desc.block_len * h.dims.num_heads
+    rows, rank = desc.num_blocks * desc.block_len * h.dims.num_heads, h.dims.kv_lora_rank
     dt = torch.float16 if h.dims.dtype == "bf16" else torch.float32
-    lse_p = _opt("lse", lse, torch.float32, (rows,), h.tensor_device)
-    with _on(stream):
-        if o_lat is None:
-            o_lat = torch.empty(rows, h.dims.kv_lora_rank, dtype=dt, device=h.tensor_device)
-        need = lib.mla_tree_attention_workspace_bytes(h.h, C.byref(desc))
-        ws = workspace if workspace is not None else (_buf(need, h.tensor_device) if need else None)
-        out = _take("o_lat", o_lat, dt, (rows, h.dims.kv_lora_rank), h.tensor_device)
-        check(lib.mla_tree_attention(h.h, q, pos, c, cache.shape[0], C.byref(desc), par, out, lse_p,
-                                     None if ws is None else ws.data_ptr(),
-                                     0 if ws is None else ws.numel(), _stream(stream)),
-              "mla_tree_attention")
+    lse_p = None if lse is None else _take("lse", lse, torch.float32, (rows,), h)
+    if o_lat is None:
+        o_lat = torch.empty((rows, rank), dtype=dt, device=cache.device)
+    out = _take("o_lat", o_lat, dt, (rows, rank), h)
+    ref = C.byref(desc)
+    if workspace is None:
+        need = lib.mla_tree_attention_workspace_bytes(h.h, ref)
+        workspace = _buf(need, cache.device) if need else None
+    _run(lib.mla_tree_attention, h, q, pos, c, cache.shape[0], ref, par, out, lse_p,
+         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     return o_lat
 
 
@@ -293,21 +287,22 @@ def mla_draft_forward_tree(h: Handle, hidden, positions, block_slot_mapping, cac
                            out=None, stream=None, workspace=None):
     """mla_draft_forward over trees of drafted tokens (``parent`` as in
     mla_tree_attention)."""
-    d, dev, dt = h.dims, h.tensor_device, torch_dtype(h.dims)
-    M = desc.num_blocks * desc.block_len
-    args = (_take("hidden", hidden, dt, (M, d.hidden_size), dev),
-            _take("positions", positions, torch.int32, (M,), dev),
-            _opt("block_slot_mapping", block_slot_mapping, torch.int64, (M,), dev),
-            _take("cache", cache, dt, (None, h.page_size, d.cache_dim), dev))
-    par = _take("parent", parent, torch.int32, (M,), dev)
-    with _on(stream):
-        if out is None:
-            out = torch.empty(M, d.hidden_size, dtype=dt, device=dev)
-        need = lib.mla_forward_tree_workspace_bytes(h.h, C.byref(desc))
-        ws = workspace if workspace is not None else _buf(need, dev)
-        check(lib.mla_draft_forward_tree(h.h, *args, cache.shape[0], C.byref(desc), par,
-                                         _take("out", out, dt, (M, d.hidden_size), dev), ws.data_ptr(),
-                                         ws.numel(), _stream(stream)), "mla_draft_forward_tree")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mla_draft_forward_tree(h, hidden, positions, block_slot_mapping, cache, desc, parent, out,
+                                          None, workspace)
+    D, dt, M = h.dims.hidden_size, torch_dtype(h.dims), desc.num_blocks * desc.block_len
+    args = (_take("hidden", hidden, dt, (M, D), h), _take("positions", positions, torch.int32, (M,), h),
+            None if block_slot_mapping is None else
+            _take("block_slot_mapping", block_slot_mapping, torch.int64, (M,), h), _take_cache(h, cache))
+    par = _take("parent", parent, torch.int32, (M,), h)
+    if out is None:
+        out = torch.empty((M, D), dtype=dt, device=cache.device)
+    ref = C.byref(desc)
+    if workspace is None:
+        workspace = _buf(lib.mla_forward_tree_workspace_bytes(h.h, ref), cache.device)
+    _run(lib.mla_draft_forward_tree, h, *args, cache.shape[0], ref, par, _take("out", out, dt, (M, D), h),
+         workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -321,19 +316,21 @@ def mla_key_weights(h: Handle, q_abs, positions, cache, desc, lse, weights_out, 
     of block b received from the block's rows, whose log-sum-exp is ``lse``
     (mla_tree_attention's with ``parent``, mla_latent_attention's without);
     ``prior`` may be ``weights_out`` itself, fp32 [blocks, keys or more]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mla_key_weights(h, q_abs, positions, cache, desc, lse, weights_out, prior, decay, parent,
+                                   None, workspace)
     q, pos, c, par = _tree_args(h, q_abs, positions, cache, desc, parent)
-    dev, nb = h.tensor_device, desc.num_blocks
-    rows = nb * desc.block_len * h.dims.num_heads
-    out = _take("weights_out", weights_out, torch.float32, (nb, None), dev)
-    ldw = weights_out.shape[1]
-    with _on(stream):
-        need = lib.mla_key_weights_workspace_bytes(h.h, C.byref(desc), ldw)
-        ws = workspace if workspace is not None else (_buf(need, dev) if need else None)
-        check(lib.mla_key_weights(h.h, q, pos, c, cache.shape[0], C.byref(desc), par,
-                                  _take("lse", lse, torch.float32, (rows,), dev), decay,
-                                  _opt("prior", prior, torch.float32, (nb, ldw), dev), out, ldw,
-                                  None if ws is None else ws.data_ptr(),
-                                  0 if ws is None else ws.numel(), _stream(stream)), "mla_key_weights")
+    nb = desc.num_blocks
+    out, ldw = _take_rows("weights_out", weights_out, torch.float32, nb, h)
+    lse_p = _take("lse", lse, torch.float32, (nb * desc.block_len * h.dims.num_heads,), h)
+    prior_p = None if prior is None else _take("prior", prior, torch.float32, (nb, ldw), h)
+    ref = C.byref(desc)
+    if workspace is None:
+        need = lib.mla_key_weights_workspace_bytes(h.h, ref, ldw)
+        workspace = _buf(need, cache.device) if need else None
+    _run(lib.mla_key_weights, h, q, pos, c, cache.shape[0], ref, par, lse_p, decay, prior_p, out, ldw,
+         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     return weights_out
 
 
@@ -346,18 +343,18 @@ def mla_cache_select(h: Handle, weights, kv_len, budget: int, sink: int = 0, rec
     """``(keep, keep_len)``: per sequence the ascending indices of the keys that
     stay under ``budget`` (the first ``sink``, the last ``recent``, then the
     heaviest; -1 behind the last) and how many they are."""
-    dev, n = h.tensor_device, kv_len.shape[0]
-    w = _take("weights", weights, torch.float32, (n, None), dev)
-    with _on(stream):
-        if keep is None:
-            keep = torch.empty(n, max(budget, 0), dtype=torch.int32, device=dev)
-        if keep_len is None:
-            keep_len = torch.empty(n, dtype=torch.int32, device=dev)
-        check(lib.mla_cache_select(h.h, w, weights.shape[1], _take("kv_len", kv_len, torch.int32, (n,), dev),
-                                   n, budget, sink, recent,
-                                   _take("keep", keep, torch.int32, (n, max(budget, 0)), dev),
-                                   _take("keep_len", keep_len, torch.int32, (n,), dev),
-                                   _stream(stream)), "mla_cache_select")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mla_cache_select(h, weights, kv_len, budget, sink, recent, keep, keep_len)
+    n = kv_len.shape[0]
+    w, ldw = _take_rows("weights", weights, torch.float32, n, h)
+    if keep is None:
+        keep = torch.empty((n, max(budget, 0)), dtype=torch.int32, device=weights.device)
+    if keep_len is None:
+        keep_len = torch.empty((n,), dtype=torch.int32, device=weights.device)
+    _run(lib.mla_cache_select, h, w, ldw, _take("kv_len", kv_len, torch.int32, (n,), h), n, budget, sink, recent,
+         _take("keep", keep, torch.int32, (n, max(budget, 0)), h),
+         _take("keep_len", keep_len, torch.int32, (n,), h))
     return keep, keep_len
 
 
@@ -368,28 +365,26 @@ def mla_cache_compact(h: Handle, cache, block_table, kv_len, keep, keep_len, fir
     place, ``weights`` with them, or into the pages of ``dst_block_table``,
     the weights into ``weights_out``.  The new lengths are ``keep_len`` (+
     ``first``)."""
-    dev, n, d = h.tensor_device, kv_len.shape[0], h.dims
-    if weights is not None and weights_out is None and dst_block_table is None:
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mla_cache_compact(h, cache, block_table, kv_len, keep, keep_len, first, dst_block_table,
+                                     weights, weights_out, None, workspace)
+    n, i32 = kv_len.shape[0], torch.int32
+    in_place = dst_block_table is None
+    if weights is not None and weights_out is None and in_place:
         weights_out = weights
-    args = (_take("cache", cache, torch_dtype(d), (None, h.page_size, d.cache_dim), dev), cache.shape[0],
-            _take("block_table", block_table, torch.int32, (n, None), dev), block_table.shape[1],
-            _take("kv_len", kv_len, torch.int32, (n,), dev), n,
-            _take("keep", keep, torch.int32, (n, None), dev), keep.shape[1],
-            _take("keep_len", keep_len, torch.int32, (n,), dev),
-            _opt("first", first, torch.int32, (n,), dev),
-            _opt("dst_block_table", dst_block_table, torch.int32, (n, None), dev),
-            0 if dst_block_table is None else dst_block_table.shape[1],
-            _opt("weights", weights, torch.float32, (n, None), dev),
-            _opt("weights_out", weights_out, torch.float32,
-                 (n, None) if weights is None else tuple(weights.shape), dev),
-            0 if weights is None else weights.shape[1])
-    with _on(stream):
-        ws = workspace
-        if ws is None and dst_block_table is None:
-            ws = _buf(lib.mla_cache_compact_workspace_bytes(h.h, n, keep.shape[1]), dev)
-        check(lib.mla_cache_compact(h.h, *args, None if ws is None else ws.data_ptr(),
-                                    0 if ws is None else ws.numel(), _stream(stream)),
-              "mla_cache_compact")
+    table, max_pages = _take_rows("block_table", block_table, i32, n, h)
+    keep_p, ldk = _take_rows("keep", keep, i32, n, h)
+    dst, dst_pages = (None, 0) if in_place else _take_rows("dst_block_table", dst_block_table, i32, n, h)
+    w, ldw = (None, 0) if weights is None else _take_rows("weights", weights, torch.float32, n, h)
+    args = (_take_cache(h, cache), cache.shape[0], table, max_pages, _take("kv_len", kv_len, i32, (n,), h), n,
+            keep_p, ldk, _take("keep_len", keep_len, i32, (n,), h),
+            None if first is None else _take("first", first, i32, (n,), h), dst, dst_pages, w,
+            None if weights_out is None else _take("weights_out", weights_out, torch.float32, (n, ldw), h), ldw)
+    if workspace is None and in_place:
+        workspace = _buf(lib.mla_cache_compact_workspace_bytes(h.h, n, ldk), cache.device)
+    _run(lib.mla_cache_compact, h, *args, None if workspace is None else workspace.data_ptr(),
+         0 if workspace is None else workspace.numel())
 
 
 def mla_cache_compact_workspace_bytes(h: Handle, num_seqs: int, ldk: int) -> int:

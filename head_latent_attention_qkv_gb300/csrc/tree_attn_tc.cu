@@ -917,7 +917,8 @@ Plan tree_plan(const mla_handle* h, const mla_attn_desc_t& d) {
   for (int cs = 1; cs <= 4; cs *= 2) {
     // clusters of 2 cs CTAs that the GPU holds at once (GPCs are not a multiple of 8)
     const long hold = cs == 1 ? h->num_sms / 2 : cs == 2 ? h->num_sms / 4 - 2 : h->num_sms / 8 - 4;
-    for (int g = 1; g <= MAX_PARTS && (long)g * cs <= (tiles > cs ? tiles : cs); ++g) {
+    for (const int g : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 40, 48, 56, MAX_PARTS}) {
+      if ((long)g * cs > (tiles > cs ? tiles : cs)) break;
       const double waves = (double)((groups * g + hold - 1) / (hold > 0 ? hold : 1));
       const double c = waves * (FIXED + (cs > 1 ? JOIN : 0.0) + (double)((tiles + g * cs - 1) / (g * cs))) +
                        (g > 1 ? MERGE + MERGE_PART * groups * g : 0.0);
