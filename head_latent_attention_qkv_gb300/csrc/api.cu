@@ -474,7 +474,8 @@ mla_status_t tree_attention(mla_handle_t* h, cudaStream_t st, const void* q_abs,
   if (h->cfg.dtype == MLA_BF16)
     return tc::tree_attention(st, h, r, d, (const __nv_bfloat16*)q_abs, (const __nv_bfloat16*)cache,
                               (__half*)o_lat, lse, ws, pdl);
-  simt::tree_attention(st, h, r, d.num_blocks, q_abs, cache, o_lat, lse, d.vis_stats);
+  simt::tree_attention(st, h, r, d.num_blocks, (const float*)q_abs, (const float*)cache, (float*)o_lat, lse,
+                       d.vis_stats);
   h->launches += 1;
   return MLA_OK;
 }
@@ -855,8 +856,8 @@ extern "C" mla_status_t mla_key_weights(mla_handle_t* h, const void* q_abs, cons
                         (const __nv_bfloat16*)cache, lse, decay, prior, weights_out, (long)ldw, workspace);
     if (s != MLA_OK) return s;
   } else {
-    simt::key_weights((cudaStream_t)stream, h, r, d.num_blocks, q_abs, cache, lse, decay, prior, weights_out,
-                      (long)ldw);
+    simt::key_weights((cudaStream_t)stream, h, r, d.num_blocks, (const float*)q_abs, (const float*)cache, lse,
+                      decay, prior, weights_out, (long)ldw);
     h->launches += 1;
   }
   MLA_CUDA_TRY(cudaGetLastError());

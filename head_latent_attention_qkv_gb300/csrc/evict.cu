@@ -47,7 +47,7 @@ struct SelectArgs {
   int32_t* keep;
   int32_t* keep_len;
   long ldw;
-  int budget, sink, recent, cluster;
+  int budget, sink, recent;
   int smem_keys;            // capacity of the shared key array
   uint32_t* status;
 };
@@ -60,9 +60,9 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ int ld_cluster_int(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ int2 ld_cluster_int2(uint32_t addr) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
 
@@ -89,12 +89,14 @@ __device__ __forceinline__ int warp_prefix(int v, int* buf, int* total) {
   return before;
 }
 
+template <int CL>
 __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a) {
   extern __shared__ uint32_t keys[];                     // this CTA's keys (when they fit)
-  __shared__ int hist[2][BINS];
-  __shared__ int buf[32], buf2[32], cta_counts[2], found[2];
+  __shared__ __align__(8) int hist[2][BINS];
+  __shared__ int buf[32], buf2[32], found[2];
+  __shared__ __align__(8) int cta_counts[2];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int CL = a.cluster, rank = CL > 1 ? (int)tc::cluster_ctarank() : 0;
+  const int rank = CL > 1 ? (int)tc::cluster_ctarank() : 0;
   const long seq = blockIdx.x / CL;
   int n = a.kv_len[seq];
   if (n < 0 || n > a.ldw) {
@@ -115,12 +117,13 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
   // this warp's run of keys
   const int nw = CL * SEL_WARPS;
   const int wlen = ((n + nw - 1) / nw + 31) & ~31;
-  const long i0 = (long)(rank * SEL_WARPS + warp) * wlen;
+  const int i0 = (int)min((long)(rank * SEL_WARPS + warp) * wlen, (long)n);   // (n < 2^30)
   const bool cached = SEL_WARPS * wlen <= a.smem_keys;
   uint32_t* mine = keys + warp * wlen;
   if (cached)
+#pragma unroll 8
     for (int o = lane; o < wlen; o += 32) {
-      const long i = i0 + o;
+      const int i = i0 + o;
       mine[o] = i < n ? order_key(w[i]) : 0u;
     }
   auto key_at = [&](int o) -> uint32_t {
@@ -135,24 +138,26 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       const uint32_t dmask = (1u << bits) - 1u;
       int* hp = hist[pass & 1];
+#pragma unroll 8
       for (int o = lane; o < wlen; o += 32) {
-        const long i = i0 + o;
+        const int i = i0 + o;
         const uint32_t u = key_at(o);
-        if (i >= mid_lo && i < mid_hi && (u & mask) == prefix) atomicAdd(&hp[(u >> shift) & dmask], 1);
+        const bool in = i >= mid_lo && i < mid_hi && (u & mask) == prefix;
+        if (in) atomicAdd(&hp[(u >> shift) & dmask], 1);
       }
       if (CL > 1) tc::cluster_sync_all(); else __syncthreads();
       // every CTA is done with the other array (pass - 1): clear it for pass + 1
       for (int i = tid; i < BINS; i += SEL_THREADS) hist[(pass + 1) & 1][i] = 0;
       // counts of this thread's two bins, from the top: bins B - 1 - 2 tid, B - 2 - 2 tid
       const int bin = BINS - 1 - 2 * tid;
-      int c0 = hp[bin], c1 = hp[bin - 1];
-      if (CL > 1) {
-        c0 = c1 = 0;
-        for (int r = 0; r < CL; ++r) {
-          c0 += ld_cluster_int(tc::mapa(tc::smem_u32(&hp[bin]), (uint32_t)r));
-          c1 += ld_cluster_int(tc::mapa(tc::smem_u32(&hp[bin - 1]), (uint32_t)r));
-        }
-      }
+      int c0 = 0, c1 = 0;
+      int2 from[CL];                                     // every CTA's counts, all loads in flight
+#pragma unroll
+      for (int r = 0; r < CL; ++r)
+        from[r] = CL == 1 ? *reinterpret_cast<const int2*>(&hp[bin - 1])
+                          : ld_cluster_int2(tc::mapa(tc::smem_u32(&hp[bin - 1]), (uint32_t)r));
+#pragma unroll
+      for (int r = 0; r < CL; ++r) { c0 += from[r].y; c1 += from[r].x; }
       const int x = lane_prefix(c0 + c1);
       if (lane == 31) buf[warp] = x;
       __syncthreads();
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
   const bool none = a.budget == a.sink + a.recent;
   // 2: stays, 1: equals the threshold, 0: goes
   auto klass = [&](int o) -> int {
-    const long i = i0 + o;
+    const int i = i0 + o;
     if (i >= n) return 0;
     if (i < mid_lo || i >= mid_hi) return 2;
     if (none) return 0;
@@ -183,6 +188,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
     return u > thr ? 2 : u == thr ? 1 : 0;
   };
   int cnt2 = 0, cnt1 = 0;
+#pragma unroll 4
   for (int o = lane; o < wlen; o += 32) {
     const int c = klass(o);
     cnt2 += __popc(__ballot_sync(0xffffffffu, c == 2));
@@ -194,11 +200,14 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
   if (CL > 1) {
     if (tid == 0) { cta_counts[0] = tot2; cta_counts[1] = tot1; }
     tc::cluster_sync_all();
-    for (int r = 0; r < rank; ++r) {
-      before2 += ld_cluster_int(tc::mapa(tc::smem_u32(&cta_counts[0]), (uint32_t)r));
-      before1 += ld_cluster_int(tc::mapa(tc::smem_u32(&cta_counts[1]), (uint32_t)r));
-    }
+    int2 from[CL];
+#pragma unroll
+    for (int r = 0; r < CL; ++r) from[r] = ld_cluster_int2(tc::mapa(tc::smem_u32(cta_counts), (uint32_t)r));
+#pragma unroll
+    for (int r = 0; r < CL; ++r)
+      if (r < rank) { before2 += from[r].x; before1 += from[r].y; }
   }
+#pragma unroll 4
   for (int o = lane; o < wlen; o += 32) {
     const int c = klass(o);
     const uint32_t b2 = __ballot_sync(0xffffffffu, c == 2), b1 = __ballot_sync(0xffffffffu, c == 1);
@@ -219,9 +228,9 @@ int select_cluster(long ldw) { return ldw <= 8192 ? 1 : ldw <= 16384 ? 2 : ldw <
 // ---------------------------------------------------------------------------
 // Compaction
 // ---------------------------------------------------------------------------
-constexpr int MV_THREADS = 256, MV_UPT = 9;              // units a thread holds
+constexpr int MV_THREADS = 128, MV_UPT = 9;              // units a thread holds
 constexpr int MV_UNITS = MV_THREADS * MV_UPT;            // 2304: 32 rows of 576 bf16
-constexpr int MV_MAX_ROWS = 256;
+constexpr int MV_MAX_ROWS = 128;
 constexpr int ZERO_ROWS = 4096;                          // weights a tail chunk clears
 constexpr uint32_t FLAG_BUDGET = 1u << 24;
 
@@ -413,15 +422,17 @@ extern "C" mla_status_t mla_cache_select(mla_handle_t* h, const float* weights, 
   const long wlen = ((ldw + nw - 1) / nw + 31) & ~31L;
   const long keys = evict::SEL_WARPS * wlen;              // of a CTA, at most
   const int smem_keys = keys <= evict::SEL_SMEM_KEYS ? (int)keys : 0;
-  evict::SelectArgs a{weights, kv_len, keep, keep_len, (long)ldw, budget, sink, recent, cl, smem_keys, h->status};
+  evict::SelectArgs a{weights, kv_len, keep, keep_len, (long)ldw, budget, sink, recent, smem_keys, h->status};
   static std::once_flag once;
   std::call_once(once, [] {
-    cudaFuncSetAttribute(evict::select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         evict::SEL_SMEM_KEYS * 4);
+    for (auto* k : {evict::select_kernel<1>, evict::select_kernel<2>, evict::select_kernel<4>, evict::select_kernel<8>})
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, evict::SEL_SMEM_KEYS * 4);
   });
   Launch L(dim3((unsigned)(num_seqs * cl)), dim3(evict::SEL_THREADS), (size_t)smem_keys * 4,
            (cudaStream_t)stream, false, dim3((unsigned)cl, 1, 1));
-  MLA_CUDA_TRY(cudaLaunchKernelEx(&L.cfg, evict::select_kernel, a));
+  MLA_CUDA_TRY(cudaLaunchKernelEx(
+      &L.cfg, cl == 1 ? evict::select_kernel<1> : cl == 2 ? evict::select_kernel<2>
+              : cl == 4 ? evict::select_kernel<4> : evict::select_kernel<8>, a));
   h->launches += 1;
   return MLA_OK;
 }

@@ -52,7 +52,9 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
-__device__ __forceinline__ bool wait_bar(Bars* B, uint64_t* bar, uint32_t parity, uint32_t* st) {
+__device__ __forceinline__ bool wait_bar(Bars* B, uint64_t* bar, uint32_t parity, uint32_t* st,
+                                         bool ready = false) {
+  if (ready) return true;
   if (*(volatile int*)&B->abort) return false;
   if (mbar_wait(bar, parity, st)) return true;
   B->abort = 1;
@@ -328,13 +330,15 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid
         for (int qt = it.qt0; qt < it.qt1 && ok; ++qt, ++tile) {
           const int buf = tile & 1;
           const uint32_t d = tmem + buf * NMAX, idesc = idesc_f16(256, it.cols(qt), false);
+          bool ready = mbar_test_wait(&B->q_full[s], qpar);
           if (!(ok = wait_bar(B, &B->s_free[buf], ((tile >> 1) & 1) ^ 1, R.status))) break;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < NCH; ++c) {
             if (qt == it.qt0 && c % 3 == 0 && ok) ok = wait_bar(B, &B->k_full[c / 3], use & 1, R.status);
-            if (!ok || !(ok = wait_bar(B, &B->q_full[s], qpar, R.status))) break;
-            tc_fence_after();
+            if (!ok || !(ok = wait_bar(B, &B->q_full[s], qpar, R.status, ready))) break;
+            // a look at the next slot, its answer used after these MMAs
+            ready = s + 1 == QSLOTS ? mbar_test_wait(&B->q_full[0], qpar ^ 1) : mbar_test_wait(&B->q_full[s + 1], qpar);
             const uint64_t db = dQ + s * U_CH;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -384,14 +388,21 @@ long key_tiles(const mla_handle* h, const mla_attn_desc_t& d, long ldw) {
   return ((ldw < cap ? ldw : cap) + PAIR_KT - 1) / PAIR_KT;
 }
 
-// Parts of a block's rows: as many as give every pair of SMs two items, by the
-// page table's bound on the keys.
+// Parts of a block's rows, so that the last round of items leaves few pairs of
+// SMs idle: the cost is rounds times an item's row tiles and a load of its keys
+// (about half a row tile), by the page table's bound on the keys; a second
+// kernel weighs as much as a row tile.
 int weight_splits(const mla_handle* h, const mla_attn_desc_t& d, long ldw) {
   const long rows = (long)d.block_len * h->lay.H, row_tiles = (rows + NMAX - 1) / NMAX;
   const long items = (long)d.num_blocks * key_tiles(h, d, ldw), pairs = h->num_sms / 2;
-  if (items >= 2 * pairs) return 1;
-  const long s = (2 * pairs + items - 1) / items;
-  return (int)(s < row_tiles ? s : row_tiles);
+  int best = 1;
+  double cost = 1e300;
+  for (long s = 1; s <= row_tiles && s <= 16 && items * s <= 32 * pairs; ++s) {
+    const double rounds = (double)((items * s + pairs - 1) / pairs);
+    const double c = rounds * ((double)((row_tiles + s - 1) / s) + 0.5) + (s > 1 ? 1.0 : 0.0);
+    if (c < cost) { cost = c; best = (int)s; }
+  }
+  return best;
 }
 
 }  // namespace

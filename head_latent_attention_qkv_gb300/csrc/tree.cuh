@@ -96,12 +96,12 @@ __device__ __forceinline__ unsigned long long key_bits(const Rule& a, long b, in
 }  // namespace tree
 
 namespace simt {
-// Tree attention and key weights of any layer, fp32 arithmetic on the CUDA
-// cores (the fp32 layers' path).
+// Tree attention and key weights of the fp32 layers, on the CUDA cores (q_abs and
+// cache 16-byte aligned).
 void tree_attention(cudaStream_t st, const mla_handle* h, const tree::Rule& r, int num_blocks,
-                    const void* q_abs, const void* cache, void* o_lat, float* lse, int32_t* vis_stats);
+                    const float* q_abs, const float* cache, float* o_lat, float* lse, int32_t* vis_stats);
 void key_weights(cudaStream_t st, const mla_handle* h, const tree::Rule& r, int num_blocks,
-                 const void* q_abs, const void* cache, const float* lse, float decay,
+                 const float* q_abs, const float* cache, const float* lse, float decay,
                  const float* prior, float* out, long ldw);
 }  // namespace simt
 }  // namespace mla
