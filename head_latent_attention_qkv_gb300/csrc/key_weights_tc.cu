@@ -19,7 +19,10 @@
 // approximation (2^-22), the arguments in fp32.  Keys wholly inside the context
 // of rows without a window need no mask; otherwise every lane works out the 32
 // keys of its warp for four columns (tree::key_bits) and the words are
-// broadcast.  When the key tiles alone do not fill the GPU the rows are cut in
+// broadcast.  A step of the issuing thread (a barrier, four MMAs, a commit)
+// takes about 530 cycles however few the columns, so blocks of at most 84 rows
+// bring Q in three chunks a slot (64 sequences x 32 rows x 1-4 k keys: 57.6 us
+// with one).  When the key tiles alone do not fill the GPU the rows are cut in
 // parts whose sums a second kernel adds in order.
 #include <math.h>
 
@@ -68,63 +71,71 @@ __device__ __forceinline__ float fast_exp2(float x) {
 __device__ __forceinline__ void sum_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // One (block, 256-key tile, row part) item; every role of both CTAs walks the
-// same items.  Called by whole warps.
+// same items.  Called by whole warps; the lanes hold 32 blocks at a time (loading
+// and scanning them anew for every item took 3.6 k cycles of a decode item's
+// 9.6 k).  num_blocks * key tiles * parts < 2^31 (2^35 keys, 256 a tile, 16 parts).
 struct Items {
   const WeightParams& P;
-  long id, step;
-  int b0 = 0;                 // blocks before b0 hold `before` key tiles
-  long before = 0;
+  uint32_t id, step;
+  int b0 = -32;               // first block of the group at hand
+  uint32_t before = 0, total = 0;     // key tiles of the blocks before the group, of the group
+  int l_n0 = 0, l_W = 0, l_ctx = 0;   // this lane's block
+  uint32_t l_tiles = 0, l_end = 0;    // its tiles, and those up to and with it
   // the item at hand
   int b, n, n0, W, ctx, kt, sp, qt0, qt1;
   bool skip;                  // no row of the block reaches the tile (windows)
 
-  __device__ Items(const WeightParams& p) : P(p), id(blockIdx.x >> 1), step(gridDim.x >> 1) {}
+  const uint32_t splits;
+  const int tiles, block_rows, cap;   // row tiles and rows of a block, columns of the output
+
+  __device__ Items(const WeightParams& p)
+      : P(p), id(blockIdx.x >> 1), step(gridDim.x >> 1), splits((uint32_t)p.splits),
+        tiles((p.rule.T * p.rule.H + NMAX - 1) / NMAX), block_rows(p.rule.T * p.rule.H),
+        cap((int)min(p.ldw, 0x7fffffffL)) {}
 
   __device__ bool next() {
     const tree::Rule& R = P.rule;
     const int lane = threadIdx.x % 32;
-    const long tile = id / P.splits;
-    sp = (int)(id - tile * P.splits);
+    const uint32_t tile = splits == 1 ? id : id / splits;
+    sp = (int)(id - tile * splits);
     id += step;
-    while (b0 < P.num_blocks) {
-      int t = 0;
-      if (b0 + lane < P.num_blocks) {
-        int w, c;
-        const long keys = min((long)tree::block_keys(R, b0 + lane, &w, &c, false), P.ldw);
-        t = (int)((keys + PAIR_KT - 1) / PAIR_KT);
-      }
-      int x = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const long total = __shfl_sync(0xffffffffu, x, 31);
-      if (tile < before + total) {
-        const uint32_t m = __ballot_sync(0xffffffffu, tile < before + x);
-        const int l = __ffs(m) - 1;
-        b = b0 + l;
-        kt = (int)(tile - before) - (__shfl_sync(0xffffffffu, x, l) - __shfl_sync(0xffffffffu, t, l));
-        n0 = tree::block_keys(R, b, &W, &ctx, false);
-        n = (int)min((long)n0, P.ldw);
-        const int tiles = (R.T * R.H + NMAX - 1) / NMAX;
-        qt0 = (int)((long)sp * tiles / P.splits);
-        qt1 = (int)((long)(sp + 1) * tiles / P.splits);
-        skip = qt0 == qt1;
-        if (W > 0 && (kt + 1) * PAIR_KT <= ctx) {
-          int pmin = 0x7fffffff;
-          for (int i = lane; i < R.T; i += 32) pmin = min(pmin, R.positions[(long)b * R.T + i]);
-          pmin = __reduce_min_sync(0xffffffffu, pmin);
-          skip |= (kt + 1) * PAIR_KT <= pmin - W + 1;
-        }
-        return true;
-      }
+    while (tile >= before + total) {
       before += total;
       b0 += 32;
+      if (b0 >= P.num_blocks) return false;
+      l_tiles = 0;
+      if (b0 + lane < P.num_blocks) {
+        l_n0 = tree::block_keys(R, b0 + lane, &l_W, &l_ctx, false);
+        l_tiles = (uint32_t)(min(l_n0, cap) + PAIR_KT - 1) / PAIR_KT;
+      }
+      l_end = l_tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, l_end, o);
+        if (lane >= o) l_end += y;
+      }
+      total = __shfl_sync(0xffffffffu, l_end, 31);
     }
-    return false;
+    const int l = __ffs(__ballot_sync(0xffffffffu, tile < before + l_end)) - 1;
+    b = b0 + l;
+    kt = (int)(tile - before - __shfl_sync(0xffffffffu, l_end - l_tiles, l));
+    n0 = __shfl_sync(0xffffffffu, l_n0, l);
+    W = __shfl_sync(0xffffffffu, l_W, l);
+    ctx = __shfl_sync(0xffffffffu, l_ctx, l);
+    n = min(n0, cap);
+    // (at most 2^31 rows a block: the product stays below 2^32)
+    qt0 = splits == 1 ? 0 : (int)((uint32_t)sp * tiles / splits);
+    qt1 = splits == 1 ? tiles : (int)((uint32_t)(sp + 1) * tiles / splits);
+    skip = qt0 == qt1;
+    if (W > 0 && (kt + 1) * PAIR_KT <= ctx) {
+      int pmin = 0x7fffffff;
+      for (int i = lane; i < R.T; i += 32) pmin = min(pmin, R.positions[(long)b * R.T + i]);
+      pmin = __reduce_min_sync(0xffffffffu, pmin);
+      skip |= (kt + 1) * PAIR_KT <= pmin - W + 1;
+    }
+    return true;
   }
-  __device__ int rows(int qt) const { return min(NMAX, P.rule.T * P.rule.H - qt * NMAX); }
+  __device__ int rows(int qt) const { return min(NMAX, block_rows - qt * NMAX); }
   // columns of row tile qt's MMA (each CTA holds half of them)
   __device__ int cols(int qt) const { return (rows(qt) + 31) & ~31; }
 };
@@ -225,6 +236,8 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
   }
 }
 
+// QC: chunks of Q a slot holds.
+template <int QC>
 __global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid_constant__ WeightParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -259,39 +272,48 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid
     uint32_t use = 0;
     bool ok = true;
     Items it(P);
-    while (ok && it.next()) {
-      if (it.skip) continue;
-      int y = past_end;
+    // the next item that loads keys, and the cache row of this lane's segment
+    auto look = [&](int* y) {
+      do {
+        if (!it.next()) return false;
+      } while (it.skip);
+      *y = past_end;
       const int j = it.kt * PAIR_KT + rank * KT + lane * seg;
       if (lane < nseg && j < it.n) {
         const int pg = R.block_table[(long)it.b * R.max_pages + j / ps];
-        if (pg >= 0 && pg < R.num_pages) y = pg * ps + j % ps;
+        if (pg >= 0 && pg < R.num_pages) *y = pg * ps + j % ps;
         else set_status(R.status, MLA_DEV_BAD_PAGE);
       }
-      for (int c3 = 0; c3 < TRIO && ok; ++c3) {
-        ok = wait_bar(B, &B->k_empty[c3], (use & 1) ^ 1, R.status);
-        if (!ok) break;
+      return true;
+    };
+    int y = 0;
+    bool more = look(&y);
+    while (ok && more) {
+      const int y0 = y;
+      for (int c3 = 0; c3 < TRIO; ++c3) {
+        if (c3 == TRIO - 1) more = look(&y);              // under the wait for the last trio
+        if (!(ok = wait_bar(B, &B->k_empty[c3], (use & 1) ^ 1, R.status))) break;
         if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&B->k_full[c3], 2 * 3 * CH_BYTES);
         __syncwarp();
         const uint32_t bar = mapa(smem_u32(&B->k_full[c3]), 0);
         uint8_t* dst = smem + OFF_K + 3 * c3 * CH_BYTES;
         if (nseg == 1) {
-          if (lane == 0) tma_load_3d_pair(dst, &P.tmC, bar, 0, y, 3 * c3);
+          if (lane == 0) tma_load_3d_pair(dst, &P.tmC, bar, 0, y0, 3 * c3);
         } else if (lane < nseg) {
           for (int c = 0; c < 3; ++c)
-            tma_load_3d_pair(dst + c * CH_BYTES + lane * seg * 128, &P.tmK, bar, (3 * c3 + c) * 64, y, 0);
+            tma_load_3d_pair(dst + c * CH_BYTES + lane * seg * 128, &P.tmK, bar, (3 * c3 + c) * 64, y0, 0);
         }
         __syncwarp();
       }
       ++use;
     }
     // every copy has landed before the pair may exit (its barriers are the even CTA's)
-    if (rank == 0 && use > 0)
+    if (rank == 0 && ok && use > 0)
       for (int i = 0; i < TRIO; ++i) mbar_wait(&B->k_full[i], (use - 1) & 1, R.status);
   } else if (warp == W_Q || warp == W_Q + 1) {
     // ---- this CTA's half of the rows, chunk by chunk; the two warps take turns ----
     if (lane == 0) prefetch_tmap(&P.tmQ);
-    uint32_t u = 0;                                       // chunks so far
+    uint32_t u = 0;                                       // slots used so far
     int last = -1;
     bool ok = true;
     Items it(P);
@@ -299,14 +321,14 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid
       if (it.skip) continue;
       for (int qt = it.qt0; qt < it.qt1 && ok; ++qt) {
         const int y = (int)((long)it.b * R.T * R.H + (long)qt * NMAX + rank * (it.cols(qt) / 2));
-        for (int c = 0; c < NCH; ++c, ++u) {
+        for (int c = 0; c < NCH; c += QC, ++u) {
           if ((u & 1) != (uint32_t)(warp - W_Q)) continue;
           const int s = u % QSLOTS;
           ok = wait_bar(B, &B->q_empty[s], ((u / QSLOTS) & 1) ^ 1, R.status);
           if (!ok) break;
           if (lane == 0) {
-            if (rank == 0) mbar_arrive_expect_tx(&B->q_full[s], 2 * P.q_box_rows * 128);
-            tma_load_3d_pair(smem + OFF_Q + s * CH_BYTES, &P.tmQ, mapa(smem_u32(&B->q_full[s]), 0), c * 64, y, 0);
+            if (rank == 0) mbar_arrive_expect_tx(&B->q_full[s], 2 * QC * P.q_box_rows * 128);
+            tma_load_3d_pair(smem + OFF_Q + s * CH_BYTES, &P.tmQ, mapa(smem_u32(&B->q_full[s]), 0), 0, y, c);
           }
           __syncwarp();
           last = (int)u;
@@ -334,17 +356,20 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid
           if (!(ok = wait_bar(B, &B->s_free[buf], ((tile >> 1) & 1) ^ 1, R.status))) break;
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < NCH; ++c) {
+          for (int c = 0; c < NCH; c += QC) {
             if (qt == it.qt0 && c % 3 == 0 && ok) ok = wait_bar(B, &B->k_full[c / 3], use & 1, R.status);
             if (!ok || !(ok = wait_bar(B, &B->q_full[s], qpar, R.status, ready))) break;
             // a look at the next slot, its answer used after these MMAs
             ready = s + 1 == QSLOTS ? mbar_test_wait(&B->q_full[0], qpar ^ 1) : mbar_test_wait(&B->q_full[s + 1], qpar);
-            const uint64_t db = dQ + s * U_CH;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16_pair(d, dK + c * U_CH + 2 * k, db + 2 * k, idesc, (c | k) ? 1u : 0u);
+            for (int x = 0; x < QC; ++x) {
+              const uint64_t db = dQ + s * U_CH + (uint64_t)x * P.q_box_rows * 8;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_f16_pair(d, dK + (c + x) * U_CH + 2 * k, db + 2 * k, idesc, (c | x | k) ? 1u : 0u);
+            }
             mma_commit_pair(&B->q_empty[s]);
-            if (qt == it.qt1 - 1 && c % 3 == 2) mma_commit_pair(&B->k_empty[c / 3]);
+            if (qt == it.qt1 - 1 && (c + QC) % 3 == 0) mma_commit_pair(&B->k_empty[c / 3]);
             if (++s == QSLOTS) { s = 0; qpar ^= 1; }
           }
           mma_commit_pair(&B->s_full[buf]);
@@ -422,7 +447,9 @@ mla_status_t key_weights(cudaStream_t st, mla_handle* h, const tree::Rule& r, co
   const long block_rows = (long)r.T * r.H;
   P.q_box_rows = (int)((block_rows < NMAX ? (block_rows + 31) & ~31L : NMAX) / 2);
   P.seg_rows = r.page_size < KT ? r.page_size : KT;
-  if (!make_tmap_2d(&P.tmQ, false, q_abs, rows, l.L, l.L, P.q_box_rows) ||
+  // 84 rows: 3 chunks of up to 42 rows a CTA fit a slot
+  const int qc = 3 * P.q_box_rows * 128 <= CH_BYTES ? 3 : 1;
+  if (!make_tmap_chunked(&P.tmQ, false, q_abs, rows, l.L, l.L, P.q_box_rows, qc) ||
       !make_tmap_chunked(&P.tmC, false, cache, slots, l.L, l.L, KT, 3) ||
       !make_tmap_2d(&P.tmK, false, cache, slots, l.L, l.L, P.seg_rows))
     return fail(MLA_ERR_CUDA, "key weights: cuTensorMapEncodeTiled failed");
@@ -439,12 +466,13 @@ mla_status_t key_weights(cudaStream_t st, mla_handle* h, const tree::Rule& r, co
   P.scale_log2 = h->scale * 1.4426950408889634f;
   static std::once_flag once;
   std::call_once(once, [] {
-    cudaFuncSetAttribute(key_weights_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    for (auto* k : {key_weights_tc_kernel<1>, key_weights_tc_kernel<3>})
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   });
   const long items = (long)d.num_blocks * key_tiles(h, d, ldw) * P.splits, pairs = h->num_sms / 2;
   Launch L(dim3((unsigned)(2 * (items < pairs ? items : pairs))), dim3(THREADS), SMEM_BYTES, st, false,
            dim3(2, 1, 1));
-  cudaError_t e = cudaLaunchKernelEx(&L.cfg, key_weights_tc_kernel, P);
+  cudaError_t e = cudaLaunchKernelEx(&L.cfg, qc == 3 ? key_weights_tc_kernel<3> : key_weights_tc_kernel<1>, P);
   if (e != cudaSuccess) return cuda_fail(e, "key weights launch");
   h->launches += 1;
   if (P.splits > 1) {

@@ -26,7 +26,7 @@ struct TreeParams {
 };
 
 struct WeightParams {
-  CUtensorMap tmQ;    // Q_abs, box 64 dims x q_box_rows
+  CUtensorMap tmQ;    // Q_abs, chunked view, box q_box_rows rows x 1 or 3 chunks
   CUtensorMap tmC;    // the cache, chunked view, box 128 rows x 3 chunks
   CUtensorMap tmK;    // the cache, box 64 dims x seg_rows
   tree::Rule rule;
