@@ -40,6 +40,7 @@
 #include "tree_tc.cuh"
 
 #include <math.h>
+#include <stddef.h>
 
 #include <mutex>
 
@@ -146,8 +147,22 @@ __device__ __forceinline__ bool dirty_tile(const Unit& U, int z_lo, int t) {
   return j0 + KT > U.ctx || j0 < z_lo;
 }
 
+// 64 of a row's first 128 dims, one thread (warps 0-3 and 8-11; zeros for rows
+// past the block's), asked for before the CTA sets up.
+__device__ __forceinline__ void load_q(const TreeParams& P, const Unit& U, uint32_t* q) {
+  const int r = threadIdx.x & (QROWS - 1), kh = threadIdx.x >= 256 ? 1 : 0;
+  const bool live = U.qt * QROWS + r < P.rule.T * P.rule.H;
+  const uint4* src = reinterpret_cast<const uint4*>(P.q_abs + (live ? U.row0 + r : 0) * 576 + 64 * kh);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
+    q[4 * i] = v.x; q[4 * i + 1] = v.y; q[4 * i + 2] = v.z; q[4 * i + 3] = v.w;
+  }
+}
+__device__ __forceinline__ bool softmax_warp(int warp) { return warp < 4 || (warp >= 8 && warp < 12); }
+
 __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8_t* smem, uint32_t tmem,
-                                             const Unit& U) {
+                                             const Unit& U, const uint32_t* q) {
   const int r = threadIdx.x & (QROWS - 1), kh = threadIdx.x >= 256 ? 1 : 0, w = r / 32, lane = r % 32;
   constexpr int KH = KT / 2;
   const uint32_t lane_base = (uint32_t)(w * 32) << 16;
@@ -165,13 +180,6 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   const uint32_t s_free = mapa(smem_u32(&B->s_free), U.lead), p_full = mapa(smem_u32(&B->p_full), U.lead);
   if (U.nt > 0) {
     // Q dims 0..127 of this row -> tensor memory (bf16 pairs), 64 dims a thread
-    const uint4* src = reinterpret_cast<const uint4*>(P.q_abs + (U.row0 + r) * 576 + 64 * kh);
-    uint32_t q[32];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint4 v = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-      q[4 * i] = v.x; q[4 * i + 1] = v.y; q[4 * i + 2] = v.z; q[4 * i + 3] = v.w;
-    }
     tmem_st32_u(tmem + TM_Q + 32 * kh + lane_base, q);
     tc_fence_before();
     __syncwarp();
@@ -326,7 +334,7 @@ __device__ __forceinline__ void store_rows(const TreeParams& P, const uint8_t* s
   const int rows = min(QROWS, P.rule.T * P.rule.H - U.qt * QROWS);
   const int y = CS > 1 ? (int)(blockIdx.y % CS) : 0, x = (int)(blockIdx.x & 1);
   const uint32_t stg = smem_u32(smem), lse_a = stg + OFF_STG_LSE;
-#pragma unroll 2
+#pragma unroll(CS == 1 ? 4 : 2)
   for (int r = y * (QROWS / CS) + warp; r < min(rows, (y + 1) * (QROWS / CS)); r += THREADS / 32) {
     float l[CS];
     float4 a[CS], c[CS];
@@ -392,47 +400,41 @@ __device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* sm
   const tree::Rule& R = P.rule;
   const int tid = threadIdx.x, lane = tid % 32;
   uint32_t* seen = (uint32_t*)(smem + OFF_SEEN);          // nodes that a row of the cluster sees
-  if (tid == 0) {
-    mbar_init(&B->q_full, 1);
-    mbar_init(&B->q_tmem, 8 * U.tiles);
-    for (int i = 0; i < 4; ++i) mbar_init(&B->k_full[i], 1);
-    for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(&B->k_empty[i], 1);
-      mbar_init(&B->v_full[i], 1);
-      mbar_init(&B->clean[i], U.tiles);
-    }
-    for (int i = 0; i < 2; ++i) mbar_init(&B->land[i], 1);
-    mbar_init(&B->rope_full, 1);
-    mbar_init(&B->s_full, 1);
-    mbar_init(&B->s_free, 8 * U.tiles);
-    mbar_init(&B->p_full, 8 * U.tiles);
-    mbar_init(&B->o_done, 1);
-    mbar_init(&B->seen_full, 2 * QROWS);
-    mbar_init(&B->drain[0], 1);
-    mbar_init(&B->drain[1], 1);
+  // a lane a barrier (one thread for all of them: about 1 k cycles)
+  constexpr int NBAR = (int)(offsetof(Bars, tmem_slot) / 8);
+  static_assert(NBAR <= 32, "a barrier a lane");
+  if (tid < NBAR) {
+    uint64_t* bar = (uint64_t*)B + tid;
+    const uint32_t count = bar == &B->q_tmem || bar == &B->s_free || bar == &B->p_full ? 8 * U.tiles
+                           : bar >= B->clean && bar < B->clean + SLOTS                  ? U.tiles
+                           : bar == &B->seen_full                                       ? 2 * QROWS
+                                                                                         : 1;
+    mbar_init(bar, count);
+    fence_mbar_init();
+  }
+  if (tid == 32) {
     B->abort = 0;
     B->issued = 0;
     B->z_lo = 0x7fffffff;
-    fence_mbar_init();
     pdl_trigger();
   }
   for (int i = tid; i < tree::MAX_NODES / 32; i += THREADS) seen[i] = 0;
   tc_fence_before();           // (the tensor memory's address)
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  pdl_wait();                  // Q_abs and the nodes' own entries come from the kernels before
-  U.n = tree::block_keys(R, U.b, &U.W, &U.ctx, tid == 0 && U.first && U.qt == 0);
   // whether a row may see anything (padding and masked rows left out), and the
-  // first tile that a row's window reaches
+  // first tile that a row's window reaches; the loads do not wait for one another
   const int q0 = U.tiles == 2 ? U.qt & ~1 : U.qt;
   const int t0 = q0 * QROWS / R.H, t1 = min(R.T - 1, ((q0 + U.tiles) * QROWS - 1) / R.H);
   bool any = false;
   int pmin = 0x7fffffff;
   for (int i = t0 + lane; i <= t1; i += 32) {
     const long m = (long)U.b * R.T + i;
-    if (R.parent[m] < -1 || (R.q_visible && !R.q_visible[m])) continue;
-    any = true;
-    if (U.W > 0) pmin = min(pmin, R.positions[m]);
+    const int parent = R.parent[m], pos = R.positions[m];
+    const bool in = parent >= -1 && (R.q_visible ? R.q_visible[m] != 0 : true);
+    any |= in;
+    if (in) pmin = min(pmin, pos);
   }
+  U.n = tree::block_keys(R, U.b, &U.W, &U.ctx, tid == 0 && U.first && U.qt == 0);
   any = __any_sync(0xffffffffu, any);
   pmin = __reduce_min_sync(0xffffffffu, pmin);
   U.j_lo = U.W > 0 ? max(0, min(pmin - U.W + 1, U.ctx)) / KT * KT : 0;
@@ -489,6 +491,9 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
   U.row0 = ((long)U.b * R.T) * R.H + (long)U.qt * QROWS;
   if (warp == W_ROPE && lane == 0) { prefetch_tmap(&P.tmK); prefetch_tmap(&P.tmC); prefetch_tmap(&P.tmQ); }
   if (warp == W_S) tmem_alloc(&B->tmem_slot, TMEM_COLS);
+  pdl_wait();                  // Q_abs and the nodes' own entries come from the kernels before
+  uint32_t q[32];
+  if (softmax_warp(warp)) load_q(P, U, q);
   set_up(P, B, smem, U);
   const uint32_t tmem = B->tmem_slot;
   const int seg = P.seg_rows, nseg = KT / seg;
@@ -638,15 +643,15 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
       mbar_wait(&B->drain[1], 0, R.status);
     }
   } else {
-    softmax_role(P, B, smem, tmem, U);
+    softmax_role(P, B, smem, tmem, U, q);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (P.cluster_parts > 1) cluster_sync_all();            // every part has staged its rows
   tc_fence_after();
-  if (warp == W_S) tmem_dealloc(tmem, TMEM_COLS);
   join_and_store(P, smem, U);
+  if (warp == W_S) tmem_dealloc(tmem, TMEM_COLS);
   if (P.cluster_parts > 1) cluster_sync_all();            // nobody leaves while its rows may be read
 }
 
@@ -668,6 +673,9 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
   U.row0 = ((long)U.b * R.T) * R.H + (long)U.qt * QROWS;
   if (warp == W_ROPE && lane == 0) { prefetch_tmap(&P.tmK); prefetch_tmap(&P.tmQ); }
   if (warp == W_S) tmem_alloc_pair(&B->tmem_slot, TMEM_COLS);
+  pdl_wait();                  // Q_abs and the nodes' own entries come from the kernels before
+  uint32_t q[32];
+  if (softmax_warp(warp)) load_q(P, U, q);
   set_up(P, B, smem, U);
   const uint32_t tmem = B->tmem_slot, both = 3u << U.lead;
   // segments: rows of a page, at most this CTA's 64 keys of a tile
@@ -697,13 +705,21 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
       for (int i = i0; i < i0 + 2; ++i) mbar_wait(&B->k_full[i], (t - 1) & 1, R.status);
   } else if (warp == W_RING + 2) {
     // ---- values: chunk 2 i + p of this half for both pairs ----
-    bool ok = U.nt > 0 && wait_bar(B, &B->seen_full, 0, R.status);
-    const int z_lo = ok ? B->z_lo : 0;
+    bool ok = true;
+    int z_lo = -1;                                        // known from seen_full on
     uint32_t nd = 0;                                      // tiles cleared so far
+    auto know_seen = [&]() {
+      if (z_lo < 0 && (ok = ok && wait_bar(B, &B->seen_full, 0, R.status))) z_lo = B->z_lo;
+    };
     for (int t = 0; t < U.nt && ok; ++t) {
       const int j0 = tile_key(U, t);
       const int y = lane < nvseg ? cache_row(R, U, j0 + lane * seg, true) : 0;
-      const bool dirty = dirty_tile(U, z_lo, t);
+      bool dirty = j0 + KT > U.ctx;                       // whatever is seen: loaded at once
+      if (!dirty) {
+        know_seen();
+        if (!ok) break;
+        dirty = dirty_tile(U, z_lo, t);
+      }
       if (!(ok = wait_bar(B, &B->o_done, (t & 1) ^ 1, R.status))) break;
       for (int i = 0; i < PV; ++i) {
         uint8_t* slot = smem + OFF_PV + i * PSLOT_BYTES;
@@ -718,7 +734,8 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
           tma_load_3d_pair(slot + lane * seg * 128, &P.tmK, bar, (4 * U.half + 2 * i + p) * 64, y, 0);
         __syncwarp();
         if (dirty) {
-          if (!(ok = wait_bar(B, &B->land[i], nd & 1, R.status))) break;
+          know_seen();
+          if (!(ok = ok && wait_bar(B, &B->land[i], nd & 1, R.status))) break;
           clear_unseen(U, smem, slot, 1, j0, z_lo);
           if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&B->clean[i]), U.lead));
         }
@@ -822,16 +839,16 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
       mbar_wait(&B->drain[1], 0, R.status);
     }
   } else {
-    softmax_role(P, B, smem, tmem, U);
+    softmax_role(P, B, smem, tmem, U, q);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();          // the pair's MMAs are done, every part has staged its rows
+  if (P.cluster_parts > 1) cluster_sync_all();            // every part has staged its rows
+  join_and_store(P, smem, U);
+  cluster_sync_all();          // nobody leaves while its rows, or its half of an MMA, may be read
   tc_fence_after();
   if (warp == W_S) tmem_dealloc_pair(tmem, TMEM_COLS);
-  join_and_store(P, smem, U);
-  if (P.cluster_parts > 1) cluster_sync_all();            // nobody leaves while its rows may be read
 }
 
 // A row and quarter of its dims: sum_s w_s o_s / sum_s w_s with w_s = 2^(lse_s -
