@@ -166,20 +166,34 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
           if (col_id < rows) l = P.lse[row0 + col_id];
           lse2[col_id] = l * kLog2e;
         }
-        // the warp's 32 keys as this lane's four columns see them
+        // the warp's 32 keys as this lane's four columns see them; where nodes'
+        // keys are among them, a lane walks from one node for all its rows
         uint32_t word[4];
         bool all = true;
+        const bool own = R.parent && jw + 32 > it.ctx && jw < it.n0;
+        const int node0 = (qt * NMAX + half * 128) / R.H;
+        const bool shared = own && (qt * NMAX + half * 128 + 127) / R.H - node0 < 32;
+        uint32_t walked = 0;
+        bool sound = true;
+        if (shared && node0 + lane < R.T) walked = tree::walk_bits(R, it.b, node0 + lane, it.W, it.ctx, jw, &sound);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int c = half * 128 + 32 * q + lane;
-          word[q] = 0;
-          if (c < rows) {
-            const int node = (qt * NMAX + c) / R.H;
+          const int c = half * 128 + 32 * q + lane, node = (qt * NMAX + c) / R.H;
+          bool ok = c < rows && jw < it.n0;
+          if (ok) {
             const long m = (long)it.b * R.T + node;
-            bool ok = (R.q_visible ? R.q_visible[m] != 0 : true) && P.lse[row0 + c] != -INFINITY;
-            if (ok && R.parent)
-              ok = tree::in_tree(R, R.parent + (long)it.b * R.T, node, jw == 0);
-            word[q] = (uint32_t)tree::key_bits(R, it.b, node, ok, it.n0, it.W, it.ctx, jw);
+            // (rows outside the tree have lse = -inf)
+            ok = (R.q_visible ? R.q_visible[m] != 0 : true) && P.lse[row0 + c] != -INFINITY;
+          }
+          word[q] = ok ? (uint32_t)tree::context_bits(R, it.b, node, it.n0, it.W, it.ctx, jw) : 0u;
+          if (shared) {
+            const uint32_t w1 = __shfl_sync(0xffffffffu, walked, node - node0);
+            const bool s1 = __shfl_sync(0xffffffffu, (int)sound, node - node0) != 0;
+            word[q] = ok && s1 ? word[q] | w1 : 0u;
+          } else if (own && ok) {
+            bool s1;
+            const uint32_t w1 = tree::walk_bits(R, it.b, node, it.W, it.ctx, jw, &s1);
+            word[q] = s1 ? word[q] | w1 : 0u;
           }
           all = all && (word[q] == 0xffffffffu || c >= cols);
         }

@@ -60,37 +60,63 @@ __device__ __forceinline__ bool in_tree(const Rule& a, const int32_t* parent, in
   }
 }
 
-// Bits of the nodes k0 .. k0 + 63 (k0 >= 0) that node i sees (i in the tree).
+// Bits of the nodes k0 .. k0 + 63 (k0 >= 0) that node i sees (i in the tree;
+// the walk ends at a parent that is no earlier node, too).
 __device__ __forceinline__ unsigned long long path_bits(const int32_t* parent, const int32_t* pos,
                                                         int W, int i, int k0) {
   unsigned long long m = 0;
   const int pi = pos[i];
-  for (int k = i; k >= k0; k = parent[k]) {
+  for (int k = i; k >= k0;) {
     const bool near = W == 0 || pi - pos[k] < W;
     if (near && k < k0 + 64) m |= 1ull << (k - k0);
+    const int p = parent[k];
+    if (p >= k) break;
+    k = p;
   }
   return m;
 }
 
-// Bits of keys j0 .. j0 + 63 that query i of block b sees.  n, W and ctx are
-// block_keys()'s; `ok`: the row sees anything at all (visible, in the tree).
+// Bits of the context's keys (the whole block's without parents) among j0 .. j0 +
+// 63 that query i of block b sees.  n, W and ctx are block_keys()'s.
+__device__ __forceinline__ unsigned long long context_bits(const Rule& a, long b, int i, int n, int W,
+                                                           int ctx, int j0) {
+  const int lo = W > 0 ? max(0, min(n, a.positions[b * a.T + i] - W + 1) - j0) : 0, hi = min(ctx - j0, 64);
+  if (hi <= lo) return 0ull;
+  return (hi >= 64 ? ~0ull : (1ull << hi) - 1ull) & (~0ull << lo);
+}
+
+// Bits of keys j0 .. j0 + 63 that query i of block b sees; `ok`: the row sees
+// anything at all (visible, in the tree).
 __device__ __forceinline__ unsigned long long key_bits(const Rule& a, long b, int i, bool ok, int n,
                                                        int W, int ctx, int j0) {
   if (!ok || j0 >= n) return 0ull;
-  const int32_t* pos = a.positions + b * a.T;
-  // [lo, hi): what the window and the context (or the whole block) leave
-  const int lo = W > 0 ? max(0, min(n, pos[i] - W + 1) - j0) : 0, hi = min(ctx - j0, 64);
-  unsigned long long m = 0;
-  if (hi > lo) {
-    m = hi >= 64 ? ~0ull : (1ull << hi) - 1ull;
-    m &= ~0ull << lo;
-  }
+  unsigned long long m = context_bits(a, b, i, n, W, ctx, j0);
   if (a.parent && j0 + 64 > ctx) {
     const int k0 = j0 - ctx;                          // node of bit 0 (negative: still context)
-    const unsigned long long t = path_bits(a.parent + b * a.T, pos, W, i, max(k0, 0));
+    const unsigned long long t = path_bits(a.parent + b * a.T, a.positions + b * a.T, W, i, max(k0, 0));
     m |= k0 >= 0 ? t : t << (-k0);
   }
   return m;
+}
+
+// in_tree() and the nodes' part of key_bits() for the 32 keys from j0 on in one
+// walk: *sound tells whether node i is in the tree.
+__device__ __forceinline__ uint32_t walk_bits(const Rule& a, long b, int i, int W, int ctx, int j0,
+                                              bool* sound) {
+  const int32_t *parent = a.parent + b * a.T, *pos = a.positions + b * a.T;
+  const int k0 = j0 - ctx, pi = W > 0 ? pos[i] : 0;
+  uint32_t m = 0;
+  while (true) {
+    const uint32_t rel = (uint32_t)(i - k0);
+    if (rel < 32u && (W == 0 || pi - pos[i] < W)) m |= 1u << rel;
+    const int p = parent[i];
+    if (p < 0 || p >= i) {
+      if (p >= i) set_status(a.status, MLA_DEV_BAD_TREE);
+      *sound = p == -1;
+      return p == -1 ? m : 0u;
+    }
+    i = p;
+  }
 }
 
 }  // namespace tree

@@ -242,7 +242,8 @@ key_weights_kernel(const tree::Rule a, const float* __restrict__ q_abs, const fl
     const int i = live ? (r0 + r) / a.H : 0;
     const float l = live ? lse[row0 + r0 + r] : -INFINITY;
     bool ok = live && l != -INFINITY && (a.q_visible ? a.q_visible[(long)b * a.T + i] != 0 : true);
-    if (ok && a.parent) ok = tree::in_tree(a, a.parent + (long)b * a.T, i, c0 == 0);
+    // rows outside the tree have lse = -inf; only tiles with nodes' keys walk
+    if (ok && a.parent && j0 + KT > ctx) ok = tree::in_tree(a, a.parent + (long)b * a.T, i, c0 == 0);
     const unsigned vis = (unsigned)tree::key_bits(a, b, i, ok, n0, W, ctx, j0);
     __syncthreads();
     const float2 d = dot2(Q + r * pitch, Es + c0 * pitch, Es + (c0 + 16) * pitch, units);

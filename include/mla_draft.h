@@ -425,8 +425,8 @@ mla_status_t mla_tree_attention(mla_handle_t *h, const void *q_abs, const int32_
 
 /* The whole layer over trees: mla_draft_forward with the tree's visibility in
  * its attention (same arguments, results and errors; block_slot_mapping
- * writes the nodes' own entries first, padding nodes take a free slot of
- * their own). */
+ * writes the nodes' own entries first; padding nodes take a free slot of
+ * their own and a position inside the table). */
 size_t mla_forward_tree_workspace_bytes(const mla_handle_t *h, const mla_attn_desc_t *desc);
 mla_status_t mla_draft_forward_tree(mla_handle_t *h, const void *hidden,
                                     const int32_t *positions,
@@ -441,8 +441,8 @@ mla_status_t mla_draft_forward_tree(mla_handle_t *h, const void *hidden,
  * over the rows m = (query, head) of block b that see key j, for j < kv_len[b]
  * (other elements are left as they are).  parent: the tree's (NULL: the rule
  * of mla_attn_desc_t).  lse: device fp32 [nb*T, H], mla_tree_attention's or
- * mla_latent_attention's for the same rows; a row with lse = -inf adds
- * nothing.  prior, weights_out: device fp32 [num_blocks, ldw], the same
+ * mla_latent_attention's for the same rows; a row with lse = -inf (so those
+ * that see no key, nodes outside the tree among them) adds nothing.  prior, weights_out: device fp32 [num_blocks, ldw], the same
  * pointer or disjoint; prior may be NULL (nothing before).  ldw < kv_len is
  * reported as MLA_DEV_BAD_LENGTH and the keys behind it are left out.  Each
  * key's sum is taken in one fixed order: equal calls give equal bits.
