@@ -175,7 +175,7 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
         const bool shared = own && (qt * NMAX + half * 128 + 127) / R.H - node0 < 32;
         uint32_t walked = 0;
         bool sound = true;
-        if (shared && node0 + lane < R.T) walked = tree::walk_bits(R, it.b, node0 + lane, it.W, it.ctx, jw, &sound);
+        if (shared && node0 + lane < R.T) walked = (uint32_t)tree::walk_bits(R, it.b, node0 + lane, it.W, jw - it.ctx, &sound, true);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int c = half * 128 + 32 * q + lane, node = (qt * NMAX + c) / R.H;
@@ -192,7 +192,7 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
             word[q] = ok && s1 ? word[q] | w1 : 0u;
           } else if (own && ok) {
             bool s1;
-            const uint32_t w1 = tree::walk_bits(R, it.b, node, it.W, it.ctx, jw, &s1);
+            const uint32_t w1 = (uint32_t)tree::walk_bits(R, it.b, node, it.W, jw - it.ctx, &s1, true);
             word[q] = s1 ? word[q] | w1 : 0u;
           }
           all = all && (word[q] == 0xffffffffu || c >= cols);

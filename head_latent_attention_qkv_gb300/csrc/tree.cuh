@@ -99,24 +99,29 @@ __device__ __forceinline__ unsigned long long key_bits(const Rule& a, long b, in
   return m;
 }
 
-// in_tree() and the nodes' part of key_bits() for the 32 keys from j0 on in one
-// walk: *sound tells whether node i is in the tree.
-__device__ __forceinline__ uint32_t walk_bits(const Rule& a, long b, int i, int W, int ctx, int j0,
-                                              bool* sound) {
+// in_tree() and the bits of nodes k0 .. k0 + 63 that node i sees in one walk: 0 when
+// it is not in the tree.  Its own bit is set otherwise (if it is among them).
+__device__ __forceinline__ unsigned long long walk_bits(const Rule& a, long b, int i, int W, int k0,
+                                                        bool* sound, bool report) {
   const int32_t *parent = a.parent + b * a.T, *pos = a.positions + b * a.T;
-  const int k0 = j0 - ctx, pi = W > 0 ? pos[i] : 0;
-  uint32_t m = 0;
+  const int pi = W > 0 ? pos[i] : 0;
+  unsigned long long m = 0;
   while (true) {
     const uint32_t rel = (uint32_t)(i - k0);
-    if (rel < 32u && (W == 0 || pi - pos[i] < W)) m |= 1u << rel;
+    if (rel < 64u && (W == 0 || pi - pos[i] < W)) m |= 1ull << rel;
     const int p = parent[i];
     if (p < 0 || p >= i) {
-      if (p >= i) set_status(a.status, MLA_DEV_BAD_TREE);
+      if (p >= i && report) set_status(a.status, MLA_DEV_BAD_TREE);
       *sound = p == -1;
-      return p == -1 ? m : 0u;
+      return p == -1 ? m : 0ull;
     }
     i = p;
   }
+}
+// Bits of nodes 0 .. 63 moved to keys j0 .. j0 + 63.
+__device__ __forceinline__ unsigned long long place_bits(unsigned long long nodes, int ctx, int j0) {
+  const int sh = ctx - j0;
+  return sh >= 64 || sh <= -64 ? 0ull : sh >= 0 ? nodes << sh : nodes >> (-sh);
 }
 
 }  // namespace tree

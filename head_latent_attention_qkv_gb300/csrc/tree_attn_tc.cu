@@ -102,7 +102,7 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The 64 threads of a row group (warps w and w + 8).
+// The 64 threads of a row group (warps w and w + 8), each warp converged.
 __device__ __forceinline__ void pair_sync(int w) { asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory"); }
 
 // What use u of the ring holds: keys (pair 0..3) or values (pair 0..1) of a
@@ -173,10 +173,6 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   const int node = live ? row_in_block / R.H : 0;
   const long m = (long)U.b * R.T + node;
   const int32_t* parent = R.parent + (long)U.b * R.T;
-  auto row_ok = [&](int nd, bool report) {
-    return U.n > 0 && (R.q_visible ? R.q_visible[(long)U.b * R.T + nd] != 0 : true) &&
-           tree::in_tree(R, parent, nd, report);
-  };
   const uint32_t s_free = mapa(smem_u32(&B->s_free), U.lead), p_full = mapa(smem_u32(&B->p_full), U.lead);
   if (U.nt > 0) {
     // Q dims 0..127 of this row -> tensor memory (bf16 pairs), 64 dims a thread
@@ -185,23 +181,55 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
     __syncwarp();
     if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&B->q_tmem), U.lead));
   }
-  // the walks over the tree run while the first scores are on their way
-  const bool ok = live && row_ok(node, U.first && kh == 0);
-  // rows that see nothing are computed like their neighbours and written as
-  // zeros, so that they do not take a warp off the unmasked path
+  // The walks over the tree run while the first scores are on their way.  Up to
+  // 64 nodes fit one word, found in one walk: a row's first thread takes its
+  // own node and its second the peer's (both CTAs of a pair need to know what
+  // either's rows see); deeper trees walk again for every tile of nodes' keys.
+  // Rows that see nothing are computed like their neighbours and written as
+  // zeros, so that they do not take a warp off the unmasked path.
   const int lo = U.W > 0 ? max(0, R.positions[m] - U.W + 1) : 0;
   float mrun = -INFINITY, lsum = 0.f;
-  // what the cluster's rows see: the first context key and the nodes on their
-  // paths (one row of a node stands for all; the second threads take the peer's)
-  if (kh < U.tiles) {
+  const bool small = R.T <= 64;
+  unsigned long long mine = 0;                            // (small) the nodes that this row sees
+  bool ok;
+  {
+    uint32_t* seen = (uint32_t*)(smem + OFF_SEEN);
+    const int32_t* pos = R.positions + (long)U.b * R.T;
     const int other = (kh ? U.qt ^ 1 : U.qt) * QROWS + r, nd = other / R.H;
-    if (other < R.T * R.H && (other % R.H == 0 || r == 0) && row_ok(nd, false)) {
-      uint32_t* seen = (uint32_t*)(smem + OFF_SEEN);
-      const int32_t* pos = R.positions + (long)U.b * R.T;
-      atomicMin(&B->z_lo, U.W > 0 ? max(0, min(pos[nd] - U.W + 1, U.ctx)) : 0);
-      for (int k = nd; k >= 0; k = parent[k])
-        if (U.W == 0 || pos[nd] - pos[k] < U.W) atomicOr(&seen[k >> 5], 1u << (k & 31));
+    const bool walks = kh < U.tiles && other < R.T * R.H && U.n > 0 &&
+                       (R.q_visible ? R.q_visible[(long)U.b * R.T + nd] != 0 : true);
+    const bool first_row = other % R.H == 0 || r == 0;     // one row of a node speaks for all
+    bool sound = false;
+    if (small) {
+      if (walks) mine = tree::walk_bits(R, U.b, nd, U.W, 0, &sound, U.first && kh == 0);
+      if (sound && first_row) {
+        atomicOr(&seen[0], (uint32_t)mine);
+        atomicOr(&seen[1], (uint32_t)(mine >> 32));
+      }
+      // through the row's own two places of xm: other rows' belong to other warps,
+      // which may be in the loop already
+      uint32_t* word = (uint32_t*)xm;
+      if (!kh) {
+        word[r] = (uint32_t)mine;
+        word[QROWS + r] = (uint32_t)(mine >> 32);
+      }
+      __syncwarp();                                        // the walks may have parted the warp
+      pair_sync(w);
+      mine = word[r] | (unsigned long long)word[QROWS + r] << 32;
+      pair_sync(w);
+      ok = live && mine != 0;
+    } else {
+      sound = walks && tree::in_tree(R, parent, nd, U.first && kh == 0);
+      if (sound && first_row)
+        for (int k = nd; k >= 0; k = parent[k])
+          if (U.W == 0 || pos[nd] - pos[k] < U.W) atomicOr(&seen[k >> 5], 1u << (k & 31));
+      if (!kh) xm[r] = sound ? 1.f : 0.f;
+      __syncwarp();
+      pair_sync(w);
+      ok = live && xm[r] != 0.f;
+      pair_sync(w);
     }
+    if (sound && first_row) atomicMin(&B->z_lo, U.W > 0 ? max(0, min(pos[nd] - U.W + 1, U.ctx)) : 0);
   }
   mbar_arrive(&B->seen_full);
   for (int t = 0; t < U.nt; ++t) {
@@ -222,7 +250,10 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
 #pragma unroll
       for (int i = 0; i < KH; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], s[i]);
     } else {
-      const unsigned long long vis = tree::key_bits(R, U.b, node, ok, U.n, U.W, U.ctx, jh);
+      const unsigned long long vis =
+          !small ? tree::key_bits(R, U.b, node, ok, U.n, U.W, U.ctx, jh)
+          : ok   ? tree::context_bits(R, U.b, node, U.n, U.W, U.ctx, jh) | tree::place_bits(mine, U.ctx, jh)
+                 : 0ull;
       const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
 #pragma unroll
       for (int i = 0; i < KH; ++i) {
@@ -301,12 +332,18 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
       if (lo < U.ctx) { cnt = U.ctx - lo; first = lo; last = U.ctx - 1; }
       const int32_t* pos = R.positions + (long)U.b * R.T;
       int low = -1, high = -1;
-      for (int k = node; k >= 0; k = parent[k])
-        if (U.W == 0 || pos[node] - pos[k] < U.W) {
-          ++cnt;
-          low = k;
-          high = max(high, k);
-        }
+      if (small) {
+        cnt += __popcll(mine);
+        low = __ffsll(mine) - 1;
+        high = 63 - __clzll(mine);
+      } else {
+        for (int k = node; k >= 0; k = parent[k])
+          if (U.W == 0 || pos[node] - pos[k] < U.W) {
+            ++cnt;
+            low = k;
+            high = max(high, k);
+          }
+      }
       if (high >= 0) {
         if (first < 0) first = U.ctx + low;
         last = U.ctx + high;
