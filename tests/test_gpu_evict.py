@@ -179,6 +179,22 @@ def test_compact_reports_lists_that_do_not_fit():
             assert torch.equal(flat[s], old[s])                 # the sequence is left alone
 
 
+def test_compact_behind_four_gigabytes():
+    from head_latent_attention_qkv_gb300 import api
+    from tests.tree_cases import Paged, i32
+    h = handle("bf16", 64)
+    rng, far = np.random.default_rng(4), 61000
+    p = Paged(rng, h.dims, 64, [500, 200])
+    cache = torch.empty(far + p.num_pages, 64, 576, dtype=torch.bfloat16, device="cuda")
+    cache[far:] = p.cache
+    keep = [pick(rng, 500, 100), list(range(100, 200))]
+    args = (i32([500, 200]), i32(keep), i32([100, 100]))
+    api.mla_cache_compact(h, p.cache, i32(p.table), *args)
+    api.mla_cache_compact(h, cache, i32(np.where(p.table >= 0, p.table + far, -1)), *args)
+    assert api.mla_get_device_status(h) == 0
+    assert torch.equal(cache[far:].view(torch.int16), p.cache.view(torch.int16))
+
+
 def test_compact_captured_and_replayed():
     from head_latent_attention_qkv_gb300 import api
     from tests.tree_cases import Paged, i32

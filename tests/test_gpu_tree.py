@@ -27,24 +27,25 @@ def _cuda():
 HANDLES = {}
 
 
-def handle(dtype, heads, page):
+def handle(dtype, heads, page, **dims):
     from tests.tree_cases import make_handle
-    key = (dtype, heads, page)
+    key = (dtype, heads, page, tuple(sorted(dims.items())))
     if key not in HANDLES:
-        HANDLES[key] = make_handle(dtype, heads, page)
+        HANDLES[key] = make_handle(dtype, heads, page, **dims)
     return HANDLES[key][0]
 
 
 class Case:
-    """Queries, cache and descriptor of one batch; entries that nobody sees are NaN."""
+    """Queries, cache and descriptor of one batch; entries that nobody sees and
+    queries of rows that see nothing are NaN."""
 
     def __init__(self, dtype, heads, page, ctx, T, seed=0, window=0, padded=False, masked=False,
-                 tree=True, parents=None, q_scale=1.0):
+                 tree=True, parents=None, q_scale=1.0, dims=None, far=0):
         from head_latent_attention_qkv_gb300 import api
         from oracle import tree as O
         from tests.tree_cases import Paged, bushy, depths, i32
         rng = np.random.default_rng(seed)
-        self.h = handle(dtype, heads, page)
+        self.h = handle(dtype, heads, page, **(dims or {}))
         self.T, self.H, self.d, self.n = T, heads, self.h.dims, len(ctx)
         self.kv = [c + T for c in ctx]
         self.parents = None
@@ -58,9 +59,7 @@ class Case:
         if masked:
             self.qv[:, : max(1, T // 3)] = 0
         self.paged = Paged(rng, self.d, page, self.kv)
-        q = rng.normal(size=(self.n * T * heads, self.d.cache_dim)) * q_scale
-        self.q = torch.from_numpy(q.astype(np.float32)).to(api.torch_dtype(self.d)).cuda()
-        self.q64 = self.q.double().cpu().numpy().reshape(self.n, T, heads, -1)
+        q = rng.normal(size=(self.n, T, heads, self.d.cache_dim)) * q_scale
         self.vis = [O.visible(self.kv[b], self.pos[b], self.windows[b], self.qv[b],
                               None if self.parents is None else self.parents[b]) for b in range(self.n)]
         for b in range(self.n):
@@ -68,6 +67,16 @@ class Case:
             if len(unseen):
                 self.paged.set_nan(b, torch.from_numpy(unseen))
                 self.paged.entries[b][unseen] = np.nan
+            q[b][~self.vis[b].any(axis=1)] = np.nan
+        q = q.reshape(self.n * T * heads, -1)
+        self.q = torch.from_numpy(q.astype(np.float32)).to(api.torch_dtype(self.d)).cuda()
+        self.q64 = self.q.double().cpu().numpy().reshape(self.n, T, heads, -1)
+        if far:                                       # the same pages behind `far` others
+            cache = torch.empty(far + self.paged.num_pages, page, self.d.cache_dim,
+                                dtype=self.paged.cache.dtype, device="cuda")
+            cache[far:] = self.paged.cache
+            self.paged.cache, self.paged.num_pages = cache, cache.shape[0]
+            self.paged.table = np.where(self.paged.table >= 0, self.paged.table + far, -1).astype(np.int32)
         self.positions = i32(np.concatenate([np.asarray(p).reshape(-1) for p in self.pos]))
         self.parent = None if self.parents is None else i32(np.concatenate(self.parents))
         self.stats = torch.full((self.n * T, 3), -7, dtype=torch.int32, device="cuda")
@@ -184,6 +193,58 @@ def test_key_weights_of_trees(dtype, heads, page, ctx, T, opt):
 def test_key_weights_of_blocks(dtype, heads, page, ctx, T, opt):
     Case(dtype, heads, page, ctx, T, **{**opt, "tree": False, "padded": False}).weights(
         decay=0.0, with_prior=False)
+
+
+@pytest.mark.parametrize("rank,rope", [(48, 6), (16, 2), (64, 18), (512, 512), (208, 40)])
+def test_fp32_layers_of_other_widths(rank, rope):
+    # entries of 54, 18 and 82 floats (no multiple of 16 bytes), and the widest
+    c = Case("fp32", 3, 16, [70, 0, 33], 7, padded=True, window=25,
+             dims=dict(kv_lora_rank=rank, qk_rope_head_dim=rope))
+    c.check_attention(*c.attention())
+    c.weights()
+
+
+@pytest.mark.parametrize("dtype,heads,T,window", [("bf16", 2, 130, 0), ("bf16", 2, 90, 17), ("bf16", 5, 65, 0),
+                                                  ("bf16", 1, 1024, 0), ("fp32", 1, 1024, 100), ("fp32", 2, 90, 17)])
+def test_deep_trees(dtype, heads, T, window):
+    # more than 64 nodes; chains as deep as the tree in one block, bushy in the other
+    from tests.tree_cases import bushy
+    rng = np.random.default_rng(T)
+    c = Case(dtype, heads, 16, [40, 3], T, parents=[list(range(-1, T - 1)), bushy(rng, T, T - 5)], window=window)
+    c.check_attention(*c.attention())
+    c.weights()
+
+
+def test_many_blocks():
+    ctx = [(37 * b) % 300 for b in range(75)]
+    c = Case("bf16", 4, 16, ctx, 3, padded=True)
+    c.check_attention(*c.attention())
+    c.weights()
+
+
+def test_pages_behind_four_gigabytes():
+    c = Case("bf16", 16, 64, [300, 77], 6, far=61000)           # 4.5 GB of pages before them
+    c.check_attention(*c.attention())
+    c.weights()
+    c = Case("fp32", 4, 64, [100, 30], 5, far=220000)
+    c.check_attention(*c.attention())
+    c.weights()
+
+
+def test_weights_rows_shorter_than_the_sequence_are_reported():
+    from head_latent_attention_qkv_gb300 import _lib, api
+    for dtype, heads in (("fp32", 4), ("bf16", 16)):
+        c = Case(dtype, heads, 16, [50, 20], 7)
+        full = c.weights(with_prior=False)
+        _, lse = c.attention()
+        w = torch.full((2, 40), -3.0, device="cuda")
+        ref = torch.zeros(2, 64, device="cuda")
+        api.mla_key_weights(c.h, c.q, c.positions, c.paged.cache, c.desc, lse, ref, parent=c.parent)
+        assert api.mla_get_device_status(c.h) == 0
+        api.mla_key_weights(c.h, c.q, c.positions, c.paged.cache, c.desc, lse, w, parent=c.parent)
+        assert api.mla_get_device_status(c.h) == _lib.MLA_DEV_BAD_LENGTH
+        assert torch.equal(w[0], ref[0, :40]) and torch.equal(w[1, :27], ref[1, :27]) and (w[1, 27:] == -3).all()
+        assert full.shape[1] == 60
 
 
 @pytest.mark.parametrize("dtype,heads", [("fp32", 4), ("bf16", 16)])

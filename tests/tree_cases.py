@@ -7,13 +7,13 @@ from head_latent_attention_qkv_gb300 import api, workloads as W
 DEV = "cuda"
 
 
-def dims_for(dtype, heads):
+def dims_for(dtype, heads, **kw):
     base = W.TINY_FP32_MLA if dtype == "fp32" else W.QWEN3_4B_MLA
-    return base.replace(num_heads=heads, hidden_size=256, q_lora_rank=0, max_position=8192)
+    return base.replace(num_heads=heads, hidden_size=256, q_lora_rank=0, max_position=8192, **kw)
 
 
-def make_handle(dtype, heads, page):
-    d = dims_for(dtype, heads)
+def make_handle(dtype, heads, page, **kw):
+    d = dims_for(dtype, heads, **kw)
     rng = np.random.default_rng(7)
     w = W.make_weights(d, rng)
     dt = api.torch_dtype(d)
