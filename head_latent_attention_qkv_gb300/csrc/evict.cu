@@ -48,7 +48,6 @@ struct SelectArgs {
   int32_t* keep_len;
   long ldw;
   int budget, sink, recent;
-  int smem_keys;            // capacity of the shared key array
   uint32_t* status;
 };
 
@@ -60,6 +59,11 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ int ld_cluster_int(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ int2 ld_cluster_int2(uint32_t addr) {
   int2 v;
   asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
@@ -89,10 +93,14 @@ __device__ __forceinline__ int warp_prefix(int v, int* buf, int* total) {
   return before;
 }
 
-template <int CL>
+// HELD: a CTA's keys stay in shared memory (at most SEL_SMEM_KEYS), so that two
+// counts fit a word: the peers' counts are most of what crosses the cluster (8
+// CTAs: 4.2 k cycles a pass with a word a count).
+template <int CL, bool HELD>
 __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a) {
-  extern __shared__ uint32_t keys[];                     // this CTA's keys (when they fit)
-  __shared__ __align__(8) int hist[2][BINS];
+  extern __shared__ uint32_t keys[];                     // this CTA's keys (HELD)
+  constexpr int WORDS = HELD ? BINS / 2 : BINS;
+  __shared__ __align__(8) uint32_t hist[2][WORDS];
   __shared__ int buf[32], buf2[32], found[2];
   __shared__ __align__(8) int cta_counts[2];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -118,44 +126,50 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
   const int nw = CL * SEL_WARPS;
   const int wlen = ((n + nw - 1) / nw + 31) & ~31;
   const int i0 = (int)min((long)(rank * SEL_WARPS + warp) * wlen, (long)n);   // (n < 2^30)
-  const bool cached = SEL_WARPS * wlen <= a.smem_keys;
   uint32_t* mine = keys + warp * wlen;
-  if (cached)
+  if (HELD)
 #pragma unroll 8
     for (int o = lane; o < wlen; o += 32) {
       const int i = i0 + o;
       mine[o] = i < n ? order_key(w[i]) : 0u;
     }
   auto key_at = [&](int o) -> uint32_t {
-    return cached ? mine[o] : (i0 + o < n ? order_key(w[i0 + o]) : 0u);
+    return HELD ? mine[o] : (i0 + o < n ? order_key(w[i0 + o]) : 0u);
   };
   uint32_t prefix = 0, mask = 0;
-  for (int i = tid; i < BINS; i += SEL_THREADS) hist[0][i] = 0;
+  for (int i = tid; i < WORDS; i += SEL_THREADS) hist[0][i] = 0;
   __syncthreads();
   // k == 0: only the protected keys stay
   if (k > 0) {
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       const uint32_t dmask = (1u << bits) - 1u;
-      int* hp = hist[pass & 1];
+      uint32_t* hp = hist[pass & 1];
 #pragma unroll 8
       for (int o = lane; o < wlen; o += 32) {
         const int i = i0 + o;
         const uint32_t u = key_at(o);
         const bool in = i >= mid_lo && i < mid_hi && (u & mask) == prefix;
-        if (in) atomicAdd(&hp[(u >> shift) & dmask], 1);
+        const uint32_t digit = (u >> shift) & dmask;
+        if (in) atomicAdd(&hp[HELD ? digit >> 1 : digit], HELD && (digit & 1) ? 0x10000u : 1u);
       }
       if (CL > 1) tc::cluster_sync_all(); else __syncthreads();
       // every CTA is done with the other array (pass - 1): clear it for pass + 1
-      for (int i = tid; i < BINS; i += SEL_THREADS) hist[(pass + 1) & 1][i] = 0;
+      for (int i = tid; i < WORDS; i += SEL_THREADS) hist[(pass + 1) & 1][i] = 0;
       // counts of this thread's two bins, from the top: bins B - 1 - 2 tid, B - 2 - 2 tid
       const int bin = BINS - 1 - 2 * tid;
       int c0 = 0, c1 = 0;
       int2 from[CL];                                     // every CTA's counts, all loads in flight
 #pragma unroll
-      for (int r = 0; r < CL; ++r)
-        from[r] = CL == 1 ? *reinterpret_cast<const int2*>(&hp[bin - 1])
-                          : ld_cluster_int2(tc::mapa(tc::smem_u32(&hp[bin - 1]), (uint32_t)r));
+      for (int r = 0; r < CL; ++r) {
+        if (HELD) {
+          const uint32_t v = CL == 1 ? hp[bin >> 1] : (uint32_t)ld_cluster_int(tc::mapa(tc::smem_u32(&hp[bin >> 1]), (uint32_t)r));
+          from[r] = make_int2((int)(v & 0xffffu), (int)(v >> 16));
+        } else {
+          from[r] = CL == 1 ? *reinterpret_cast<const int2*>(&hp[bin - 1])
+                            : ld_cluster_int2(tc::mapa(tc::smem_u32(&hp[bin - 1]), (uint32_t)r));
+        }
+      }
 #pragma unroll
       for (int r = 0; r < CL; ++r) { c0 += from[r].y; c1 += from[r].x; }
       const int x = lane_prefix(c0 + c1);
@@ -188,11 +202,14 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
     return u > thr ? 2 : u == thr ? 1 : 0;
   };
   int cnt2 = 0, cnt1 = 0;
+  uint32_t held2 = 0, held1 = 0;                         // (HELD) lane i: the votes of step i
 #pragma unroll 4
   for (int o = lane; o < wlen; o += 32) {
     const int c = klass(o);
-    cnt2 += __popc(__ballot_sync(0xffffffffu, c == 2));
-    cnt1 += __popc(__ballot_sync(0xffffffffu, c == 1));
+    const uint32_t b2 = __ballot_sync(0xffffffffu, c == 2), b1 = __ballot_sync(0xffffffffu, c == 1);
+    cnt2 += __popc(b2);
+    cnt1 += __popc(b1);
+    if (o / 32 == lane) { held2 = b2; held1 = b1; }
   }
   int tot2, tot1;
   int before2 = warp_prefix(cnt2, buf, &tot2);
@@ -207,13 +224,20 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
     for (int r = 0; r < CL; ++r)
       if (r < rank) { before2 += from[r].x; before1 += from[r].y; }
   }
+  const uint32_t lt = (1u << lane) - 1u;
 #pragma unroll 4
   for (int o = lane; o < wlen; o += 32) {
-    const int c = klass(o);
-    const uint32_t b2 = __ballot_sync(0xffffffffu, c == 2), b1 = __ballot_sync(0xffffffffu, c == 1);
-    const uint32_t lt = (1u << lane) - 1u;
+    uint32_t b2, b1;
+    if (HELD) {
+      b2 = __shfl_sync(0xffffffffu, held2, o / 32);
+      b1 = __shfl_sync(0xffffffffu, held1, o / 32);
+    } else {
+      const int c = klass(o);
+      b2 = __ballot_sync(0xffffffffu, c == 2);
+      b1 = __ballot_sync(0xffffffffu, c == 1);
+    }
     const int r2 = before2 + __popc(b2 & lt), r1 = before1 + __popc(b1 & lt);
-    if (c == 2 || (c == 1 && r1 < need)) keep[r2 + min(r1, need)] = (int32_t)(i0 + o);
+    if (((b2 >> lane) & 1u) || (((b1 >> lane) & 1u) && r1 < need)) keep[r2 + min(r1, need)] = i0 + o;
     before2 += __popc(b2);
     before1 += __popc(b1);
   }
@@ -421,18 +445,22 @@ extern "C" mla_status_t mla_cache_select(mla_handle_t* h, const float* weights, 
   const long nw = (long)cl * evict::SEL_WARPS;
   const long wlen = ((ldw + nw - 1) / nw + 31) & ~31L;
   const long keys = evict::SEL_WARPS * wlen;              // of a CTA, at most
-  const int smem_keys = keys <= evict::SEL_SMEM_KEYS ? (int)keys : 0;
-  evict::SelectArgs a{weights, kv_len, keep, keep_len, (long)ldw, budget, sink, recent, smem_keys, h->status};
+  const bool held = keys <= evict::SEL_SMEM_KEYS;
+  evict::SelectArgs a{weights, kv_len, keep, keep_len, (long)ldw, budget, sink, recent, h->status};
   static std::once_flag once;
   std::call_once(once, [] {
-    for (auto* k : {evict::select_kernel<1>, evict::select_kernel<2>, evict::select_kernel<4>, evict::select_kernel<8>})
+    for (auto* k : {evict::select_kernel<1, true>, evict::select_kernel<2, true>, evict::select_kernel<4, true>,
+                    evict::select_kernel<8, true>})
       cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, evict::SEL_SMEM_KEYS * 4);
   });
-  Launch L(dim3((unsigned)(num_seqs * cl)), dim3(evict::SEL_THREADS), (size_t)smem_keys * 4,
+  Launch L(dim3((unsigned)(num_seqs * cl)), dim3(evict::SEL_THREADS), held ? (size_t)keys * 4 : 0,
            (cudaStream_t)stream, false, dim3((unsigned)cl, 1, 1));
-  MLA_CUDA_TRY(cudaLaunchKernelEx(
-      &L.cfg, cl == 1 ? evict::select_kernel<1> : cl == 2 ? evict::select_kernel<2>
-              : cl == 4 ? evict::select_kernel<4> : evict::select_kernel<8>, a));
+  // (only clusters of 8 share more keys than fit)
+  MLA_CUDA_TRY(cudaLaunchKernelEx(&L.cfg, !held      ? evict::select_kernel<8, false>
+                                          : cl == 1  ? evict::select_kernel<1, true>
+                                          : cl == 2  ? evict::select_kernel<2, true>
+                                          : cl == 4  ? evict::select_kernel<4, true>
+                                                     : evict::select_kernel<8, true>, a));
   h->launches += 1;
   return MLA_OK;
 }

@@ -146,9 +146,11 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
   const int key = threadIdx.x & (KT - 1), half = threadIdx.x >= 256 ? 1 : 0;
   const int w = key / 32, lane = threadIdx.x % 32, col_id = half * 128 + key;
   const uint32_t lane_base = (uint32_t)(w * 32) << 16;
-  float* lse2 = (float*)(smem + OFF_LSE);
+  float* lses = (float*)(smem + OFF_LSE);
+  // exp(scale s - lse): the difference first, so that the factor log2(e) rounds a
+  // small number (rounding lse log2(e) of each row instead cost ten times the error)
+  auto weight = [&](float s, float lse) { return fast_exp2(fmaf(s, P.scale, -lse) * 1.4426950408889634f); };
   const uint32_t s_free0 = mapa(smem_u32(&B->s_free[0]), 0), s_free1 = mapa(smem_u32(&B->s_free[1]), 0);
-  constexpr float kLog2e = 1.4426950408889634f;
   uint32_t tile = 0;                                      // row tiles so far, over all items
   Items it(P);
   while (it.next()) {
@@ -164,7 +166,7 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
         {
           float l = -INFINITY;
           if (col_id < rows) l = P.lse[row0 + col_id];
-          lse2[col_id] = l * kLog2e;
+          lses[col_id] = l;
         }
         // the warp's 32 keys as this lane's four columns see them; where nodes'
         // keys are among them, a lane walks from one node for all its rows
@@ -212,17 +214,17 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
             if (all) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
-                const float4 l = *reinterpret_cast<const float4*>(lse2 + c0 + i);
-                part[0] += fast_exp2(fmaf(s[i], P.scale_log2, -l.x));
-                part[1] += fast_exp2(fmaf(s[i + 1], P.scale_log2, -l.y));
-                part[2] += fast_exp2(fmaf(s[i + 2], P.scale_log2, -l.z));
-                part[3] += fast_exp2(fmaf(s[i + 3], P.scale_log2, -l.w));
+                const float4 l = *reinterpret_cast<const float4*>(lses + c0 + i);
+                part[0] += weight(s[i], l.x);
+                part[1] += weight(s[i + 1], l.y);
+                part[2] += weight(s[i + 2], l.z);
+                part[3] += weight(s[i + 3], l.w);
               }
             } else {
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const uint32_t m = __shfl_sync(0xffffffffu, word[q], i);
-                const float p = fast_exp2(fmaf(s[i], P.scale_log2, -lse2[c0 + i]));
+                const float p = weight(s[i], lses[c0 + i]);
                 part[i & 3] += ((m >> lane) & 1u) ? p : 0.f;
               }
             }
@@ -236,10 +238,10 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
     }
     // the key's two halves; half 0 writes
     sum_sync();
-    if (half) lse2[key] = sum;
+    if (half) lses[key] = sum;
     sum_sync();
     if (!half && j < it.n) {
-      const float t = sum + lse2[key];
+      const float t = sum + lses[key];
       if (P.splits > 1) {
         P.part[((long)it.sp * P.num_blocks + it.b) * P.ldp + j] = t;
       } else {
@@ -477,7 +479,7 @@ mla_status_t key_weights(cudaStream_t st, mla_handle* h, const tree::Rule& r, co
   P.num_blocks = d.num_blocks;
   P.splits = weight_splits(h, d, ldw);
   P.decay = decay;
-  P.scale_log2 = h->scale * 1.4426950408889634f;
+  P.scale = h->scale;
   static std::once_flag once;
   std::call_once(once, [] {
     for (auto* k : {key_weights_tc_kernel<1>, key_weights_tc_kernel<3>})

@@ -36,7 +36,7 @@ struct WeightParams {
   float* part;        // [splits, num_blocks, ldp] when splits > 1
   long ldw, ldp;
   int num_blocks, splits, seg_rows, q_box_rows;
-  float decay, scale_log2;
+  float decay, scale;
 };
 
 size_t tree_attention_ws(const mla_handle* h, const mla_attn_desc_t& d);
