@@ -76,7 +76,7 @@ struct Bars {
   uint64_t q_full, q_tmem;            // Q in shared memory (TMA) / in tensor memory
   // keys and values land on barriers of their own: each has one consumer, which
   // never falls two phases behind (a parity tells only two apart)
-  uint64_t k_full[4], k_empty[SLOTS], v_full[SLOTS], clean[SLOTS], land[2];
+  uint64_t k_full[SLOTS], k_empty[SLOTS], v_full[SLOTS], clean[SLOTS], land;
   uint64_t rope_full;
   uint64_t s_full, s_free;            // S(t) complete (the rope chunk is free) / read
   uint64_t p_full, o_done;            // P(t) written / P(t) V(t) complete
@@ -719,27 +719,29 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
   const int seg = P.seg_rows, nkseg = 64 / seg, nvseg = KT / seg;
 
   if (warp == W_RING || warp == W_RING + 1) {
-    // ---- keys: this CTA's 64 of every tile, chunk pairs 2 w and 2 w + 1 ----
-    const int i0 = 2 * (warp - W_RING), c = lane / nkseg, sg = lane % nkseg;
+    // ---- keys: this CTA's 64 of every tile, chunk pairs 2 w and 2 w + 1 (and
+    // the rope chunk): one barrier and one release for both, each costing the
+    // issuing thread 100 to 200 cycles ----
+    const int w = warp - W_RING, c = lane / nkseg, sg = lane % nkseg;
+    const uint32_t bar = mapa(smem_u32(&B->k_full[w]), U.lead);
+    uint64_t* freed = w == 0 ? &B->k_empty[0] : &B->s_full;
     int t = 0;
     bool ok = true;
     for (; t < U.nt && ok; ++t) {
       const int y = lane < 2 * nkseg ? cache_row(R, U, tile_key(U, t) + 64 * p + sg * seg, true) : 0;
-      // a commit costs the issuing thread 125 cycles: one frees pairs 0 and 1, that
-      // of the finished scores pairs 2 and 3
-      if (!(ok = wait_bar(B, i0 == 0 ? &B->k_empty[0] : &B->s_full, (t & 1) ^ 1, R.status))) break;
-      for (int i = i0; i < i0 + 2; ++i) {
-        if (p == 0 && lane == 0) mbar_arrive_expect_tx(&B->k_full[i], 2 * PSLOT_BYTES);
-        __syncwarp();
-        if (lane < 2 * nkseg)
-          tma_load_3d_pair(smem + OFF_PK + i * PSLOT_BYTES + c * (CH_BYTES / 2) + sg * seg * 128, &P.tmK,
-                           mapa(smem_u32(&B->k_full[i]), U.lead), (2 * i + c) * 64, y, 0);
-        __syncwarp();
+      if (!(ok = wait_bar(B, freed, (t & 1) ^ 1, R.status))) break;
+      if (p == 0 && lane == 0) mbar_arrive_expect_tx(&B->k_full[w], 4 * PSLOT_BYTES + (w ? CH_BYTES : 0));
+      __syncwarp();
+      if (lane < 2 * nkseg) {
+        for (int i = 2 * w; i < 2 * w + 2; ++i)
+          tma_load_3d_pair(smem + OFF_PK + i * PSLOT_BYTES + c * (CH_BYTES / 2) + sg * seg * 128, &P.tmK, bar,
+                           (2 * i + c) * 64, y, 0);
+        if (w == 1 && c == 0) tma_load_3d_pair(smem + OFF_ROPE + sg * seg * 128, &P.tmK, bar, 512, y, 0);
       }
+      __syncwarp();
     }
     // every copy of the pair has landed before its shared memory is used again
-    if (p == 0 && ok && t > 0)
-      for (int i = i0; i < i0 + 2; ++i) mbar_wait(&B->k_full[i], (t - 1) & 1, R.status);
+    if (p == 0 && ok && t > 0) mbar_wait(&B->k_full[w], (t - 1) & 1, R.status);
   } else if (warp == W_RING + 2) {
     // ---- values: chunk 2 i + p of this half for both pairs ----
     bool ok = true;
@@ -758,50 +760,31 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
         dirty = dirty_tile(U, z_lo, t);
       }
       if (!(ok = wait_bar(B, &B->o_done, (t & 1) ^ 1, R.status))) break;
-      for (int i = 0; i < PV; ++i) {
-        uint8_t* slot = smem + OFF_PV + i * PSLOT_BYTES;
-        // a tile to be cleared lands on a barrier of this CTA's own
-        const uint32_t bar = dirty ? smem_u32(&B->land[i]) : mapa(smem_u32(&B->v_full[i]), U.lead);
-        if (lane == 0) {
-          if (dirty) mbar_arrive_expect_tx(&B->land[i], PSLOT_BYTES);
-          else if (p == 0) mbar_arrive_expect_tx(&B->v_full[i], 2 * PSLOT_BYTES);
-        }
-        __syncwarp();
-        if (lane < nvseg)
-          tma_load_3d_pair(slot + lane * seg * 128, &P.tmK, bar, (4 * U.half + 2 * i + p) * 64, y, 0);
-        __syncwarp();
-        if (dirty) {
-          know_seen();
-          if (!(ok = ok && wait_bar(B, &B->land[i], nd & 1, R.status))) break;
-          clear_unseen(U, smem, slot, 1, j0, z_lo);
-          if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&B->clean[i]), U.lead));
-        }
+      // a tile to be cleared lands on a barrier of this CTA's own
+      const uint32_t bar = dirty ? smem_u32(&B->land) : mapa(smem_u32(&B->v_full[0]), U.lead);
+      if (lane == 0) {
+        if (dirty) mbar_arrive_expect_tx(&B->land, PV * PSLOT_BYTES);
+        else if (p == 0) mbar_arrive_expect_tx(&B->v_full[0], 2 * PV * PSLOT_BYTES);
+      }
+      __syncwarp();
+      if (lane < nvseg)
+        for (int i = 0; i < PV; ++i)
+          tma_load_3d_pair(smem + OFF_PV + i * PSLOT_BYTES + lane * seg * 128, &P.tmK, bar,
+                           (4 * U.half + 2 * i + p) * 64, y, 0);
+      __syncwarp();
+      if (dirty) {
+        know_seen();
+        if (!(ok = ok && wait_bar(B, &B->land, nd & 1, R.status))) break;
+        clear_unseen(U, smem, smem + OFF_PV, PV, j0, z_lo);
+        if (lane == 0) mbar_arrive_pair(mapa(smem_u32(&B->clean[0]), U.lead));
       }
       nd += dirty;
     }
   } else if (warp == W_ROPE) {
-    // ---- Q once, then the rope chunk of this CTA's 64 keys of every tile ----
-    if (U.nt > 0) {
-      if (lane == 0) {
-        if (p == 0) mbar_arrive_expect_tx(&B->q_full, 2 * NQS * CH_BYTES);
-        tma_load_3d_pair(smem + OFF_Q, &P.tmQ, mapa(smem_u32(&B->q_full), U.lead), 0, (int)U.row0, NQT);
-      }
-      __syncwarp();
-      int t = 0;
-      for (; t < U.nt; ++t) {
-        const int y = lane < nkseg ? cache_row(R, U, tile_key(U, t) + 64 * p + lane * seg, false) : 0;
-        if (!wait_bar(B, &B->s_full, (t & 1) ^ 1, R.status)) break;
-        if (p == 0 && lane == 0) mbar_arrive_expect_tx(&B->rope_full, CH_BYTES);
-        __syncwarp();
-        if (lane < nkseg)
-          tma_load_3d_pair(smem + OFF_ROPE + lane * seg * 128, &P.tmK, mapa(smem_u32(&B->rope_full), U.lead), 512,
-                           y, 0);
-        __syncwarp();
-      }
-      if (p == 0) {
-        mbar_wait(&B->q_full, 0, R.status);
-        if (t > 0) mbar_wait(&B->rope_full, (t - 1) & 1, R.status);
-      }
+    if (U.nt > 0 && lane == 0) {
+      if (p == 0) mbar_arrive_expect_tx(&B->q_full, 2 * NQS * CH_BYTES);
+      tma_load_3d_pair(smem + OFF_Q, &P.tmQ, mapa(smem_u32(&B->q_full), U.lead), 0, (int)U.row0, NQT);
+      if (p == 0) mbar_wait(&B->q_full, 0, R.status);
     }
   } else if (warp == W_S) {
     if (p == 0 && lane == 0 && U.nt > 0) {
@@ -821,9 +804,11 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
         }
 #pragma unroll
         for (int i = 0; i < PK; ++i) {
-          if (!(ok = ok && wait_bar(B, &B->k_full[i], par, R.status, ready))) break;
-          // a look at the next barrier, its answer used after these MMAs
-          ready = mbar_test_wait(i < PK - 1 ? &B->k_full[i + 1] : &B->rope_full, par);
+          if (i % 2 == 0) {
+            if (!(ok = ok && wait_bar(B, &B->k_full[i / 2], par, R.status, ready))) break;
+            // a look at the next barrier, its answer used after these MMAs
+            if (i == 0) ready = mbar_test_wait(&B->k_full[1], par);
+          }
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -836,7 +821,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
             }
           if (i == 1) mma_commit_pair(&B->k_empty[0], both);
         }
-        if (!(ok = ok && wait_bar(B, &B->rope_full, par, R.status, ready))) break;
+        if (!ok) break;
 #pragma unroll
         for (int d = 0; d < 4; ++d) mma_f16_pair(tS, dQ + (NQS - 1) * U_CH + 2 * d, dRope + 2 * d, idesc, 1u);
         mma_commit_pair(&B->s_full, both);          // keys 2 and 3 and the rope chunk are free, too
@@ -859,16 +844,13 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
         behind_scores(B, min(t + 2, U.nt));
         if (!(ok = wait_bar(B, &B->p_full, t & 1, R.status))) break;
         tc_fence_after();
-        bool ready = false;
+        uint64_t* bar = dirty ? &B->clean[0] : &B->v_full[0];     // (both CTAs have cleared their halves)
+        if (!(ok = wait_bar(B, bar, (dirty ? nd : nf) & 1, R.status))) break;
 #pragma unroll
-        for (int i = 0; i < PV; ++i) {
-          uint64_t* bar = dirty ? &B->clean[i] : &B->v_full[i];   // (both CTAs have cleared their halves)
-          if (!(ok = ok && wait_bar(B, bar, (dirty ? nd : nf) & 1, R.status, ready))) break;
-          if (i == 0) ready = mbar_test_wait(bar + 1, (dirty ? nd : nf) & 1);
+        for (int i = 0; i < PV; ++i)
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
             mma_f16_ts_pair(tO + 128 * i, tP + 8 * k, dV + i * U_SLOT + U_KSTEP * k, idesc, (t | k) ? 1u : 0u);
-        }
         mma_commit_pair(&B->o_done, both);
         if (dirty) ++nd; else ++nf;
       }
