@@ -50,6 +50,10 @@ struct Bars {
   uint64_t q_full[QSLOTS], q_empty[QSLOTS];
   uint64_t s_full[2], s_free[2];
   uint64_t drain;
+  // row tiles [first, end) of the item whose keys k_full[0] announces, by its
+  // parity; end < 0: no more.  The key warp looks items up (2 k cycles) under its waits; the
+  // issuing thread, which has no time to spare, reads them here.
+  int first[2], end[2];
   uint32_t tmem_slot;
   int abort;
 };
@@ -306,10 +310,17 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid
     bool more = look(&y);
     while (ok && more) {
       const int y0 = y;
+      const int first = it.qt0, end = it.qt1;
       for (int c3 = 0; c3 < TRIO; ++c3) {
         if (c3 == TRIO - 1) more = look(&y);              // under the wait for the last trio
         if (!(ok = wait_bar(B, &B->k_empty[c3], (use & 1) ^ 1, R.status))) break;
-        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&B->k_full[c3], 2 * 3 * CH_BYTES);
+        if (rank == 0 && lane == 0) {
+          if (c3 == 0) {
+            B->first[use & 1] = first;
+            B->end[use & 1] = end;
+          }
+          mbar_arrive_expect_tx(&B->k_full[c3], 2 * 3 * CH_BYTES);
+        }
         __syncwarp();
         const uint32_t bar = mapa(smem_u32(&B->k_full[c3]), 0);
         uint8_t* dst = smem + OFF_K + 3 * c3 * CH_BYTES;
@@ -323,9 +334,16 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid
       }
       ++use;
     }
-    // every copy has landed before the pair may exit (its barriers are the even CTA's)
-    if (rank == 0 && ok && use > 0)
-      for (int i = 0; i < TRIO; ++i) mbar_wait(&B->k_full[i], (use - 1) & 1, R.status);
+    // the end, once the last item's first keys are done with (its other copies land
+    // before the pair may exit: the barriers are the even CTA's)
+    if (rank == 0 && ok && wait_bar(B, &B->k_empty[0], (use & 1) ^ 1, R.status)) {
+      if (lane == 0) {
+        B->end[use & 1] = -1;
+        mbar_arrive(&B->k_full[0]);
+      }
+      if (use > 0)
+        for (int i = 1; i < TRIO; ++i) mbar_wait(&B->k_full[i], (use - 1) & 1, R.status);
+    }
   } else if (warp == W_Q || warp == W_Q + 1) {
     // ---- this CTA's half of the rows, chunk by chunk; the two warps take turns ----
     if (lane == 0) prefetch_tmap(&P.tmQ);
@@ -357,23 +375,23 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid
     // ---- MMA issue for the pair (the even CTA) ----
     constexpr uint64_t U_CH = CH_BYTES / 16;
     const uint64_t dK = smem_desc_sw128(smem + OFF_K), dQ = smem_desc_sw128(smem + OFF_Q);
-    uint32_t use = 0, tile = 0;
-    int s = 0;
-    uint32_t qpar = 0;
-    bool ok = true;
-    Items it(P);
-    while (ok && it.next()) {
-      if (it.skip) continue;
-      if (lane == 0) {
-        for (int qt = it.qt0; qt < it.qt1 && ok; ++qt, ++tile) {
-          const int buf = tile & 1;
-          const uint32_t d = tmem + buf * NMAX, idesc = idesc_f16(256, it.cols(qt), false);
+    if (lane == 0) {
+      const int block_rows = R.T * R.H;
+      uint32_t use = 0, tile = 0, qpar = 0;
+      int s = 0;
+      for (bool ok = true; ok; ++use) {
+        if (!(ok = wait_bar(B, &B->k_full[0], use & 1, R.status))) break;
+        const int first = *(volatile int*)&B->first[use & 1], end = *(volatile int*)&B->end[use & 1];
+        if (end < 0) break;
+        for (int qt = first; qt < end && ok; ++qt, ++tile) {
+          const int buf = tile & 1, cols = (min(NMAX, block_rows - qt * NMAX) + 31) & ~31;
+          const uint32_t d = tmem + buf * NMAX, idesc = idesc_f16(256, cols, false);
           bool ready = mbar_test_wait(&B->q_full[s], qpar);
           if (!(ok = wait_bar(B, &B->s_free[buf], ((tile >> 1) & 1) ^ 1, R.status))) break;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < NCH; c += QC) {
-            if (qt == it.qt0 && c % 3 == 0 && ok) ok = wait_bar(B, &B->k_full[c / 3], use & 1, R.status);
+            if (qt == first && c > 0 && c % 3 == 0 && ok) ok = wait_bar(B, &B->k_full[c / 3], use & 1, R.status);
             if (!ok || !(ok = wait_bar(B, &B->q_full[s], qpar, R.status, ready))) break;
             // a look at the next slot, its answer used after these MMAs
             ready = s + 1 == QSLOTS ? mbar_test_wait(&B->q_full[0], qpar ^ 1) : mbar_test_wait(&B->q_full[s + 1], qpar);
@@ -385,16 +403,12 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_tc_kernel(const __grid
                 mma_f16_pair(d, dK + (c + x) * U_CH + 2 * k, db + 2 * k, idesc, (c | x | k) ? 1u : 0u);
             }
             mma_commit_pair(&B->q_empty[s]);
-            if (qt == it.qt1 - 1 && (c + QC) % 3 == 0) mma_commit_pair(&B->k_empty[c / 3]);
+            if (qt == end - 1 && (c + QC) % 3 == 0) mma_commit_pair(&B->k_empty[c / 3]);
             if (++s == QSLOTS) { s = 0; qpar ^= 1; }
           }
           mma_commit_pair(&B->s_full[buf]);
         }
       }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-      ++use;
-    }
-    if (lane == 0) {
       mma_commit_pair(&B->drain);
       mbar_wait(&B->drain, 0, R.status);
     }
