@@ -63,6 +63,8 @@ constexpr int SMEM_BYTES = 1024 + OFF_XM + 2 * QROWS * 4;
 // the pair kernel's slots (a CTA's halves): four key pairs and two value pairs of 16 KB
 constexpr int PK = 4, PV = 2, PSLOT_BYTES = CH_BYTES, OFF_PK = OFF_RING, OFF_PV = OFF_PK + PK * PSLOT_BYTES;
 static_assert(OFF_PV + PV * PSLOT_BYTES <= OFF_ROPE, "slots");
+static_assert(NQT == 2 && PV * PSLOT_BYTES == NQT * CH_BYTES && SLOT_BYTES == NQT * CH_BYTES, "Q's way through a slot");
+constexpr int OFF_Q01 = OFF_RING + (SLOTS - 1) * SLOT_BYTES;   // the other kernel's: its last ring slot
 // the epilogue's rows, over Q and the slots: fp32, 256 dims, padded against bank
 // conflicts, then their log2-sum-exps
 constexpr int STG_PITCH = 260, OFF_STG_LSE = QROWS * STG_PITCH * 4;
@@ -74,6 +76,7 @@ constexpr float RESCALE_LOG2 = 8.f, kLn2 = 0.6931471805599453f;
 
 struct Bars {
   uint64_t q_full, q_tmem;            // Q in shared memory (TMA) / in tensor memory
+  uint64_t q01_full, q01_read;        // its first two chunks, on their way through a value or ring slot
   // keys and values land on barriers of their own: each has one consumer, which
   // never falls two phases behind (a parity tells only two apart)
   uint64_t k_full[SLOTS], k_empty[SLOTS], v_full[SLOTS], clean[SLOTS], land;
@@ -147,22 +150,8 @@ __device__ __forceinline__ bool dirty_tile(const Unit& U, int z_lo, int t) {
   return j0 + KT > U.ctx || j0 < z_lo;
 }
 
-// 64 of a row's first 128 dims, one thread (warps 0-3 and 8-11; zeros for rows
-// past the block's), asked for before the CTA sets up.
-__device__ __forceinline__ void load_q(const TreeParams& P, const Unit& U, uint32_t* q) {
-  const int r = threadIdx.x & (QROWS - 1), kh = threadIdx.x >= 256 ? 1 : 0;
-  const bool live = U.qt * QROWS + r < P.rule.T * P.rule.H;
-  const uint4* src = reinterpret_cast<const uint4*>(P.q_abs + (live ? U.row0 + r : 0) * 576 + 64 * kh);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
-    q[4 * i] = v.x; q[4 * i + 1] = v.y; q[4 * i + 2] = v.z; q[4 * i + 3] = v.w;
-  }
-}
-__device__ __forceinline__ bool softmax_warp(int warp) { return warp < 4 || (warp >= 8 && warp < 12); }
-
 __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8_t* smem, uint32_t tmem,
-                                             const Unit& U, const uint32_t* q) {
+                                             const Unit& U, const uint8_t* q01) {
   const int r = threadIdx.x & (QROWS - 1), kh = threadIdx.x >= 256 ? 1 : 0, w = r / 32, lane = r % 32;
   constexpr int KH = KT / 2;
   const uint32_t lane_base = (uint32_t)(w * 32) << 16;
@@ -175,7 +164,16 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   const int32_t* parent = R.parent + (long)U.b * R.T;
   const uint32_t s_free = mapa(smem_u32(&B->s_free), U.lead), p_full = mapa(smem_u32(&B->p_full), U.lead);
   if (U.nt > 0) {
-    // Q dims 0..127 of this row -> tensor memory (bf16 pairs), 64 dims a thread
+    // Q dims 0..127 of this row -> tensor memory (bf16 pairs), 64 dims a thread,
+    // by way of shared memory (row by row from global memory they took 2 us)
+    uint32_t q[32];
+    wait_bar(B, &B->q01_full, 0, P.rule.status);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(q01 + kh * CH_BYTES + r * 128 + ((i ^ (r & 7)) * 16));
+      q[4 * i] = v.x; q[4 * i + 1] = v.y; q[4 * i + 2] = v.z; q[4 * i + 3] = v.w;
+    }
+    mbar_arrive(&B->q01_read);
     tmem_st32_u(tmem + TM_Q + 32 * kh + lane_base, q);
     tc_fence_before();
     __syncwarp();
@@ -371,14 +369,14 @@ __device__ __forceinline__ void store_rows(const TreeParams& P, const uint8_t* s
   const int rows = min(QROWS, P.rule.T * P.rule.H - U.qt * QROWS);
   const int y = CS > 1 ? (int)(blockIdx.y % CS) : 0, x = (int)(blockIdx.x & 1);
   const uint32_t stg = smem_u32(smem), lse_a = stg + OFF_STG_LSE;
-#pragma unroll(CS == 1 ? 4 : 2)
+#pragma unroll(CS == 4 ? 2 : 4)
   for (int r = y * (QROWS / CS) + warp; r < min(rows, (y + 1) * (QROWS / CS)); r += THREADS / 32) {
     float l[CS];
     float4 a[CS], c[CS];
 #pragma unroll
     for (int s = 0; s < CS; ++s) {
       const uint32_t rank = (uint32_t)(x + 2 * s), at = stg + (uint32_t)(r * STG_PITCH + 8 * lane) * 4;
-      if (CS == 1) {
+      if (CS == 1 || s == y) {                            // this CTA's own
         l[s] = ((const float*)(smem + OFF_STG_LSE))[r];
         a[s] = *(const float4*)((const float*)smem + r * STG_PITCH + 8 * lane);
         c[s] = *(const float4*)((const float*)smem + r * STG_PITCH + 8 * lane + 4);
@@ -444,7 +442,7 @@ __device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* sm
     uint64_t* bar = (uint64_t*)B + tid;
     const uint32_t count = bar == &B->q_tmem || bar == &B->s_free || bar == &B->p_full ? 8 * U.tiles
                            : bar >= B->clean && bar < B->clean + SLOTS                  ? U.tiles
-                           : bar == &B->seen_full                                       ? 2 * QROWS
+                           : bar == &B->seen_full || bar == &B->q01_read                ? 2 * QROWS
                                                                                          : 1;
     mbar_init(bar, count);
     fence_mbar_init();
@@ -526,11 +524,9 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
   U.b = unit / P.tiles_per_block;
   U.qt = unit % P.tiles_per_block;
   U.row0 = ((long)U.b * R.T) * R.H + (long)U.qt * QROWS;
-  if (warp == W_ROPE && lane == 0) { prefetch_tmap(&P.tmK); prefetch_tmap(&P.tmC); prefetch_tmap(&P.tmQ); }
+  if (warp == W_ROPE && lane == 0) { prefetch_tmap(&P.tmQ01); prefetch_tmap(&P.tmK); prefetch_tmap(&P.tmC); prefetch_tmap(&P.tmQ); }
   if (warp == W_S) tmem_alloc(&B->tmem_slot, TMEM_COLS);
   pdl_wait();                  // Q_abs and the nodes' own entries come from the kernels before
-  uint32_t q[32];
-  if (softmax_warp(warp)) load_q(P, U, q);
   set_up(P, B, smem, U);
   const uint32_t tmem = B->tmem_slot;
   const int seg = P.seg_rows, nseg = KT / seg;
@@ -547,6 +543,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
       const int ch = it.value ? 4 * U.half + 2 * it.pair : 2 * it.pair;
       uint64_t* full = it.value ? &B->v_full[s] : &B->k_full[s];
       const int y = lane < nseg ? cache_row(R, U, j0 + lane * seg, true) : 0;
+      if (u == SLOTS - 1 && !wait_bar(B, &B->q01_read, 0, R.status)) break;   // Q passes through it first
       if (!wait_bar(B, &B->k_empty[s], ((u / SLOTS) & 1) ^ 1, R.status)) break;
       if (lane == 0) mbar_arrive_expect_tx(full, SLOT_BYTES);
       __syncwarp();
@@ -579,6 +576,8 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
     // ---- Q once, then the rope chunk of every tile ----
     if (U.nt > 0) {
       if (lane == 0) {
+        mbar_arrive_expect_tx(&B->q01_full, NQT * CH_BYTES);
+        tma_load_3d(smem + OFF_Q01, &P.tmQ01, &B->q01_full, 0, (int)U.row0, 0);
         mbar_arrive_expect_tx(&B->q_full, NQS * CH_BYTES);
         tma_load_3d(smem + OFF_Q, &P.tmQ, &B->q_full, 0, (int)U.row0, NQT);
       }
@@ -592,6 +591,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
         if (lane < nseg) tma_load_3d(smem + OFF_ROPE + lane * seg * 128, &P.tmK, &B->rope_full, 512, y, 0);
         __syncwarp();
       }
+      mbar_wait(&B->q01_full, 0, R.status);
       mbar_wait(&B->q_full, 0, R.status);
       if (t > 0) mbar_wait(&B->rope_full, (t - 1) & 1, R.status);
     }
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
       mbar_wait(&B->drain[1], 0, R.status);
     }
   } else {
-    softmax_role(P, B, smem, tmem, U, q);
+    softmax_role(P, B, smem, tmem, U, smem + OFF_Q01);
   }
   __syncwarp();
   tc_fence_before();
@@ -708,11 +708,9 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
   U.b = unit / units;
   U.qt = 2 * (unit % units) + p;
   U.row0 = ((long)U.b * R.T) * R.H + (long)U.qt * QROWS;
-  if (warp == W_ROPE && lane == 0) { prefetch_tmap(&P.tmK); prefetch_tmap(&P.tmQ); }
+  if (warp == W_ROPE && lane == 0) { prefetch_tmap(&P.tmQ01); prefetch_tmap(&P.tmK); prefetch_tmap(&P.tmQ); }
   if (warp == W_S) tmem_alloc_pair(&B->tmem_slot, TMEM_COLS);
   pdl_wait();                  // Q_abs and the nodes' own entries come from the kernels before
-  uint32_t q[32];
-  if (softmax_warp(warp)) load_q(P, U, q);
   set_up(P, B, smem, U);
   const uint32_t tmem = B->tmem_slot, both = 3u << U.lead;
   // segments: rows of a page, at most this CTA's 64 keys of a tile
@@ -744,7 +742,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
     if (p == 0 && ok && t > 0) mbar_wait(&B->k_full[w], (t - 1) & 1, R.status);
   } else if (warp == W_RING + 2) {
     // ---- values: chunk 2 i + p of this half for both pairs ----
-    bool ok = true;
+    bool ok = U.nt > 0 && wait_bar(B, &B->q01_read, 0, R.status);   // Q passes through the slots first
     int z_lo = -1;                                        // known from seen_full on
     uint32_t nd = 0;                                      // tiles cleared so far
     auto know_seen = [&]() {
@@ -782,8 +780,11 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
     }
   } else if (warp == W_ROPE) {
     if (U.nt > 0 && lane == 0) {
+      mbar_arrive_expect_tx(&B->q01_full, NQT * CH_BYTES);
+      tma_load_3d(smem + OFF_PV, &P.tmQ01, &B->q01_full, 0, (int)U.row0, 0);
       if (p == 0) mbar_arrive_expect_tx(&B->q_full, 2 * NQS * CH_BYTES);
       tma_load_3d_pair(smem + OFF_Q, &P.tmQ, mapa(smem_u32(&B->q_full), U.lead), 0, (int)U.row0, NQT);
+      mbar_wait(&B->q01_full, 0, R.status);
       if (p == 0) mbar_wait(&B->q_full, 0, R.status);
     }
   } else if (warp == W_S) {
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
       mbar_wait(&B->drain[1], 0, R.status);
     }
   } else {
-    softmax_role(P, B, smem, tmem, U, q);
+    softmax_role(P, B, smem, tmem, U, smem + OFF_PV);
   }
   __syncwarp();
   tc_fence_before();
@@ -986,11 +987,11 @@ mla_status_t tree_attention(cudaStream_t st, mla_handle* h, const tree::Rule& r,
   const int max_seg = plan.pair ? KT / 2 : KT;
   P.seg_rows = r.page_size < max_seg ? r.page_size : max_seg;
   if (!make_tmap_chunked(&P.tmQ, false, q_abs, rows, l.L, l.L, QROWS, NQS) ||
+      !make_tmap_chunked(&P.tmQ01, false, q_abs, rows, l.L, l.L, QROWS, NQT) ||
       !make_tmap_chunked(&P.tmC, false, cache, slots, l.L, l.L, KT, 2) ||
       !make_tmap_2d(&P.tmK, false, cache, slots, l.L, l.L, P.seg_rows))
     return fail(MLA_ERR_CUDA, "tree attention: cuTensorMapEncodeTiled failed");
   P.rule = r;
-  P.q_abs = q_abs;
   P.o_lat = o_lat;
   P.lse = lse;
   P.vis_stats = d.vis_stats;
