@@ -10,8 +10,8 @@
 // end, so repeated calls agree bit for bit.  Rows are read 16 bytes at a time
 // with an odd number of 16-byte units between them, which keeps eight threads
 // on eight rows off one another's banks.  Such layers and their calls are
-// small: what counts is the chain of latencies (4 heads x 8 nodes, 64 keys: 22.9
-// us with scalar loads and one buffer).
+// small: what counts is the chain of latencies (4 heads x 8 nodes, 64 keys: 12.4
+// us; 22.9 with scalar loads and one buffer).
 #include "simt.cuh"
 #include "tree.cuh"
 
@@ -86,7 +86,7 @@ __device__ __forceinline__ void stage_rows(const float* q, long row0, int rows, 
 // <q, k0> and <q, k1> over `units` 16-byte units.
 __device__ __forceinline__ float2 dot2(const float* q, const float* k0, const float* k1, int units) {
   float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
-#pragma unroll 4
+#pragma unroll 10
   for (int u = 0; u < units; ++u) {
     const float4 x = reinterpret_cast<const float4*>(q)[u];
     const float4 y = reinterpret_cast<const float4*>(k0)[u], z = reinterpret_cast<const float4*>(k1)[u];
@@ -161,19 +161,28 @@ tree_attn_kernel(const tree::Rule a, const float* __restrict__ q_abs, const floa
     Ps[r * KT + c0] = p0;
     Ps[r * KT + c0 + 16] = p1;
     __syncwarp();                               // a row's 16 threads share a warp
-    // unseen keys are left out of the sum: their entries may hold anything
+    // unseen keys (weight 0) are taken as zeros: their entries may hold anything.  A
+    // select, not a branch: the two rows of a warp see different keys, and
+    // branching took 3.4 k cycles a tile
+    const bool whole = __all_sync(0xffffffffu, vis == 0xffffffffu);
 #pragma unroll
     for (int k = 0; k < MAX_OUT; ++k) {
       const int c = 4 * c0 + 64 * k;
       if (k < nout && c < rkv) {
         float4 acc = make_float4(o[k].x * alpha, o[k].y * alpha, o[k].z * alpha, o[k].w * alpha);
-#pragma unroll 8
-        for (int kk = 0; kk < KT; ++kk) {
-          if ((vis >> kk) & 1u) {
-            const float p = Ps[r * KT + kk];
-            const float4 v = *reinterpret_cast<const float4*>(E + kk * pitch + c);
-            acc.x = fmaf(p, v.x, acc.x); acc.y = fmaf(p, v.y, acc.y);
-            acc.z = fmaf(p, v.z, acc.z); acc.w = fmaf(p, v.w, acc.w);
+#pragma unroll 2
+        for (int k4 = 0; k4 < KT; k4 += 4) {
+          const float4 p4 = *reinterpret_cast<const float4*>(Ps + r * KT + k4);
+          const float p[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float4 v = *reinterpret_cast<const float4*>(E + (k4 + u) * pitch + c);
+            if (!whole) {
+              const bool seen = (vis >> (k4 + u)) & 1u;
+              v.x = seen ? v.x : 0.f; v.y = seen ? v.y : 0.f; v.z = seen ? v.z : 0.f; v.w = seen ? v.w : 0.f;
+            }
+            acc.x = fmaf(p[u], v.x, acc.x); acc.y = fmaf(p[u], v.y, acc.y);
+            acc.z = fmaf(p[u], v.z, acc.z); acc.w = fmaf(p[u], v.w, acc.w);
           }
         }
         o[k] = acc;
