@@ -13,7 +13,7 @@
 // no sort.  A cluster of up to 8 CTAs shares one sequence (their counts meet
 // through distributed shared memory, every CTA adding the same counts in rank
 // order).  4 bytes read per key and 4 written per kept one: the work is a chain
-// of latencies, not of bytes.
+// of latencies, not of bytes (64 sequences of 1-4 k keys 10.4 us, 2 of 131 k 24).
 //
 // Compaction.  Row d of the result is row src(d) >= d of the sequence (src
 // ascending).  A CTA moves a chunk of rows through registers: every load of
@@ -23,7 +23,8 @@
 // flags of the earlier chunks that read its destination.  Chunks are numbered
 // by a ticket taken when a CTA starts: whoever is waited for has started, and
 // loading waits for nobody, so every wait ends.  2 entry rows of traffic per
-// moved row: HBM bound.
+// moved row: HBM bound (64 sequences to 1024 entries of 1152 bytes, 151 MB: 31
+// us, 4.9 TB/s; 16 rows a CTA, 33 us with 32).
 #include "common.cuh"
 #include "tc_ptx.cuh"
 

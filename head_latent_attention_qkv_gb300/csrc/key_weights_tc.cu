@@ -21,8 +21,10 @@
 // keys of its warp for four columns (tree::key_bits) and the words are
 // broadcast.  A step of the issuing thread (a barrier, four MMAs, a commit)
 // takes about 530 cycles however few the columns, so blocks of at most 84 rows
-// bring Q in three chunks a slot (64 sequences x 32 rows x 1-4 k keys: 57.6 us
-// with one).  When the key tiles alone do not fill the GPU the rows are cut in
+// bring Q in three chunks a slot (64 sequences x 32 rows x 1-4 k keys: 53 us
+// against 57 with one, 43 with the items looked up by the key warp: 4.4 TB/s of
+// cache).  2048 rows x 8 k keys x 4 sequences: 67 us, the tensor pipe active half
+// of the cycles: Q's slots (80 KB in flight a CTA) turn over in 2.5 k cycles.  When the key tiles alone do not fill the GPU the rows are cut in
 // parts whose sums a second kernel adds in order.
 #include <math.h>
 
@@ -204,6 +206,7 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
           all = all && (word[q] == 0xffffffffu || c >= cols);
         }
         all = __all_sync(0xffffffffu, all);
+        __syncwarp();                                     // the walks may have parted the warp
         sum_sync();
         const int buf = tile & 1;
         wait_bar(B, &B->s_full[buf], (tile >> 1) & 1, R.status);

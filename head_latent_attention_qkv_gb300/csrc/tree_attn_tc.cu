@@ -9,9 +9,12 @@
 //  - tree_attn_pair_kernel, blocks of more than 128 rows: two row tiles and one
 //    value half; their MMAs run as one over the pair (cta_group::2), so each
 //    CTA fetches and reads half of the keys' and values' bytes (2560 cycles of
-//    shared-memory traffic a tile against 3328 of MMAs);
+//    shared-memory traffic a tile against 3328 of MMAs).  8192 rows x 6-8 k keys x
+//    4 sequences: 482 us, the tensor pipe active 79% of the cycles, 1.05 PFLOP/s
+//    on the algorithm's flops;
 //  - tree_attn_tc_kernel, blocks of at most 128 rows: one row tile, a CTA per
-//    value half (4224 cycles of shared-memory traffic a tile, the bound).
+//    value half (4224 cycles of shared-memory traffic a tile, the bound; 2.7 us a
+//    tile, 4.2 TB/s of cache over the GPU while it lasts).
 //
 // What a tile costs beyond its MMAs is hidden by running the scores one tile
 // ahead: the tensor pipe executes S(0), S(1), PV(0), S(2), PV(1), ..., and
@@ -22,7 +25,13 @@
 // L2.  Per tile the stream has four pairs of 64-dim key chunks, two pairs of
 // value chunks and the rope chunk.  Scores and P V are issued by two threads,
 // and each looks at its next barrier before it issues the MMAs of the one at
-// hand (a look takes about 340 cycles, the eight MMAs of a pair 512).
+// hand (a look takes 100 to 340 cycles, a commit 125, the eight MMAs of a pair
+// 512, so barriers are shared where the operands allow it).  P V(t) is held back
+// until S(t + 1) is in the pipe: it then fills the 1.1 k cycles until the softmax
+// has read S(t + 1), instead of delaying it (5.7 k -> 4.9 k cycles a tile).
+//
+// A cluster's fixed cost is about 13 us (set-up, Q and the first keys, the first
+// scores, the last P V, the join and the store), which is what small calls take.
 //
 // Softmax: warps 0-3 and 8-11, two threads a row (64 keys and 128 value
 // columns each) that exchange their half maxima; fp32, exp2 domain, O rescaled
@@ -930,15 +939,16 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict
 }  // namespace
 
 // Row tiles in pairs, parts of a unit's key range (a multiple of the parts of a
-// cluster).  Cost in tiles (2.6 us) of the waves of CTAs that a choice needs:
-// FIXED beyond a part's share of the keys, JOIN for a cluster's join, MERGE and
-// MERGE_PART for the second kernel.  Measured, us: 512 rows x 2064 keys x 8
-// sequences 51 whole, 43 in two parts merged, 41 in two joined; 8192 rows x
-// 6-8 k keys x 4 sequences 544, 605, 607; 128 rows x 32 k keys 70 in 16 parts, 41
-// in 48, 39 in 64.  Keys are bounded by the page table (shorter sequences only
-// split finer than they need) and, when windows are given, taken as at most 16
-// tiles, since the windows are on the device: 800 rows x 5 sequences with a
-// window of 512 keys 31 us whole, 45 in three parts.
+// cluster).  Cost in tiles (about 2.5 us) of the waves of CTAs that a choice
+// needs: FIXED beyond a part's share of the keys, JOIN for a cluster's join,
+// MERGE and MERGE_PART for the second kernel.  Measured, us: 512 rows x 2064
+// keys x 8 sequences 47 whole, 41 in two parts merged, 37 in two joined; 8192
+// rows x 6-8 k keys x 4 sequences 483, 538, 561; 128 rows x 32 k keys 47 in 32
+// parts, 41 in 48, 39 in 56 or 64, 40 in 60 joined by fours.  Keys are bounded by
+// the page table (shorter sequences only split finer than they need) and, when
+// windows are given, taken as at most 16 tiles, since the windows are on the
+// device: 800 rows x 5 sequences with a window of 512 keys 29 us whole, 41 in
+// three parts.
 struct Plan {
   bool pair;
   int parts, cluster_parts;
