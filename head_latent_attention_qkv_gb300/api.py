@@ -221,7 +221,7 @@ def mla_latent_attention_backward(h: Handle, q_abs, positions, cache, desc, o_la
 def _take(name, t, dtype, shape, h):
     """The pointer of `t`, checked: on the handle's device, contiguous, of this
     type and shape."""
-    if t.dtype is not dtype or t.get_device() != h.device_index or not t.is_contiguous() or t.shape != shape:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != h.device_index or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:"
                          f"{h.device_index}, got {t.dtype} {tuple(t.shape)} on {t.device}"
                          f"{'' if t.is_contiguous() else ', not contiguous'}")
@@ -268,12 +268,12 @@ def mla_tree_attention(h: Handle, q_abs, positions, cache, desc, parent, o_lat=N
     dt = torch.float16 if h.dims.dtype == "bf16" else torch.float32
     lse_p = None if lse is None else _take("lse", lse, torch.float32, (rows,), h)
     if o_lat is None:
-        o_lat = torch.empty((rows, rank), dtype=dt, device=cache.device)
+        o_lat = cache.new_empty((rows, rank), dtype=dt)
     out = _take("o_lat", o_lat, dt, (rows, rank), h)
     ref = C.byref(desc)
     if workspace is None:
         need = lib.mla_tree_attention_workspace_bytes(h.h, ref)
-        workspace = _buf(need, cache.device) if need else None
+        workspace = cache.new_empty((need,), dtype=torch.uint8) if need else None
     _run(lib.mla_tree_attention, h, q, pos, c, cache.shape[0], ref, par, out, lse_p,
          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     return o_lat
@@ -297,7 +297,7 @@ def mla_draft_forward_tree(h: Handle, hidden, positions, block_slot_mapping, cac
             _take("block_slot_mapping", block_slot_mapping, torch.int64, (M,), h), _take_cache(h, cache))
     par = _take("parent", parent, torch.int32, (M,), h)
     if out is None:
-        out = torch.empty((M, D), dtype=dt, device=cache.device)
+        out = cache.new_empty((M, D))
     ref = C.byref(desc)
     if workspace is None:
         workspace = _buf(lib.mla_forward_tree_workspace_bytes(h.h, ref), cache.device)
@@ -328,7 +328,7 @@ def mla_key_weights(h: Handle, q_abs, positions, cache, desc, lse, weights_out, 
     ref = C.byref(desc)
     if workspace is None:
         need = lib.mla_key_weights_workspace_bytes(h.h, ref, ldw)
-        workspace = _buf(need, cache.device) if need else None
+        workspace = cache.new_empty((need,), dtype=torch.uint8) if need else None
     _run(lib.mla_key_weights, h, q, pos, c, cache.shape[0], ref, par, lse_p, decay, prior_p, out, ldw,
          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     return weights_out
@@ -349,9 +349,9 @@ def mla_cache_select(h: Handle, weights, kv_len, budget: int, sink: int = 0, rec
     n = kv_len.shape[0]
     w, ldw = _take_rows("weights", weights, torch.float32, n, h)
     if keep is None:
-        keep = torch.empty((n, max(budget, 0)), dtype=torch.int32, device=weights.device)
+        keep = kv_len.new_empty((n, max(budget, 0)), dtype=torch.int32)
     if keep_len is None:
-        keep_len = torch.empty((n,), dtype=torch.int32, device=weights.device)
+        keep_len = kv_len.new_empty((n,), dtype=torch.int32)
     _run(lib.mla_cache_select, h, w, ldw, _take("kv_len", kv_len, torch.int32, (n,), h), n, budget, sink, recent,
          _take("keep", keep, torch.int32, (n, max(budget, 0)), h),
          _take("keep_len", keep_len, torch.int32, (n,), h))
