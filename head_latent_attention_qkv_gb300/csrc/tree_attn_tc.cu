@@ -239,6 +239,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
     if (sound && first_row) atomicMin(&B->z_lo, U.W > 0 ? max(0, min(pos[nd] - U.W + 1, U.ctx)) : 0);
   }
   mbar_arrive(&B->seen_full);
+  __syncwarp();
   for (int t = 0; t < U.nt; ++t) {
     const int jh = tile_key(U, t) + KH * kh;              // first key of this thread's half
     float s[KH];
@@ -318,7 +319,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   lsum += xm[(1 - kh) * QROWS + r];
   if (U.nt > 0) wait_bar(B, &B->o_done, (U.nt - 1) & 1, P.rule.status);
   tc_fence_after();
-  const bool any = ok && U.nt > 0 && lsum > 0.f;
+  const bool any = ok && U.nt > 0 && lsum != 0.f;         // (a NaN that a row sees reaches its output)
   const float inv = any ? 1.f / lsum : 0.f;
   float* prow = (float*)smem + r * STG_PITCH + 128 * kh;
 #pragma unroll 1
@@ -405,15 +406,15 @@ __device__ __forceinline__ void store_rows(const TreeParams& P, const uint8_t* s
       for (int i = 0; i < 8; ++i) v[i] = 0.f;
 #pragma unroll
       for (int s = 0; s < CS; ++s) {
-        const float w = mx == -INFINITY ? 0.f : exp2f(l[s] - mx);
+        const float w = l[s] == -INFINITY ? 0.f : exp2f(l[s] - mx);
         den += w;
         v[0] += w * a[s].x; v[1] += w * a[s].y; v[2] += w * a[s].z; v[3] += w * a[s].w;
         v[4] += w * c[s].x; v[5] += w * c[s].y; v[6] += w * c[s].z; v[7] += w * c[s].w;
       }
-      const float inv = den > 0.f ? 1.f / den : 0.f;
+      const float inv = den != 0.f ? 1.f / den : 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= inv;
-      l2 = den > 0.f ? mx + log2f(den) : -INFINITY;
+      l2 = den != 0.f ? mx + log2f(den) : -INFINITY;
     }
     const long row = U.row0 + r;
     const int parts = gridDim.y / CS;
@@ -906,8 +907,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict
     mx = fmaxf(l0, l1);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    w0 = mx == -INFINITY ? 0.f : exp2f(l0 - mx);
-    w1 = mx == -INFINITY ? 0.f : exp2f(l1 - mx);
+    w0 = l0 == -INFINITY ? 0.f : exp2f(l0 - mx);
+    w1 = l1 == -INFINITY ? 0.f : exp2f(l1 - mx);
     den = w0 + w1;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
@@ -930,10 +931,10 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict
     }
   }
   if (!live) return;
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float inv = den != 0.f ? 1.f / den : 0.f;
   __half2 h2[2] = {__floats2half2_rn(acc.x * inv, acc.y * inv), __floats2half2_rn(acc.z * inv, acc.w * inv)};
   *reinterpret_cast<uint2*>(o_lat + row * 512 + quarter * 128 + 4 * lane) = *reinterpret_cast<uint2*>(h2);
-  if (lse && lane == 0 && quarter == 0) lse[row] = den > 0.f ? (mx + log2f(den)) * kLn2 : -INFINITY;
+  if (lse && lane == 0 && quarter == 0) lse[row] = den != 0.f ? (mx + log2f(den)) * kLn2 : -INFINITY;
 }
 
 }  // namespace
@@ -998,7 +999,7 @@ mla_status_t tree_attention(cudaStream_t st, mla_handle* h, const tree::Rule& r,
   P.seg_rows = r.page_size < max_seg ? r.page_size : max_seg;
   if (!make_tmap_chunked(&P.tmQ, false, q_abs, rows, l.L, l.L, QROWS, NQS) ||
       !make_tmap_chunked(&P.tmQ01, false, q_abs, rows, l.L, l.L, QROWS, NQT) ||
-      !make_tmap_chunked(&P.tmC, false, cache, slots, l.L, l.L, KT, 2) ||
+      (!plan.pair && !make_tmap_chunked(&P.tmC, false, cache, slots, l.L, l.L, KT, 2)) ||
       !make_tmap_2d(&P.tmK, false, cache, slots, l.L, l.L, P.seg_rows))
     return fail(MLA_ERR_CUDA, "tree attention: cuTensorMapEncodeTiled failed");
   P.rule = r;

@@ -198,16 +198,17 @@ tree_attn_kernel(const tree::Rule a, const float* __restrict__ q_abs, const floa
   }
   copy_wait<0>();
   if (live) {
-    const float inv = lrow > 0.f ? 1.f / lrow : 0.f;
+    const bool any = lrow != 0.f;                // (a NaN that a row sees reaches its output)
+    const float inv = 1.f / lrow;
 #pragma unroll
     for (int k = 0; k < MAX_OUT; ++k) {
       const int c = 4 * c0 + 64 * k;
       if (k < nout && c < rkv)
         *reinterpret_cast<float4*>(o_lat + row * rkv + c) =
-            lrow > 0.f ? make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+            any ? make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv)
+                : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    if (lse && c0 == 0) lse[row] = lrow > 0.f ? mrow + logf(lrow) : -INFINITY;
+    if (lse && c0 == 0) lse[row] = any ? mrow + logf(lrow) : -INFINITY;
     if (vis_stats && (r0 + r) % a.H == 0 && c0 == 0) {
       vis_stats[m * 3 + 0] = cnt;
       vis_stats[m * 3 + 1] = first;

@@ -11,7 +11,7 @@ namespace tc {
 struct TreeParams {
   CUtensorMap tmQ;    // Q_abs bf16 [rows, 576], chunked view, box 128 rows x 7 chunks
   CUtensorMap tmQ01;  // the same, box 128 rows x 2 chunks
-  CUtensorMap tmC;    // the cache, chunked view, box 128 rows x 2 chunks
+  CUtensorMap tmC;    // the cache, chunked view, box 128 rows x 2 chunks (not for pairs)
   CUtensorMap tmK;    // the cache, box 64 dims x seg_rows
   tree::Rule rule;
   __half* o_lat;      // [rows, 512]

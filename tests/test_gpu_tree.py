@@ -215,6 +215,24 @@ def test_deep_trees(dtype, heads, T, window):
     c.weights()
 
 
+@pytest.mark.parametrize("dtype,heads,ctx", [("fp32", 4, [60, 20]), ("bf16", 16, [60, 20]), ("bf16", 16, [4000, 20]),
+                                             ("bf16", 2, [3000, 20])])
+def test_a_nan_that_a_row_sees_reaches_its_output(dtype, heads, ctx):
+    from head_latent_attention_qkv_gb300 import api
+    c = Case(dtype, heads, 16, ctx, 9)
+    c.paged.set_nan(0, torch.tensor([ctx[0] // 2]))
+    o, lse = c.attention()
+    torch.cuda.synchronize()
+    rows = 9 * heads
+    assert torch.isnan(o[:rows]).all() and torch.isnan(lse[:rows]).all()
+    assert torch.isfinite(o[rows:]).all() and torch.isfinite(lse[rows:]).all()
+    w = torch.zeros(2, max(c.kv), device="cuda")
+    api.mla_key_weights(c.h, c.q, c.positions, c.paged.cache, c.desc, torch.zeros_like(lse), w, parent=c.parent)
+    bad = torch.isnan(w)
+    assert bad[0, ctx[0] // 2] and bad.sum() == 1
+    assert api.mla_get_device_status(c.h) == 0
+
+
 def test_many_blocks():
     ctx = [(37 * b) % 300 for b in range(75)]
     c = Case("bf16", 4, 16, ctx, 3, padded=True)
