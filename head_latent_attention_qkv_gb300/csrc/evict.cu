@@ -254,7 +254,7 @@ int select_cluster(long ldw) { return ldw <= 8192 ? 1 : ldw <= 16384 ? 2 : ldw <
 // Compaction
 // ---------------------------------------------------------------------------
 constexpr int MV_THREADS = 128, MV_UPT = 9;              // units a thread holds
-constexpr int MV_UNITS = MV_THREADS * MV_UPT;            // 2304: 32 rows of 576 bf16
+constexpr int MV_UNITS = MV_THREADS * MV_UPT;            // 1152: 16 rows of 576 bf16
 constexpr int MV_MAX_ROWS = 128;
 constexpr int ZERO_ROWS = 4096;                          // weights a tail chunk clears
 constexpr uint32_t FLAG_BUDGET = 1u << 24;
@@ -269,7 +269,7 @@ struct CompactArgs {
   int units, rows;            // 16- or 4-byte units of an entry; rows of a chunk
   int data_chunks, chunks;    // per sequence: chunks that may move rows; with those that clear weights
   int in_place;
-  int* ticket;                // [1 + num_seqs * data_chunks] zeroed, or NULL: no chunk waits
+  int* ticket;                // [1 + num_seqs * data_chunks] zeroed, or NULL: no chunk waits for another
   uint32_t* status;
 };
 
@@ -399,6 +399,8 @@ __global__ void __launch_bounds__(MV_THREADS) compact_kernel(const CompactArgs a
     }
     __syncthreads();
     if (!s_ok) return;
+  } else {
+    __syncthreads();                                     // in place: a row stored may be another thread's source
   }
   if (!data) {
     for (int i = tid; i < wn; i += MV_THREADS) a.weights_out[(long)seq * a.ldw + w0 + i] = 0.f;

@@ -141,6 +141,15 @@ def test_compact(dtype, page, in_place):
     run_compact(dtype, page, lens, keeps, in_place=in_place, weights=False, ldk=1003)
 
 
+@pytest.mark.parametrize("dtype,rows", [("bf16", 16), ("fp32", 16)])
+def test_compact_of_one_chunk_a_sequence_in_place(dtype, rows):
+    # no other chunk to wait for, yet every row stored is the source of the row before it
+    n = 608
+    for seed in range(4):
+        run_compact(dtype, 16, [rows] * n, [list(range(1 + (b + seed) % 3, rows)) for b in range(n)], weights=False,
+                    seed=seed)
+
+
 @pytest.mark.parametrize("in_place", [True, False])
 def test_compact_of_an_accepted_path(in_place):
     # the context stays; of 16 drafted nodes the accepted path moves up behind it
