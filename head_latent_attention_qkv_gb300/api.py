@@ -237,6 +237,14 @@ def _take_rows(name, t, dtype, n, h):
     return _take(name, t, dtype, (n, t.shape[-1]), h), t.shape[-1]
 
 
+def _take_workspace(workspace, h):
+    """The pointer and the bytes of a workspace, None for none."""
+    if workspace is None:
+        return None, 0
+    return (_take("workspace", workspace, workspace.dtype, workspace.shape, h),
+            workspace.numel() * workspace.element_size())
+
+
 def _run(fn, h: Handle, *args):
     """The entry point `fn` on the current stream (a caller's stream argument is
     made the current one, so that what the call allocates belongs to it)."""
@@ -275,7 +283,7 @@ def mla_tree_attention(h: Handle, q_abs, positions, cache, desc, parent, o_lat=N
         need = lib.mla_tree_attention_workspace_bytes(h.h, ref)
         workspace = cache.new_empty((need,), dtype=torch.uint8) if need else None
     _run(lib.mla_tree_attention, h, q, pos, c, cache.shape[0], ref, par, out, lse_p,
-         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
+         *_take_workspace(workspace, h))
     return o_lat
 
 
@@ -302,7 +310,7 @@ def mla_draft_forward_tree(h: Handle, hidden, positions, block_slot_mapping, cac
     if workspace is None:
         workspace = _buf(lib.mla_forward_tree_workspace_bytes(h.h, ref), cache.device)
     _run(lib.mla_draft_forward_tree, h, *args, cache.shape[0], ref, par, _take("out", out, dt, (M, D), h),
-         workspace.data_ptr(), workspace.numel())
+         *_take_workspace(workspace, h))
     return out
 
 
@@ -330,7 +338,7 @@ def mla_key_weights(h: Handle, q_abs, positions, cache, desc, lse, weights_out, 
         need = lib.mla_key_weights_workspace_bytes(h.h, ref, ldw)
         workspace = cache.new_empty((need,), dtype=torch.uint8) if need else None
     _run(lib.mla_key_weights, h, q, pos, c, cache.shape[0], ref, par, lse_p, decay, prior_p, out, ldw,
-         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
+         *_take_workspace(workspace, h))
     return weights_out
 
 
@@ -383,8 +391,7 @@ def mla_cache_compact(h: Handle, cache, block_table, kv_len, keep, keep_len, fir
             None if weights_out is None else _take("weights_out", weights_out, torch.float32, (n, ldw), h), ldw)
     if workspace is None and in_place:
         workspace = _buf(lib.mla_cache_compact_workspace_bytes(h.h, n, ldk), cache.device)
-    _run(lib.mla_cache_compact, h, *args, None if workspace is None else workspace.data_ptr(),
-         0 if workspace is None else workspace.numel())
+    _run(lib.mla_cache_compact, h, *args, *_take_workspace(workspace, h))
 
 
 def mla_cache_compact_workspace_bytes(h: Handle, num_seqs: int, ldk: int) -> int:

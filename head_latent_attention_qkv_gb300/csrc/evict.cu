@@ -308,15 +308,15 @@ __global__ void __launch_bounds__(MV_THREADS) compact_kernel(const CompactArgs a
   const int seq = s_ticket / a.chunks, c = s_ticket % a.chunks;
   const long row_cap = a.weights_out ? a.ldw : 0x7fffffffL;
   const int cap = (int)min((long)a.max_pages * a.page_size, row_cap);
-  int n = a.kv_len[seq];
+  const int n = a.kv_len[seq];
   if (n < 0 || n > cap) {
     if (tid == 0 && c == 0) set_status(a.status, MLA_DEV_BAD_LENGTH);
-    n = max(0, min(n, cap));
+    return;                                              // the sequence is left as it was
   }
   const int first = a.first ? a.first[seq] : 0, nk = a.keep_len[seq];
   if (first < 0 || first > n || nk < 0 || nk > a.ldk || nk > n - first) {
     if (tid == 0 && c == 0) set_status(a.status, MLA_DEV_BAD_KEEP);
-    return;                                              // the sequence is left as it was
+    return;                                              // as above
   }
   const int total = first + nk;
   const int base = a.in_place ? first : 0;               // rows before it are where they belong

@@ -408,7 +408,8 @@ mla_status_t mla_latent_attention_backward(mla_handle_t *h, const void *q_abs,
  * block; T = 1 is the one-token decode.  At most 1024 nodes a block
  * (MLA_ERR_UNSUPPORTED beyond).  Entries of the context that a window leaves
  * to some rows only, and of the tree's nodes, must be finite; entries that no
- * row sees may hold anything. */
+ * row sees may hold anything; a NaN that every row sees makes o_lat and lse
+ * NaN. */
 
 /* Latent attention of trees: mla_latent_attention with the visibility above
  * (same q_abs, cache, desc, o_lat, lse; vis_stats counts what a node sees).
@@ -442,9 +443,10 @@ mla_status_t mla_draft_forward_tree(mla_handle_t *h, const void *hidden,
  * (other elements are left as they are).  parent: the tree's (NULL: the rule
  * of mla_attn_desc_t).  lse: device fp32 [nb*T, H], mla_tree_attention's or
  * mla_latent_attention's for the same rows; a row with lse = -inf (so those
- * that see no key, nodes outside the tree among them) adds nothing.  prior, weights_out: device fp32 [num_blocks, ldw], the same
- * pointer or disjoint; prior may be NULL (nothing before).  ldw < kv_len is
- * reported as MLA_DEV_BAD_LENGTH and the keys behind it are left out.  Each
+ * that see no key, nodes outside the tree among them) adds nothing.  prior,
+ * weights_out: device fp32 [num_blocks, ldw], the same pointer or disjoint;
+ * prior may be NULL (nothing before).  ldw < kv_len is reported as
+ * MLA_DEV_BAD_LENGTH and the keys behind it are left out.  Each
  * key's sum is taken in one fixed order: equal calls give equal bits.
  * vis_stats of desc is not written.  q_abs and cache 16-byte aligned.
  * workspace: mla_key_weights_workspace_bytes() bytes, 256-byte aligned (NULL
@@ -480,8 +482,9 @@ mla_status_t mla_cache_select(mla_handle_t *h, const float *weights, int64_t ldw
  * position, so positions go on counting tokens while logical indices move
  * up.  A sliding window counts logical indices of the context: after an
  * eviction use window 0.
- *   dst_block_table NULL: in place.  No page may belong to two sequences of
- * the call (or twice to one).  Else the rows go to the pages of
+ *   dst_block_table NULL: in place.  No page that holds a row from first[b] on
+ * may belong to two sequences of the call (or twice to one); pages wholly
+ * before first[b], a shared prompt's, are neither read nor written.  Else the rows go to the pages of
  * dst_block_table [num_seqs, dst_max_pages], none of which is read by the call
  * and none named twice.
  *   weights, weights_out: NULL, or device fp32 [num_seqs, ldw], moved the same

@@ -188,6 +188,62 @@ def test_compact_reports_lists_that_do_not_fit():
             assert torch.equal(flat[s], old[s])                 # the sequence is left alone
 
 
+@pytest.mark.parametrize("kv", [100, -1, 41])
+def test_compact_leaves_a_sequence_of_a_bad_length_alone(kv):
+    # behind the page table, negative, behind the rows of weights
+    from head_latent_attention_qkv_gb300 import _lib, api
+    from tests.tree_cases import Paged, i32
+    h = handle("bf16", 16)
+    p = Paged(np.random.default_rng(0), h.dims, 16, [40, 40])
+    before = p.cache.view(torch.int16).clone()
+    w = torch.rand(2, 40, device="cuda")
+    w0 = w.clone()
+    api.mla_cache_compact(h, p.cache, i32(p.table), i32([kv, 40]), i32([[1, 2, 3], [0, 1, 2]]), i32([3, 3]), weights=w)
+    assert api.mla_get_device_status(h) == _lib.MLA_DEV_BAD_LENGTH
+    assert torch.equal(p.cache.view(torch.int16), before) and torch.equal(w[0], w0[0])
+    assert torch.equal(w[1, :3], w0[1, :3]) and not w[1, 3:].any()
+
+
+def test_compact_in_place_of_sequences_that_share_a_prompt():
+    from head_latent_attention_qkv_gb300 import api
+    from tests.tree_cases import Paged, i32
+    h = handle("bf16", 16)
+    rng = np.random.default_rng(6)
+    p = Paged(rng, h.dims, 16, [100, 120, 64])
+    p.table[1:, :4] = p.table[0, :4]                        # 64 keys of a shared prompt
+    first = [64, 70, 64]
+    keeps = [pick(rng, 100, 9, 64), pick(rng, 120, 20, 70), []]
+    keep = np.full((3, 20), -1, dtype=np.int32)
+    for b, k in enumerate(keeps):
+        keep[b, :len(k)] = k
+    want = p.cache.view(-1, 576).clone()
+    for b, k in enumerate(keeps):
+        s = p.slots(b, p.lens[b])
+        want[s[first[b]:first[b] + len(k)].cuda()] = p.cache.view(-1, 576)[s[k].cuda()]
+    api.mla_cache_compact(h, p.cache, i32(p.table), i32(p.lens), i32(keep), i32([len(k) for k in keeps]),
+                          first=i32(first))
+    assert api.mla_get_device_status(h) == 0
+    assert torch.equal(p.cache.view(-1, 576).view(torch.int16), want.view(torch.int16))
+
+
+def test_compact_takes_any_workspace_that_is_large_enough():
+    from head_latent_attention_qkv_gb300 import _lib, api
+    from tests.tree_cases import Paged, i32
+    h = handle("bf16", 16)
+    p = Paged(np.random.default_rng(0), h.dims, 16, [400])
+    args = (p.cache, i32(p.table), i32([400]), i32([list(range(0, 400, 2))]), i32([200]))
+    need = api.mla_cache_compact_workspace_bytes(h, 1, 200)
+    for bad in (torch.empty(need, dtype=torch.uint8), torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            api.mla_cache_compact(h, *args, workspace=bad)
+    with pytest.raises(_lib.MLAError):
+        api.mla_cache_compact(h, *args, workspace=torch.empty(need // 8 - 1, dtype=torch.int64, device="cuda"))
+    want = p.cache.view(-1, 576)[p.slots(0, 400)[::2].cuda()].clone()
+    api.mla_cache_compact(h, *args, workspace=torch.empty(need // 8, dtype=torch.int64, device="cuda"))
+    assert api.mla_get_device_status(h) == 0
+    assert torch.equal(p.cache.view(-1, 576)[p.slots(0, 200).cuda()], want)
+
+
 def test_compact_behind_four_gigabytes():
     from head_latent_attention_qkv_gb300 import api
     from tests.tree_cases import Paged, i32
