@@ -663,10 +663,10 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
       for (int t = 0; t < U.nt && ok; ++t) {
         int s = first_value_use(t, U.nt) % SLOTS;
         const bool dirty = dirty_tile(U, z_lo, t);
-        behind_scores(B, min(t + 2, U.nt));
         if (!(ok = wait_bar(B, &B->p_full, t & 1, R.status))) break;
         tc_fence_after();
-        bool ready = false;
+        bool ready = mbar_test_wait(&B->v_full[s], (par >> s) & 1);
+        behind_scores(B, min(t + 2, U.nt));
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           if (dirty) {
@@ -852,11 +852,11 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
       const int z_lo = B->z_lo;
       for (int t = 0; t < U.nt && ok; ++t) {
         const bool dirty = dirty_tile(U, z_lo, t);
-        behind_scores(B, min(t + 2, U.nt));
-        if (!(ok = wait_bar(B, &B->p_full, t & 1, R.status))) break;
-        tc_fence_after();
         uint64_t* bar = dirty ? &B->clean[0] : &B->v_full[0];     // (both CTAs have cleared their halves)
         if (!(ok = wait_bar(B, bar, (dirty ? nd : nf) & 1, R.status))) break;
+        if (!(ok = wait_bar(B, &B->p_full, t & 1, R.status))) break;
+        tc_fence_after();
+        behind_scores(B, min(t + 2, U.nt));
 #pragma unroll
         for (int i = 0; i < PV; ++i)
 #pragma unroll
