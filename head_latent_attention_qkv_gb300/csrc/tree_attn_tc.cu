@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
     // every copy of the pair has landed before its shared memory is used again
     if (p == 0 && ok && t > 0) mbar_wait(&B->k_full[w], (t - 1) & 1, R.status);
   } else if (warp == W_RING + 2) {
-    // ---- values: chunk 2 i + p of this half for both pairs ----
+    // ---- values: chunks 2 p and 2 p + 1 of this half ----
     bool ok = U.nt > 0 && wait_bar(B, &B->q01_read, 0, R.status);   // Q passes through the slots first
     int z_lo = -1;                                        // known from seen_full on
     uint32_t nd = 0;                                      // tiles cleared so far
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
       if (lane < nvseg)
         for (int i = 0; i < PV; ++i)
           tma_load_3d_pair(smem + OFF_PV + i * PSLOT_BYTES + lane * seg * 128, &P.tmK, bar,
-                           (4 * U.half + 2 * i + p) * 64, y, 0);
+                           (4 * U.half + 2 * p + i) * 64, y, 0);
       __syncwarp();
       if (dirty) {
         know_seen();
@@ -844,8 +844,8 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
   } else if (warp == W_PV) {
     if (p == 0 && lane == 0 && U.nt > 0) {
       // ---- O += P(t) V(t) of both row tiles ----
-      const uint32_t idesc = idesc_f16_bmn(2 * QROWS, 128, false), tO = tmem + TM_O, tP = tmem + TM_P;
-      constexpr uint64_t U_SLOT = PSLOT_BYTES / 16, U_KSTEP = 16 * 128 / 16;
+      const uint32_t idesc = idesc_f16_bmn(2 * QROWS, 256, false), tO = tmem + TM_O, tP = tmem + TM_P;
+      constexpr uint64_t U_KSTEP = 16 * 128 / 16;
       const uint64_t dV = smem_desc_sw128_mn(smem + OFF_PV, CH_BYTES);
       uint32_t nd = 0, nf = 0;                            // tiles cleared / not cleared so far
       bool ok = wait_bar(B, &B->seen_full, 0, R.status);
@@ -858,10 +858,8 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
         tc_fence_after();
         behind_scores(B, min(t + 2, U.nt));
 #pragma unroll
-        for (int i = 0; i < PV; ++i)
-#pragma unroll
-          for (int k = 0; k < KT / 16; ++k)
-            mma_f16_ts_pair(tO + 128 * i, tP + 8 * k, dV + i * U_SLOT + U_KSTEP * k, idesc, (t | k) ? 1u : 0u);
+        for (int k = 0; k < KT / 16; ++k)
+          mma_f16_ts_pair(tO, tP + 8 * k, dV + U_KSTEP * k, idesc, (t | k) ? 1u : 0u);
         mma_commit_pair(&B->o_done, both);
         if (dirty) ++nd; else ++nf;
       }
