@@ -10,8 +10,7 @@
 //    value half; their MMAs run as one over the pair (cta_group::2), so each
 //    CTA fetches and reads half of the keys' and values' bytes (2560 cycles of
 //    shared-memory traffic a tile against 3328 of MMAs).  8192 rows x 6-8 k keys x
-//    4 sequences: 482 us, the tensor pipe active 79% of the cycles, 1.05 PFLOP/s
-//    on the algorithm's flops;
+//    4 sequences: 434 us, 1.17 PFLOP/s on the algorithm's flops;
 //  - tree_attn_tc_kernel, blocks of at most 128 rows: one row tile, a CTA per
 //    value half (4224 cycles of shared-memory traffic a tile, the bound; 2.7 us a
 //    tile, 4.2 TB/s of cache over the GPU while it lasts).
@@ -525,7 +524,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
   Bars* B = (Bars*)(smem + OFF_BAR);
   const tree::Rule& R = P.rule;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int unit = blockIdx.x >> 1;
+  const int unit = (int)(blockIdx.x >> 1) + P.group0;
   Unit U;
   U.half = blockIdx.x & 1;
   U.tiles = 1;
@@ -536,7 +535,9 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
   U.row0 = ((long)U.b * R.T) * R.H + (long)U.qt * QROWS;
   if (warp == W_ROPE && lane == 0) { prefetch_tmap(&P.tmQ01); prefetch_tmap(&P.tmK); prefetch_tmap(&P.tmC); prefetch_tmap(&P.tmQ); }
   if (warp == W_S) tmem_alloc(&B->tmem_slot, TMEM_COLS);
-  pdl_wait();                  // Q_abs and the nodes' own entries come from the kernels before
+  // Q_abs and the nodes' own entries come from the kernels before; a launch of the
+  // rest starts after every CTA of the first has seen their end
+  if (!P.rest) pdl_wait();
   set_up(P, B, smem, U);
   const uint32_t tmem = B->tmem_slot;
   const int seg = P.seg_rows, nseg = KT / seg;
@@ -700,6 +701,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
   join_and_store(P, smem, U);
   if (warp == W_S) tmem_dealloc(tmem, TMEM_COLS);
   if (P.cluster_parts > 1) cluster_sync_all();            // nobody leaves while its rows may be read
+  if (P.rest) pdl_wait();
 }
 
 __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid_constant__ TreeParams P) {
@@ -708,10 +710,11 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
   Bars* B = (Bars*)(smem + OFF_BAR);
   const tree::Rule& R = P.rule;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int unit = blockIdx.x >> 2, p = blockIdx.x & 1, units = (P.tiles_per_block + 1) / 2;
+  const int group = (int)(blockIdx.x >> 1) + P.group0, unit = group >> 1, p = blockIdx.x & 1;
+  const int units = (P.tiles_per_block + 1) / 2;
   const uint32_t rank = cluster_ctarank();
   Unit U;
-  U.half = (blockIdx.x >> 1) & 1;
+  U.half = group & 1;
   U.tiles = 2;
   U.lead = rank & ~1u;
   U.first = U.half == 0 && blockIdx.y == 0;
@@ -720,7 +723,9 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
   U.row0 = ((long)U.b * R.T) * R.H + (long)U.qt * QROWS;
   if (warp == W_ROPE && lane == 0) { prefetch_tmap(&P.tmQ01); prefetch_tmap(&P.tmK); prefetch_tmap(&P.tmQ); }
   if (warp == W_S) tmem_alloc_pair(&B->tmem_slot, TMEM_COLS);
-  pdl_wait();                  // Q_abs and the nodes' own entries come from the kernels before
+  // Q_abs and the nodes' own entries come from the kernels before; a launch of the
+  // rest starts after every CTA of the first has seen their end
+  if (!P.rest) pdl_wait();
   set_up(P, B, smem, U);
   const uint32_t tmem = B->tmem_slot, both = 3u << U.lead;
   // segments: rows of a page, at most this CTA's 64 keys of a tile
@@ -877,6 +882,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
   cluster_sync_all();          // nobody leaves while its rows, or its half of an MMA, may be read
   tc_fence_after();
   if (warp == W_S) tmem_dealloc_pair(tmem, TMEM_COLS);
+  if (P.rest) pdl_wait();
 }
 
 // A row and quarter of its dims: sum_s w_s o_s / sum_s w_s with w_s = 2^(lse_s -
@@ -948,30 +954,48 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict
 // windows are given, taken as at most 16 tiles, since the windows are on the
 // device: 800 rows x 5 sequences with a window of 512 keys 29 us whole, 41 in
 // three parts.
+//
+// Clusters of whole units that do not fill their last wave have that wave's
+// units cut in parts of a second launch, joined in clusters: 256 clusters, of
+// which the GPU holds 76, 434 us in two launches (28 of them in two parts), 466 in
+// one.
 struct Plan {
   bool pair;
   int parts, cluster_parts;
+  long groups, rest;       // clusters of one part; those of them in the second launch
+  int rest_parts;          // their parts
 };
 Plan tree_plan(const mla_handle* h, const mla_attn_desc_t& d) {
   constexpr double FIXED = 4.0, JOIN = 2.8, MERGE = 3.5, MERGE_PART = 0.05;
   const long rows = (long)d.block_len * h->lay.H, tpb = (rows + QROWS - 1) / QROWS;
   long tiles = ((long)d.max_pages * h->cfg.page_size + KT - 1) / KT;
   if (d.window && tiles > 16) tiles = 16;
-  Plan best{tpb > 1, 1, 1};
-  const long groups = (long)d.num_blocks * (best.pair ? 2 * ((tpb + 1) / 2) : tpb);   // clusters of one part
+  Plan best{tpb > 1, 1, 1, 0, 0, 1};
+  const long groups = best.groups = (long)d.num_blocks * (best.pair ? 2 * ((tpb + 1) / 2) : tpb);
+  // clusters of 2 cs CTAs that the GPU holds at once (GPCs are not a multiple of 8)
+  auto held = [&](int cs) -> long {
+    const long n = cs == 1 ? h->num_sms / 2 : cs == 2 ? h->num_sms / 4 - 2 : h->num_sms / 8 - 4;
+    return n > 0 ? n : 1;
+  };
   double cost = 1e300;
   for (int cs = 1; cs <= 4; cs *= 2) {
-    // clusters of 2 cs CTAs that the GPU holds at once (GPCs are not a multiple of 8)
-    const long hold = cs == 1 ? h->num_sms / 2 : cs == 2 ? h->num_sms / 4 - 2 : h->num_sms / 8 - 4;
+    const long hold = held(cs);
     for (const int g : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 40, 48, 56, MAX_PARTS}) {
       if ((long)g * cs > (tiles > cs ? tiles : cs)) break;
-      const double waves = (double)((groups * g + hold - 1) / (hold > 0 ? hold : 1));
+      const double waves = (double)((groups * g + hold - 1) / hold);
       const double c = waves * (FIXED + (cs > 1 ? JOIN : 0.0) + (double)((tiles + g * cs - 1) / (g * cs))) +
                        (g > 1 ? MERGE + MERGE_PART * groups * g : 0.0);
       if (c < cost) { cost = c; best.parts = g * cs; best.cluster_parts = cs; }
       if (groups * g > 8 * hold) break;
     }
   }
+  const long rest = groups % held(1);
+  if (best.parts == 1 && rest && groups > rest)
+    for (int cs = 2; cs <= 4 && cs <= tiles; cs *= 2) {
+      const double c = (double)(groups / held(1)) * (FIXED + (double)tiles) +
+                       (double)((rest + held(cs) - 1) / held(cs)) * (FIXED + JOIN + (double)((tiles + cs - 1) / cs));
+      if (c < cost) { cost = c; best.rest = rest; best.rest_parts = cs; }
+    }
   return best;
 }
 
@@ -1010,18 +1034,28 @@ mla_status_t tree_attention(cudaStream_t st, mla_handle* h, const tree::Rule& r,
   P.part_lse = parts > 1 ? (float*)((char*)ws + align256((size_t)parts * rows * 512 * 4)) : nullptr;
   P.tiles_per_block = (int)(((long)d.block_len * l.H + QROWS - 1) / QROWS);
   P.scale_log2 = h->scale * 1.4426950408889634f;
-  const long ctas = 2L * d.num_blocks * (plan.pair ? 2 * ((P.tiles_per_block + 1) / 2) : P.tiles_per_block);
-  if (ctas > 0x7fffffffL) return fail(MLA_ERR_INVALID_ARG, "tree attention: too many rows");
+  if (2 * plan.groups > 0x7fffffffL) return fail(MLA_ERR_INVALID_ARG, "tree attention: too many rows");
   static std::once_flag once;
   std::call_once(once, [] {
     cudaFuncSetAttribute(tree_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     cudaFuncSetAttribute(tree_attn_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   });
-  Launch L(dim3((unsigned)ctas, (unsigned)plan.parts), dim3(THREADS), SMEM_BYTES, st, pdl,
-           dim3(2, (unsigned)plan.cluster_parts, 1));
-  cudaError_t e = cudaLaunchKernelEx(&L.cfg, plan.pair ? tree_attn_pair_kernel : tree_attn_tc_kernel, P);
+  auto launch = [&](long groups, int key_parts, bool dependent) {
+    Launch L(dim3((unsigned)(2 * groups), (unsigned)key_parts), dim3(THREADS), SMEM_BYTES, st, dependent,
+             dim3(2, (unsigned)P.cluster_parts, 1));
+    h->launches += 1;
+    return cudaLaunchKernelEx(&L.cfg, plan.pair ? tree_attn_pair_kernel : tree_attn_tc_kernel, P);
+  };
+  P.group0 = 0;
+  P.rest = 0;
+  cudaError_t e = launch(plan.groups - plan.rest, plan.parts, pdl);
+  if (e == cudaSuccess && plan.rest) {
+    P.group0 = (int)(plan.groups - plan.rest);
+    P.rest = 1;
+    P.cluster_parts = plan.rest_parts;
+    e = launch(plan.rest, plan.rest_parts, true);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
-  h->launches += 1;
   if (parts > 1) {
     const int wpi = parts > 8 ? 8 : 1;
     const long blocks = (rows * 4 * wpi + 7) / 8;

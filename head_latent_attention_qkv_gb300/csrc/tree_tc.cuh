@@ -21,6 +21,7 @@ struct TreeParams {
   float* part_lse;    // [parts, rows] log2-sum-exp
   long rows;
   int cluster_parts;  // parts of a key range that share a cluster: 1, 2, 4
+  int group0, rest;   // first cluster's number; whether this is the launch of the last wave's units
   int seg_rows, tiles_per_block;
   float scale_log2;
 };

@@ -240,6 +240,25 @@ def test_many_blocks():
     c.weights()
 
 
+@pytest.mark.parametrize("heads,T,n,window", [(16, 9, 40, 0), (4, 5, 83, 0), (16, 9, 79, 700)])
+def test_blocks_of_a_last_wave_cut_in_parts(heads, T, n, window):
+    # more clusters than the GPU holds: the last wave's are a launch of their own
+    ctx = [2000 - 61 * (b % 29) - (1900 if b % 13 == 5 else 0) for b in range(n)]
+    from head_latent_attention_qkv_gb300 import api
+    c = Case("bf16", heads, 16, [max(x, 0) for x in ctx], T, padded=True, window=window)
+    before = api.mla_kernel_launches(c.h)
+    c.check_attention(*c.attention())
+    assert api.mla_kernel_launches(c.h) == before + 2
+    g = torch.cuda.CUDAGraph()
+    want = c.attention()
+    with torch.cuda.graph(g):
+        got = c.attention()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_pages_behind_four_gigabytes():
     c = Case("bf16", 16, 64, [300, 77], 6, far=61000)           # 4.5 GB of pages before them
     c.check_attention(*c.attention())
