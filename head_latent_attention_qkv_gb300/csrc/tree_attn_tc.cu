@@ -370,8 +370,8 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
 }
 
 // The staged rows of the cluster's parts, joined and written whole: part y of
-// the cluster takes rows [128 y / CS, 128 (y + 1) / CS), a warp per row, 8 dims
-// a lane, parts in order; a row that no part saw is zero.
+// the cluster takes rows [128 y / CS, 128 (y + 1) / CS), a warp per row, 4 and
+// 4 dims a lane (no bank conflicts), parts in order; a row that no part saw is zero.
 template <int CS>
 __device__ __forceinline__ void store_rows(const TreeParams& P, const uint8_t* smem, const Unit& U) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -384,15 +384,15 @@ __device__ __forceinline__ void store_rows(const TreeParams& P, const uint8_t* s
     float4 a[CS], c[CS];
 #pragma unroll
     for (int s = 0; s < CS; ++s) {
-      const uint32_t rank = (uint32_t)(x + 2 * s), at = stg + (uint32_t)(r * STG_PITCH + 8 * lane) * 4;
+      const uint32_t rank = (uint32_t)(x + 2 * s), at = stg + (uint32_t)(r * STG_PITCH + 4 * lane) * 4;
       if (CS == 1 || s == y) {                            // this CTA's own
         l[s] = ((const float*)(smem + OFF_STG_LSE))[r];
-        a[s] = *(const float4*)((const float*)smem + r * STG_PITCH + 8 * lane);
-        c[s] = *(const float4*)((const float*)smem + r * STG_PITCH + 8 * lane + 4);
+        a[s] = *(const float4*)((const float*)smem + r * STG_PITCH + 4 * lane);
+        c[s] = *(const float4*)((const float*)smem + r * STG_PITCH + 4 * lane + 128);
       } else {
         l[s] = ld_cluster_f32(mapa(lse_a + 4 * r, rank));
         a[s] = ld_cluster_v4(mapa(at, rank));
-        c[s] = ld_cluster_v4(mapa(at + 16, rank));
+        c[s] = ld_cluster_v4(mapa(at + 512, rank));
       }
     }
     float mx = l[0];
@@ -421,13 +421,15 @@ __device__ __forceinline__ void store_rows(const TreeParams& P, const uint8_t* s
       __half2 h2[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) h2[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-      *reinterpret_cast<uint4*>(P.o_lat + row * 512 + U.half * 256 + 8 * lane) = *reinterpret_cast<uint4*>(h2);
+      uint2* dst = reinterpret_cast<uint2*>(P.o_lat + row * 512 + U.half * 256 + 4 * lane);
+      dst[0] = *reinterpret_cast<uint2*>(h2);
+      dst[32] = *reinterpret_cast<uint2*>(h2 + 2);
       if (P.lse && U.half == 0 && lane == 0) P.lse[row] = l2 == -INFINITY ? l2 : l2 * kLn2;
     } else {
       const long at = (long)(blockIdx.y / CS) * P.rows + row;
-      float4* dst = reinterpret_cast<float4*>(P.part + at * 512 + U.half * 256 + 8 * lane);
+      float4* dst = reinterpret_cast<float4*>(P.part + at * 512 + U.half * 256 + 4 * lane);
       dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-      dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+      dst[32] = make_float4(v[4], v[5], v[6], v[7]);
       if (U.half == 0 && lane == 0) P.part_lse[at] = l2;
     }
   }
