@@ -62,17 +62,27 @@ namespace {
 constexpr int QROWS = 128, KT = 128, NCH = 9;
 constexpr int CH_BYTES = 128 * 64 * 2;                    // a 64-dim chunk of 128 rows
 constexpr int NQT = 2, NQS = NCH - NQT;                   // Q chunks in tensor / shared memory
-constexpr int SLOTS = 3, SLOT_BYTES = 2 * CH_BYTES;
+constexpr int SLOT_BYTES = 2 * CH_BYTES, MAX_SLOTS = 5;
 constexpr int THREADS = 448;                              // softmax x4, S, loads x3, softmax x4, PV, Q and rope
 constexpr int W_S = 4, W_RING = 5, W_PV = 12, W_ROPE = 13;
-constexpr int OFF_Q = 0, OFF_RING = OFF_Q + NQS * CH_BYTES, OFF_ROPE = OFF_RING + SLOTS * SLOT_BYTES;
-constexpr int OFF_BAR = OFF_ROPE + CH_BYTES, OFF_SEEN = OFF_BAR + 256, OFF_XM = OFF_SEEN + tree::MAX_NODES / 8;
+constexpr int OFF_Q = 0, OFF_RING = OFF_Q + NQS * CH_BYTES, OFF_ROPE = OFF_RING + 3 * SLOT_BYTES;
+constexpr int OFF_BAR = OFF_ROPE + CH_BYTES, OFF_SEEN = OFF_BAR + 320, OFF_XM = OFF_SEEN + tree::MAX_NODES / 8;
 constexpr int SMEM_BYTES = 1024 + OFF_XM + 2 * QROWS * 4;
 // the pair kernel's slots (a CTA's halves): four key pairs and two value pairs of 16 KB
 constexpr int PK = 4, PV = 2, PSLOT_BYTES = CH_BYTES, OFF_PK = OFF_RING, OFF_PV = OFF_PK + PK * PSLOT_BYTES;
 static_assert(OFF_PV + PV * PSLOT_BYTES <= OFF_ROPE, "slots");
 static_assert(NQT == 2 && PV * PSLOT_BYTES == NQT * CH_BYTES && SLOT_BYTES == NQT * CH_BYTES, "Q's way through a slot");
-constexpr int OFF_Q01 = OFF_RING + (SLOTS - 1) * SLOT_BYTES;   // the other kernel's: its last ring slot
+// The other kernel, for blocks of up to QR rows: Q's chunks take QR rows each (the MMAs
+// read 128; what follows them is scores of rows that do not exist), which leaves
+// space for more slots, each with a warp of its own.
+template <int QR>
+struct Ring {
+  static constexpr int SLOTS = QR == 128 ? 3 : QR == 64 ? 4 : 5, QCH = QR * 128;
+  static constexpr int OFF_RING = OFF_Q + NQS * QCH, OFF_ROPE = OFF_RING + SLOTS * SLOT_BYTES;
+  static constexpr int OFF_Q01 = OFF_RING + (SLOTS - 1) * SLOT_BYTES;       // Q passes through the last slot
+  static constexpr int NT = THREADS + 32 * (SLOTS - 3);
+  static_assert(SLOTS <= MAX_SLOTS && OFF_ROPE + CH_BYTES <= OFF_BAR, "ring");
+};
 // the epilogue's rows, over Q and the slots: fp32, 256 dims, padded against bank
 // conflicts, then their log2-sum-exps
 constexpr int STG_PITCH = 260, OFF_STG_LSE = QROWS * STG_PITCH * 4;
@@ -87,7 +97,7 @@ struct Bars {
   uint64_t q01_full, q01_read;        // its first two chunks, on their way through a value or ring slot
   // keys and values land on barriers of their own: each has one consumer, which
   // never falls two phases behind (a parity tells only two apart)
-  uint64_t k_full[SLOTS], k_empty[SLOTS], v_full[SLOTS], clean[SLOTS], land;
+  uint64_t k_full[MAX_SLOTS], k_empty[MAX_SLOTS], v_full[MAX_SLOTS], clean[MAX_SLOTS], land;
   uint64_t rope_full;
   uint64_t s_full, s_free;            // S(t) complete (the rope chunk is free) / read
   uint64_t p_full, o_done;            // P(t) written / P(t) V(t) complete
@@ -97,7 +107,7 @@ struct Bars {
   int abort, z_lo;
   int issued;                         // tiles whose scores are in the tensor pipe
 };
-static_assert(sizeof(Bars) <= 256, "barrier block");
+static_assert(sizeof(Bars) <= OFF_SEEN - OFF_BAR, "barrier block");
 
 __device__ __forceinline__ bool wait_bar(Bars* B, uint64_t* bar, uint32_t parity, uint32_t* st,
                                          bool ready = false) {
@@ -159,7 +169,7 @@ __device__ __forceinline__ bool dirty_tile(const Unit& U, int z_lo, int t) {
 }
 
 __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8_t* smem, uint32_t tmem,
-                                             const Unit& U, const uint8_t* q01) {
+                                             const Unit& U, const uint8_t* q01, int q01_bytes) {
   const int r = threadIdx.x & (QROWS - 1), kh = threadIdx.x >= 256 ? 1 : 0, w = r / 32, lane = r % 32;
   constexpr int KH = KT / 2;
   const uint32_t lane_base = (uint32_t)(w * 32) << 16;
@@ -178,7 +188,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
     wait_bar(B, &B->q01_full, 0, P.rule.status);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint4 v = *reinterpret_cast<const uint4*>(q01 + kh * CH_BYTES + r * 128 + ((i ^ (r & 7)) * 16));
+      const uint4 v = *reinterpret_cast<const uint4*>(q01 + kh * q01_bytes + r * 128 + ((i ^ (r & 7)) * 16));
       q[4 * i] = v.x; q[4 * i + 1] = v.y; q[4 * i + 2] = v.z; q[4 * i + 3] = v.w;
     }
     mbar_arrive(&B->q01_read);
@@ -239,10 +249,18 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   }
   mbar_arrive(&B->seen_full);
   __syncwarp();
+  const bool dead = U.qt * QROWS + 32 * w >= R.T * R.H;   // a warp without rows: its P stays undefined
   for (int t = 0; t < U.nt; ++t) {
     const int jh = tile_key(U, t) + KH * kh;              // first key of this thread's half
     float s[KH];
     wait_bar(B, &B->s_full, t & 1, P.rule.status);
+    if (dead) {
+      if (lane == 0) mbar_arrive_pair(s_free);
+      if (t > 0) wait_bar(B, &B->o_done, (t - 1) & 1, P.rule.status);   // (no phase of p_full ahead of the others)
+      if (lane == 0) mbar_arrive_pair(p_full);
+      __syncwarp();
+      continue;
+    }
     tc_fence_after();
 #pragma unroll
     for (int c = 0; c < KH; c += 32) tmem_ld32_nowait(tmem + TM_S + KH * kh + c + lane_base, s + c);
@@ -379,7 +397,7 @@ __device__ __forceinline__ void store_rows(const TreeParams& P, const uint8_t* s
   const int y = CS > 1 ? (int)(blockIdx.y % CS) : 0, x = (int)(blockIdx.x & 1);
   const uint32_t stg = smem_u32(smem), lse_a = stg + OFF_STG_LSE;
 #pragma unroll(CS == 4 ? 2 : 4)
-  for (int r = y * (QROWS / CS) + warp; r < min(rows, (y + 1) * (QROWS / CS)); r += THREADS / 32) {
+  for (int r = y * (QROWS / CS) + warp; r < min(rows, (y + 1) * (QROWS / CS)); r += blockDim.x / 32) {
     float l[CS];
     float4 a[CS], c[CS];
 #pragma unroll
@@ -446,13 +464,13 @@ __device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* sm
   const tree::Rule& R = P.rule;
   const int tid = threadIdx.x, lane = tid % 32;
   uint32_t* seen = (uint32_t*)(smem + OFF_SEEN);          // nodes that a row of the cluster sees
-  // a lane a barrier (one thread for all of them: about 1 k cycles)
+  // a thread a barrier (one thread for all of them: about 1 k cycles)
   constexpr int NBAR = (int)(offsetof(Bars, tmem_slot) / 8);
-  static_assert(NBAR <= 32, "a barrier a lane");
+  static_assert(NBAR <= THREADS, "a barrier a thread");
   if (tid < NBAR) {
     uint64_t* bar = (uint64_t*)B + tid;
     const uint32_t count = bar == &B->q_tmem || bar == &B->s_free || bar == &B->p_full ? 8 * U.tiles
-                           : bar >= B->clean && bar < B->clean + SLOTS                  ? U.tiles
+                           : bar >= B->clean && bar < B->clean + MAX_SLOTS                  ? U.tiles
                            : bar == &B->seen_full || bar == &B->q01_read                ? 2 * QROWS
                                                                                          : 1;
     mbar_init(bar, count);
@@ -520,7 +538,10 @@ __device__ __forceinline__ void clear_unseen(const Unit& U, const uint8_t* smem,
   __syncwarp();
 }
 
-__global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_constant__ TreeParams P) {
+template <int QR>
+__global__ void __launch_bounds__(Ring<QR>::NT, 1) tree_attn_tc_kernel(const __grid_constant__ TreeParams P) {
+  using G = Ring<QR>;
+  constexpr int SLOTS = G::SLOTS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   Bars* B = (Bars*)(smem + OFF_BAR);
@@ -544,10 +565,11 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
   const uint32_t tmem = B->tmem_slot;
   const int seg = P.seg_rows, nseg = KT / seg;
 
-  if (warp >= W_RING && warp < W_RING + SLOTS) {
-    // ---- ring slot `s`: uses s, s + 3, ... ----
-    const int s = warp - W_RING;
-    uint8_t* slot = smem + OFF_RING + s * SLOT_BYTES;
+  const int s_of = warp > W_ROPE ? warp - W_ROPE + 2 : warp - W_RING;        // a load warp's slot
+  if (warp > W_ROPE || (warp >= W_RING && warp < W_RING + 3)) {
+    // ---- ring slot `s`: uses s, s + SLOTS, ... ----
+    const int s = s_of;
+    uint8_t* slot = smem + G::OFF_RING + s * SLOT_BYTES;
     int nk = 0, nv = 0;                                   // key and value uses issued
     int z_lo = -1;                                        // known from seen_full on
     for (int u = s; u < 6 * U.nt; u += SLOTS) {
@@ -589,9 +611,9 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
     // ---- Q once, then the rope chunk of every tile ----
     if (U.nt > 0) {
       if (lane == 0) {
-        mbar_arrive_expect_tx(&B->q01_full, NQT * CH_BYTES);
-        tma_load_3d(smem + OFF_Q01, &P.tmQ01, &B->q01_full, 0, (int)U.row0, 0);
-        mbar_arrive_expect_tx(&B->q_full, NQS * CH_BYTES);
+        mbar_arrive_expect_tx(&B->q01_full, NQT * G::QCH);
+        tma_load_3d(smem + G::OFF_Q01, &P.tmQ01, &B->q01_full, 0, (int)U.row0, 0);
+        mbar_arrive_expect_tx(&B->q_full, NQS * G::QCH);
         tma_load_3d(smem + OFF_Q, &P.tmQ, &B->q_full, 0, (int)U.row0, NQT);
       }
       __syncwarp();
@@ -601,7 +623,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
         if (!wait_bar(B, &B->s_full, (t & 1) ^ 1, R.status)) break;
         if (lane == 0) mbar_arrive_expect_tx(&B->rope_full, CH_BYTES);
         __syncwarp();
-        if (lane < nseg) tma_load_3d(smem + OFF_ROPE + lane * seg * 128, &P.tmK, &B->rope_full, 512, y, 0);
+        if (lane < nseg) tma_load_3d(smem + G::OFF_ROPE + lane * seg * 128, &P.tmK, &B->rope_full, 512, y, 0);
         __syncwarp();
       }
       mbar_wait(&B->q01_full, 0, R.status);
@@ -612,9 +634,9 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
     if (lane == 0 && U.nt > 0) {
       // ---- S(t) = Q K(t)^T ----
       const uint32_t idesc = idesc_f16(QROWS, KT, false), tS = tmem + TM_S, tQ = tmem + TM_Q;
-      constexpr uint64_t U_CH = CH_BYTES / 16, U_SLOT = SLOT_BYTES / 16;
-      const uint64_t dQ = smem_desc_sw128(smem + OFF_Q), dR = smem_desc_sw128(smem + OFF_RING);
-      const uint64_t dRope = smem_desc_sw128(smem + OFF_ROPE);
+      constexpr uint64_t U_Q = G::QCH / 16, U_CH = CH_BYTES / 16, U_SLOT = SLOT_BYTES / 16;
+      const uint64_t dQ = smem_desc_sw128(smem + OFF_Q), dR = smem_desc_sw128(smem + G::OFF_RING);
+      const uint64_t dRope = smem_desc_sw128(smem + G::OFF_ROPE);
       bool ok = wait_bar(B, &B->q_full, 0, R.status) && wait_bar(B, &B->q_tmem, 0, R.status);
       tc_fence_after();
       uint32_t par = 0;                                   // bit i: parity of k_full[i]
@@ -640,14 +662,14 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
               if (i == 0)
                 mma_f16_ts(tS, tQ + 32 * c + 8 * d, db + c * U_CH + 2 * d, idesc, (c | d) ? 1u : 0u);
               else
-                mma_f16(tS, dQ + (2 * i - 2 + c) * U_CH + 2 * d, db + c * U_CH + 2 * d, idesc, 1u);
+                mma_f16(tS, dQ + (2 * i - 2 + c) * U_Q + 2 * d, db + c * U_CH + 2 * d, idesc, 1u);
             }
           mma_commit(&B->k_empty[s]);
           s = s1;
         }
         if (!(ok = ok && wait_bar(B, &B->rope_full, t & 1, R.status, ready))) break;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) mma_f16(tS, dQ + (NQS - 1) * U_CH + 2 * d, dRope + 2 * d, idesc, 1u);
+        for (int d = 0; d < 4; ++d) mma_f16(tS, dQ + (NQS - 1) * U_Q + 2 * d, dRope + 2 * d, idesc, 1u);
         mma_commit(&B->s_full);
         *(volatile int*)&B->issued = t + 1;
       }
@@ -659,7 +681,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
       // ---- O += P(t) V(t) ----
       const uint32_t idesc = idesc_f16_bmn(QROWS, 128, false), tO = tmem + TM_O, tP = tmem + TM_P;
       constexpr uint64_t U_SLOT = SLOT_BYTES / 16, U_KSTEP = 16 * 128 / 16;
-      const uint64_t dV = smem_desc_sw128_mn(smem + OFF_RING, CH_BYTES);
+      const uint64_t dV = smem_desc_sw128_mn(smem + G::OFF_RING, CH_BYTES);
       uint32_t par = 0, cpar = 0;                         // bit i: parity of v_full[i], clean[i]
       bool ok = wait_bar(B, &B->seen_full, 0, R.status);
       const int z_lo = B->z_lo;
@@ -693,7 +715,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_tc_kernel(const __grid_c
       mbar_wait(&B->drain[1], 0, R.status);
     }
   } else {
-    softmax_role(P, B, smem, tmem, U, smem + OFF_Q01);
+    softmax_role(P, B, smem, tmem, U, smem + G::OFF_Q01, G::QCH);
   }
   __syncwarp();
   tc_fence_before();
@@ -874,7 +896,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
       mbar_wait(&B->drain[1], 0, R.status);
     }
   } else {
-    softmax_role(P, B, smem, tmem, U, smem + OFF_PV);
+    softmax_role(P, B, smem, tmem, U, smem + OFF_PV, CH_BYTES);
   }
   __syncwarp();
   tc_fence_before();
@@ -1021,8 +1043,10 @@ mla_status_t tree_attention(cudaStream_t st, mla_handle* h, const tree::Rule& r,
   TreeParams P;
   const int max_seg = plan.pair ? KT / 2 : KT;
   P.seg_rows = r.page_size < max_seg ? r.page_size : max_seg;
-  if (!make_tmap_chunked(&P.tmQ, false, q_abs, rows, l.L, l.L, QROWS, NQS) ||
-      !make_tmap_chunked(&P.tmQ01, false, q_abs, rows, l.L, l.L, QROWS, NQT) ||
+  const long block_rows = (long)d.block_len * l.H;
+  const int q_rows = block_rows <= 32 ? 32 : block_rows <= 64 ? 64 : QROWS;      // pairs have more than 128
+  if (!make_tmap_chunked(&P.tmQ, false, q_abs, rows, l.L, l.L, q_rows, NQS) ||
+      !make_tmap_chunked(&P.tmQ01, false, q_abs, rows, l.L, l.L, q_rows, NQT) ||
       (!plan.pair && !make_tmap_chunked(&P.tmC, false, cache, slots, l.L, l.L, KT, 2)) ||
       !make_tmap_2d(&P.tmK, false, cache, slots, l.L, l.L, P.seg_rows))
     return fail(MLA_ERR_CUDA, "tree attention: cuTensorMapEncodeTiled failed");
@@ -1039,14 +1063,18 @@ mla_status_t tree_attention(cudaStream_t st, mla_handle* h, const tree::Rule& r,
   if (2 * plan.groups > 0x7fffffffL) return fail(MLA_ERR_INVALID_ARG, "tree attention: too many rows");
   static std::once_flag once;
   std::call_once(once, [] {
-    cudaFuncSetAttribute(tree_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    cudaFuncSetAttribute(tree_attn_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    for (auto* k : {tree_attn_tc_kernel<32>, tree_attn_tc_kernel<64>, tree_attn_tc_kernel<128>, tree_attn_pair_kernel})
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   });
   auto launch = [&](long groups, int key_parts, bool dependent) {
-    Launch L(dim3((unsigned)(2 * groups), (unsigned)key_parts), dim3(THREADS), SMEM_BYTES, st, dependent,
+    const int threads = plan.pair || q_rows == 128 ? THREADS : q_rows == 64 ? Ring<64>::NT : Ring<32>::NT;
+    Launch L(dim3((unsigned)(2 * groups), (unsigned)key_parts), dim3((unsigned)threads), SMEM_BYTES, st, dependent,
              dim3(2, (unsigned)P.cluster_parts, 1));
     h->launches += 1;
-    return cudaLaunchKernelEx(&L.cfg, plan.pair ? tree_attn_pair_kernel : tree_attn_tc_kernel, P);
+    return cudaLaunchKernelEx(&L.cfg, plan.pair       ? tree_attn_pair_kernel
+                                      : q_rows == 32  ? tree_attn_tc_kernel<32>
+                                      : q_rows == 64  ? tree_attn_tc_kernel<64>
+                                                      : tree_attn_tc_kernel<128>, P);
   };
   P.group0 = 0;
   P.rest = 0;
