@@ -12,8 +12,11 @@
 //    shared-memory traffic a tile against 3328 of MMAs).  8192 rows x 6-8 k keys x
 //    4 sequences: 434 us, 1.17 PFLOP/s on the algorithm's flops;
 //  - tree_attn_tc_kernel, blocks of at most 128 rows: one row tile, a CTA per
-//    value half (4224 cycles of shared-memory traffic a tile, the bound; 2.7 us a
-//    tile, 4.2 TB/s of cache over the GPU while it lasts).
+//    value half (4224 cycles of shared-memory traffic a tile, and a slot's next
+//    copy waits for P V, 2 k cycles from L2: 6 to 7 k cycles a tile).  Blocks of at
+//    most 64 and 32 rows give the space of the rows that they lack to a fourth and
+//    a fifth slot: 64 sequences x 32 rows x 4 k keys 127 us with three, 108 with
+//    five; x 64 rows 127 and, with four, 114.
 //
 // What a tile costs beyond its MMAs is hidden by running the scores one tile
 // ahead: the tensor pipe executes S(0), S(1), PV(0), S(2), PV(1), ..., and
@@ -168,6 +171,7 @@ __device__ __forceinline__ bool dirty_tile(const Unit& U, int z_lo, int t) {
   return j0 + KT > U.ctx || j0 < z_lo;
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8_t* smem, uint32_t tmem,
                                              const Unit& U, const uint8_t* q01, int q01_bytes) {
   const int r = threadIdx.x & (QROWS - 1), kh = threadIdx.x >= 256 ? 1 : 0, w = r / 32, lane = r % 32;
@@ -249,12 +253,14 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   }
   mbar_arrive(&B->seen_full);
   __syncwarp();
-  const bool dead = U.qt * QROWS + 32 * w >= R.T * R.H;   // a warp without rows: its P stays undefined
+  // a warp without rows: its P stays undefined.  (Not in pairs, where it is rare and
+  // the test alone made the loop slower: 128 heads x 64 nodes 434 -> 445 us)
+  const bool dead = U.qt * QROWS + 32 * w >= R.T * R.H;
   for (int t = 0; t < U.nt; ++t) {
     const int jh = tile_key(U, t) + KH * kh;              // first key of this thread's half
     float s[KH];
     wait_bar(B, &B->s_full, t & 1, P.rule.status);
-    if (dead) {
+    if (!PAIR && dead) {
       if (lane == 0) mbar_arrive_pair(s_free);
       if (t > 0) wait_bar(B, &B->o_done, (t - 1) & 1, P.rule.status);   // (no phase of p_full ahead of the others)
       if (lane == 0) mbar_arrive_pair(p_full);
@@ -715,7 +721,7 @@ __global__ void __launch_bounds__(Ring<QR>::NT, 1) tree_attn_tc_kernel(const __g
       mbar_wait(&B->drain[1], 0, R.status);
     }
   } else {
-    softmax_role(P, B, smem, tmem, U, smem + G::OFF_Q01, G::QCH);
+    softmax_role<false>(P, B, smem, tmem, U, smem + G::OFF_Q01, G::QCH);
   }
   __syncwarp();
   tc_fence_before();
@@ -896,7 +902,7 @@ __global__ void __launch_bounds__(THREADS, 1) tree_attn_pair_kernel(const __grid
       mbar_wait(&B->drain[1], 0, R.status);
     }
   } else {
-    softmax_role(P, B, smem, tmem, U, smem + OFF_PV, CH_BYTES);
+    softmax_role<true>(P, B, smem, tmem, U, smem + OFF_PV, CH_BYTES);
   }
   __syncwarp();
   tc_fence_before();
@@ -971,12 +977,12 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict
 // cluster).  Cost in tiles (about 2.5 us) of the waves of CTAs that a choice
 // needs: FIXED beyond a part's share of the keys, JOIN for a cluster's join,
 // MERGE and MERGE_PART for the second kernel.  Measured, us: 512 rows x 2064
-// keys x 8 sequences 47 whole, 41 in two parts merged, 37 in two joined; 8192
-// rows x 6-8 k keys x 4 sequences 483, 538, 561; 128 rows x 32 k keys 47 in 32
-// parts, 41 in 48, 39 in 56 or 64, 40 in 60 joined by fours.  Keys are bounded by
+// keys x 8 sequences 45 whole, 39 in two parts merged, 35 in two joined; 8192
+// rows x 6-8 k keys x 4 sequences 468, 513, 528; 128 rows x 32 k keys 45 in 32
+// parts, 37 in 48, 35 in 56 or 64, 37 in 60 joined by fours.  Keys are bounded by
 // the page table (shorter sequences only split finer than they need) and, when
 // windows are given, taken as at most 16 tiles, since the windows are on the
-// device: 800 rows x 5 sequences with a window of 512 keys 29 us whole, 41 in
+// device: 800 rows x 5 sequences with a window of 512 keys 28 us whole, 37 in
 // three parts.
 //
 // Clusters of whole units that do not fill their last wave have that wave's

@@ -240,6 +240,15 @@ def test_many_blocks():
     c.weights()
 
 
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("heads,T", [(2, 8), (2, 9), (8, 4), (3, 11), (16, 4), (13, 5), (32, 4), (43, 3)])
+def test_rows_of_a_block_around_the_sizes_of_its_tile(heads, T, page):
+    # up to 32, 64, 128 and more rows; the neighbours' queries in a tile may be NaN
+    c = Case("bf16", heads, page, [1900, 3, 700, 0], T, padded=True, masked=T > 8, seed=page + T)
+    c.check_attention(*c.attention())
+    c.weights()
+
+
 @pytest.mark.parametrize("heads,T,n,window", [(16, 9, 40, 0), (4, 5, 83, 0), (16, 9, 79, 700)])
 def test_blocks_of_a_last_wave_cut_in_parts(heads, T, n, window):
     # more clusters than the GPU holds: the last wave's are a launch of their own
