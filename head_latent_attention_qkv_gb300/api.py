@@ -228,6 +228,22 @@ def _take(name, t, dtype, shape, h):
     return t.data_ptr()
 
 
+_empty_strided_cuda = torch._C._dynamo.guards._empty_strided_cuda
+
+
+def _new(h: Handle, shape, dtype):
+    """An uninitialised tensor on the handle's device.  Right after a launch
+    torch.empty takes 5 us of host time and this allocation of the same pool 2;
+    it takes place on the current device, which a handle needs to be its own."""
+    if torch._C._cuda_getDevice() != h.device_index:
+        return torch.empty(shape, dtype=dtype, device=h.device)
+    return _empty_strided_cuda(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype)
+
+
+def _new_workspace(h: Handle, nbytes):
+    return _new(h, (nbytes,), torch.uint8) if nbytes else None
+
+
 def _take_cache(h: Handle, cache):
     return _take("cache", cache, torch_dtype(h.dims), (cache.shape[0], h.page_size, h.dims.cache_dim), h)
 
@@ -276,12 +292,11 @@ def mla_tree_attention(h: Handle, q_abs, positions, cache, desc, parent, o_lat=N
     dt = torch.float16 if h.dims.dtype == "bf16" else torch.float32
     lse_p = None if lse is None else _take("lse", lse, torch.float32, (rows,), h)
     if o_lat is None:
-        o_lat = cache.new_empty((rows, rank), dtype=dt)
+        o_lat = _new(h, (rows, rank), dt)
     out = _take("o_lat", o_lat, dt, (rows, rank), h)
     ref = C.byref(desc)
     if workspace is None:
-        need = lib.mla_tree_attention_workspace_bytes(h.h, ref)
-        workspace = cache.new_empty((need,), dtype=torch.uint8) if need else None
+        workspace = _new_workspace(h, lib.mla_tree_attention_workspace_bytes(h.h, ref))
     _run(lib.mla_tree_attention, h, q, pos, c, cache.shape[0], ref, par, out, lse_p,
          *_take_workspace(workspace, h))
     return o_lat
@@ -305,10 +320,10 @@ def mla_draft_forward_tree(h: Handle, hidden, positions, block_slot_mapping, cac
             _take("block_slot_mapping", block_slot_mapping, torch.int64, (M,), h), _take_cache(h, cache))
     par = _take("parent", parent, torch.int32, (M,), h)
     if out is None:
-        out = cache.new_empty((M, D))
+        out = _new(h, (M, D), dt)
     ref = C.byref(desc)
     if workspace is None:
-        workspace = _buf(lib.mla_forward_tree_workspace_bytes(h.h, ref), cache.device)
+        workspace = _new_workspace(h, lib.mla_forward_tree_workspace_bytes(h.h, ref))
     _run(lib.mla_draft_forward_tree, h, *args, cache.shape[0], ref, par, _take("out", out, dt, (M, D), h),
          *_take_workspace(workspace, h))
     return out
@@ -335,8 +350,7 @@ def mla_key_weights(h: Handle, q_abs, positions, cache, desc, lse, weights_out, 
     prior_p = None if prior is None else _take("prior", prior, torch.float32, (nb, ldw), h)
     ref = C.byref(desc)
     if workspace is None:
-        need = lib.mla_key_weights_workspace_bytes(h.h, ref, ldw)
-        workspace = cache.new_empty((need,), dtype=torch.uint8) if need else None
+        workspace = _new_workspace(h, lib.mla_key_weights_workspace_bytes(h.h, ref, ldw))
     _run(lib.mla_key_weights, h, q, pos, c, cache.shape[0], ref, par, lse_p, decay, prior_p, out, ldw,
          *_take_workspace(workspace, h))
     return weights_out
@@ -357,9 +371,9 @@ def mla_cache_select(h: Handle, weights, kv_len, budget: int, sink: int = 0, rec
     n = kv_len.shape[0]
     w, ldw = _take_rows("weights", weights, torch.float32, n, h)
     if keep is None:
-        keep = kv_len.new_empty((n, max(budget, 0)), dtype=torch.int32)
+        keep = _new(h, (n, max(budget, 0)), torch.int32)
     if keep_len is None:
-        keep_len = kv_len.new_empty((n,), dtype=torch.int32)
+        keep_len = _new(h, (n,), torch.int32)
     _run(lib.mla_cache_select, h, w, ldw, _take("kv_len", kv_len, torch.int32, (n,), h), n, budget, sink, recent,
          _take("keep", keep, torch.int32, (n, max(budget, 0)), h),
          _take("keep_len", keep_len, torch.int32, (n,), h))
@@ -390,7 +404,7 @@ def mla_cache_compact(h: Handle, cache, block_table, kv_len, keep, keep_len, fir
             None if first is None else _take("first", first, i32, (n,), h), dst, dst_pages, w,
             None if weights_out is None else _take("weights_out", weights_out, torch.float32, (n, ldw), h), ldw)
     if workspace is None and in_place:
-        workspace = _buf(lib.mla_cache_compact_workspace_bytes(h.h, n, ldk), cache.device)
+        workspace = _new_workspace(h, lib.mla_cache_compact_workspace_bytes(h.h, n, ldk))
     _run(lib.mla_cache_compact, h, *args, *_take_workspace(workspace, h))
 
 
