@@ -164,16 +164,22 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
     const int jw = j - lane;                              // the warp's first key
     float sum = 0.f;
     if (!it.skip) {
+      // the context's keys among the warp's 32 (without a window), alike for all rows
+      const uint32_t context = (uint32_t)tree::context_bits(R, it.b, 0, it.n0, 0, it.ctx, jw);
+      // this thread's column of a row tile: its row's log-sum-exp, -inf for none
+      auto load_lse = [&](int qt) {
+        const int c = qt * NMAX + col_id;
+        if (c >= R.T * R.H) return -INFINITY;
+        if (R.q_visible && !R.q_visible[(long)it.b * R.T + c / R.H]) return -INFINITY;
+        return P.lse[(long)it.b * R.T * R.H + c];
+      };
+      float l = load_lse(it.qt0);
       for (int qt = it.qt0; qt < it.qt1; ++qt, ++tile) {
-        const int rows = it.rows(qt), cols = it.cols(qt);
-        const long row0 = (long)it.b * R.T * R.H + (long)qt * NMAX;
-        // each thread's own column: its row's log-sum-exp, and whether the row counts
+        const int cols = it.cols(qt);
         sum_sync();                                       // the last tile's values have been read
-        {
-          float l = -INFINITY;
-          if (col_id < rows) l = P.lse[row0 + col_id];
-          lses[col_id] = l;
-        }
+        lses[col_id] = l;
+        sum_sync();
+        if (qt + 1 < it.qt1) l = load_lse(qt + 1);        // on its way while this tile is summed
         // the warp's 32 keys as this lane's four columns see them; where nodes'
         // keys are among them, a lane walks from one node for all its rows
         uint32_t word[4];
@@ -186,28 +192,26 @@ __device__ __forceinline__ void sum_role(const WeightParams& P, Bars* B, uint8_t
         if (shared && node0 + lane < R.T) walked = (uint32_t)tree::walk_bits(R, it.b, node0 + lane, it.W, jw - it.ctx, &sound, true);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int c = half * 128 + 32 * q + lane, node = (qt * NMAX + c) / R.H;
-          bool ok = c < rows && jw < it.n0;
-          if (ok) {
-            const long m = (long)it.b * R.T + node;
-            // (rows outside the tree have lse = -inf)
-            ok = (R.q_visible ? R.q_visible[m] != 0 : true) && P.lse[row0 + c] != -INFINITY;
-          }
-          word[q] = ok ? (uint32_t)tree::context_bits(R, it.b, node, it.n0, it.W, it.ctx, jw) : 0u;
-          if (shared) {
-            const uint32_t w1 = __shfl_sync(0xffffffffu, walked, node - node0);
-            const bool s1 = __shfl_sync(0xffffffffu, (int)sound, node - node0) != 0;
-            word[q] = ok && s1 ? word[q] | w1 : 0u;
-          } else if (own && ok) {
-            bool s1;
-            const uint32_t w1 = (uint32_t)tree::walk_bits(R, it.b, node, it.W, jw - it.ctx, &s1, true);
-            word[q] = s1 ? word[q] | w1 : 0u;
+          const int c = half * 128 + 32 * q + lane;
+          const bool ok = lses[c] != -INFINITY;           // (rows outside the tree have lse = -inf)
+          word[q] = ok ? context : 0u;
+          if (it.W > 0 || own) {
+            const int node = (qt * NMAX + c) / R.H;
+            if (it.W > 0 && ok) word[q] = (uint32_t)tree::context_bits(R, it.b, node, it.n0, it.W, it.ctx, jw);
+            if (shared) {
+              const uint32_t w1 = __shfl_sync(0xffffffffu, walked, node - node0);
+              const bool s1 = __shfl_sync(0xffffffffu, (int)sound, node - node0) != 0;
+              word[q] = ok && s1 ? word[q] | w1 : 0u;
+            } else if (own && ok) {
+              bool s1;
+              const uint32_t w1 = (uint32_t)tree::walk_bits(R, it.b, node, it.W, jw - it.ctx, &s1, true);
+              word[q] = s1 ? word[q] | w1 : 0u;
+            }
           }
           all = all && (word[q] == 0xffffffffu || c >= cols);
         }
         all = __all_sync(0xffffffffu, all);
         __syncwarp();                                     // the walks may have parted the warp
-        sum_sync();
         const int buf = tile & 1;
         wait_bar(B, &B->s_full[buf], (tile >> 1) & 1, R.status);
         tc_fence_after();
