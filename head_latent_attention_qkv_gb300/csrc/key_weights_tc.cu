@@ -22,10 +22,11 @@
 // broadcast.  A step of the issuing thread (a barrier, four MMAs, a commit)
 // takes about 530 cycles however few the columns, so blocks of at most 84 rows
 // bring Q in three chunks a slot (64 sequences x 32 rows x 1-4 k keys: 53 us
-// against 57 with one, 43 with the items looked up by the key warp: 4.4 TB/s of
-// cache).  2048 rows x 8 k keys x 4 sequences: 67 us, the tensor pipe active half
-// of the cycles: Q's slots (80 KB in flight a CTA) turn over in 2.5 k cycles.  When the key tiles alone do not fill the GPU the rows are cut in
-// parts whose sums a second kernel adds in order.
+// against 57 with one, 43 with the items looked up by the key warp, 41 with the
+// log-sum-exps read ahead: 4.6 TB/s of cache).  2048 rows x 8 k keys x 4 sequences:
+// 65 us, the tensor pipe active half of the cycles: Q's slots (80 KB in flight a
+// CTA) turn over in 2.5 k cycles.  When the key tiles alone do not fill the GPU
+// the rows are cut in parts whose sums a second kernel adds in order.
 #include <math.h>
 
 #include <mutex>
