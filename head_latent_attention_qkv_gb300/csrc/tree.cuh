@@ -26,22 +26,25 @@ struct Rule {
   uint32_t* status;
 };
 
-// Keys of block b (0 when its length or window is rejected), its window and,
-// with a tree, the context length.
-__device__ __forceinline__ int block_keys(const Rule& a, int b, int* W, int* ctx, bool report) {
-  int n = a.kv_len[b];
+// Keys of a block of length n and window *W (0 when one of them is rejected)
+// and, with a tree, the context length.
+__device__ __forceinline__ int checked_keys(const Rule& a, int n, int* W, int* ctx, bool report) {
   const int cap = a.max_pages * a.page_size;
   if (n < 0 || n > cap || (a.parent && n < a.T)) {
     if (report) set_status(a.status, MLA_DEV_BAD_LENGTH);
     n = a.parent ? 0 : max(0, min(n, cap));
   }
-  *W = a.window ? a.window[b] : 0;
   if (*W < 0) {
     if (report) set_status(a.status, MLA_DEV_BAD_WINDOW);
     n = 0;
   }
   *ctx = a.parent ? max(0, n - a.T) : n;
   return n;
+}
+// Those of block b, and its window.
+__device__ __forceinline__ int block_keys(const Rule& a, int b, int* W, int* ctx, bool report) {
+  *W = a.window ? a.window[b] : 0;
+  return checked_keys(a, a.kv_len[b], W, ctx, report);
 }
 
 // Whether node i's path to the context is sound (its ancestors and itself in

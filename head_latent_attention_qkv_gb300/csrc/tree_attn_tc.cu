@@ -470,6 +470,20 @@ __device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* sm
   const tree::Rule& R = P.rule;
   const int tid = threadIdx.x, lane = tid % 32;
   uint32_t* seen = (uint32_t*)(smem + OFF_SEEN);          // nodes that a row of the cluster sees
+  // the loads that the unit depends on first, their answers (1.5 k cycles) after
+  // the barriers are set: the block's length, and this lane's first node
+  const int q0 = U.tiles == 2 ? U.qt & ~1 : U.qt;
+  const int t0 = q0 * QROWS / R.H, t1 = min(R.T - 1, ((q0 + U.tiles) * QROWS - 1) / R.H);
+  auto load_node = [&](int i, int* parent, int* pos, bool* shown) {
+    const long m = (long)U.b * R.T + i;
+    *parent = R.parent[m];
+    *pos = R.positions[m];
+    *shown = R.q_visible ? R.q_visible[m] != 0 : true;
+  };
+  int parent = -2, pos = 0;
+  bool shown = false;
+  if (t0 + lane <= t1) load_node(t0 + lane, &parent, &pos, &shown);
+  const int kv_len = R.kv_len[U.b], window = R.window ? R.window[U.b] : 0;
   // a thread a barrier (one thread for all of them: about 1 k cycles)
   constexpr int NBAR = (int)(offsetof(Bars, tmem_slot) / 8);
   static_assert(NBAR <= THREADS, "a barrier a thread");
@@ -492,19 +506,17 @@ __device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* sm
   tc_fence_before();           // (the tensor memory's address)
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   // whether a row may see anything (padding and masked rows left out), and the
-  // first tile that a row's window reaches; the loads do not wait for one another
-  const int q0 = U.tiles == 2 ? U.qt & ~1 : U.qt;
-  const int t0 = q0 * QROWS / R.H, t1 = min(R.T - 1, ((q0 + U.tiles) * QROWS - 1) / R.H);
+  // first tile that a row's window reaches
   bool any = false;
   int pmin = 0x7fffffff;
   for (int i = t0 + lane; i <= t1; i += 32) {
-    const long m = (long)U.b * R.T + i;
-    const int parent = R.parent[m], pos = R.positions[m];
-    const bool in = parent >= -1 && (R.q_visible ? R.q_visible[m] != 0 : true);
+    if (i >= t0 + 32) load_node(i, &parent, &pos, &shown);
+    const bool in = parent >= -1 && shown;
     any |= in;
     if (in) pmin = min(pmin, pos);
   }
-  U.n = tree::block_keys(R, U.b, &U.W, &U.ctx, tid == 0 && U.first && U.qt == 0);
+  U.W = window;
+  U.n = tree::checked_keys(R, kv_len, &U.W, &U.ctx, tid == 0 && U.first && U.qt == 0);
   any = __any_sync(0xffffffffu, any);
   pmin = __reduce_min_sync(0xffffffffu, pmin);
   U.j_lo = U.W > 0 ? max(0, min(pmin - U.W + 1, U.ctx)) / KT * KT : 0;
