@@ -504,7 +504,10 @@ __device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* sm
   }
   for (int i = tid; i < tree::MAX_NODES / 32; i += THREADS) seen[i] = 0;
   tc_fence_before();           // (the tensor memory's address)
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  __syncthreads();
+  // the peers need the barriers only, which their own fence has published (a release
+  // of everything took 800 cycles)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   // whether a row may see anything (padding and masked rows left out), and the
   // first tile that a row's window reaches
   bool any = false;
