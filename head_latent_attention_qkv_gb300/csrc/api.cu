@@ -808,6 +808,8 @@ extern "C" mla_status_t mla_draft_forward_tree(mla_handle_t* h, const void* hidd
   if (!hidden || !positions || !cache || !parent || !out || !workspace || !d.block_table || !d.kv_len)
     return fail(MLA_ERR_INVALID_ARG, "forward_tree: null pointer");
   if (num_pages <= 0) return fail(MLA_ERR_INVALID_ARG, "forward_tree: num_pages <= 0");
+  // (the attention's 16-byte copies; the plain forward of fp32 layers reads floats)
+  if ((uintptr_t)cache % 16) return fail(MLA_ERR_INVALID_ARG, "forward_tree: cache must be 16-byte aligned");
   if (workspace_bytes < mla_forward_tree_workspace_bytes(h, desc) || (uintptr_t)workspace % 256)
     return fail(MLA_ERR_INVALID_ARG, "forward_tree: workspace smaller than "
                                      "mla_forward_tree_workspace_bytes() or not 256-byte aligned");

@@ -427,7 +427,8 @@ mla_status_t mla_tree_attention(mla_handle_t *h, const void *q_abs, const int32_
 /* The whole layer over trees: mla_draft_forward with the tree's visibility in
  * its attention (same arguments, results and errors; block_slot_mapping
  * writes the nodes' own entries first; padding nodes take a free slot of
- * their own and a position inside the table). */
+ * their own and a position inside the table).  cache must be 16-byte aligned,
+ * on fp32 layers too. */
 size_t mla_forward_tree_workspace_bytes(const mla_handle_t *h, const mla_attn_desc_t *desc);
 mla_status_t mla_draft_forward_tree(mla_handle_t *h, const void *hidden,
                                     const int32_t *positions,

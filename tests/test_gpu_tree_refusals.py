@@ -1,0 +1,65 @@
+"""Arguments that the tree and eviction entry points refuse on the host, before
+anything is launched, through the raw entry points (needs a GB300 for a handle).
+"""
+import ctypes as C
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+class Layer:
+    """A layer, one sequence of `ctx` keys and a tree of `nodes`, and what the
+    entry points need beside them; `off` moves the cache by bytes."""
+
+    def __init__(self, dtype, heads, ctx, nodes, page=16):
+        from head_latent_attention_qkv_gb300 import api
+        from tests.tree_cases import i32, make_handle
+        self.h = make_handle(dtype, heads, page)[0]
+        d, self.nodes, self.rows = self.h.dims, nodes, nodes * heads
+        dt = api.torch_dtype(d)
+        mp = -(-(ctx + nodes) // page)
+        self.pages = mp
+        self.store = torch.zeros(mp * page * d.cache_dim + 16, dtype=dt, device="cuda")
+        self.table, self.kv = i32([list(range(mp))]), i32([ctx + nodes])
+        self.positions, self.parent = i32([ctx + i for i in range(nodes)]), i32(list(range(-1, nodes - 1)))
+        self.hidden = torch.zeros(nodes, d.hidden_size, dtype=dt, device="cuda")
+        self.out = torch.zeros_like(self.hidden)
+        self.desc = api.make_desc(self.table, self.kv, block_len=nodes)
+        self.ref = C.byref(self.desc)
+
+    def forward(self, off=0, ws=None, nws=None):
+        from head_latent_attention_qkv_gb300 import api
+        from head_latent_attention_qkv_gb300._lib import lib
+        need = api.mla_forward_tree_workspace_bytes(self.h, self.desc)
+        own = torch.empty(need, dtype=torch.uint8, device="cuda")
+        return lib.mla_draft_forward_tree(
+            self.h.h, self.hidden.data_ptr(), self.positions.data_ptr(), None, self.store.data_ptr() + off,
+            self.pages, self.ref, self.parent.data_ptr(), self.out.data_ptr(),
+            own.data_ptr() if ws is None else ws, need if nws is None else nws,
+            torch.cuda.current_stream().cuda_stream)
+
+    def launches(self):
+        from head_latent_attention_qkv_gb300 import api
+        return api.mla_kernel_launches(self.h)
+
+
+@pytest.mark.parametrize("dtype,heads", [("fp32", 4), ("bf16", 16)])
+def test_the_layer_refuses_a_cache_that_is_not_aligned(dtype, heads):
+    from head_latent_attention_qkv_gb300 import _lib, api
+    c = Layer(dtype, heads, 20, 3)
+    before = c.launches()
+    for off in (2, 4, 8, 12):
+        assert c.forward(off) == _lib.MLA_ERR_INVALID_ARG, off
+        assert b"aligned" in _lib.lib.mla_last_error()
+    assert c.launches() == before                              # nothing was launched
+    assert c.forward(16) == _lib.MLA_OK
+    torch.cuda.synchronize()
+    assert api.mla_get_device_status(c.h) == 0
