@@ -490,6 +490,7 @@ extern "C" mla_status_t mla_cache_compact(mla_handle_t* h, void* cache, int32_t 
   if (num_seqs == 0) return MLA_OK;
   if (!cache || !block_table || !kv_len || !keep_len || (!keep && ldk > 0))
     return fail(MLA_ERR_INVALID_ARG, "compact: null pointer");
+  if ((uintptr_t)cache % 4) return fail(MLA_ERR_INVALID_ARG, "compact: cache must be 4-byte aligned");
   if (dst_block_table && dst_max_pages <= 0)
     return fail(MLA_ERR_INVALID_ARG, "compact: dst_max_pages > 0 with a destination table");
   const long cap = (long)max_pages * h->cfg.page_size;

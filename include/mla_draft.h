@@ -494,6 +494,7 @@ mla_status_t mla_cache_select(mla_handle_t *h, const float *weights, int64_t ldw
  * Reported on the device, the row or sequence left alone: an index that is not
  * ascending or outside its sequence, keep_len > ldk or > kv_len - first
  * (MLA_DEV_BAD_KEEP), a bad page, a kv_len beyond the table or ldw.
+ * cache: 4-byte aligned (16-byte aligned is faster).
  * workspace: mla_cache_compact_workspace_bytes() bytes, 256-byte aligned,
  * needed in place only; two calls that may overlap on the GPU need two. */
 size_t mla_cache_compact_workspace_bytes(const mla_handle_t *h, int32_t num_seqs, int64_t ldk);

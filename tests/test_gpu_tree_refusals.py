@@ -63,3 +63,37 @@ def test_the_layer_refuses_a_cache_that_is_not_aligned(dtype, heads):
     assert c.forward(16) == _lib.MLA_OK
     torch.cuda.synchronize()
     assert api.mla_get_device_status(c.h) == 0
+
+
+@pytest.mark.parametrize("dtype,heads", [("fp32", 4), ("bf16", 16)])
+def test_compaction_refuses_a_cache_that_splits_words(dtype, heads):
+    from head_latent_attention_qkv_gb300 import _lib, api
+    from head_latent_attention_qkv_gb300._lib import lib
+    from tests.tree_cases import i32
+    c = Layer(dtype, heads, 40, 1)
+    keep, num = i32([[1, 3, 7]]), i32([3])
+    dst = i32([[0]])
+    ws = torch.empty(api.mla_cache_compact_workspace_bytes(c.h, 1, 3), dtype=torch.uint8, device="cuda")
+
+    def run(off, table):
+        return lib.mla_cache_compact(c.h.h, c.store.data_ptr() + off, c.pages, c.table.data_ptr(), c.table.shape[1],
+                                     c.kv.data_ptr(), 1, keep.data_ptr(), 3, num.data_ptr(), None, table, 1, None,
+                                     None, 0, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+
+    before = c.launches()
+    for off in (1, 2, 6, 15):
+        for table in (None, dst.data_ptr()):
+            assert run(off, table) == _lib.MLA_ERR_INVALID_ARG, off
+            assert b"aligned" in lib.mla_last_error()
+    assert c.launches() == before
+    # words, but not 16-byte units: rows move by words
+    d = c.h.dims.cache_dim
+    off = 4 // c.store.element_size()
+    rows = c.store[off:off + c.pages * 16 * d].view(-1, d)
+    rows.copy_(torch.arange(rows.shape[0], device="cuda")[:, None] + torch.arange(d, device="cuda") / 8)
+    want = rows.clone()
+    want[:3] = rows[[1, 3, 7]]
+    assert run(4, None) == _lib.MLA_OK
+    torch.cuda.synchronize()
+    assert api.mla_get_device_status(c.h) == 0
+    assert torch.equal(rows, want)
