@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
   int32_t* keep = a.keep + seq * a.budget;
   const int kept = min(n, a.budget);
   if (rank == 0 && tid == 0) a.keep_len[seq] = kept;
-  for (int i = kept + rank * SEL_THREADS + tid; i < a.budget; i += CL * SEL_THREADS) keep[i] = -1;
+  // (a step behind a budget near 2^31 passes it)
+  for (long i = (long)kept + rank * SEL_THREADS + tid; i < a.budget; i += CL * SEL_THREADS) keep[i] = -1;
   if (n <= a.budget) {                                   // uniform over the cluster
     for (int i = rank * SEL_THREADS + tid; i < n; i += CL * SEL_THREADS) keep[i] = i;
     return;

@@ -65,6 +65,22 @@ def test_select_orders_ties_zeros_infinities_and_nan(width):
     check_select(np.zeros((1, width), dtype=np.float32), [width], width // 2, 1, 1)
 
 
+@pytest.mark.parametrize("width", [5, 9000])
+def test_select_under_the_largest_budget(width):
+    # the list's end is 2^31 - 1: an index that steps over it must not wrap
+    from head_latent_attention_qkv_gb300 import api
+    from tests.tree_cases import i32
+    h = handle("fp32", 16)
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs a list of 8.6 GB")
+    keep, num = api.mla_cache_select(h, torch.rand(1, width, device="cuda"), i32([5]), 2 ** 31 - 1, 2, 1)
+    torch.cuda.synchronize()
+    assert api.mla_get_device_status(h) == 0 and num.tolist() == [5]
+    assert keep[0, :5].tolist() == [0, 1, 2, 3, 4]
+    for part in keep[0, 5:].split(1 << 28):
+        assert (part == -1).all()
+
+
 def test_select_length_behind_the_row_is_reported():
     from head_latent_attention_qkv_gb300 import _lib, api
     from tests.tree_cases import i32
