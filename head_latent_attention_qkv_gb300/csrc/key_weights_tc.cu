@@ -138,7 +138,7 @@ struct Items {
       int pmin = 0x7fffffff;
       for (int i = lane; i < R.T; i += 32) pmin = min(pmin, R.positions[(long)b * R.T + i]);
       pmin = __reduce_min_sync(0xffffffffu, pmin);
-      skip |= (kt + 1) * PAIR_KT <= pmin - W + 1;
+      skip |= (kt + 1) * PAIR_KT <= tree::window_start(pmin, W);
     }
     return true;
   }

@@ -47,6 +47,11 @@ __device__ __forceinline__ int block_keys(const Rule& a, int b, int* W, int* ctx
   return checked_keys(a, a.kv_len[b], W, ctx, report);
 }
 
+// First context key that a window W > 0 leaves to position p.  The least position of
+// a block's rows is taken over padding, too, whose entries may hold anything: a
+// difference that wraps would hide keys from the other rows.
+__device__ __forceinline__ int window_start(int p, int W) { return p < W ? 0 : p - W + 1; }
+
 // Whether node i's path to the context is sound (its ancestors and itself in
 // the tree).  `parent` points at the block's T entries; every step goes to an
 // earlier node, so the walk ends.
@@ -83,7 +88,7 @@ __device__ __forceinline__ unsigned long long path_bits(const int32_t* parent, c
 // 63 that query i of block b sees.  n, W and ctx are block_keys()'s.
 __device__ __forceinline__ unsigned long long context_bits(const Rule& a, long b, int i, int n, int W,
                                                            int ctx, int j0) {
-  const int lo = W > 0 ? max(0, min(n, a.positions[b * a.T + i] - W + 1) - j0) : 0, hi = min(ctx - j0, 64);
+  const int lo = W > 0 ? max(0, min(n, window_start(a.positions[b * a.T + i], W)) - j0) : 0, hi = min(ctx - j0, 64);
   if (hi <= lo) return 0ull;
   return (hi >= 64 ? ~0ull : (1ull << hi) - 1ull) & (~0ull << lo);
 }

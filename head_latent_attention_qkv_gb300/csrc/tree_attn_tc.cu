@@ -207,7 +207,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   // either's rows see); deeper trees walk again for every tile of nodes' keys.
   // Rows that see nothing are computed like their neighbours and written as
   // zeros, so that they do not take a warp off the unmasked path.
-  const int lo = U.W > 0 ? max(0, R.positions[m] - U.W + 1) : 0;
+  const int lo = U.W > 0 ? tree::window_start(R.positions[m], U.W) : 0;
   float mrun = -INFINITY, lsum = 0.f;
   const bool small = R.T <= 64;
   unsigned long long mine = 0;                            // (small) the nodes that this row sees
@@ -249,7 +249,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
       ok = live && xm[r] != 0.f;
       pair_sync(w);
     }
-    if (sound && first_row) atomicMin(&B->z_lo, U.W > 0 ? max(0, min(pos[nd] - U.W + 1, U.ctx)) : 0);
+    if (sound && first_row) atomicMin(&B->z_lo, U.W > 0 ? min(tree::window_start(pos[nd], U.W), U.ctx) : 0);
   }
   mbar_arrive(&B->seen_full);
   __syncwarp();
@@ -522,7 +522,7 @@ __device__ __forceinline__ void set_up(const TreeParams& P, Bars* B, uint8_t* sm
   U.n = tree::checked_keys(R, kv_len, &U.W, &U.ctx, tid == 0 && U.first && U.qt == 0);
   any = __any_sync(0xffffffffu, any);
   pmin = __reduce_min_sync(0xffffffffu, pmin);
-  U.j_lo = U.W > 0 ? max(0, min(pmin - U.W + 1, U.ctx)) / KT * KT : 0;
+  U.j_lo = U.W > 0 ? min(tree::window_start(pmin, U.W), U.ctx) / KT * KT : 0;
   const int all = any && U.n > 0 ? (U.n - U.j_lo + KT - 1) / KT : 0;
   const int tb = (int)((long)blockIdx.y * all / gridDim.y), te = (int)((long)(blockIdx.y + 1) * all / gridDim.y);
   U.j_lo += tb * KT;

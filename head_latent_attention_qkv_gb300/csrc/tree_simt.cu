@@ -118,7 +118,7 @@ tree_attn_kernel(const tree::Rule a, const float* __restrict__ q_abs, const floa
     int pmin = 0x7fffffff;
     for (int t = r0 / a.H; t <= (r0 + rows - 1) / a.H; ++t) pmin = min(pmin, a.positions[(long)b * a.T + t]);
     // own nodes are held against the nodes' positions: none of them is skipped
-    j_lo = max(0, min(min(n, pmin - W + 1), ctx)) / KT * KT;
+    j_lo = min(min(n, tree::window_start(pmin, W)), ctx) / KT * KT;
   }
   if (j_lo < n) stage_keys(a, cache, b, j_lo, n, L, Es);
   copy_commit();

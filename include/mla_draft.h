@@ -396,8 +396,8 @@ mla_status_t mla_latent_attention_backward(mla_handle_t *h, const void *q_abs,
  * parent: device int32 [num_blocks * block_len], per block: -1 for a child of
  * the context, else the index of an earlier node of the block (parent < node).
  * A node whose parent is below -1 (padding), and every node under it, is not
- * in the tree: its row sees no key and no row sees its key, whose entry may
- * hold anything.  A parent >= the node is reported as MLA_DEV_BAD_TREE and
+ * in the tree: its row sees no key and no row sees its key, whose entry and
+ * position may hold anything.  A parent >= the node is reported as MLA_DEV_BAD_TREE and
  * treated the same.  Node i sees, with q_visible and window as in
  * mla_attn_desc_t, the context keys j with window == 0 or positions[i] - j <
  * window, and of the own keys those of the nodes a on its path from the

@@ -233,6 +233,23 @@ def test_a_nan_that_a_row_sees_reaches_its_output(dtype, heads, ctx):
     assert api.mla_get_device_status(c.h) == 0
 
 
+@pytest.mark.parametrize("dtype,heads", [("fp32", 4), ("bf16", 8), ("bf16", 48)])
+def test_positions_of_rows_that_see_nothing_may_hold_anything(dtype, heads):
+    # a window's first key is worked out from the least position: not from those of
+    # padding, of nodes under padding, or of queries that are masked
+    low = -2 ** 31
+    par = [-1, 0, 0, 1, 3, -2, 5]
+    for tree in (True, False):
+        c = Case(dtype, heads, 16, [700, 650], 7, window=100, masked=True, tree=tree, parents=[par, par])
+        dead = torch.from_numpy(np.stack([~v.any(axis=1) for v in c.vis]).reshape(-1)).cuda()
+        assert dead.sum() == (8 if tree else 4)
+        for junk in (low, low + 50, 2 ** 31 - 1):
+            c.positions[dead] = junk
+            if tree:
+                c.check_attention(*c.attention())
+            c.weights()
+
+
 def test_many_blocks():
     ctx = [(37 * b) % 300 for b in range(75)]
     c = Case("bf16", 4, 16, ctx, 3, padded=True)
