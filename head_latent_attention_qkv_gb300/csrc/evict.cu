@@ -345,12 +345,13 @@ __global__ void __launch_bounds__(MV_THREADS) compact_kernel(const CompactArgs a
       if (s < 0 || s >= n || s < d || s <= prev) {
         set_status(a.status, MLA_DEV_BAD_KEEP);          // not ascending within the sequence: skipped
       } else {
-        if (!a.in_place || s != d) {
+        const bool moves = !a.in_place || s != d;
+        if (moves) {
           ss = slot_of(a, a.block_table + (long)seq * a.max_pages, a.max_pages, s);
           ds = a.in_place ? slot_of(a, a.block_table + (long)seq * a.max_pages, a.max_pages, d)
                           : slot_of(a, a.dst_table + (long)seq * a.dst_pages, a.dst_pages, d);
         }
-        if (a.weights_out) {
+        if (a.weights_out && (!moves || (ss >= 0 && ds >= 0))) {   // a weight goes with its entry
           wt = a.weights[(long)seq * a.ldw + s];
           wt_ok = true;
         }

@@ -220,6 +220,44 @@ def test_compact_leaves_a_sequence_of_a_bad_length_alone(kv):
     assert torch.equal(w[1, :3], w0[1, :3]) and not w[1, 3:].any()
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("bad", [-1, "behind"])
+def test_compact_leaves_rows_of_a_bad_page_alone(dtype, bad, in_place):
+    # neither the entry nor the weight of a row moves when its old or its new page is bad
+    from head_latent_attention_qkv_gb300 import _lib, api
+    from tests.tree_cases import Paged, i32
+    h = handle(dtype, 16)
+    p = Paged(np.random.default_rng(1), h.dims, 16, [80, 60], spare=8)
+    bad = p.num_pages if bad == "behind" else bad
+    keeps = [list(range(0, 80, 2)), list(range(20, 60))]
+    table = p.table.copy()
+    table[0, 2] = bad
+    dst = None
+    if not in_place:
+        dst = p.spare[:6].reshape(2, 3).astype(np.int32).copy()
+        dst[0, 1] = bad
+    w0 = torch.rand(2, 80, device="cuda")
+    w = w0.clone()
+    w_out = w if in_place else torch.full_like(w, -5.0)
+    flat = p.cache.view(-1, h.dims.cache_dim)
+    want, want_w = flat.clone(), w_out.clone()
+    for b, k in enumerate(keeps):
+        want_w[b, len(k):p.lens[b]] = 0.0
+        for d, s in enumerate(k):
+            to = (table if in_place else dst)[b, d // 16]
+            if table[b, s // 16] == bad or to == bad:
+                continue
+            want[int(to) * 16 + d % 16] = flat[int(table[b, s // 16]) * 16 + s % 16]
+            want_w[b, d] = w0[b, s]
+    api.mla_cache_compact(h, p.cache, i32(table), i32(p.lens), i32([k + [-1] * (40 - len(k)) for k in keeps]),
+                          i32([40, 40]), dst_block_table=None if in_place else i32(dst), weights=w, weights_out=w_out)
+    assert api.mla_get_device_status(h) == _lib.MLA_DEV_BAD_PAGE
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    assert torch.equal(flat.view(bits), want.view(bits))
+    assert torch.equal(w_out, want_w)
+
+
 def test_compact_in_place_of_sequences_that_share_a_prompt():
     from head_latent_attention_qkv_gb300 import api
     from tests.tree_cases import Paged, i32
