@@ -22,8 +22,10 @@
 // later ones), so a chunk announces its loads with a flag and waits for the
 // flags of the earlier chunks that read its destination.  Chunks are numbered
 // by a ticket taken when a CTA starts: whoever is waited for has started, and
-// loading waits for nobody, so every wait ends.  2 entry rows of traffic per
-// moved row: HBM bound (64 sequences to 1024 entries of 1152 bytes, 151 MB: 31
+// loading waits for nobody, so every wait ends.  Which chunks to wait for is read
+// from the list, which has to ascend for that: a first kernel, which also clears
+// the flags, looks at every list, and a sequence whose list does not ascend is
+// left alone.  2 entry rows of traffic per moved row: HBM bound (64 sequences to 1024 entries of 1152 bytes, 151 MB: 31
 // us, 4.9 TB/s; 16 rows a CTA, 33 us with 32).
 #include "common.cuh"
 #include "tc_ptx.cuh"
@@ -258,6 +260,7 @@ constexpr int MV_THREADS = 128, MV_UPT = 9;              // units a thread holds
 constexpr int MV_UNITS = MV_THREADS * MV_UPT;            // 1152: 16 rows of 576 bf16
 constexpr int MV_MAX_ROWS = 128;
 constexpr int ZERO_ROWS = 4096;                          // weights a tail chunk clears
+constexpr int LIST_THREADS = 256, LIST_PART = 4096;      // entries of a list that a CTA looks at
 constexpr uint32_t FLAG_BUDGET = 1u << 24;
 
 struct CompactArgs {
@@ -270,7 +273,11 @@ struct CompactArgs {
   int units, rows;            // 16- or 4-byte units of an entry; rows of a chunk
   int data_chunks, chunks;    // per sequence: chunks that may move rows; with those that clear weights
   int in_place;
-  int* ticket;                // [1 + num_seqs * data_chunks] zeroed, or NULL: no chunk waits for another
+  // in place, more than one chunk: the ticket, a flag per sequence and data chunk, and
+  // per sequence and LIST_PART of its list whether that is out of order; else NULL
+  int* ticket;
+  int list_parts;             // parts of a list (0 without a ticket)
+  int num_seqs;
   uint32_t* status;
 };
 
@@ -294,6 +301,31 @@ __device__ __forceinline__ long slot_of(const CompactArgs& a, const int32_t* tab
     return -1;
   }
   return (long)pg * a.page_size + j % a.page_size;
+}
+
+// Ahead of a compaction in place: clears the ticket and the flags, and notes for
+// part `blockIdx.x` (of list_parts a sequence) of the lists whether every entry lies
+// above the one before it and inside the sequence.
+__global__ void __launch_bounds__(LIST_THREADS) compact_lists_kernel(const CompactArgs a) {
+  const long flags = 1 + (long)a.num_seqs * a.data_chunks;
+  for (long i = blockIdx.x * (long)LIST_THREADS + threadIdx.x; i < flags; i += (long)gridDim.x * LIST_THREADS)
+    a.ticket[i] = 0;
+  if (a.list_parts == 0) return;
+  const int seq = blockIdx.x / a.list_parts, part = blockIdx.x % a.list_parts;
+  const int32_t* keep = a.keep + (long)seq * a.ldk;
+  const int n = a.kv_len[seq], first = a.first ? a.first[seq] : 0;
+  const int end = (int)min((long)a.keep_len[seq], a.ldk);
+  int bad = 0;
+#pragma unroll
+  for (int k = 0; k < LIST_PART / LIST_THREADS; ++k) {
+    const int i = part * LIST_PART + k * LIST_THREADS + threadIdx.x;
+    if (i < end) {
+      const int s = keep[i];
+      bad |= s >= n || (i ? s <= keep[i - 1] : s < first);
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) a.ticket[flags + blockIdx.x] = bad;
 }
 
 template <typename V>
@@ -324,6 +356,9 @@ __global__ void __launch_bounds__(MV_THREADS) compact_kernel(const CompactArgs a
   const int32_t* keep = a.keep + (long)seq * a.ldk;
   auto src_of = [&](int d) { return d < first ? d : keep[d - first]; };
   int* flags = a.ticket ? a.ticket + 1 + (long)seq * a.data_chunks : nullptr;
+  int out_of_order = 0;                                  // in place: the list is
+  for (int i = tid; i < a.list_parts; i += MV_THREADS)
+    out_of_order |= a.ticket[1 + (long)a.num_seqs * a.data_chunks + (long)seq * a.list_parts + i];
   const bool data = c < a.data_chunks;
   const int d0 = data ? base + c * a.rows : 0;
   const int rows = data ? min(a.rows, total - d0) : 0;
@@ -344,6 +379,7 @@ __global__ void __launch_bounds__(MV_THREADS) compact_kernel(const CompactArgs a
       long ss = -1, ds = -1;
       if (s < 0 || s >= n || s < d || s <= prev) {
         set_status(a.status, MLA_DEV_BAD_KEEP);          // not ascending within the sequence: skipped
+        out_of_order = 1;
       } else {
         const bool moves = !a.in_place || s != d;
         if (moves) {
@@ -359,7 +395,12 @@ __global__ void __launch_bounds__(MV_THREADS) compact_kernel(const CompactArgs a
       src_slot[tid] = ds < 0 ? -1 : ss;
       dst_slot[tid] = ds;
     }
-    __syncthreads();
+  }
+  if (__syncthreads_or(out_of_order) && a.in_place) {    // (uniform over the sequence's chunks)
+    if (tid == 0) set_status(a.status, MLA_DEV_BAD_KEEP);
+    return;                                              // the sequence is left as it was
+  }
+  if (data) {
     const int live = rows * a.units;
 #pragma unroll
     for (int i = 0; i < MV_UPT; ++i) {
@@ -475,7 +516,8 @@ extern "C" size_t mla_cache_compact_workspace_bytes(const mla_handle_t* h, int32
   if (!h || num_seqs < 0 || ldk < 0) return 0;
   int units, rows;
   evict::chunk_shape((size_t)h->lay.L * h->lay.elt, false, &units, &rows);   // the smaller chunks
-  return align256(((size_t)num_seqs * ((ldk + rows - 1) / rows) + 1) * sizeof(int));
+  const size_t parts = (size_t)((ldk + evict::LIST_PART - 1) / evict::LIST_PART);
+  return align256(((size_t)num_seqs * ((ldk + rows - 1) / rows + parts) + 1) * sizeof(int));
 }
 
 extern "C" mla_status_t mla_cache_compact(mla_handle_t* h, void* cache, int32_t num_pages,
@@ -519,14 +561,17 @@ extern "C" mla_status_t mla_cache_compact(mla_handle_t* h, void* cache, int32_t 
   a.page_size = h->cfg.page_size; a.max_pages = max_pages; a.dst_pages = dst_max_pages;
   a.data_chunks = (int)dc; a.chunks = (int)(dc + zc); a.in_place = in_place; a.status = h->status;
   cudaStream_t st = (cudaStream_t)stream;
-  a.ticket = nullptr;
+  a.num_seqs = num_seqs;
   if (in_place && a.chunks > 1) {
     const size_t need = mla_cache_compact_workspace_bytes(h, num_seqs, ldk);
     if (!workspace || workspace_bytes < need || (uintptr_t)workspace % 256)
       return fail(MLA_ERR_INVALID_ARG,
                   "compact: workspace smaller than mla_cache_compact_workspace_bytes() or not 256-byte aligned");
     a.ticket = (int*)workspace;
-    MLA_CUDA_TRY(cudaMemsetAsync(workspace, 0, ((size_t)num_seqs * dc + 1) * sizeof(int), st));
+    a.list_parts = (int)((ldk + evict::LIST_PART - 1) / evict::LIST_PART);
+    const long parts = (long)num_seqs * a.list_parts;     // (at most as many as there are data chunks)
+    evict::compact_lists_kernel<<<(unsigned)(parts ? parts : 1), evict::LIST_THREADS, 0, st>>>(a);
+    h->launches += 1;
   }
   const unsigned grid = (unsigned)((dc + zc) * num_seqs);
   if (wide)

@@ -491,9 +491,11 @@ mla_status_t mla_cache_select(mla_handle_t *h, const float *weights, int64_t ldw
  *   weights, weights_out: NULL, or device fp32 [num_seqs, ldw], moved the same
  * way (weights_out == weights exactly in place); elements first + keep_len ..
  * kv_len - 1 of weights_out become 0.
- * Reported on the device, the row or sequence left alone: an index that is not
- * ascending or outside its sequence, keep_len > ldk or > kv_len - first
- * (MLA_DEV_BAD_KEEP), a bad page, a kv_len beyond the table or ldw.
+ * Reported on the device: a bad page (the row, its weight too, is left alone),
+ * a kv_len beyond the table or ldw, and (MLA_DEV_BAD_KEEP) keep_len > ldk or >
+ * kv_len - first (the sequence is left alone), and an index outside
+ * its sequence or not above the one before it: in place the whole sequence is
+ * left alone then, into other pages that row.
  * cache: 4-byte aligned (16-byte aligned is faster).
  * workspace: mla_cache_compact_workspace_bytes() bytes, 256-byte aligned,
  * needed in place only; two calls that may overlap on the GPU need two. */

@@ -220,6 +220,55 @@ def test_compact_leaves_a_sequence_of_a_bad_length_alone(kv):
     assert torch.equal(w[1, :3], w0[1, :3]) and not w[1, 3:].any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,at,value", [
+    (400, 15, 3), (400, 16, 5), (400, 31, "same"), (400, 100, 400), (400, 199, -1), (400, 0, -5), (400, 150, 2 ** 30),
+    (30000, 4095, 0), (30000, 4096, "same"), (30000, 14999, 29000), (12, 5, 2), (12, 0, 12)])
+def test_compact_of_a_list_that_does_not_ascend(dtype, n, at, value):
+    # in place a row could be the source of a row that no longer waits for it: the
+    # whole sequence is left alone.  Into other pages only the row is.
+    from head_latent_attention_qkv_gb300 import _lib, api
+    from tests.tree_cases import Paged, i32
+    h = handle(dtype, 16)
+    rng = np.random.default_rng(n + at)
+    k = n // 2
+    keep = np.stack([np.arange(0, n, 2), np.sort(rng.choice(n, k, replace=False))]).astype(np.int32)
+    keep[0, at] = keep[0, at - 1] if value == "same" else value
+    pages = -(-k // 16)
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    for in_place in (True, False):
+        p = Paged(np.random.default_rng(1), h.dims, 16, [n, n], spare=2 * pages)
+        dst = None if in_place else p.spare[:2 * pages].reshape(2, pages).astype(np.int32)
+        w0 = torch.rand(2, n, device="cuda")
+        w = w0.clone()
+        w_out = w if in_place else torch.full_like(w, -5.0)
+        flat = p.cache.view(-1, h.dims.cache_dim)
+        want, want_w = flat.clone(), w_out.clone()
+        for b in range(2):
+            if in_place and b == 0:
+                continue
+            rows = np.arange(k)
+            if b == 0:                                       # an index above the one before it, inside the sequence
+                prev = np.concatenate([[-1], keep[0, :-1]])
+                rows = rows[(keep[0] > prev) & (keep[0] < n) & (keep[0] >= rows)]
+            old = p.slots(b, n).cuda()
+            to = p.slots(b, k, dst).cuda()
+            src = torch.from_numpy(keep[b][rows].astype(np.int64)).cuda()
+            d = torch.from_numpy(rows).cuda()
+            want[to[d]] = flat[old[src]]
+            want_w[b, k:] = 0.0
+            want_w[b, d] = w0[b, src]
+        api.mla_cache_compact(h, p.cache, i32(p.table), i32([n, n]), i32(keep), i32([k, k]),
+                              dst_block_table=None if in_place else i32(dst), weights=w, weights_out=w_out)
+        assert api.mla_get_device_status(h) == _lib.MLA_DEV_BAD_KEEP
+        assert torch.equal(flat.view(bits), want.view(bits)), in_place
+        assert torch.equal(w_out, want_w), in_place
+        if in_place:                                         # without weights (12 keys: a single chunk, no flags)
+            api.mla_cache_compact(h, p.cache, i32(p.table), i32([n, 0]), i32(keep), i32([k, 0]))
+            assert api.mla_get_device_status(h) == _lib.MLA_DEV_BAD_KEEP
+            assert torch.equal(flat.view(bits), want.view(bits))
+
+
 @pytest.mark.parametrize("in_place", [True, False])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("bad", [-1, "behind"])
