@@ -309,7 +309,9 @@ def mla_tree_attention_workspace_bytes(h: Handle, desc) -> int:
 def mla_draft_forward_tree(h: Handle, hidden, positions, block_slot_mapping, cache, desc, parent,
                            out=None, stream=None, workspace=None):
     """mla_draft_forward over trees of drafted tokens (``parent`` as in
-    mla_tree_attention)."""
+    mla_tree_attention).  A ``workspace`` of the caller's keeps the absorbed
+    queries and their log-sum-exps for mla_key_weights
+    (mla_forward_workspace_offset, MLA_WS_Q_ABS and MLA_WS_LSE)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return mla_draft_forward_tree(h, hidden, positions, block_slot_mapping, cache, desc, parent, out,

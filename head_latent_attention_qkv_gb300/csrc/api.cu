@@ -461,6 +461,10 @@ tree::Rule tree_rule(const mla_handle* h, const int32_t* positions, int num_page
                     h->cfg.page_size, d.max_pages, d.block_len, h->lay.H, h->status};
 }
 
+// Behind a forward's workspace, that of the layer over trees: the rows' log-sum-exps,
+// then what the attention itself needs.
+size_t tree_lse_bytes(const mla_handle* h, long M) { return align256((size_t)M * h->lay.H * sizeof(float)); }
+
 // The attention of trees (mla_draft.h); `ws`: tree_ws() bytes.
 size_t tree_ws(const mla_handle* h, const mla_attn_desc_t& d) {
   return h->cfg.dtype == MLA_BF16 ? tc::tree_attention_ws(h, d) : 0;
@@ -588,7 +592,8 @@ mla_status_t forward_impl(mla_handle_t* h, const void* hidden, const int32_t* po
   // launch after the wait: no programmatic edge crosses it)
   if (kv_ready) MLA_CUDA_TRY(cudaStreamWaitEvent(st, kv_ready, 0));
   if (parent) {
-    s = tree_attention(h, st, q_abs, pos, cache, num_pages, d, parent, o_lat, nullptr, ws + w.total, pdl);
+    s = tree_attention(h, st, q_abs, pos, cache, num_pages, d, parent, o_lat, (float*)(ws + w.total),
+                       ws + w.total + tree_lse_bytes(h, M), pdl);
     if (s != MLA_OK) return s;
     h->launches -= 1;     // counted with the other non-GEMM kernels below
   } else if constexpr (std::is_same<TX, float>::value) {
@@ -791,7 +796,8 @@ extern "C" mla_status_t mla_tree_attention(mla_handle_t* h, const void* q_abs,
 
 extern "C" size_t mla_forward_tree_workspace_bytes(const mla_handle_t* h, const mla_attn_desc_t* desc) {
   if (!h || !desc || desc->num_blocks <= 0 || desc->block_len <= 0 || desc->max_pages <= 0) return 0;
-  return forward_ws(h, (long)desc->num_blocks * desc->block_len).total + tree_ws(h, *desc);
+  const long M = (long)desc->num_blocks * desc->block_len;
+  return forward_ws(h, M).total + tree_lse_bytes(h, M) + tree_ws(h, *desc);
 }
 
 extern "C" mla_status_t mla_draft_forward_tree(mla_handle_t* h, const void* hidden,
@@ -874,6 +880,7 @@ extern "C" size_t mla_forward_workspace_offset(const mla_handle_t* h, int32_t nu
     case MLA_WS_Q_ABS: return w.q_abs;
     case MLA_WS_O_LAT: return w.o_lat;
     case MLA_WS_O: return w.o;
+    case MLA_WS_LSE: return w.total;
     default: return (size_t)-1;
   }
 }

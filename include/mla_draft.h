@@ -81,7 +81,7 @@ enum {
 
 /* Intermediate tensors the forward leaves in its workspace
  * (mla_forward_workspace_offset). */
-enum { MLA_WS_Q_ABS = 0, MLA_WS_O_LAT = 1, MLA_WS_O = 2 };
+enum { MLA_WS_Q_ABS = 0, MLA_WS_O_LAT = 1, MLA_WS_O = 2, MLA_WS_LSE = 3 };
 
 /* Layer configuration.  Structural dims follow the HF DeepSeek-V2/V3 fields;
  * q_lora_rank == 0 selects the non-low-rank path (q_proj +
@@ -325,7 +325,9 @@ int64_t mla_append_noalloc_max_tokens(const mla_handle_t *h);
  * MLA_WS_O_LAT, the latent attention output [num_tokens, H, kv_lora_rank]
  * (fp16 for bf16 layers, fp32 for fp32 layers), or MLA_WS_O, the per-head
  * output [num_tokens, H, v_head_dim] that o_proj reads (same types; in a
- * workspace of mla_draft_forward_shared too, at the same offsets).  Valid after the forward's
+ * workspace of mla_draft_forward_shared too, at the same offsets); in a
+ * workspace of mla_draft_forward_tree only (the others end there), MLA_WS_LSE,
+ * the log-sum-exp of its attention's rows, fp32 [num_tokens, H].  Valid after the forward's
  * work on the stream has completed, until the workspace is reused.  Returns
  * (size_t)-1 for a NULL handle, a negative count or an unknown part. */
 size_t mla_forward_workspace_offset(const mla_handle_t *h, int32_t num_tokens,
@@ -428,7 +430,9 @@ mla_status_t mla_tree_attention(mla_handle_t *h, const void *q_abs, const int32_
  * its attention (same arguments, results and errors; block_slot_mapping
  * writes the nodes' own entries first; padding nodes take a free slot of
  * their own and a position inside the table).  cache must be 16-byte aligned,
- * on fp32 layers too. */
+ * on fp32 layers too.  The workspace keeps the absorbed queries and their
+ * log-sum-exps (mla_forward_workspace_offset, MLA_WS_Q_ABS and MLA_WS_LSE),
+ * from which mla_key_weights goes on. */
 size_t mla_forward_tree_workspace_bytes(const mla_handle_t *h, const mla_attn_desc_t *desc);
 mla_status_t mla_draft_forward_tree(mla_handle_t *h, const void *hidden,
                                     const int32_t *positions,
