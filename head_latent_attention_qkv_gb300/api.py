@@ -228,14 +228,17 @@ def _take(name, t, dtype, shape, h):
     return t.data_ptr()
 
 
-_empty_strided_cuda = torch._C._dynamo.guards._empty_strided_cuda
+# torch's allocation without the dispatcher: not a public name, so a torch that
+# lacks it takes torch.empty
+_empty_strided_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 
 
 def _new(h: Handle, shape, dtype):
-    """An uninitialised tensor on the handle's device.  Right after a launch
-    torch.empty takes 5 us of host time and this allocation of the same pool 2;
-    it takes place on the current device, which a handle needs to be its own."""
-    if torch._C._cuda_getDevice() != h.device_index:
+    """An uninitialised tensor on the handle's device, of which the call writes
+    every element.  Right after a launch torch.empty takes 5 us of host time and
+    the other allocation of the same pool 2; that one takes place on the current
+    device, which a handle needs to be its own."""
+    if _empty_strided_cuda is None or torch._C._cuda_getDevice() != h.device_index:
         return torch.empty(shape, dtype=dtype, device=h.device)
     return _empty_strided_cuda(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype)
 
