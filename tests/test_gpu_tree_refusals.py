@@ -97,3 +97,56 @@ def test_compaction_refuses_a_cache_that_splits_words(dtype, heads):
     torch.cuda.synchronize()
     assert api.mla_get_device_status(c.h) == 0
     assert torch.equal(rows, want)
+
+
+# Plans that need a workspace: a long sequence of few rows (parts to be merged), of
+# pairs of row tiles, and row parts of the key weights.
+WORKSPACES = [("tree", 16, 9000, 4), ("layer", 16, 8000, 4), ("tree", 48, 9000, 7), ("layer", 48, 8000, 7),
+              ("weights", 128, 1000, 16)]
+
+
+@pytest.mark.parametrize("what,heads,ctx,nodes", WORKSPACES)
+def test_workspaces_that_are_missing_short_or_not_aligned_are_refused(what, heads, ctx, nodes):
+    from head_latent_attention_qkv_gb300 import _lib, api
+    from head_latent_attention_qkv_gb300._lib import lib
+    c = Layer("bf16", heads, ctx, nodes)
+    stream = torch.cuda.current_stream().cuda_stream
+    q = torch.zeros(c.rows, c.h.dims.cache_dim, dtype=torch.bfloat16, device="cuda")
+    o = torch.zeros(c.rows, 512, dtype=torch.float16, device="cuda")
+    lse, ldw = torch.zeros(c.rows, device="cuda"), c.pages * 16
+    w = torch.zeros(1, ldw, device="cuda")
+    if what == "tree":
+        need = api.mla_tree_attention_workspace_bytes(c.h, c.desc)
+
+        def run(ws, n):
+            return lib.mla_tree_attention(c.h.h, q.data_ptr(), c.positions.data_ptr(), c.store.data_ptr(), c.pages,
+                                          c.ref, c.parent.data_ptr(), o.data_ptr(), lse.data_ptr(), ws, n, stream)
+    elif what == "layer":
+        need = api.mla_forward_tree_workspace_bytes(c.h, c.desc)
+        plain = api.mla_tree_attention_workspace_bytes(c.h, c.desc)
+        lse_at = api.mla_forward_workspace_offset(c.h, nodes, _lib.MLA_WS_LSE)
+        assert plain > 0 and need >= lse_at + 4 * c.rows + plain
+
+        def run(ws, n):
+            return lib.mla_draft_forward_tree(c.h.h, c.hidden.data_ptr(), c.positions.data_ptr(), None,
+                                              c.store.data_ptr(), c.pages, c.ref, c.parent.data_ptr(),
+                                              c.out.data_ptr(), ws, n, stream)
+    else:
+        need = api.mla_key_weights_workspace_bytes(c.h, c.desc, ldw)
+
+        def run(ws, n):
+            return lib.mla_key_weights(c.h.h, q.data_ptr(), c.positions.data_ptr(), c.store.data_ptr(), c.pages, c.ref,
+                                       c.parent.data_ptr(), lse.data_ptr(), 1.0, None, w.data_ptr(), ldw, ws, n, stream)
+    assert need > 0
+    buf = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+    at = buf.data_ptr()
+    assert at % 256 == 0
+    before = c.launches()
+    for ws, n in ((None, need), (None, 0), (at, need - 1), (at, 0), (at + 16, need), (at + 128, need + 128)):
+        assert run(ws, n) == _lib.MLA_ERR_INVALID_ARG, (ws, n)
+        assert b"workspace" in lib.mla_last_error() or ws is None
+    assert c.launches() == before                              # nothing was launched
+    assert run(at, need) == _lib.MLA_OK
+    assert run(at + 256, need) == _lib.MLA_OK
+    torch.cuda.synchronize()
+    assert api.mla_get_device_status(c.h) == 0 and c.launches() > before
