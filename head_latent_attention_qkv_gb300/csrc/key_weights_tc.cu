@@ -20,7 +20,7 @@
 // of rows without a window need no mask; otherwise every lane works out the 32
 // keys of its warp for four columns (tree::key_bits) and the words are
 // broadcast.  A step of the issuing thread (a barrier, four MMAs, a commit)
-// takes about 530 cycles however few the columns, so blocks of at most 84 rows
+// takes about 530 cycles however few the columns, so blocks of at most 64 rows
 // bring Q in three chunks a slot (64 sequences x 32 rows x 1-4 k keys: 53 us
 // against 57 with one, 43 with the items looked up by the key warp, 41 with the
 // log-sum-exps read ahead: 4.6 TB/s of cache).  2048 rows x 8 k keys x 4 sequences:
@@ -485,7 +485,8 @@ mla_status_t key_weights(cudaStream_t st, mla_handle* h, const tree::Rule& r, co
   const long block_rows = (long)r.T * r.H;
   P.q_box_rows = (int)((block_rows < NMAX ? (block_rows + 31) & ~31L : NMAX) / 2);
   P.seg_rows = r.page_size < KT ? r.page_size : KT;
-  // 84 rows: 3 chunks of up to 42 rows a CTA fit a slot
+  // up to 64 rows: 3 chunks of at most 32 rows a CTA (rows go up to whole 16s a CTA, the
+  // next, 48, would take 18 KB) fit a slot of 16 KB
   const int qc = 3 * P.q_box_rows * 128 <= CH_BYTES ? 3 : 1;
   if (!make_tmap_chunked(&P.tmQ, false, q_abs, rows, l.L, l.L, P.q_box_rows, qc) ||
       !make_tmap_chunked(&P.tmC, false, cache, slots, l.L, l.L, KT, 3) ||

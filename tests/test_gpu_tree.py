@@ -266,6 +266,13 @@ def test_rows_of_a_block_around_the_sizes_of_its_tile(heads, T, page):
     c.weights()
 
 
+@pytest.mark.parametrize("rows", [32, 33, 64, 65, 66, 80, 84, 85, 96, 97])
+def test_key_weights_around_the_rows_that_share_a_slot(rows):
+    # up to 64 rows a block bring three chunks of Q at once, more bring one
+    Case("bf16", 1, 64, [700, 255, 0], rows, padded=True).weights()
+    Case("bf16", rows, 128, [900], 1, tree=False).weights()
+
+
 @pytest.mark.parametrize("heads,T,n,window", [(16, 9, 40, 0), (4, 5, 83, 0), (16, 9, 79, 700)])
 def test_blocks_of_a_last_wave_cut_in_parts(heads, T, n, window):
     # more clusters than the GPU holds: the last wave's are a launch of their own
