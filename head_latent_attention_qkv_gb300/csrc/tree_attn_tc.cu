@@ -10,7 +10,8 @@
 //    value half; their MMAs run as one over the pair (cta_group::2), so each
 //    CTA fetches and reads half of the keys' and values' bytes (2560 cycles of
 //    shared-memory traffic a tile against 3328 of MMAs).  8192 rows x 6-8 k keys x
-//    4 sequences: 434 us, 1.17 PFLOP/s on the algorithm's flops;
+//    4 sequences: 457 us, 1.1 PFLOP/s on the algorithm's flops, at an SM clock of
+//    2.07 GHz (462 at the 1.93 GHz of a second of such calls);
 //  - tree_attn_tc_kernel, blocks of at most 128 rows: one row tile, a CTA per
 //    value half (4224 cycles of shared-memory traffic a tile, and a slot's next
 //    copy waits for P V, 2 k cycles from L2: 6 to 7 k cycles a tile).  Blocks of at
@@ -254,7 +255,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& P, Bars* B, uint8
   mbar_arrive(&B->seen_full);
   __syncwarp();
   // a warp without rows: its P stays undefined.  (Not in pairs, where it is rare and
-  // the test alone made the loop slower: 128 heads x 64 nodes 434 -> 445 us)
+  // the test alone made the loop of 128 heads x 64 nodes 2.5% slower)
   const bool dead = U.qt * QROWS + 32 * w >= R.T * R.H;
   for (int t = 0; t < U.nt; ++t) {
     const int jh = tile_key(U, t) + KH * kh;              // first key of this thread's half
@@ -994,16 +995,19 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict
 // MERGE and MERGE_PART for the second kernel.  Measured, us: 512 rows x 2064
 // keys x 8 sequences 45 whole, 39 in two parts merged, 35 in two joined; 8192
 // rows x 6-8 k keys x 4 sequences 468, 513, 528; 128 rows x 32 k keys 45 in 32
-// parts, 37 in 48, 35 in 56 or 64, 37 in 60 joined by fours.  Keys are bounded by
-// the page table (shorter sequences only split finer than they need) and, when
-// windows are given, taken as at most 16 tiles, since the windows are on the
-// device: 800 rows x 5 sequences with a window of 512 keys 28 us whole, 37 in
-// three parts.
+// parts, 37 in 48, 35 in 56 or 64, 37 in 60 joined by fours.  The lengths and
+// windows are on the device: keys are bounded by the page table and, when windows
+// are given, taken as at most 16 tiles (800 rows x 5 sequences with a window of 512
+// keys 28 us whole, 37 in three parts).  Both can be far off.  A table much wider
+// than its sequences splits them too finely (512 rows x 2064 keys x 8 sequences
+// under a table of 131072 keys: 16 parts, 147 us for 35, and a workspace of 135 MB),
+// and long ranges beside windows, or windows of 0, too coarsely (128 rows x 32 k
+// keys with a window tensor of zeros: 65 us for 35).
 //
 // Clusters of whole units that do not fill their last wave have that wave's
 // units cut in parts of a second launch, joined in clusters: 256 clusters, of
-// which the GPU holds 76, 434 us in two launches (28 of them in two parts), 466 in
-// one.
+// which the GPU holds 76, 457 us in two launches (28 of them in two parts), 484 in
+// one; 80 clusters 61 and 75, both at 2.07 GHz and in turns.
 struct Plan {
   bool pair;
   int parts, cluster_parts;

@@ -418,7 +418,10 @@ mla_status_t mla_latent_attention_backward(mla_handle_t *h, const void *q_abs,
  *   s_j = scale * <q_abs[m], entry_j>,  o_lat = sum_j softmax(s)_j entry_j[:r],
  *   lse = log sum_j exp(s_j)
  * workspace: mla_tree_attention_workspace_bytes() bytes, 256-byte aligned
- * (NULL when that is 0). */
+ * (NULL when that is 0).  The launch and its workspace are planned from
+ * max_pages and from whether window is NULL, since lengths and windows are on
+ * the device: a table much wider than its sequences, and windows that leave
+ * long ranges (0 among them), are right but slower. */
 size_t mla_tree_attention_workspace_bytes(const mla_handle_t *h, const mla_attn_desc_t *desc);
 mla_status_t mla_tree_attention(mla_handle_t *h, const void *q_abs, const int32_t *positions,
                                 const void *cache, int32_t num_pages,
