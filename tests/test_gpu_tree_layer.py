@@ -75,6 +75,7 @@ CASES = [
     ("bf16", 16, [2000] * 3 + [1700, 900, 2044, 0, 1990], 32, 1, dict(page=16)),   # parts joined in their clusters
     ("bf16", 16, [2000 - 61 * (b % 29) for b in range(40)], 9, 2, dict(page=64)),  # a last wave's launch
     ("bf16", 32, [2500, 1300, 700], 12, 1, dict(page=64, window=300, masked=True)),
+    ("bf16", 16, [40 + b % 50 for b in range(110)], 64, 1, dict(page=64)),         # enough tokens for the fused append
 ]
 
 
