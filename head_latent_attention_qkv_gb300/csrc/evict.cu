@@ -26,7 +26,7 @@
 // from the list, which has to ascend for that: a first kernel, which also clears
 // the flags, looks at every list, and a sequence whose list does not ascend is
 // left alone.  2 entry rows of traffic per moved row: HBM bound (64 sequences to 1024 entries of 1152 bytes, 151 MB: 31
-// us, 4.9 TB/s; 16 rows a CTA, 33 us with 32).  In place the same takes 55 us: the
+// us, 4.9 TB/s; 16 rows a CTA, 33 us with 32).  In place the same takes 53 us: the
 // lists' kernel, the tickets and the waits for earlier chunks' loads.
 #include "common.cuh"
 #include "tc_ptx.cuh"
@@ -308,6 +308,7 @@ __device__ __forceinline__ long slot_of(const CompactArgs& a, const int32_t* tab
 // part `blockIdx.x` (of list_parts a sequence) of the lists whether every entry lies
 // above the one before it and inside the sequence.
 __global__ void __launch_bounds__(LIST_THREADS) compact_lists_kernel(const CompactArgs a) {
+  pdl_trigger();
   const long flags = 1 + (long)a.num_seqs * a.data_chunks;
   for (long i = blockIdx.x * (long)LIST_THREADS + threadIdx.x; i < flags; i += (long)gridDim.x * LIST_THREADS)
     a.ticket[i] = 0;
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(MV_THREADS) compact_kernel(const CompactArgs a
   __shared__ long src_slot[MV_MAX_ROWS], dst_slot[MV_MAX_ROWS];
   __shared__ int s_ticket, s_ok;
   const int tid = threadIdx.x;
+  pdl_wait();                                            // (in place: compact_lists_kernel)
   if (tid == 0) {
     s_ticket = a.ticket ? atomicAdd(a.ticket, 1) : (int)blockIdx.x;
     s_ok = 1;
@@ -572,14 +574,12 @@ extern "C" mla_status_t mla_cache_compact(mla_handle_t* h, void* cache, int32_t 
     a.list_parts = (int)((ldk + evict::LIST_PART - 1) / evict::LIST_PART);
     const long parts = (long)num_seqs * a.list_parts;     // (at most as many as there are data chunks)
     evict::compact_lists_kernel<<<(unsigned)(parts ? parts : 1), evict::LIST_THREADS, 0, st>>>(a);
+    MLA_CUDA_TRY(cudaGetLastError());
     h->launches += 1;
   }
   const unsigned grid = (unsigned)((dc + zc) * num_seqs);
-  if (wide)
-    evict::compact_kernel<uint4><<<grid, evict::MV_THREADS, 0, st>>>(a);
-  else
-    evict::compact_kernel<uint32_t><<<grid, evict::MV_THREADS, 0, st>>>(a);
-  MLA_CUDA_TRY(cudaGetLastError());
+  Launch L(dim3(grid), dim3(evict::MV_THREADS), 0, st, a.ticket != nullptr);
+  MLA_CUDA_TRY(cudaLaunchKernelEx(&L.cfg, wide ? evict::compact_kernel<uint4> : evict::compact_kernel<uint32_t>, a));
   h->launches += 1;
   return MLA_OK;
 }
