@@ -13,11 +13,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmla_draft.so")
 
 MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA, MLA_ERR_DEVICE_CHECK, MLA_ERR_TIMEOUT = range(6)
-MLA_BF16, MLA_FP32 = 0, 1
+MLA_BF16, MLA_FP32, MLA_FP16 = 0, 1, 2
 MLA_ROPE_NEOX, MLA_ROPE_INTERLEAVED = 0, 1
 MLA_DEV_BAD_SLOT, MLA_DEV_BAD_POSITION, MLA_DEV_BAD_PAGE, MLA_DEV_TIMEOUT, MLA_DEV_BAD_LENGTH = 1, 2, 4, 8, 16
 MLA_DEV_BAD_WINDOW = 32
-MLA_DEV_BAD_TREE, MLA_DEV_BAD_KEEP = 64, 128
+MLA_DEV_BAD_TREE, MLA_DEV_BAD_KEEP, MLA_DEV_BAD_DRAFT = 64, 128, 256
 MLA_WS_Q_ABS, MLA_WS_O_LAT, MLA_WS_O, MLA_WS_LSE = 0, 1, 2, 3
 
 
@@ -46,6 +46,10 @@ class mla_attn_desc_t(C.Structure):
 class mla_shared_ctx_t(C.Structure):
     _fields_ = [("num_ctx", C.c_int32), ("ctx_rows", C.c_int32), ("ctx_len", C.c_void_p),
                 ("ctx_block_start", C.c_void_p)]
+
+
+class mla_cache8_t(C.Structure):
+    _fields_ = [("latent", C.c_void_p), ("rope", C.c_void_p), ("scale", C.c_void_p)]
 
 
 class MLAError(RuntimeError):
@@ -103,6 +107,18 @@ def _load():
         "mla_cache_compact_workspace_bytes": (SZ, [P, I32, C.c_int64]),
         "mla_cache_compact": (I32, [P, P, I32, P, I32, P, I32, P, C.c_int64, P, P, P, I32, P, P,
                                     C.c_int64, P, SZ, P]),
+        "mla_cache8_store": (I32, [P, P, P, I32, C.POINTER(mla_cache8_t), I32, P]),
+        "mla_cache8_load": (I32, [P, C.POINTER(mla_cache8_t), I32, P, I32, P, P]),
+        "mla_append8_workspace_bytes": (SZ, [P, I32]),
+        "mla_latent_cache_append8": (I32, [P, P, P, P, I32, C.POINTER(mla_cache8_t), I32, P, SZ, P]),
+        "mla_latent_attention8_workspace_bytes": (SZ, [P, C.POINTER(mla_attn_desc_t)]),
+        "mla_latent_attention8": (I32, [P, P, P, C.POINTER(mla_cache8_t), I32, C.POINTER(mla_attn_desc_t),
+                                        P, P, P, P, SZ, P]),
+        "mla_forward8_workspace_bytes": (SZ, [P, C.POINTER(mla_attn_desc_t)]),
+        "mla_draft_forward8": (I32, [P, P, P, P, C.POINTER(mla_cache8_t), I32, C.POINTER(mla_attn_desc_t),
+                                     P, P, P, SZ, P]),
+        "mla_verify_drafts": (I32, [P, P, C.c_int64, P, C.c_int64, I32, P, P, P, P, I32, I32, I32, P, P, P,
+                                    P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

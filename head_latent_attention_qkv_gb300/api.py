@@ -8,6 +8,7 @@ layer's dtype (weights, hidden, cache, out) or int32/int64/uint8 for indices.
 from __future__ import annotations
 
 import ctypes as C
+from typing import NamedTuple
 
 import torch
 
@@ -415,6 +416,174 @@ def mla_cache_compact(h: Handle, cache, block_table, kv_len, keep, keep_len, fir
 
 def mla_cache_compact_workspace_bytes(h: Handle, num_seqs: int, ldk: int) -> int:
     return int(lib.mla_cache_compact_workspace_bytes(h.h, num_seqs, ldk))
+
+
+class Cache8(NamedTuple):
+    """The latent cache in 8 bits (mla_cache8_t): an entry stands for latent *
+    scale and rope."""
+    latent: torch.Tensor      # float8_e4m3fn [num_pages, page_size, 512]
+    rope: torch.Tensor        # bfloat16 [num_pages, page_size, 64]
+    scale: torch.Tensor       # float32 [num_pages, page_size]
+
+
+def make_cache8(h: Handle, num_pages: int) -> Cache8:
+    """An 8-bit cache of ``num_pages`` pages whose entries are all zero."""
+    def zeros(*width, dtype):
+        return torch.zeros(num_pages, h.page_size, *width, dtype=dtype, device=h.device)
+    return Cache8(zeros(h.dims.kv_lora_rank, dtype=torch.uint8).view(torch.float8_e4m3fn),
+                  zeros(h.dims.qk_rope_head_dim, dtype=torch.bfloat16), zeros(dtype=torch.float32) + 1)
+
+
+def _take_cache8(h: Handle, c: Cache8):
+    """The cache's C form, by reference, and its pages."""
+    n, d = c.scale.shape[0], h.dims
+    s = _lib.mla_cache8_t(
+        _take("cache latent", c.latent, torch.float8_e4m3fn, (n, h.page_size, d.kv_lora_rank), h),
+        _take("cache rope", c.rope, torch.bfloat16, (n, h.page_size, d.qk_rope_head_dim), h),
+        _take("cache scale", c.scale, torch.float32, (n, h.page_size), h))
+    return C.byref(s), n
+
+
+def mla_cache8_store(h: Handle, entries, slot_mapping, cache: Cache8, stream=None):
+    """bf16 ``entries`` [n, 576] into the slots ``slot_mapping`` (int64 [n]) of the 8-bit cache."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mla_cache8_store(h, entries, slot_mapping, cache)
+    n = slot_mapping.shape[0]
+    _run(lib.mla_cache8_store, h, _take("entries", entries, torch.bfloat16, (n, h.dims.cache_dim), h),
+         _take("slot_mapping", slot_mapping, torch.int64, (n,), h), n, *_take_cache8(h, cache))
+
+
+def mla_cache8_load(h: Handle, cache: Cache8, slot_mapping, out=None, stream=None):
+    """The entries of the slots ``slot_mapping`` (int64 [n]) in bf16, [n, 576]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mla_cache8_load(h, cache, slot_mapping, out)
+    n, width = slot_mapping.shape[0], h.dims.cache_dim
+    if out is None:
+        out = torch.zeros(n, width, dtype=torch.bfloat16, device=h.device)   # (bad slots leave their rows)
+    _run(lib.mla_cache8_load, h, *_take_cache8(h, cache),
+         _take("slot_mapping", slot_mapping, torch.int64, (n,), h), n,
+         _take("out", out, torch.bfloat16, (n, width), h))
+    return out
+
+
+def mla_latent_cache_append8(h: Handle, hidden, positions, slot_mapping, cache: Cache8, stream=None,
+                             workspace=None):
+    """mla_latent_cache_append into the 8-bit cache."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mla_latent_cache_append8(h, hidden, positions, slot_mapping, cache, None, workspace)
+    n = slot_mapping.shape[0]
+    args = (_take("hidden", hidden, torch_dtype(h.dims), (n, h.dims.hidden_size), h),
+            _take("positions", positions, torch.int32, (n,), h),
+            _take("slot_mapping", slot_mapping, torch.int64, (n,), h), n, *_take_cache8(h, cache))
+    if workspace is None:
+        workspace = _new_workspace(h, lib.mla_append8_workspace_bytes(h.h, n))
+    _run(lib.mla_latent_cache_append8, h, *args, *_take_workspace(workspace, h))
+
+
+def mla_append8_workspace_bytes(h: Handle, n: int) -> int:
+    return int(lib.mla_append8_workspace_bytes(h.h, n))
+
+
+def mla_latent_attention8(h: Handle, q_abs, positions, cache: Cache8, desc, parent=None, o_lat=None,
+                          lse=None, stream=None, workspace=None):
+    """mla_latent_attention, or mla_tree_attention where ``parent`` is given, over the
+    8-bit cache: ``o_lat`` fp16 [rows, kv_lora_rank] and, when ``lse`` is given, its
+    fp32 [rows] log-sum-exp."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mla_latent_attention8(h, q_abs, positions, cache, desc, parent, o_lat, lse, None, workspace)
+    d, tokens = h.dims, desc.num_blocks * desc.block_len
+    rows = tokens * d.num_heads
+    if q_abs.numel() != rows * d.cache_dim:
+        raise ValueError(f"q_abs: expected {rows} rows of {d.cache_dim}, got {tuple(q_abs.shape)}")
+    c, num_pages = _take_cache8(h, cache)
+    q = _take("q_abs", q_abs, torch.bfloat16, q_abs.shape, h)
+    pos = _take("positions", positions, torch.int32, (tokens,), h)
+    par = None if parent is None else _take("parent", parent, torch.int32, (tokens,), h)
+    lse_p = None if lse is None else _take("lse", lse, torch.float32, (rows,), h)
+    if o_lat is None:
+        o_lat = _new(h, (rows, d.kv_lora_rank), torch.float16)
+    out = _take("o_lat", o_lat, torch.float16, (rows, d.kv_lora_rank), h)
+    ref = C.byref(desc)
+    if workspace is None:
+        workspace = _new_workspace(h, lib.mla_latent_attention8_workspace_bytes(h.h, ref))
+    _run(lib.mla_latent_attention8, h, q, pos, c, num_pages, ref, par, out, lse_p,
+         *_take_workspace(workspace, h))
+    return o_lat
+
+
+def mla_latent_attention8_workspace_bytes(h: Handle, desc) -> int:
+    return int(lib.mla_latent_attention8_workspace_bytes(h.h, C.byref(desc)))
+
+
+def mla_draft_forward8(h: Handle, hidden, positions, block_slot_mapping, cache: Cache8, desc, parent=None,
+                       out=None, stream=None, workspace=None):
+    """mla_draft_forward, or mla_draft_forward_tree where ``parent`` is given, over the 8-bit cache."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mla_draft_forward8(h, hidden, positions, block_slot_mapping, cache, desc, parent, out, None,
+                                      workspace)
+    D, dt, M = h.dims.hidden_size, torch_dtype(h.dims), desc.num_blocks * desc.block_len
+    c, num_pages = _take_cache8(h, cache)
+    args = (_take("hidden", hidden, dt, (M, D), h), _take("positions", positions, torch.int32, (M,), h),
+            None if block_slot_mapping is None else
+            _take("block_slot_mapping", block_slot_mapping, torch.int64, (M,), h))
+    par = None if parent is None else _take("parent", parent, torch.int32, (M,), h)
+    if out is None:
+        out = _new(h, (M, D), dt)
+    ref = C.byref(desc)
+    if workspace is None:
+        workspace = _new_workspace(h, lib.mla_forward8_workspace_bytes(h.h, ref))
+    _run(lib.mla_draft_forward8, h, *args, c, num_pages, ref, par, _take("out", out, dt, (M, D), h),
+         *_take_workspace(workspace, h))
+    return out
+
+
+def mla_forward8_workspace_bytes(h: Handle, desc) -> int:
+    return int(lib.mla_forward8_workspace_bytes(h.h, C.byref(desc)))
+
+
+_PROBABILITIES = {torch.float32: _lib.MLA_FP32, torch.bfloat16: _lib.MLA_BF16, torch.float16: _lib.MLA_FP16}
+
+
+def _take_probabilities(name, t, n, rows, vocab, dtype, h):
+    """The pointer and row stride of probabilities [n, rows, vocab], whose rows may be
+    parts of longer ones."""
+    if (t.shape != (n, rows, vocab) or t.dtype is not dtype or t.get_device() != h.device_index or
+            t.stride(2) != 1 or t.stride(1) < vocab or t.stride(0) != rows * t.stride(1)):
+        raise ValueError(f"{name}: expected {dtype} {(n, rows, vocab)} on cuda:{h.device_index}, rows evenly "
+                         f"spaced and contiguous, got {t.dtype} {tuple(t.shape)} of strides {t.stride()} on "
+                         f"{t.device}")
+    return t.data_ptr(), t.stride(1)
+
+
+def mla_verify_drafts(h: Handle, target, draft, tokens, uniforms, parent=None, first=None, stream=None):
+    """``(accepted, num_accepted, next_token)`` of drafted tokens (int32 [n, T]) against the
+    probabilities ``target`` [n, T + 1, vocab] and ``draft`` [n, T, vocab] (None: the
+    tokens were certain) by the random numbers ``uniforms`` (fp32 [n, T + 1]).
+    ``parent``: int32 [n, T], None a chain; ``first``: int32 [n], added to the taken
+    nodes, so that they are mla_cache_compact's ``keep``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mla_verify_drafts(h, target, draft, tokens, uniforms, parent, first)
+    (n, T), vocab, i32 = tokens.shape, target.shape[-1], torch.int32
+    if target.dtype not in _PROBABILITIES:
+        raise ValueError(f"target: expected fp32, bf16 or fp16 probabilities, got {target.dtype}")
+    if n == 0 or T == 0:                               # (a stride of no rows says nothing)
+        draft = None
+    p, ldt = ((target.data_ptr(), vocab) if n == 0 else
+              _take_probabilities("target", target, n, T + 1, vocab, target.dtype, h))
+    q, ldd = (None, 0) if draft is None else _take_probabilities("draft", draft, n, T, vocab, target.dtype, h)
+    tok, u = _take("tokens", tokens, i32, (n, T), h), _take("uniforms", uniforms, torch.float32, (n, T + 1), h)
+    par = None if parent is None else _take("parent", parent, i32, (n, T), h)
+    fst = None if first is None else _take("first", first, i32, (n,), h)
+    accepted, count, token = _new(h, (n, T), i32), _new(h, (n,), i32), _new(h, (n,), i32)
+    _run(lib.mla_verify_drafts, h, p, ldt, q, ldd, _PROBABILITIES[target.dtype], tok, par, u, fst, n, T, vocab,
+         accepted.data_ptr(), count.data_ptr(), token.data_ptr())
+    return accepted, count, token
 
 
 def mla_check_wait_timeout(h: Handle, max_rounds: int, gave_up, stream=None):

@@ -10,6 +10,7 @@
 #include "common.cuh"
 #include "append_tc.cuh"
 #include "attn_tc.cuh"
+#include "cache8.cuh"
 #include "decode_tc.cuh"
 #include "expand_tc.cuh"
 #include "gemm_tc.cuh"
@@ -449,6 +450,39 @@ extern "C" mla_status_t mla_latent_cache_append(mla_handle_t* h, const void* hid
   return MLA_OK;
 }
 
+extern "C" size_t mla_append8_workspace_bytes(const mla_handle_t* h, int32_t n) {
+  return (h && n >= 0) ? align256((size_t)n * h->lay.L * 4) : 0;
+}
+
+// Always the projection into a workspace and the row kernel: the fused kernel's epilogue
+// would need a second meeting of its cluster for the row's largest magnitude, and
+// the fp32 rows cost 2.3 KB a token beside 2 D 576 flops.
+extern "C" mla_status_t mla_latent_cache_append8(mla_handle_t* h, const void* hidden,
+                                                 const int32_t* positions, const int64_t* slot_mapping,
+                                                 int32_t n, const mla_cache8_t* cache, int32_t num_pages,
+                                                 void* workspace, size_t workspace_bytes, void* stream) {
+  mla_status_t s = cache8::check_cache(h, cache, num_pages, "append8");
+  if (s != MLA_OK) return s;
+  if (n < 0) return fail(MLA_ERR_INVALID_ARG, "append8: n < 0");
+  if (n == 0) return MLA_OK;
+  if (!hidden || !positions || !slot_mapping || !workspace)
+    return fail(MLA_ERR_INVALID_ARG, "append8: null pointer");
+  if ((uintptr_t)hidden % 16) return fail(MLA_ERR_INVALID_ARG, "append8: hidden must be 16-byte aligned");
+  if (workspace_bytes < mla_append8_workspace_bytes(h, n) || (uintptr_t)workspace % 256)
+    return fail(MLA_ERR_INVALID_ARG, "append8: workspace smaller than mla_append8_workspace_bytes() or not "
+                                     "256-byte aligned");
+  const Layout& l = h->lay;
+  cudaStream_t st = (cudaStream_t)stream;
+  s = proj<__nv_bfloat16, float>(h, st, false, n, l.L, l.D, 1, (const __nv_bfloat16*)hidden, l.D, 0,
+                                 (const __nv_bfloat16*)h->WA, l.D, 0, (float*)workspace, l.L, 0);
+  if (s != MLA_OK) return s;
+  cache8::kv_finish8(st, h, (const float*)workspace, l.L, n, positions, slot_mapping, *cache,
+                     (long)num_pages * h->cfg.page_size, true);
+  h->launches += 1;
+  MLA_CUDA_TRY(cudaGetLastError());
+  return MLA_OK;
+}
+
 // ---------------------------------------------------------------------------
 // Forward
 // ---------------------------------------------------------------------------
@@ -488,7 +522,7 @@ template <typename TX, typename TI>
 mla_status_t forward_impl(mla_handle_t* h, const void* hidden, const int32_t* pos, const int64_t* bslots,
                   void* cache, int num_pages, const mla_attn_desc_t& d, void* out, char* ws,
                   cudaStream_t st, cudaEvent_t kv_ready, const mla_shared_ctx_t* ctx = nullptr,
-                  const int32_t* parent = nullptr) {
+                  const int32_t* parent = nullptr, const mla_cache8_t* c8 = nullptr) {
   const Layout& l = h->lay;
   const int M = d.num_blocks * d.block_len;
   const FwdWs w = forward_ws(h, M);
@@ -502,7 +536,7 @@ mla_status_t forward_impl(mla_handle_t* h, const void* hidden, const int32_t* po
   // rotates and stores them.
   constexpr bool kBf16 = std::is_same<TX, __nv_bfloat16>::value;
   const long num_slots = (long)num_pages * h->cfg.page_size;
-  const bool fused_kv = kBf16 && bslots && 3L * ((M + 127) / 128) >= h->num_sms;
+  const bool fused_kv = kBf16 && bslots && !c8 && 3L * ((M + 127) / 128) >= h->num_sms;
   const int r0 = (bslots && !fused_kv) ? 0 : l.L;
   // every kernel (bf16 layers) may start while the previous kernel of the
   // stream finishes (programmatic dependent launch) and waits for it on the
@@ -520,6 +554,8 @@ mla_status_t forward_impl(mla_handle_t* h, const void* hidden, const int32_t* po
         s = tc::kv_append(st, h, x, M, pos, bslots, (TX*)cache, num_slots, pdl);
         if (s != MLA_OK) return s;
       }
+    } else if (c8) {
+      cache8::kv_finish8(st, h, a_out, l.NA, M, pos, bslots, *c8, num_slots, pdl);
     } else {
       simt::kv_finish<TX>(st, h, a_out, l.NA, M, pos, bslots, (TX*)cache, num_slots, pdl);
     }
@@ -591,7 +627,13 @@ mla_status_t forward_impl(mla_handle_t* h, const void* hidden, const int32_t* po
   // the cache writes of another stream the attention depends on (a plain
   // launch after the wait: no programmatic edge crosses it)
   if (kv_ready) MLA_CUDA_TRY(cudaStreamWaitEvent(st, kv_ready, 0));
-  if (parent) {
+  if (c8) {
+    if constexpr (kBf16)
+      s = cache8::attention(st, h, tree_rule(h, pos, num_pages, d, parent), d, q_abs, *c8, (__half*)o_lat,
+                            nullptr, ws + w.total, pdl);
+    if (s != MLA_OK) return s;
+    h->launches -= 1;     // counted with the other non-GEMM kernels below
+  } else if (parent) {
     s = tree_attention(h, st, q_abs, pos, cache, num_pages, d, parent, o_lat, (float*)(ws + w.total),
                        ws + w.total + tree_lse_bytes(h, M), pdl);
     if (s != MLA_OK) return s;
@@ -825,6 +867,76 @@ extern "C" mla_status_t mla_draft_forward_tree(mla_handle_t* h, const void* hidd
                                                 d, out, (char*)workspace, st, nullptr, nullptr, parent)
           : forward_impl<float, float>(h, hidden, positions, block_slot_mapping, cache, num_pages, d,
                                        out, (char*)workspace, st, nullptr, nullptr, parent);
+  if (s != MLA_OK) return s;
+  MLA_CUDA_TRY(cudaGetLastError());
+  return MLA_OK;
+}
+
+extern "C" size_t mla_latent_attention8_workspace_bytes(const mla_handle_t* h, const mla_attn_desc_t* desc) {
+  if (!h || !desc || desc->num_blocks <= 0 || desc->block_len <= 0 || desc->max_pages <= 0) return 0;
+  return cache8::attention_ws(h, *desc);
+}
+
+// What the attention over the 8-bit cache asks of its arguments (`who` opens the message).
+static mla_status_t check_attention8(const mla_handle* h, const mla_cache8_t* c, int32_t num_pages,
+                                     const mla_attn_desc_t* desc, const int32_t* parent, const char* who) {
+  const std::string w(who);
+  mla_status_t s = check_tree_desc(h, desc, who);
+  if (s == MLA_OK) s = cache8::check_cache(h, c, num_pages, who);
+  if (s != MLA_OK) return s;
+  if (parent && desc->block_len > tree::MAX_NODES)
+    return fail(MLA_ERR_UNSUPPORTED, w + ": at most 1024 nodes a block");
+  if ((long)num_pages * h->cfg.page_size > 0x7fffffffL)
+    return fail(MLA_ERR_INVALID_ARG, w + ": num_pages * page_size < 2^31");
+  if (!desc->block_table || !desc->kv_len) return fail(MLA_ERR_INVALID_ARG, w + ": null pointer");
+  return MLA_OK;
+}
+
+extern "C" mla_status_t mla_latent_attention8(mla_handle_t* h, const void* q_abs, const int32_t* positions,
+                                              const mla_cache8_t* cache, int32_t num_pages,
+                                              const mla_attn_desc_t* desc, const int32_t* parent,
+                                              void* o_lat, float* lse, void* workspace,
+                                              size_t workspace_bytes, void* stream) {
+  if (h && desc && desc->num_blocks == 0) return MLA_OK;
+  mla_status_t s = check_attention8(h, cache, num_pages, desc, parent, "attention8");
+  if (s != MLA_OK) return s;
+  const mla_attn_desc_t& d = *desc;
+  if (!q_abs || !positions || !o_lat) return fail(MLA_ERR_INVALID_ARG, "attention8: null pointer");
+  if ((uintptr_t)q_abs % 16 || (uintptr_t)o_lat % 16)
+    return fail(MLA_ERR_INVALID_ARG, "attention8: q_abs and o_lat must be 16-byte aligned");
+  const size_t need = cache8::attention_ws(h, d);
+  if (need && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 256))
+    return fail(MLA_ERR_INVALID_ARG, "attention8: workspace smaller than "
+                                     "mla_latent_attention8_workspace_bytes() or not 256-byte aligned");
+  s = cache8::attention((cudaStream_t)stream, h, tree_rule(h, positions, num_pages, d, parent), d,
+                        (const __nv_bfloat16*)q_abs, *cache, (__half*)o_lat, lse, workspace, false);
+  if (s != MLA_OK) return s;
+  MLA_CUDA_TRY(cudaGetLastError());
+  return MLA_OK;
+}
+
+extern "C" size_t mla_forward8_workspace_bytes(const mla_handle_t* h, const mla_attn_desc_t* desc) {
+  if (!h || !desc || desc->num_blocks <= 0 || desc->block_len <= 0 || desc->max_pages <= 0) return 0;
+  return forward_ws(h, (long)desc->num_blocks * desc->block_len).total + cache8::attention_ws(h, *desc);
+}
+
+extern "C" mla_status_t mla_draft_forward8(mla_handle_t* h, const void* hidden, const int32_t* positions,
+                                           const int64_t* block_slot_mapping, const mla_cache8_t* cache,
+                                           int32_t num_pages, const mla_attn_desc_t* desc,
+                                           const int32_t* parent, void* out, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  if (h && desc && desc->num_blocks == 0) return MLA_OK;
+  mla_status_t s = check_attention8(h, cache, num_pages, desc, parent, "forward8");
+  if (s != MLA_OK) return s;
+  if (!hidden || !positions || !out || !workspace) return fail(MLA_ERR_INVALID_ARG, "forward8: null pointer");
+  if ((uintptr_t)hidden % 16 || (uintptr_t)out % 16)
+    return fail(MLA_ERR_INVALID_ARG, "forward8: hidden and out must be 16-byte aligned");
+  if (workspace_bytes < mla_forward8_workspace_bytes(h, desc) || (uintptr_t)workspace % 256)
+    return fail(MLA_ERR_INVALID_ARG, "forward8: workspace smaller than mla_forward8_workspace_bytes() or not "
+                                     "256-byte aligned");
+  s = forward_impl<__nv_bfloat16, __half>(h, hidden, positions, block_slot_mapping, nullptr, num_pages, *desc,
+                                          out, (char*)workspace, (cudaStream_t)stream, nullptr, nullptr,
+                                          parent, cache);
   if (s != MLA_OK) return s;
   MLA_CUDA_TRY(cudaGetLastError());
   return MLA_OK;

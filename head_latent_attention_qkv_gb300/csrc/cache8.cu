@@ -1,0 +1,240 @@
+// Writing and reading the latent cache in 8 bits (mla_cache8_store, mla_cache8_load,
+// and the row kernel of mla_latent_cache_append8).
+//
+// A warp takes an entry: each lane 16 latent dims and 2 rotary ones.  The largest
+// magnitude is a maximum of integers (a bf16 number's bits without its sign
+// order like its magnitude, NaN above infinity above the rest), one warp
+// reduction; the scale follows from its exponent.  A store reads 1160 bytes and
+// writes 644, a load the other way round.
+#include "cache8.cuh"
+
+#include <algorithm>
+
+namespace mla {
+namespace cache8 {
+namespace {
+
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+
+struct Rows8 {
+  uint8_t* latent;
+  uint32_t* rope;                          // pairs of bf16
+  float* scale;
+  const int64_t* slots;
+  long num_slots;
+  int n;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t pair) {
+  return max(m, max(pair & 0x7fffu, (pair >> 16) & 0x7fffu));
+}
+__device__ __forceinline__ float lo_f32(uint32_t pair) { return __uint_as_float(pair << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
+// Four bf16 numbers times `inv` as four e4m3 bytes.
+__device__ __forceinline__ uint32_t quantise4(uint32_t a, uint32_t b, float inv) {
+  return e4m3x2(lo_f32(a) * inv, hi_f32(a) * inv) | e4m3x2(lo_f32(b) * inv, hi_f32(b) * inv) << 16;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__global__ void __launch_bounds__(THREADS) store8_kernel(const Rows8 a, const uint4* __restrict__ entries) {
+  const int lane = threadIdx.x % 32;
+  for (long t = blockIdx.x * (long)WARPS + threadIdx.x / 32; t < a.n; t += (long)gridDim.x * WARPS) {
+    const uint4* src = entries + t * (ENTRY / 8);
+    const uint4 x = src[lane], y = src[32 + lane];
+    const uint32_t r = reinterpret_cast<const uint32_t*>(src + RANK / 8)[lane];
+    const long slot = a.slots[t];
+    if (slot < 0 || slot >= a.num_slots) {
+      if (lane == 0) set_status(a.status, MLA_DEV_BAD_SLOT);
+      continue;
+    }
+    uint32_t m = abs_max2(abs_max2(abs_max2(abs_max2(0u, x.x), x.y), x.z), x.w);
+    m = abs_max2(abs_max2(abs_max2(abs_max2(m, y.x), y.y), y.z), y.w);
+    m = __reduce_max_sync(0xffffffffu, m);
+    const bool bad = poisoned(m, __reduce_max_sync(0xffffffffu, abs_max2(0u, r)));
+    const int k = scale_exponent(m);
+    const float inv = pow2(-k);
+    uint2* dst = reinterpret_cast<uint2*>(a.latent + slot * RANK);
+    dst[lane] = bad ? make_uint2(0, 0) : make_uint2(quantise4(x.x, x.y, inv), quantise4(x.z, x.w, inv));
+    dst[32 + lane] = bad ? make_uint2(0, 0) : make_uint2(quantise4(y.x, y.y, inv), quantise4(y.z, y.w, inv));
+    a.rope[slot * (ROPE / 2) + lane] = r;
+    if (lane == 0) a.scale[slot] = bad ? __uint_as_float(0x7fc00000u) : pow2(k);
+  }
+}
+
+__global__ void __launch_bounds__(THREADS) load8_kernel(const Rows8 a, uint4* __restrict__ entries) {
+  const int lane = threadIdx.x % 32;
+  for (long t = blockIdx.x * (long)WARPS + threadIdx.x / 32; t < a.n; t += (long)gridDim.x * WARPS) {
+    const long slot = a.slots[t];
+    if (slot < 0 || slot >= a.num_slots) {
+      if (lane == 0) set_status(a.status, MLA_DEV_BAD_SLOT);
+      continue;
+    }
+    const uint2* src = reinterpret_cast<const uint2*>(a.latent + slot * RANK);
+    const uint2 x = src[lane], y = src[32 + lane];
+    const uint32_t r = a.rope[slot * (ROPE / 2) + lane];
+    const float s = a.scale[slot];
+    auto two = [&](uint32_t q) {
+      const float2 f = from_e4m3x2(q & 0xffffu);
+      return bf16_pair(f.x * s, f.y * s);
+    };
+    uint4* dst = entries + t * (ENTRY / 8);
+    dst[lane] = make_uint4(two(x.x), two(x.x >> 16), two(x.y), two(x.y >> 16));
+    dst[32 + lane] = make_uint4(two(y.x), two(y.x >> 16), two(y.y), two(y.y >> 16));
+    reinterpret_cast<uint32_t*>(dst + RANK / 8)[lane] = r;
+  }
+}
+
+// RMSNorm, rotation and the 8-bit form of one token's raw row in one pass; the
+// arithmetic up to the bf16 rounding is that of the bf16 cache's finish.
+constexpr int FIN_THREADS = 128, FIN_WARPS = FIN_THREADS / 32;
+__global__ void __launch_bounds__(FIN_THREADS)
+kv_finish8_kernel(const Rows8 a, const float* __restrict__ kv, long ld, const int32_t* __restrict__ positions,
+                  float eps, const float* __restrict__ gamma, const float2* __restrict__ rope_table,
+                  int max_pos, int interleaved) {
+  __shared__ float part[FIN_WARPS];
+  __shared__ uint32_t top[FIN_WARPS], top_rope[FIN_WARPS];
+  pdl_trigger();
+  pdl_wait();
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const float* row = kv + (long)t * ld;
+  const long slot = a.slots[t];
+  const int p = positions[t];
+  const bool bad_slot = slot < 0 || slot >= a.num_slots, bad_pos = p < 0 || p >= max_pos;
+  if (bad_slot || bad_pos) {
+    if (tid == 0) set_status(a.status, (bad_slot ? MLA_DEV_BAD_SLOT : 0) | (bad_pos ? MLA_DEV_BAD_POSITION : 0));
+    return;
+  }
+  // (the sum over a thread's elements in the order of the bf16 cache's finish)
+  float v[4], ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = row[tid + i * FIN_THREADS];
+    ss = fmaf(v[i], v[i], ss);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (lane == 0) part[warp] = ss;
+  __syncthreads();
+  ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < FIN_WARPS; ++i) ss += part[i];
+  const float rstd = 1.f / sqrtf(ss / (float)RANK + eps);
+  uint32_t m = 0, mr = 0;
+  __nv_bfloat16 e[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    e[i] = __float2bfloat16_rn(v[i] * rstd * gamma[tid + i * FIN_THREADS]);
+    m = max(m, (uint32_t)__bfloat16_as_ushort(e[i]) & 0x7fffu);
+  }
+  uint16_t ra = 0, rb = 0;
+  int ia = 0, ib = 0;
+  if (tid < ROPE / 2) {
+    ia = interleaved ? 2 * tid : tid;
+    ib = interleaved ? 2 * tid + 1 : tid + ROPE / 2;
+    const float2 cs = rope_table[(long)p * (ROPE / 2) + tid];
+    const float x = row[RANK + ia], y = row[RANK + ib];
+    ra = __bfloat16_as_ushort(__float2bfloat16_rn(x * cs.x - y * cs.y));
+    rb = __bfloat16_as_ushort(__float2bfloat16_rn(y * cs.x + x * cs.y));
+    mr = max(ra & 0x7fffu, rb & 0x7fffu);
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  mr = __reduce_max_sync(0xffffffffu, mr);
+  if (lane == 0) {
+    top[warp] = m;
+    top_rope[warp] = mr;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < FIN_WARPS; ++i) {
+    m = max(m, top[i]);
+    mr = max(mr, top_rope[i]);
+  }
+  const bool bad = poisoned(m, mr);
+  const int k = scale_exponent(m);
+  const float inv = pow2(-k);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    a.latent[slot * RANK + tid + i * FIN_THREADS] =
+        bad ? 0 : (uint8_t)__nv_cvt_float_to_fp8(__bfloat162float(e[i]) * inv, __NV_SATFINITE, __NV_E4M3);
+  if (tid < ROPE / 2) {
+    uint16_t* dst = reinterpret_cast<uint16_t*>(a.rope) + slot * ROPE;
+    dst[ia] = ra;
+    dst[ib] = rb;
+  }
+  if (tid == 0) a.scale[slot] = bad ? __uint_as_float(0x7fc00000u) : pow2(k);
+}
+
+Rows8 rows8(const mla_handle* h, const mla_cache8_t& c, const int64_t* slots, long num_slots, int n) {
+  return Rows8{(uint8_t*)c.latent, (uint32_t*)c.rope, c.scale, slots, num_slots, n, h->status};
+}
+
+mla_status_t check_rows(const mla_handle* h, const mla_cache8_t* c, int num_pages, const void* entries,
+                        const int64_t* slots, int n, const char* who) {
+  const std::string w(who);
+  mla_status_t s = check_cache(h, c, num_pages, who);
+  if (s != MLA_OK) return s;
+  if (n < 0) return fail(MLA_ERR_INVALID_ARG, w + ": n < 0");
+  if (n > 0 && (!entries || !slots)) return fail(MLA_ERR_INVALID_ARG, w + ": null pointer");
+  if ((uintptr_t)entries % 16) return fail(MLA_ERR_INVALID_ARG, w + ": entries must be 16-byte aligned");
+  return MLA_OK;
+}
+
+unsigned rows_grid(const mla_handle* h, int n) {
+  return (unsigned)std::min<long>(((long)n + WARPS - 1) / WARPS, 8L * h->num_sms);
+}
+
+}  // namespace
+
+mla_status_t check_cache(const mla_handle* h, const mla_cache8_t* c, int num_pages, const char* who) {
+  const std::string w(who);
+  if (!h || !c) return fail(MLA_ERR_INVALID_ARG, w + ": null handle or cache");
+  if (h->cfg.dtype != MLA_BF16) return fail(MLA_ERR_UNSUPPORTED, w + ": the 8-bit cache is for bf16 layers");
+  if (!c->latent || !c->rope || !c->scale) return fail(MLA_ERR_INVALID_ARG, w + ": null cache pointer");
+  if ((uintptr_t)c->latent % 16 || (uintptr_t)c->rope % 16 || (uintptr_t)c->scale % 4)
+    return fail(MLA_ERR_INVALID_ARG, w + ": latent and rope must be 16-byte aligned, scale 4-byte");
+  if (num_pages <= 0) return fail(MLA_ERR_INVALID_ARG, w + ": num_pages <= 0");
+  return MLA_OK;
+}
+
+void kv_finish8(cudaStream_t st, const mla_handle* h, const float* kv, long ld, int n,
+                const int32_t* positions, const int64_t* slots, const mla_cache8_t& c, long num_slots,
+                bool pdl) {
+  if (n <= 0) return;
+  Launch L(dim3(n), dim3(FIN_THREADS), 0, st, pdl);
+  cudaLaunchKernelEx(&L.cfg, kv_finish8_kernel, rows8(h, c, slots, num_slots, n), kv, ld, positions,
+                     (float)h->cfg.rms_norm_eps, h->gamma_kv, h->rope, h->cfg.max_position,
+                     (int)(h->cfg.rope == MLA_ROPE_INTERLEAVED));
+}
+
+}  // namespace cache8
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" mla_status_t mla_cache8_store(mla_handle_t* h, const void* entries, const int64_t* slot_mapping,
+                                         int32_t n, const mla_cache8_t* cache, int32_t num_pages,
+                                         void* stream) {
+  const mla_status_t s = cache8::check_rows(h, cache, num_pages, entries, slot_mapping, n, "cache8 store");
+  if (s != MLA_OK || n == 0) return s;
+  cache8::store8_kernel<<<cache8::rows_grid(h, n), cache8::THREADS, 0, (cudaStream_t)stream>>>(
+      cache8::rows8(h, *cache, slot_mapping, (long)num_pages * h->cfg.page_size, n), (const uint4*)entries);
+  MLA_CUDA_TRY(cudaGetLastError());
+  h->launches += 1;
+  return MLA_OK;
+}
+
+extern "C" mla_status_t mla_cache8_load(mla_handle_t* h, const mla_cache8_t* cache, int32_t num_pages,
+                                        const int64_t* slot_mapping, int32_t n, void* entries,
+                                        void* stream) {
+  const mla_status_t s = cache8::check_rows(h, cache, num_pages, entries, slot_mapping, n, "cache8 load");
+  if (s != MLA_OK || n == 0) return s;
+  cache8::load8_kernel<<<cache8::rows_grid(h, n), cache8::THREADS, 0, (cudaStream_t)stream>>>(
+      cache8::rows8(h, *cache, slot_mapping, (long)num_pages * h->cfg.page_size, n), (uint4*)entries);
+  MLA_CUDA_TRY(cudaGetLastError());
+  h->launches += 1;
+  return MLA_OK;
+}

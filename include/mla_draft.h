@@ -63,7 +63,8 @@ enum {
   MLA_ERR_TIMEOUT = 5        /* a bounded device wait expired                 */
 };
 
-enum { MLA_BF16 = 0, MLA_FP32 = 1 };              /* mla_config_t.dtype */
+enum { MLA_BF16 = 0, MLA_FP32 = 1,                /* mla_config_t.dtype */
+       MLA_FP16 = 2 };                            /* probabilities only (mla_verify_drafts) */
 enum { MLA_ROPE_NEOX = 0, MLA_ROPE_INTERLEAVED = 1 }; /* mla_config_t.rope */
 
 /* Bits of the device status word (mla_get_device_status). */
@@ -75,8 +76,10 @@ enum {
   MLA_DEV_BAD_LENGTH = 16,   /* kv_len < 0 or > max_pages * page_size         */
   MLA_DEV_BAD_WINDOW = 32,   /* window < 0 (the block's rows are zeroed)      */
   MLA_DEV_BAD_TREE = 64,     /* a node's parent is not an earlier node        */
-  MLA_DEV_BAD_KEEP = 128     /* a list of kept keys that is not ascending in
+  MLA_DEV_BAD_KEEP = 128,    /* a list of kept keys that is not ascending in
                                 [0, kv_len), or longer than its sequence      */
+  MLA_DEV_BAD_DRAFT = 256    /* a drafted token outside the vocabulary, or a
+                                row of the target without any mass            */
 };
 
 /* Intermediate tensors the forward leaves in its workspace
@@ -514,6 +517,109 @@ mla_status_t mla_cache_compact(mla_handle_t *h, void *cache, int32_t num_pages,
                                const int32_t *dst_block_table, int32_t dst_max_pages,
                                const float *weights, float *weights_out, int64_t ldw,
                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- the latent cache in 8 bits ------------------------------------------
+ * bf16 layers.  An entry of 576 bf16 numbers (1152 bytes) is kept in 644: its
+ * 512 latent dims in e4m3 over one power of two of its own, its 64 rotary dims
+ * in bf16 as they are.  Three arrays, page by page like the bf16 cache:
+ *   latent: device e4m3 [num_pages, page_size, 512], 16-byte aligned
+ *   rope:   device bf16 [num_pages, page_size, 64], 16-byte aligned
+ *   scale:  device fp32 [num_pages, page_size], 4-byte aligned
+ * and the entry stands for latent * scale and rope.  scale is the least power of two
+ * that brings the latent's largest magnitude to 448 or below, 2^-64 at least; the
+ * elements are rounded to nearest, ties to even (off by 2^-4 of their value at
+ * most, or 2^-10 scale below 2^-6 scale).  Reading back into bf16 is exact, and what
+ * was read back and is stored again stands for the same numbers.  An entry with an
+ * element that is NaN, infinite, or a latent of 2^127 or more has scale NaN and
+ * latent 0: its latent reads back as NaN, a row that sees it becomes NaN, and
+ * rows that do not see it are as without it. */
+typedef struct {
+  void *latent, *rope;
+  float *scale;
+} mla_cache8_t;
+
+/* Entries into the 8-bit cache: entry t (device bf16 [n, 576], 16-byte aligned)
+ * goes to slot slot_mapping[t] (device int64 [n], slot = page * page_size + row).
+ * A slot outside the cache is reported as MLA_DEV_BAD_SLOT and skipped; of a slot
+ * named twice one entry stays, or parts of both.  n == 0 is a no-op. */
+mla_status_t mla_cache8_store(mla_handle_t *h, const void *entries, const int64_t *slot_mapping,
+                              int32_t n, const mla_cache8_t *cache, int32_t num_pages, void *stream);
+
+/* Entries read back: row t of entries (device bf16 [n, 576], 16-byte aligned)
+ * becomes the entry of slot slot_mapping[t].  A slot outside the cache is reported
+ * as MLA_DEV_BAD_SLOT and its row left as it is. */
+mla_status_t mla_cache8_load(mla_handle_t *h, const mla_cache8_t *cache, int32_t num_pages,
+                             const int64_t *slot_mapping, int32_t n, void *entries, void *stream);
+
+/* mla_latent_cache_append into the 8-bit cache: the entries are rounded to bf16 as
+ * the bf16 cache would hold them and stored as mla_cache8_store does.
+ * workspace: mla_append8_workspace_bytes() bytes, 256-byte aligned. */
+size_t mla_append8_workspace_bytes(const mla_handle_t *h, int32_t n);
+mla_status_t mla_latent_cache_append8(mla_handle_t *h, const void *hidden,
+                                      const int32_t *positions, const int64_t *slot_mapping,
+                                      int32_t n, const mla_cache8_t *cache, int32_t num_pages,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Latent attention over the 8-bit cache: mla_latent_attention (parent NULL) or
+ * mla_tree_attention (parent as there, at most 1024 nodes a block) with the
+ * entries that the cache stands for; same q_abs, positions, desc, o_lat, lse,
+ * same checks on the device, any block_len.  Entries that no row sees may hold
+ * anything.  num_pages * page_size < 2^31.  Every block's keys are split over the SMs and joined by
+ * log-sum-exp.  workspace: mla_latent_attention8_workspace_bytes() bytes,
+ * 256-byte aligned; two calls that may overlap on the GPU need two. */
+size_t mla_latent_attention8_workspace_bytes(const mla_handle_t *h, const mla_attn_desc_t *desc);
+mla_status_t mla_latent_attention8(mla_handle_t *h, const void *q_abs, const int32_t *positions,
+                                   const mla_cache8_t *cache, int32_t num_pages,
+                                   const mla_attn_desc_t *desc, const int32_t *parent,
+                                   void *o_lat, float *lse, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* The whole layer over the 8-bit cache: mla_draft_forward (parent NULL) or
+ * mla_draft_forward_tree with mla_latent_attention8 as its attention and the block's own
+ * entries written as mla_latent_cache_append8 writes them.  workspace:
+ * mla_forward8_workspace_bytes() bytes, 256-byte aligned, with mla_draft_forward's
+ * intermediates (mla_forward_workspace_offset, not MLA_WS_LSE). */
+size_t mla_forward8_workspace_bytes(const mla_handle_t *h, const mla_attn_desc_t *desc);
+mla_status_t mla_draft_forward8(mla_handle_t *h, const void *hidden, const int32_t *positions,
+                                const int64_t *block_slot_mapping, const mla_cache8_t *cache,
+                                int32_t num_pages, const mla_attn_desc_t *desc,
+                                const int32_t *parent, void *out, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* ---- verification of drafted tokens ---------------------------------------
+ * Which of a sequence's num_nodes drafted tokens (T) the target keeps, and the
+ * token behind them, from given random numbers, so that what is kept is
+ * distributed as the target's own tokens.  Node i drafts tokens[b, i] after its
+ * parent (device int32 [num_seqs, T]; -1: after the context; -2: not in the tree; NULL:
+ * the chain parent[i] = i - 1).  target [num_seqs, T + 1, ldt]: row 0 the
+ * target's probabilities after the context, row i + 1 those after node i; draft
+ * [num_seqs, T, ldd]: row 0 the distribution from which the context's children
+ * were drawn, each for itself, row i + 1 that of node i's children; NULL: every token was
+ * certain (a likeliest one, siblings distinct).  Both of `dtype` (MLA_FP32,
+ * MLA_BF16, MLA_FP16), the first `vocab` elements of each row; an element that is
+ * negative, NaN or infinite counts as 0.
+ *   The sequence stands at the context (w = target row 0, s = 1).  Its nodes are
+ * looked at in their order; one whose parent is where the sequence stands is taken if
+ *   uniforms[b, i] s q(x) < w(x)       (x = tokens[b, i], q the draft's row there, 1 for NULL)
+ * and the sequence then stands at it (w = target row i + 1, s = 1); else w becomes
+ * max(w - s q, 0) and s its sum (draft NULL: w(x) becomes 0 and s loses it).
+ * At the end next_token[b] is the least x with sum_{y <= x} w(y) >
+ * uniforms[b, T] sum w.  Where nothing is left of w it is drawn from the target's row
+ * itself; without any mass there it is -1 (MLA_DEV_BAD_DRAFT).
+ *   accepted: device int32 [num_seqs, T], the taken nodes in order, first[b] added
+ * to each (device int32 [num_seqs], NULL = 0), -1 behind the last; num_accepted: device
+ * int32 [num_seqs].  With first = context length they are mla_cache_compact's
+ * keep, keep_len and first.  uniforms: device fp32 [num_seqs, T + 1] in [0, 1).
+ * A token outside the vocabulary is reported as MLA_DEV_BAD_DRAFT, its node
+ * refused and w left as it was; a parent >= the node as MLA_DEV_BAD_TREE, its
+ * node never reached.  Sums and differences are carried to 2^-44 or better.  T at most
+ * 1024 (MLA_ERR_UNSUPPORTED beyond); T == 0 draws from row 0. */
+mla_status_t mla_verify_drafts(mla_handle_t *h, const void *target, int64_t ldt, const void *draft,
+                               int64_t ldd, int32_t dtype, const int32_t *tokens,
+                               const int32_t *parent, const float *uniforms, const int32_t *first,
+                               int32_t num_seqs, int32_t num_nodes, int32_t vocab,
+                               int32_t *accepted, int32_t *num_accepted, int32_t *next_token,
+                               void *stream);
 
 /* Synchronise `stream`, read and clear the device status word.  Returns
  * MLA_OK, MLA_ERR_TIMEOUT (MLA_DEV_TIMEOUT set) or MLA_ERR_DEVICE_CHECK; the
