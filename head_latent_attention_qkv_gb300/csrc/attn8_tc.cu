@@ -1,0 +1,977 @@
+// Latent attention over the 8-bit cache (mla_latent_attention8), on the tensor cores.
+//
+// Mathematics.  128 keys fill the MMA's M, and 32 query rows its N, twice:
+//   S^T = K8 [Qhi | Qlo]^T     (e4m3, M = 128 keys, N = 64, K = 512 dims; 16 MMAs)
+//   R^T = Kpe Qpe^T            (bf16, N = 32, K = 64; 4 MMAs)
+//   O^T += V8^T [Phi | Plo]^T  (e4m3, M = 128 value dims x 4, N = 64, K = 128 keys; 16 MMAs)
+// so the cache's own bytes are the operands of both products: nothing is widened, a
+// tile is read from memory once and from shared memory twice, by dims and, MN-major, by
+// keys.  A bf16 number has 8 significant bits and e4m3 4: q / 2^k is hi + lo exactly
+// (down to 2^-10 where the row's largest is 224 or more), and the halves' products are added in
+// fp32.  The score of key j is then
+//   t_j = c 2^k s_j (S_hi + S_lo) + c R + log2 s_j        (c = scale log2 e, s_j the key's scale)
+// whose maximum is the softmax's reference: w_j = 2^(t_j - M) <= 2^1.75 is the weight times
+// the key's scale, what meets the codes.  2^7 w_j is split like q, its rest by 2^4 more:
+// e4m3 spans 2^17, and a weight is off by 2^-8 of itself and 2^-21 of 2^M.  The smallest
+// weights round to nothing, so that n of them may lose n 2^-21: after 64 tiles a piece is
+// put away and joined by its log-sum-exp.  The sum of the softmax, l = sum w_j / s_j, is fp32.
+//
+// Work split.  One persistent CTA per SM.  The 128-key tiles of all units (a block's groups
+// of 32 rows), in order, are cut into equal ranges; a (unit, CTA) piece writes its
+// normalised partial to slot unit + CTA (unique: neither ever falls along the order and
+// one of them grows), or the output itself where the unit lies in one CTA; the join
+// kernel adds the pieces by log-sum-exp in order.
+//   warps 0-7  : softmax, two groups of 128 threads, thread = key, 16 rows each
+//   warp 8     : tensor-memory allocation, MMA issue: S(0) S(1) O(0) S(2) O(1) ...
+//   warps 9-11 : copies; a tile is five 16 KB chunks, each refilled once its product is done
+//   warps 12-15: the next unit's queries, held in registers until the last S is done
+#include "cache8.cuh"
+#include "gemm_tc.cuh"
+#include "tc_ptx.cuh"
+
+#include <math.h>
+
+#include <mutex>
+
+namespace mla {
+namespace cache8 {
+namespace {
+
+using namespace tc;
+
+constexpr int KT = 128, NR = 32, HALF = 16;          // keys a tile, rows a unit, rows a softmax thread
+constexpr int SEG_TILES = 64;                        // tiles after which a piece is put away
+constexpr int THREADS = 512, SM_THREADS = 256;
+constexpr int STAGES = 2, CHUNKS = 5;                // 4 chunks of 128 latent dims, one of 64 rotary ones
+constexpr int CH_BYTES = KT * 128;                   // 16 KB
+constexpr int STAGE_BYTES = CHUNKS * CH_BYTES;
+constexpr int Q_CH_BYTES = 2 * NR * 128;             // [hi rows | lo rows] x 128 dims
+constexpr int QR_BYTES = NR * 128;
+constexpr int P_BYTES = KT * 2 * NR;                 // [key][hi | lo], 64 bytes a key
+constexpr int OFF_Q = STAGES * STAGE_BYTES;
+constexpr int OFF_QR = OFF_Q + 4 * Q_CH_BYTES;
+constexpr int OFF_P = OFF_QR + QR_BYTES;
+constexpr int OFF_RED = OFF_P + 2 * P_BYTES;
+constexpr int COPY_WARPS = 3, Q_WARPS = 4, Q_ROWS = NR / Q_WARPS;
+// TMEM: S of tile g at column 128 (g % 2): hi 0-31, lo 32-63, rotary 64-95; O at 256: 4 x (hi | lo)
+constexpr uint32_t TMEM_COLS = 512, TM_O = 256;
+constexpr float SLACK_LOG2 = 1.75f;                  // 2^7 2^1.75 < 448
+constexpr float P_LOG2 = 7.f, LO_UP = 16.f;
+
+struct Params {
+  CUtensorMap tmL;    // the latents' bytes as [slots, 256] 16-bit numbers, chunked, box seg_rows x 1 chunk
+  CUtensorMap tmR;    // rotary dims [slots, 64], box seg_rows
+  tree::Rule rule;
+  const float* scale;
+  const __nv_bfloat16* q;
+  __half* o_lat;      // [rows, 512]
+  float* lse;         // [rows] or NULL
+  float* part;        // [slots, 32, 512] normalised partial outputs
+  float* part_lse;    // [slots, 32]
+  long long* first_tile;   // [blocks + 1] tiles of a group's worth of keys before each block
+  int num_blocks, groups, seg_rows;
+  float scale_log2;
+};
+
+struct Bars {
+  uint64_t full[STAGES];            // a tile landed
+  uint64_t empty[STAGES][CHUNKS];   // the products of a chunk are done
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2];               // S(g) done (and all before it), by g % 2
+  uint64_t p_full[2];               // P(g) in shared memory
+  uint64_t o_done;                  // O(g) done (waited on for a rescale only)
+  uint64_t o_seg;                   // the segment's last O done
+  uint64_t drain;
+  uint32_t tmem_slot;
+  int abort;
+};
+
+struct __align__(16) Shared {
+  float wpart[2][2][4][HALF];       // by tile parity, group, warp: row maxima
+  float m[NR];                      // reference of each row (log2)
+  float inv[NR], keep[NR];          // factors of a segment's O and of what its piece has put away
+  float q_scale[2][NR];             // c 2^k of each row, by segment parity
+  int lo[NR], hi[NR];               // context keys that each row sees
+  float sum[2][4][HALF];
+  float run_lse[NR];                // log2-sum-exp of what a piece has put away
+  uint32_t seen[2][NR][4];          // by group: which keys of a tile each row sees
+  int fast_lo, fast_hi, any_lo, any_hi;
+  uint32_t alive;
+  int first_unit, first_tile;
+  long long scan[THREADS / 32];
+  Bars bars;
+};
+constexpr int SMEM_BYTES = 1024 + OFF_RED + (int)sizeof(Shared);
+static_assert(SMEM_BYTES <= 232448, "shared memory");
+
+__device__ __forceinline__ bool wait_bar(Bars* B, uint64_t* bar, uint32_t parity, uint32_t* st) {
+  if (*(volatile int*)&B->abort) return false;
+  if (mbar_wait(bar, parity, st)) return true;
+  B->abort = 1;
+  return false;
+}
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(2 + g) : "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 4, 256;" ::: "memory"); }
+
+// D[tmem] (+)= A B^T, e4m3 operands, fp32 sums.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// Instruction descriptor of kind::f8f6f4: fp32 D, e4m3 A and B.
+constexpr uint32_t idesc_f8(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
+// MN-major operand of 64 MN bytes a row with 64-byte swizzle: 8-row groups of K 512 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_sw64_mn(const void* tile) {
+  uint64_t d = (smem_u32(tile) & 0x3FFFFull) >> 4;
+  d |= (uint64_t)(512 >> 4) << 16;
+  d |= (uint64_t)(512 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)4 << 61;
+  return d;
+}
+
+// 16 consecutive fp32 columns of this thread's TMEM lane, no wait.
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_reg_fence16(float* v) {
+  asm volatile(""
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                 "+f"(v[15]));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void lds16(const float* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < HALF; i += 4) *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(p + i);
+}
+
+// Lane l ends with op over the warp's lanes of x[l % 16] (x[0 .. 15] per lane).
+template <bool kMax>
+__device__ __forceinline__ float transpose_reduce16(float* x, int lane) {
+#pragma unroll
+  for (int s = 8; s >= 1; s >>= 1) {
+    const bool upper = (lane & s) != 0;
+#pragma unroll
+    for (int i = 0; i < s; ++i) {
+      const float send = upper ? x[i] : x[i + s], keep = upper ? x[i + s] : x[i];
+      const float recv = __shfl_xor_sync(0xffffffffu, send, s);
+      x[i] = kMax ? fmaxf(keep, recv) : keep + recv;
+    }
+  }
+  const float y = __shfl_xor_sync(0xffffffffu, x[0], 16);
+  return kMax ? fmaxf(x[0], y) : x[0] + y;
+}
+
+// Keys of block b: [j_lo, n) in nt tiles, j_lo the first key that any row's window reaches,
+// rounded down to a tile.
+struct Keys {
+  int n, W, ctx, j_lo, nt;
+};
+__device__ __forceinline__ Keys keys_of(const Params& P, int b, bool report) {
+  Keys k;
+  k.n = tree::block_keys(P.rule, b, &k.W, &k.ctx, report);
+  k.j_lo = 0;
+  if (k.W > 0 && k.n > 0) {
+    int p = 0x7fffffff;
+    for (int t = 0; t < P.rule.T; ++t) p = min(p, P.rule.positions[(long)b * P.rule.T + t]);
+    k.j_lo = min(tree::window_start(p, k.W), k.n) / KT * KT;
+  }
+  k.nt = k.n > k.j_lo ? (k.n - k.j_lo + KT - 1) / KT : 0;
+  return k;
+}
+
+// The CTA whose range [c U / G, (c + 1) U / G) holds tile u (G <= U).
+__device__ __forceinline__ int cta_of(long long u, long long U, int G) { return (int)(((u + 1) * G - 1) / U); }
+
+// Segments of a CTA's range, in order: tiles [t0, t0 + n) of unit u; a (unit, CTA) piece is one or
+// more of them.
+struct Seg {
+  int unit, b, t0, n;
+  bool first, last;                        // of the piece
+  Keys k;
+};
+struct SegIter {
+  int unit, t;
+  long long left;
+  bool cont;
+};
+__device__ __forceinline__ bool next_seg(const Params& P, SegIter& it, Seg& s) {
+  const int units = P.num_blocks * P.groups;
+  while (it.left > 0 && it.unit < units) {
+    s.b = it.unit / P.groups;
+    s.k = keys_of(P, s.b, false);
+    if (it.t < s.k.nt) {
+      s.unit = it.unit;
+      s.t0 = it.t;
+      const int rest = (int)min((long long)(s.k.nt - it.t), it.left);
+      s.n = min(rest, SEG_TILES);
+      s.first = !it.cont;
+      s.last = s.n == rest;
+      it.cont = !s.last;
+      it.left -= s.n;
+      it.t += s.n;
+      if (it.t == s.k.nt) {
+        ++it.unit;
+        it.t = 0;
+      }
+      return true;
+    }
+    it.unit = s.k.nt == 0 ? (s.b + 1) * P.groups : it.unit + 1;
+    it.t = 0;
+  }
+  return false;
+}
+
+__global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant__ Params P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  Shared* sh = (Shared*)(smem + OFF_RED);
+  Bars* B = &sh->bars;
+  uint32_t* status = P.rule.status;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int c = blockIdx.x, nb = P.num_blocks;
+
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&B->full[s], 1);
+      for (int q = 0; q < CHUNKS; ++q) mbar_init(&B->empty[s][q], 1);
+    }
+    mbar_init(&B->q_full, Q_WARPS);
+    mbar_init(&B->q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B->s_full[i], 2);
+      mbar_init(&B->p_full[i], SM_THREADS);
+    }
+    mbar_init(&B->o_done, 1);
+    mbar_init(&B->o_seg, 1);
+    mbar_init(&B->drain, 1);
+    B->abort = 0;
+    sh->first_unit = nb * P.groups;
+    sh->first_tile = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(&B->tmem_slot, TMEM_COLS);
+
+  // ---- schedule: the tiles of one group before each block, then this CTA's first unit and tile
+  long long U = 0, u0 = 0, u1 = 0;
+  int G = 1;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long run = 0;
+    for (int base = 0; base < nb; base += THREADS) {
+      const int b = base + tid;
+      const int nt = b < nb ? keys_of(P, b, c == 0 && pass == 0).nt : 0;
+      int x = nt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) sh->scan[warp] = x;
+      __syncthreads();
+      long long before = run, tot = 0;
+      for (int w = 0; w < THREADS / 32; ++w) {
+        before += w < warp ? sh->scan[w] : 0;
+        tot += sh->scan[w];
+      }
+      const long long excl = before + x - nt;
+      run += tot;
+      __syncthreads();
+      if (pass == 1 && b < nb) {
+        if (nt > 0 && u1 > u0 && u0 >= excl * P.groups && u0 < (excl + nt) * P.groups) {
+          const long long in = u0 - excl * P.groups;
+          sh->first_unit = b * P.groups + (int)(in / nt);
+          sh->first_tile = (int)(in % nt);
+        }
+        if (c == 0) {
+          pdl_wait();                      // the workspace may still be read by the kernel before
+          P.first_tile[b] = excl;
+          if (b == nb - 1) P.first_tile[nb] = excl + nt;
+        }
+      }
+    }
+    if (pass == 0) {
+      // the first min(gridDim, U) CTAs take one range each, so none is empty
+      U = run * P.groups;
+      G = (int)min((long long)gridDim.x, max(U, 1LL));
+      u0 = c < G ? U * c / G : U;
+      u1 = c < G ? U * (c + 1) / G : U;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem_slot;
+  const SegIter start{sh->first_unit, sh->first_tile, u1 - u0, false};
+  const bool work = u1 > u0;
+  if (tid == 0) pdl_trigger();
+  // (lengths, windows, positions and page rows are inputs of the call; what the kernel
+  // before wrote, queries and entries, is read behind pdl_wait only)
+
+  if (warp == 8) {
+    if (lane == 0 && work) {
+      // ---- MMA issue ----
+      const uint32_t id_s = idesc_f8(KT, 2 * NR);                            // K-major A and B
+      const uint32_t id_r = idesc_f16(KT, NR, false);
+      const uint32_t id_o = idesc_f8(KT, 2 * NR) | (1u << 15) | (1u << 16);  // A and B MN-major
+      const uint64_t dK = smem_desc_sw128(smem), dV = smem_desc_sw128_mn(smem, CH_BYTES);
+      const uint64_t dQ = smem_desc_sw128(smem + OFF_Q), dR = smem_desc_sw128(smem + OFF_QR);
+      const uint64_t dP = smem_desc_sw64_mn(smem + OFF_P);
+      constexpr uint32_t U_STAGE = STAGE_BYTES / 16, U_CH = CH_BYTES / 16, U_Q = Q_CH_BYTES / 16;
+      constexpr uint32_t U_P = P_BYTES / 16, U_VSTEP = 32 * 128 / 16, U_PSTEP = 32 * 64 / 16;
+      SegIter it = start;
+      Seg s;
+      uint32_t g = 0, kseg = 0;
+      bool ok = true;
+      while (ok && next_seg(P, it, s)) {
+        if (!(ok = wait_bar(B, &B->q_full, kseg & 1, status))) break;
+        tc_fence_after();
+        for (int t = 0; t <= s.n && ok; ++t) {
+          if (t < s.n) {
+            const uint32_t gg = g + t, st = gg % STAGES;
+            if (!(ok = wait_bar(B, &B->full[st], (gg / STAGES) & 1, status))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + 128 * (gg & 1);
+            const uint64_t a = dK + st * U_STAGE;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_f16(d + 64, a + 4 * U_CH + 2 * i, dR + 2 * i, id_r, i > 0);
+            mma_commit(&B->empty[st][4]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mma_f8(d, a + q * U_CH + 2 * i, dQ + q * U_Q + 2 * i, id_s, q + i > 0);
+            mma_commit(&B->s_full[gg & 1]);
+            mbar_arrive(&B->s_full[gg & 1]);       // (hands on the query warps' row scales)
+            if (t == s.n - 1) mma_commit(&B->q_empty);
+          }
+          if (t >= 1) {
+            const uint32_t gg = g + t - 1, st = gg % STAGES;
+            if (!(ok = wait_bar(B, &B->p_full[gg & 1], (gg >> 1) & 1, status))) break;
+            tc_fence_after();
+            const uint64_t a = dV + st * U_STAGE, p = dP + (gg & 1) * U_P;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_f8(tmem + TM_O + 64 * q, a + q * U_CH + i * U_VSTEP, p + i * U_PSTEP, id_o, t > 1 || i > 0);
+              mma_commit(&B->empty[st][q]);
+            }
+            mma_commit(&B->o_done);
+            if (t == s.n) mma_commit(&B->o_seg);
+          }
+        }
+        g += s.n;
+        ++kseg;
+      }
+      mma_commit(&B->drain);
+      mbar_wait(&B->drain, 0, status);
+    }
+  } else if (warp >= 9 && warp < 9 + COPY_WARPS) {
+    if (lane == 0 && work) {
+      // ---- copies: this warp takes every third of a tile's (chunk, page segment) copies ----
+      const int me = warp - 9;
+      const int ps = P.rule.page_size, past_end = P.rule.num_pages * ps, segs = KT / P.seg_rows;
+      prefetch_tmap(&P.tmL);
+      prefetch_tmap(&P.tmR);
+      SegIter it = start;
+      Seg s;
+      uint32_t g = 0;
+      bool ok = true, waited = false;
+      while (ok && next_seg(P, it, s)) {
+        const int32_t* table = P.rule.block_table + (long)s.b * P.rule.max_pages;
+        for (int t = 0; t < s.n && ok; ++t, ++g) {
+          const uint32_t st = g % STAGES, ph = (g / STAGES) & 1;
+          const int j0 = s.k.j_lo + (s.t0 + t) * KT;
+          uint8_t* dst = smem + st * STAGE_BYTES;
+          int y = 0, have = -1;
+          if (!waited) {
+            pdl_wait();
+            waited = true;
+          }
+          // copy i: segment i / 5, chunk i % 5 (the rotary chunk first: its place is free first)
+          for (int i = me; i < segs * CHUNKS; i += COPY_WARPS) {
+            const int sg = i / CHUNKS, q = (i % CHUNKS + 4) % CHUNKS;
+            if (sg != have) {
+              have = sg;
+              const int j = j0 + sg * P.seg_rows;
+              y = past_end;                        // (zeros)
+              if (j < s.k.n) {
+                const int pg = table[j / ps];
+                if (pg >= 0 && pg < P.rule.num_pages) y = pg * ps + j % ps;
+                else set_status(status, MLA_DEV_BAD_PAGE);
+              }
+            }
+            if (!(ok = wait_bar(B, &B->empty[st][q], ph ^ 1, status))) break;
+            if (i == 0) mbar_arrive_expect_tx(&B->full[st], STAGE_BYTES);
+            uint8_t* to = dst + q * CH_BYTES + sg * P.seg_rows * 128;
+            if (q < 4) tma_load_3d(to, &P.tmL, &B->full[st], 0, y, q);
+            else tma_load_3d(to, &P.tmR, &B->full[st], 0, y, 0);
+          }
+        }
+      }
+      // the copies in flight land before the CTA exits (after a wait that gave up, a part of
+      // one tile more; that wait gives up, too)
+      if (!ok) ++g;
+      for (uint32_t i = g > STAGES ? g - STAGES : 0; i < g; ++i)
+        mbar_wait(&B->full[i % STAGES], (i / STAGES) & 1, status);
+    }
+  } else if (warp >= 9 + COPY_WARPS) {
+    if (work) {
+      // ---- queries of each segment: split in two e4m3 numbers ----
+      const int w = warp - 9 - COPY_WARPS;
+      uint4 x[Q_ROWS][2];
+      uint32_t xr[Q_ROWS];
+      auto load = [&](const Seg& s) {
+        const int r0 = (s.unit % P.groups) * NR, live = P.rule.T * P.rule.H;
+        const long base = (long)s.b * live + r0;
+#pragma unroll
+        for (int i = 0; i < Q_ROWS; ++i) {
+          const int r = w * Q_ROWS + i;
+          const bool in = r0 + r < live;
+          const uint4* src = reinterpret_cast<const uint4*>(P.q + (base + (in ? r : 0)) * ENTRY);
+          x[i][0] = in ? src[2 * lane] : make_uint4(0, 0, 0, 0);
+          x[i][1] = in ? src[2 * lane + 1] : make_uint4(0, 0, 0, 0);
+          xr[i] = in ? reinterpret_cast<const uint32_t*>(src + RANK / 8)[lane] : 0u;
+        }
+      };
+      SegIter it = start;
+      Seg s;
+      uint32_t kseg = 0;
+      bool ok = true, have = next_seg(P, it, s);
+      pdl_wait();
+      if (have) load(s);
+      while (have && ok) {
+        if (kseg > 0) ok = __all_sync(0xffffffffu, wait_bar(B, &B->q_empty, (kseg - 1) & 1, status));
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < Q_ROWS; ++i) {
+          const int r = w * Q_ROWS + i;
+          const uint32_t u[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+          uint32_t m = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = max(m, max(u[e] & 0x7fffu, (u[e] >> 16) & 0x7fffu));
+          m = __reduce_max_sync(0xffffffffu, m);
+          const int k = max((int)(m >> 7) - 127 - 8 + ((m & 0x7fu) > 96u ? 1 : 0), -100);
+          const float inv = pow2(-k);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f[4] = {__uint_as_float(u[2 * e] << 16) * inv, __uint_as_float(u[2 * e] & 0xffff0000u) * inv,
+                                __uint_as_float(u[2 * e + 1] << 16) * inv,
+                                __uint_as_float(u[2 * e + 1] & 0xffff0000u) * inv};
+            const uint32_t h0 = e4m3x2(f[0], f[1]), h1 = e4m3x2(f[2], f[3]);
+            const float2 g0 = from_e4m3x2(h0), g1 = from_e4m3x2(h1);
+            hi[e] = h0 | h1 << 16;
+            lo[e] = e4m3x2(f[0] - g0.x, f[1] - g0.y) | e4m3x2(f[2] - g1.x, f[3] - g1.y) << 16;
+          }
+          uint8_t* q = smem + OFF_Q + (lane / 8) * Q_CH_BYTES + (((lane % 8) ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4*>(q + r * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(q + (NR + r) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint32_t*>(smem + OFF_QR + r * 128 + (((lane / 4) ^ (r & 7)) << 4) + (lane % 4) * 4) = xr[i];
+          // (a query that is no number makes its row none, whatever its bytes became)
+          if (lane == 0) sh->q_scale[kseg & 1][r] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(k) * P.scale_log2;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B->q_full);
+        ++kseg;
+        have = next_seg(P, it, s);
+        if (have) load(s);
+      }
+    }
+  } else if (work) {
+    // ---- softmax: thread = key (TMEM lane), rows 16 grp .. 16 grp + 15.  After a wait
+    // that gave up everything runs on to its end (the barriers below count every thread). ----
+    const int grp = warp / 4, wq = warp % 4, key = tid % 128;
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const int r0 = grp * HALF, ps = P.rule.page_size, live = P.rule.T * P.rule.H;
+    const float c2 = P.scale_log2;
+    SegIter it = start;
+    Seg s{};
+    uint32_t g = 0, kseg = 0;
+    long long u_seg = u0;                  // global index of the segment's first tile
+    // the scale of a tile's key, 1 where there is none
+    auto scale_at = [&](int t) {
+      const int j = s.k.j_lo + (s.t0 + t) * KT + key;
+      if (t >= s.n || j >= s.k.n) return 1.f;
+      const int pg = P.rule.block_table[(long)s.b * P.rule.max_pages + j / ps];
+      if (pg < 0 || pg >= P.rule.num_pages) return 1.f;
+      return __ldg(P.scale + (long)pg * ps + j % ps);
+    };
+    pdl_wait();
+    while (next_seg(P, it, s)) {
+      const int grp0 = (s.unit % P.groups) * NR;         // the unit's first row in its block
+      const int k_begin = s.k.j_lo + s.t0 * KT;
+      float ks = scale_at(0);
+      softmax_sync();                      // the segment before is done with the rows' state
+      if (warp == 0) {
+        const int row = grp0 + lane, i = row / P.rule.H;
+        int lo = 0, hi = 0;
+        bool see = row < live;
+        if (see) {
+          see = !P.rule.q_visible || P.rule.q_visible[(long)s.b * P.rule.T + i] != 0;
+          if (P.rule.parent)
+            see = tree::in_tree(P.rule, P.rule.parent + (long)s.b * P.rule.T, i, true) && see;
+          if (see) {
+            lo = s.k.W > 0 ? min(tree::window_start(P.rule.positions[(long)s.b * P.rule.T + i], s.k.W), s.k.n) : 0;
+            hi = s.k.ctx;
+          }
+        }
+        sh->lo[lane] = lo;
+        sh->hi[lane] = hi;
+        sh->m[lane] = -INFINITY;
+        if (s.first) sh->run_lse[lane] = -INFINITY;
+        const int fl = __reduce_max_sync(0xffffffffu, see ? lo : 0);
+        const int fh = __reduce_min_sync(0xffffffffu, see ? hi : 0x7fffffff);
+        const int al = __reduce_min_sync(0xffffffffu, see ? lo : 0x7fffffff);
+        const int ah = __reduce_max_sync(0xffffffffu, see ? hi : 0);
+        const uint32_t alive = __ballot_sync(0xffffffffu, see);
+        if (lane == 0) {
+          sh->fast_lo = fl;
+          sh->fast_hi = alive ? fh : 0;
+          sh->any_lo = al;
+          sh->any_hi = ah;
+          sh->alive = alive;
+        }
+      }
+      softmax_sync();
+      const uint32_t alive = sh->alive;
+      const int fast_lo = sh->fast_lo, fast_hi = sh->fast_hi, any_lo = sh->any_lo, any_hi = sh->any_hi;
+      float l[HALF];
+#pragma unroll
+      for (int r = 0; r < HALF; ++r) l[r] = 0.f;
+      for (int t = 0; t < s.n; ++t) {
+        const uint32_t gg = g + t, buf = gg & 1;
+        const int j0 = k_begin + t * KT, j = j0 + key;
+        const float ks_next = scale_at(t + 1);
+        const bool fast = j0 >= fast_lo && j0 + KT <= fast_hi;
+        const bool bits = !fast && P.rule.parent && j0 + KT > s.k.ctx;
+        if (bits) {
+          // which keys each row sees: the group's first 64 threads take half a tile of a row each
+          group_sync(grp);                 // (the tile before is done with the words)
+          if (key < 2 * NR) {
+            const int r = key / 2, h = key % 2;
+            unsigned long long m = 0;
+            if ((alive >> r) & 1)
+              m = tree::key_bits(P.rule, s.b, (grp0 + r) / P.rule.H, true, s.k.n, s.k.W, s.k.ctx, j0 + 64 * h);
+            sh->seen[grp][r][2 * h] = (uint32_t)m;
+            sh->seen[grp][r][2 * h + 1] = (uint32_t)(m >> 32);
+          }
+          group_sync(grp);
+        }
+        wait_bar(B, &B->s_full[buf], (gg >> 1) & 1, status);
+        tc_fence_after();
+        float x[HALF];
+        {
+          float y[HALF], z[HALF];
+          const uint32_t ts = tmem + 128 * buf + lanes;
+          tmem_ld16_nowait(ts + r0, x);
+          tmem_ld16_nowait(ts + NR + r0, y);
+          tmem_ld16_nowait(ts + 2 * NR + r0, z);
+          tmem_ld_wait();
+          tmem_reg_fence16(x);
+          tmem_reg_fence16(y);
+          tmem_reg_fence16(z);
+          float qs[HALF];
+          lds16(sh->q_scale[kseg & 1] + r0, qs);
+          const float kexp = (float)((int)(__float_as_uint(ks) >> 23) - 127);    // log2 of a power of two
+#pragma unroll
+          for (int r = 0; r < HALF; ++r) x[r] = fmaf(x[r] + y[r], qs[r] * ks, fmaf(z[r], c2, kexp));
+        }
+        if (!fast) {
+          bool seen = false;
+          if (bits) {
+#pragma unroll
+            for (int r = 0; r < HALF; ++r)
+              if (!((sh->seen[grp][r0 + r][wq] >> lane) & 1)) x[r] = -INFINITY;
+            for (int r = 0; r < NR; ++r) seen |= (sh->seen[grp][r][wq] >> lane) & 1;
+          } else {
+#pragma unroll
+            for (int r = 0; r < HALF; ++r)
+              if (j < sh->lo[r0 + r] || j >= sh->hi[r0 + r]) x[r] = -INFINITY;
+            seen = j >= any_lo && j < any_hi;
+          }
+          // a key that no row of the unit sees may hold any bytes: its latent becomes zero before
+          // it meets its weights, which are zero (S is done with it, and O waits for P)
+          if (!seen) {
+            uint8_t* row = smem + (gg % STAGES) * STAGE_BYTES + 2 * grp * CH_BYTES + key * 128;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(row + q * CH_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        float m[HALF];
+        {
+          float y[HALF];
+#pragma unroll
+          for (int r = 0; r < HALF; ++r) y[r] = x[r];
+          const float top = transpose_reduce16<true>(y, lane);
+          if (lane < HALF) sh->wpart[buf][grp][wq][lane] = top;
+          group_sync(grp);
+          lds16(sh->m + r0, m);
+          bool grow = false;
+#pragma unroll
+          for (int r = 0; r < HALF; r += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(&sh->wpart[buf][grp][0][r]);
+            const float4 b = *reinterpret_cast<const float4*>(&sh->wpart[buf][grp][1][r]);
+            const float4 d = *reinterpret_cast<const float4*>(&sh->wpart[buf][grp][2][r]);
+            const float4 e = *reinterpret_cast<const float4*>(&sh->wpart[buf][grp][3][r]);
+            y[r] = fmaxf(fmaxf(a.x, b.x), fmaxf(d.x, e.x));
+            y[r + 1] = fmaxf(fmaxf(a.y, b.y), fmaxf(d.y, e.y));
+            y[r + 2] = fmaxf(fmaxf(a.z, b.z), fmaxf(d.z, e.z));
+            y[r + 3] = fmaxf(fmaxf(a.w, b.w), fmaxf(d.w, e.w));
+          }
+#pragma unroll
+          for (int r = 0; r < HALF; ++r) grow |= y[r] > m[r] + SLACK_LOG2;
+          if (grow) {                      // (the same for every thread of the group)
+            group_sync(grp);               // everyone has read the references
+#pragma unroll
+            for (int r = 0; r < HALF; ++r) {
+              const float m_new = y[r] > m[r] + SLACK_LOG2 ? ceilf(y[r]) : m[r];
+              y[r] = m[r] == -INFINITY ? 1.f : fast_exp2(m[r] - m_new);
+              m[r] = m_new;
+              l[r] *= y[r];
+            }
+            if (key < HALF) {
+              float own = m[0];
+#pragma unroll
+              for (int r = 1; r < HALF; ++r) own = key == r ? m[r] : own;
+              sh->m[r0 + key] = own;
+            }
+            if (t > 0) {
+              // O(g - 1) is issued behind S(g), and O(g) only behind this tile's P
+              wait_bar(B, &B->o_done, (gg - 1) & 1, status);
+              tc_fence_after();
+#pragma unroll 1
+              for (int q = 0; q < 8; ++q) {
+                float o[HALF];
+                const uint32_t at = tmem + TM_O + NR * q + r0 + lanes;
+                tmem_ld16_nowait(at, o);
+                tmem_ld_wait();
+                tmem_reg_fence16(o);
+#pragma unroll
+                for (int r = 0; r < HALF; ++r) o[r] *= y[r];
+                tmem_st16(at, o);
+              }
+            }
+          }
+        }
+        // weights 2^7 w and their split; the sum takes them over the key's scale
+        // (finite also for the scale of an entry that holds nothing, whose weights are 0 or NaN)
+        const uint32_t ks_exp = __float_as_uint(ks) >> 23;
+        const float inv_ks = ks_exp - 1u < 253u ? __uint_as_float((254u - ks_exp) << 23) : 1.f;
+        uint32_t hi[HALF / 4], lo[HALF / 4];
+#pragma unroll
+        for (int r = 0; r < HALF; r += 2) {
+          const float w0 = fast_exp2(x[r] - (m[r] == -INFINITY ? 0.f : m[r] - P_LOG2));
+          const float w1 = fast_exp2(x[r + 1] - (m[r + 1] == -INFINITY ? 0.f : m[r + 1] - P_LOG2));
+          l[r] = fmaf(w0, inv_ks, l[r]);
+          l[r + 1] = fmaf(w1, inv_ks, l[r + 1]);
+          const uint32_t h = e4m3x2(w0, w1);
+          const float2 f = from_e4m3x2(h);
+          const uint32_t e = e4m3x2((w0 - f.x) * LO_UP, (w1 - f.y) * LO_UP);
+          if (r % 4 == 0) {
+            hi[r / 4] = h;
+            lo[r / 4] = e;
+          } else {
+            hi[r / 4] |= h << 16;
+            lo[r / 4] |= e << 16;
+          }
+        }
+        uint8_t* p = smem + OFF_P + buf * P_BYTES + key * 64;
+        const int sw = (key >> 1) & 3;
+        *reinterpret_cast<uint4*>(p + ((grp ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(p + (((2 + grp) ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&B->p_full[buf]);
+        ks = ks_next;
+      }
+      // ---- end of the segment: its sums, then the output or the piece's slot
+      const long long unit0 = u_seg - s.t0;              // the unit's first tile
+      const bool direct = cta_of(unit0, U, G) == cta_of(unit0 + s.k.nt - 1, U, G);
+      const long slot = (long)s.unit + c;
+      {
+        const float sum = transpose_reduce16<false>(l, lane);
+        if (lane < HALF) sh->sum[grp][wq][lane] = sum;
+      }
+      softmax_sync();
+      if (warp == 0) {
+        const int h = lane / HALF, r = lane % HALF;
+        const float sum = (sh->sum[h][0][r] + sh->sum[h][1][r]) + (sh->sum[h][2][r] + sh->sum[h][3][r]);
+        const bool dead = !((alive >> lane) & 1) || sum == 0.f;
+        const float l2 = dead ? -INFINITY : sh->m[lane] - P_LOG2 + log2f(sum);
+        float inv = dead ? 0.f : 1.f / sum, keep = 0.f, all = l2;
+        if (!s.first) {
+          const float old = sh->run_lse[lane], top = fmaxf(old, l2);
+          const float a = old == -INFINITY ? 0.f : exp2f(old - top), b = l2 == -INFINITY ? 0.f : exp2f(l2 - top);
+          keep = a + b == 0.f ? 0.f : a / (a + b);
+          inv = dead ? 0.f : inv * (b / (a + b));
+          all = a + b == 0.f ? -INFINITY : top + log2f(a + b);
+        }
+        sh->run_lse[lane] = all;
+        sh->inv[lane] = inv;
+        sh->keep[lane] = keep;
+        if (s.last) {
+          if (!direct) P.part_lse[slot * NR + lane] = all;
+          else if (P.lse && grp0 + lane < live)
+            P.lse[(long)s.b * live + grp0 + lane] = all == -INFINITY ? all : all * 0.6931471805599453f;
+        }
+      }
+      softmax_sync();
+      wait_bar(B, &B->o_seg, kseg & 1, status);
+      tc_fence_after();
+      float inv[HALF];
+      lds16(sh->inv + r0, inv);
+      const uint64_t stay = l2_policy_evict_last();
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        float o[HALF], e[HALF];
+        const uint32_t at = tmem + TM_O + 2 * NR * q + r0 + lanes;
+        tmem_ld16_nowait(at, o);
+        tmem_ld16_nowait(at + NR, e);
+        tmem_ld_wait();
+        tmem_reg_fence16(o);
+        tmem_reg_fence16(e);
+        float* part = P.part + (slot * NR + r0) * RANK + 128 * q + key;
+#pragma unroll
+        for (int r = 0; r < HALF; ++r) {
+          const float v = fmaf(e[r], 1.f / LO_UP, o[r]);
+          o[r] = inv[r] == 0.f ? 0.f : v * inv[r];
+        }
+        if (!s.first) {
+#pragma unroll
+          for (int r = 0; r < HALF; ++r) {
+            const float k = sh->keep[r0 + r];
+            if (k != 0.f) o[r] = fmaf(part[r * RANK], k, o[r]);
+          }
+        }
+        if (s.last && direct) {
+#pragma unroll
+          for (int r = 0; r < HALF; ++r)
+            if (grp0 + r0 + r < live)
+              P.o_lat[((long)s.b * live + grp0 + r0 + r) * RANK + 128 * q + key] = __float2half_rn(o[r]);
+        } else {
+          // (kept in L2 for the join: the cache's stream would push them out)
+#pragma unroll
+          for (int r = 0; r < HALF; ++r) st_global_hint(part + r * RANK, o[r], stay);
+        }
+      }
+      tc_fence_before();
+      u_seg += s.n;
+      g += s.n;
+      ++kseg;
+    }
+  }
+  pdl_wait();        // (a no-op for the threads that waited already)
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+// Grid (unit, quarter of the value dims): the pieces of each row added by log-sum-exp in CTA
+// order.  Thread i: dims 128 quarter + 4 (i % 32) .. + 3 of rows i / 32 + 8 j; JOIN_LOADS
+// pieces' rows are in flight at once.
+constexpr int JOIN_THREADS = 256, JOIN_LOADS = 4;
+__global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_constant__ Params P, int ctas) {
+  extern __shared__ float w_s[];           // [pieces][32]
+  __shared__ float lse_s[NR];
+  const int unit = blockIdx.x, part = blockIdx.y, tid = threadIdx.x;
+  const int b = unit / P.groups, grp0 = (unit % P.groups) * NR, live = P.rule.T * P.rule.H;
+  const long long t0 = P.first_tile[b], nt = P.first_tile[b + 1] - t0, U = P.first_tile[P.num_blocks] * P.groups;
+  const long row0 = (long)b * live + grp0;
+  const int d = 128 * part + 4 * (tid % 32);
+  float acc[4][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+  const int ra = tid / 32;
+  if (nt > 0) {
+    const int G = (int)min((long long)ctas, U);
+    const long long u = t0 * P.groups + (unit % P.groups) * nt;
+    const int f = cta_of(u, U, G), cnt = cta_of(u + nt - 1, U, G) - f + 1;
+    if (cnt == 1) return;
+    const long slot0 = (long)unit + f;
+    for (int i = tid; i < cnt * NR; i += JOIN_THREADS) w_s[i] = P.part_lse[slot0 * NR + i];
+    __syncthreads();
+    {
+      const int r = tid / 8, sl = tid % 8;
+      float mx = -INFINITY, den = 0.f;
+      bool nan = false;
+      for (int s = sl; s < cnt; s += 8) {
+        mx = fmaxf(mx, w_s[s * NR + r]);
+        nan |= isnan(w_s[s * NR + r]);
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      for (int s = sl; s < cnt; s += 8) {
+        const float l = w_s[s * NR + r];
+        const float w = l == -INFINITY ? 0.f : exp2f(l - mx);
+        w_s[s * NR + r] = w;
+        den += w;
+      }
+      if (nan) den = __uint_as_float(0x7fc00000u);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+      const float inv = den == 0.f ? 0.f : 1.f / den;
+      for (int s = sl; s < cnt; s += 8) w_s[s * NR + r] *= inv;
+      if (sl == 0) lse_s[r] = den == 0.f ? -INFINITY : mx + log2f(den);
+    }
+    __syncthreads();
+    for (int s0 = 0; s0 < cnt; s0 += JOIN_LOADS) {
+      float4 v[JOIN_LOADS][4];
+#pragma unroll
+      for (int i = 0; i < JOIN_LOADS; ++i)
+        if (s0 + i < cnt) {
+          const float* src = P.part + ((slot0 + s0 + i) * NR + ra) * RANK + d;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[i][j] = *reinterpret_cast<const float4*>(src + 8 * j * RANK);
+        }
+#pragma unroll
+      for (int i = 0; i < JOIN_LOADS; ++i)
+        if (s0 + i < cnt) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float w = w_s[(s0 + i) * NR + ra + 8 * j];
+            acc[j][0] = fmaf(w, v[i][j].x, acc[j][0]);
+            acc[j][1] = fmaf(w, v[i][j].y, acc[j][1]);
+            acc[j][2] = fmaf(w, v[i][j].z, acc[j][2]);
+            acc[j][3] = fmaf(w, v[i][j].w, acc[j][3]);
+          }
+        }
+    }
+  } else if (tid < NR) {
+    lse_s[tid] = -INFINITY;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = ra + 8 * j;
+    if (grp0 + r < live) {
+      const __half2 lo = __floats2half2_rn(acc[j][0], acc[j][1]), hi = __floats2half2_rn(acc[j][2], acc[j][3]);
+      uint2 u;
+      u.x = *reinterpret_cast<const uint32_t*>(&lo);
+      u.y = *reinterpret_cast<const uint32_t*>(&hi);
+      *reinterpret_cast<uint2*>(P.o_lat + (row0 + r) * RANK + d) = u;
+    }
+  }
+  if (part == 0 && tid < NR && grp0 + tid < live && P.lse) {
+    const float l2 = lse_s[tid];
+    P.lse[row0 + tid] = l2 == -INFINITY ? l2 : l2 * 0.6931471805599453f;
+  }
+}
+
+// The keys that each query sees, counted with the kernel's own rule: a warp a token.
+__global__ void __launch_bounds__(128) seen8_kernel(const tree::Rule a, long tokens, int32_t* stats) {
+  const long m = blockIdx.x * 4L + threadIdx.x / 32;
+  if (m >= tokens) return;
+  const long b = m / a.T;
+  const int i = (int)(m % a.T), lane = threadIdx.x % 32;
+  int W, ctx, count = 0, first = 0x7fffffff, last = -1;
+  const int n = tree::block_keys(a, (int)b, &W, &ctx, false);
+  bool ok = !a.q_visible || a.q_visible[m] != 0;
+  if (a.parent && n > 0) ok = tree::in_tree(a, a.parent + b * a.T, i, false) && ok;
+  for (int j = 64 * lane; j < n; j += 64 * 32) {
+    const unsigned long long bits = tree::key_bits(a, b, i, ok, n, W, ctx, j);
+    if (!bits) continue;
+    count += __popcll(bits);
+    first = min(first, j + __ffsll((long long)bits) - 1);
+    last = max(last, j + 63 - __clzll((long long)bits));
+  }
+  count = __reduce_add_sync(0xffffffffu, count);
+  first = __reduce_min_sync(0xffffffffu, first);
+  last = __reduce_max_sync(0xffffffffu, last);
+  if (lane == 0) {
+    stats[m * 3] = count;
+    stats[m * 3 + 1] = count ? first : -1;
+    stats[m * 3 + 2] = last;
+  }
+}
+
+// Workspace: a slot for every (unit, CTA) piece, units + CTAs at most.
+size_t ws_layout(const mla_handle* h, const mla_attn_desc_t& d, size_t* off_lse, size_t* off_first) {
+  const long groups = ((long)d.block_len * h->lay.H + NR - 1) / NR;
+  const long slots = d.num_blocks * groups + h->num_sms;
+  size_t o = align256((size_t)slots * NR * RANK * 4);
+  *off_lse = o;
+  o += align256((size_t)slots * NR * 4);
+  *off_first = o;
+  return o + align256((size_t)(d.num_blocks + 1) * 8);
+}
+
+}  // namespace
+
+size_t attention_ws(const mla_handle* h, const mla_attn_desc_t& d) {
+  size_t a, b;
+  return ws_layout(h, d, &a, &b);
+}
+
+mla_status_t attention(cudaStream_t st, mla_handle* h, const tree::Rule& r, const mla_attn_desc_t& d,
+                       const __nv_bfloat16* q_abs, const mla_cache8_t& c, __half* o_lat, float* lse,
+                       void* ws, bool pdl) {
+  const int ps = h->cfg.page_size;
+  const long slots = (long)r.num_pages * ps;
+  Params P;
+  P.seg_rows = ps < KT ? ps : KT;
+  if (!make_tmap_chunked(&P.tmL, false, c.latent, slots, RANK / 2, RANK / 2, P.seg_rows, 1) ||
+      !make_tmap_2d(&P.tmR, false, c.rope, slots, ROPE, ROPE, P.seg_rows))
+    return fail(MLA_ERR_CUDA, "attention8: cuTensorMapEncodeTiled failed");
+  size_t off_lse, off_first;
+  ws_layout(h, d, &off_lse, &off_first);
+  P.rule = r;
+  P.scale = c.scale;
+  P.q = q_abs;
+  P.o_lat = o_lat;
+  P.lse = lse;
+  P.part = (float*)ws;
+  P.part_lse = (float*)((char*)ws + off_lse);
+  P.first_tile = (long long*)((char*)ws + off_first);
+  P.num_blocks = d.num_blocks;
+  P.groups = (int)(((long)d.block_len * h->lay.H + NR - 1) / NR);
+  P.scale_log2 = h->scale * 1.4426950408889634f;
+  if ((long)P.num_blocks * P.groups > 0x3fffffffL) return fail(MLA_ERR_INVALID_ARG, "attention8: too many rows");
+  const size_t join_smem = (size_t)h->num_sms * NR * 4;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    cudaFuncSetAttribute(attn8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  });
+  Launch L(dim3((unsigned)h->num_sms), dim3(THREADS), SMEM_BYTES, st, pdl);
+  MLA_CUDA_TRY(cudaLaunchKernelEx(&L.cfg, attn8_kernel, P));
+  join8_kernel<<<dim3((unsigned)(P.num_blocks * P.groups), 4), JOIN_THREADS, join_smem, st>>>(P, h->num_sms);
+  MLA_CUDA_TRY(cudaGetLastError());
+  h->launches += 2;
+  if (d.vis_stats) {
+    const long tokens = (long)d.num_blocks * d.block_len;
+    seen8_kernel<<<(unsigned)((tokens + 3) / 4), 128, 0, st>>>(r, tokens, d.vis_stats);
+    MLA_CUDA_TRY(cudaGetLastError());
+    h->launches += 1;
+  }
+  return MLA_OK;
+}
+
+}  // namespace cache8
+}  // namespace mla

@@ -1,5 +1,5 @@
 // The latent cache in 8 bits: one entry's form, and the launchers of the kernels that
-// write it and attend it (cache8.cu, attn8.cu).
+// write it and attend it (cache8.cu, attn8_tc.cu).
 //
 // An entry is 512 latent dims in e4m3 over a scale 2^k of its own, 64 rotary dims in
 // bf16, and the scale.  A power of two, so that every number the cache holds is a
