@@ -21,10 +21,11 @@
 // normalised partial to slot unit + CTA (unique: neither ever falls along the order and
 // one of them grows), or the output itself where the unit lies in one CTA; the join
 // kernel adds the pieces by log-sum-exp in order.
-//   warps 0-7  : softmax, two groups of 128 threads, thread = key, 16 rows each
+//   warps 0-7  : softmax, two groups of 128 threads, thread = key, 16 rows each; between
+//                segments the next one's queries are split before the last one's output is
+//                stored, so that its first S runs meanwhile
 //   warp 8     : tensor-memory allocation, MMA issue: S(0) S(1) O(0) S(2) O(1) ...
 //   warps 9-11 : copies; a tile is five 16 KB chunks, each refilled once its product is done
-//   warps 12-15: the next unit's queries, held in registers until the last S is done
 #include "cache8.cuh"
 #include "gemm_tc.cuh"
 #include "tc_ptx.cuh"
@@ -41,7 +42,7 @@ using namespace tc;
 
 constexpr int KT = 128, NR = 32, HALF = 16;          // keys a tile, rows a unit, rows a softmax thread
 constexpr int SEG_TILES = 64;                        // tiles after which a piece is put away
-constexpr int THREADS = 512, SM_THREADS = 256;
+constexpr int THREADS = 384, SM_THREADS = 256;
 constexpr int STAGES = 2, CHUNKS = 5;                // 4 chunks of 128 latent dims, one of 64 rotary ones
 constexpr int CH_BYTES = KT * 128;                   // 16 KB
 constexpr int STAGE_BYTES = CHUNKS * CH_BYTES;
@@ -52,7 +53,7 @@ constexpr int OFF_Q = STAGES * STAGE_BYTES;
 constexpr int OFF_QR = OFF_Q + 4 * Q_CH_BYTES;
 constexpr int OFF_P = OFF_QR + QR_BYTES;
 constexpr int OFF_RED = OFF_P + 2 * P_BYTES;
-constexpr int COPY_WARPS = 3, Q_WARPS = 4, Q_ROWS = NR / Q_WARPS;
+constexpr int COPY_WARPS = 3, Q_ROWS = NR / (SM_THREADS / 32), Q_BATCH = 2;
 // TMEM: S of tile g at column 128 (g % 2): hi 0-31, lo 32-63, rotary 64-95; O at 256: 4 x (hi | lo)
 constexpr uint32_t TMEM_COLS = 512, TM_O = 256;
 constexpr float SLACK_LOG2 = 1.75f;                  // 2^7 2^1.75 < 448
@@ -76,7 +77,7 @@ struct Params {
 struct Bars {
   uint64_t full[STAGES];            // a tile landed
   uint64_t empty[STAGES][CHUNKS];   // the products of a chunk are done
-  uint64_t q_full, q_empty;
+  uint64_t q_full;
   uint64_t s_full[2];               // S(g) done (and all before it), by g % 2
   uint64_t p_full[2];               // P(g) in shared memory
   uint64_t o_done;                  // O(g) done (waited on for a rescale only)
@@ -88,9 +89,9 @@ struct Bars {
 
 struct __align__(16) Shared {
   float wpart[2][2][4][HALF];       // by tile parity, group, warp: row maxima
-  float m[NR];                      // reference of each row (log2)
+  float m[NR];                      // reference of each row (log2), at a segment's end
   float inv[NR], keep[NR];          // factors of a segment's O and of what its piece has put away
-  float q_scale[2][NR];             // c 2^k of each row, by segment parity
+  float q_scale[NR];                // c 2^k of each row
   int lo[NR], hi[NR];               // context keys that each row sees
   float sum[2][4][HALF];
   float run_lse[NR];                // log2-sum-exp of what a piece has put away
@@ -257,10 +258,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       mbar_init(&B->full[s], 1);
       for (int q = 0; q < CHUNKS; ++q) mbar_init(&B->empty[s][q], 1);
     }
-    mbar_init(&B->q_full, Q_WARPS);
-    mbar_init(&B->q_empty, 1);
+    mbar_init(&B->q_full, SM_THREADS / 32);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&B->s_full[i], 2);
+      mbar_init(&B->s_full[i], 1);
       mbar_init(&B->p_full[i], SM_THREADS);
     }
     mbar_init(&B->o_done, 1);
@@ -274,48 +274,52 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
   if (warp == 8) tmem_alloc(&B->tmem_slot, TMEM_COLS);
 
   // ---- schedule: the tiles of one group before each block, then this CTA's first unit and tile
+  // (from the same numbers when every block has a thread)
   long long U = 0, u0 = 0, u1 = 0;
-  int G = 1;
-  for (int pass = 0; pass < 2; ++pass) {
-    long long run = 0;
-    for (int base = 0; base < nb; base += THREADS) {
-      const int b = base + tid;
-      const int nt = b < nb ? keys_of(P, b, c == 0 && pass == 0).nt : 0;
-      int x = nt;
+  int G = 1, nt = 0;
+  long long excl = 0;
+  auto count = [&](int base, long long run, bool report) {
+    const int b = base + tid;
+    nt = b < nb ? keys_of(P, b, report).nt : 0;
+    int x = nt;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (lane == 31) sh->scan[warp] = x;
-      __syncthreads();
-      long long before = run, tot = 0;
-      for (int w = 0; w < THREADS / 32; ++w) {
-        before += w < warp ? sh->scan[w] : 0;
-        tot += sh->scan[w];
-      }
-      const long long excl = before + x - nt;
-      run += tot;
-      __syncthreads();
-      if (pass == 1 && b < nb) {
-        if (nt > 0 && u1 > u0 && u0 >= excl * P.groups && u0 < (excl + nt) * P.groups) {
-          const long long in = u0 - excl * P.groups;
-          sh->first_unit = b * P.groups + (int)(in / nt);
-          sh->first_tile = (int)(in % nt);
-        }
-        if (c == 0) {
-          pdl_wait();                      // the workspace may still be read by the kernel before
-          P.first_tile[b] = excl;
-          if (b == nb - 1) P.first_tile[nb] = excl + nt;
-        }
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    if (pass == 0) {
-      // the first min(gridDim, U) CTAs take one range each, so none is empty
-      U = run * P.groups;
-      G = (int)min((long long)gridDim.x, max(U, 1LL));
-      u0 = c < G ? U * c / G : U;
-      u1 = c < G ? U * (c + 1) / G : U;
+    if (lane == 31) sh->scan[warp] = x;
+    __syncthreads();
+    long long before = run, all = run;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      before += w < warp ? sh->scan[w] : 0;
+      all += sh->scan[w];
+    }
+    __syncthreads();
+    excl = before + x - nt;
+    return all;
+  };
+  long long run = 0;
+  for (int base = 0; base < nb; base += THREADS) run = count(base, run, c == 0);
+  U = run * P.groups;
+  // the first min(gridDim, U) CTAs take one range each, so none is empty
+  G = (int)min((long long)gridDim.x, max(U, 1LL));
+  u0 = c < G ? U * c / G : U;
+  u1 = c < G ? U * (c + 1) / G : U;
+  run = 0;
+  for (int base = 0; base < nb; base += THREADS) {
+    if (nb > THREADS) run = count(base, run, false);
+    const int b = base + tid;
+    if (b < nb) {
+      if (nt > 0 && u1 > u0 && u0 >= excl * P.groups && u0 < (excl + nt) * P.groups) {
+        const long long in = u0 - excl * P.groups;
+        sh->first_unit = b * P.groups + (int)(in / nt);
+        sh->first_tile = (int)(in % nt);
+      }
+      if (c == 0) {
+        pdl_wait();                        // the workspace may still be read by the kernel before
+        P.first_tile[b] = excl;
+        if (b == nb - 1) P.first_tile[nb] = excl + nt;
+      }
     }
   }
   tc_fence_before();
@@ -361,8 +365,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
 #pragma unroll
               for (int i = 0; i < 4; ++i) mma_f8(d, a + q * U_CH + 2 * i, dQ + q * U_Q + 2 * i, id_s, q + i > 0);
             mma_commit(&B->s_full[gg & 1]);
-            mbar_arrive(&B->s_full[gg & 1]);       // (hands on the query warps' row scales)
-            if (t == s.n - 1) mma_commit(&B->q_empty);
           }
           if (t >= 1) {
             const uint32_t gg = g + t - 1, st = gg % STAGES;
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       mma_commit(&B->drain);
       mbar_wait(&B->drain, 0, status);
     }
-  } else if (warp >= 9 && warp < 9 + COPY_WARPS) {
+  } else if (warp >= 9) {
     if (lane == 0 && work) {
       // ---- copies: this warp takes every third of a tile's (chunk, page segment) copies ----
       const int me = warp - 9;
@@ -435,70 +437,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       for (uint32_t i = g > STAGES ? g - STAGES : 0; i < g; ++i)
         mbar_wait(&B->full[i % STAGES], (i / STAGES) & 1, status);
     }
-  } else if (warp >= 9 + COPY_WARPS) {
-    if (work) {
-      // ---- queries of each segment: split in two e4m3 numbers ----
-      const int w = warp - 9 - COPY_WARPS;
-      uint4 x[Q_ROWS][2];
-      uint32_t xr[Q_ROWS];
-      auto load = [&](const Seg& s) {
-        const int r0 = (s.unit % P.groups) * NR, live = P.rule.T * P.rule.H;
-        const long base = (long)s.b * live + r0;
-#pragma unroll
-        for (int i = 0; i < Q_ROWS; ++i) {
-          const int r = w * Q_ROWS + i;
-          const bool in = r0 + r < live;
-          const uint4* src = reinterpret_cast<const uint4*>(P.q + (base + (in ? r : 0)) * ENTRY);
-          x[i][0] = in ? src[2 * lane] : make_uint4(0, 0, 0, 0);
-          x[i][1] = in ? src[2 * lane + 1] : make_uint4(0, 0, 0, 0);
-          xr[i] = in ? reinterpret_cast<const uint32_t*>(src + RANK / 8)[lane] : 0u;
-        }
-      };
-      SegIter it = start;
-      Seg s;
-      uint32_t kseg = 0;
-      bool ok = true, have = next_seg(P, it, s);
-      pdl_wait();
-      if (have) load(s);
-      while (have && ok) {
-        if (kseg > 0) ok = __all_sync(0xffffffffu, wait_bar(B, &B->q_empty, (kseg - 1) & 1, status));
-        if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < Q_ROWS; ++i) {
-          const int r = w * Q_ROWS + i;
-          const uint32_t u[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
-          uint32_t m = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = max(m, max(u[e] & 0x7fffu, (u[e] >> 16) & 0x7fffu));
-          m = __reduce_max_sync(0xffffffffu, m);
-          const int k = max((int)(m >> 7) - 127 - 8 + ((m & 0x7fu) > 96u ? 1 : 0), -100);
-          const float inv = pow2(-k);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f[4] = {__uint_as_float(u[2 * e] << 16) * inv, __uint_as_float(u[2 * e] & 0xffff0000u) * inv,
-                                __uint_as_float(u[2 * e + 1] << 16) * inv,
-                                __uint_as_float(u[2 * e + 1] & 0xffff0000u) * inv};
-            const uint32_t h0 = e4m3x2(f[0], f[1]), h1 = e4m3x2(f[2], f[3]);
-            const float2 g0 = from_e4m3x2(h0), g1 = from_e4m3x2(h1);
-            hi[e] = h0 | h1 << 16;
-            lo[e] = e4m3x2(f[0] - g0.x, f[1] - g0.y) | e4m3x2(f[2] - g1.x, f[3] - g1.y) << 16;
-          }
-          uint8_t* q = smem + OFF_Q + (lane / 8) * Q_CH_BYTES + (((lane % 8) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(q + r * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(q + (NR + r) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          *reinterpret_cast<uint32_t*>(smem + OFF_QR + r * 128 + (((lane / 4) ^ (r & 7)) << 4) + (lane % 4) * 4) = xr[i];
-          // (a query that is no number makes its row none, whatever its bytes became)
-          if (lane == 0) sh->q_scale[kseg & 1][r] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(k) * P.scale_log2;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&B->q_full);
-        ++kseg;
-        have = next_seg(P, it, s);
-        if (have) load(s);
-      }
-    }
   } else if (work) {
     // ---- softmax: thread = key (TMEM lane), rows 16 grp .. 16 grp + 15.  After a wait
     // that gave up everything runs on to its end (the barriers below count every thread). ----
@@ -519,8 +457,140 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       return __ldg(P.scale + (long)pg * ps + j % ps);
     };
     pdl_wait();
-    while (next_seg(P, it, s)) {
+    uint32_t alive = 0;
+    float l[HALF], m[HALF];
+    Seg done{};                            // the segment whose tiles are done
+    bool have = next_seg(P, it, s), ended = false;
+    while (true) {
       const int grp0 = (s.unit % P.groups) * NR;         // the unit's first row in its block
+      if (have) {
+        // ---- queries: four rows a warp, each split in two e4m3 numbers over a power of two (the
+        // S of the segment before are done: its last tile's weights have been made) ----
+#pragma unroll 1
+        for (int i0 = 0; i0 < Q_ROWS; i0 += Q_BATCH) {
+          uint4 v[Q_BATCH][2];
+          uint32_t vr[Q_BATCH];
+#pragma unroll
+          for (int i = 0; i < Q_BATCH; ++i) {
+            const int r = warp * Q_ROWS + i0 + i;
+            const bool in = grp0 + r < live;
+            const uint4* src =
+                reinterpret_cast<const uint4*>(P.q + ((long)s.b * live + (in ? grp0 + r : 0)) * ENTRY);
+            v[i][0] = in ? src[2 * lane] : make_uint4(0, 0, 0, 0);
+            v[i][1] = in ? src[2 * lane + 1] : make_uint4(0, 0, 0, 0);
+            vr[i] = in ? reinterpret_cast<const uint32_t*>(src + RANK / 8)[lane] : 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < Q_BATCH; ++i) {
+            const int r = warp * Q_ROWS + i0 + i;
+            const uint32_t u[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = max(top, max(u[e] & 0x7fffu, (u[e] >> 16) & 0x7fffu));
+            top = __reduce_max_sync(0xffffffffu, top);
+            const int k = max((int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 96u ? 1 : 0), -100);
+            const float inv = pow2(-k);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float f[4] = {__uint_as_float(u[2 * e] << 16) * inv, __uint_as_float(u[2 * e] & 0xffff0000u) * inv,
+                                  __uint_as_float(u[2 * e + 1] << 16) * inv,
+                                  __uint_as_float(u[2 * e + 1] & 0xffff0000u) * inv};
+              const uint32_t h0 = e4m3x2(f[0], f[1]), h1 = e4m3x2(f[2], f[3]);
+              const float2 g0 = from_e4m3x2(h0), g1 = from_e4m3x2(h1);
+              hi[e] = h0 | h1 << 16;
+              lo[e] = e4m3x2(f[0] - g0.x, f[1] - g0.y) | e4m3x2(f[2] - g1.x, f[3] - g1.y) << 16;
+            }
+            uint8_t* q = smem + OFF_Q + (lane / 8) * Q_CH_BYTES + (((lane % 8) ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(q + r * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(q + (NR + r) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint32_t*>(smem + OFF_QR + r * 128 + (((lane / 4) ^ (r & 7)) << 4) + (lane % 4) * 4) = vr[i];
+            // (a query that is no number makes its row none, whatever its bytes became)
+            if (lane == 0) sh->q_scale[r] = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(k) * c2;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B->q_full);
+      }
+      if (ended) {
+        // ---- end of a segment: its sums, then the output or the piece's slot ----
+        const int row0 = (done.unit % P.groups) * NR;
+        const long long unit0 = u_seg - done.t0;              // the unit's first tile
+        const bool direct = cta_of(unit0, U, G) == cta_of(unit0 + done.k.nt - 1, U, G);
+        const long slot = (long)done.unit + c;
+        {
+          const float sum = transpose_reduce16<false>(l, lane);
+          if (lane < HALF) sh->sum[grp][wq][lane] = sum;
+        }
+        softmax_sync();
+        if (warp == 0) {
+          const int h = lane / HALF, r = lane % HALF;
+          const float sum = (sh->sum[h][0][r] + sh->sum[h][1][r]) + (sh->sum[h][2][r] + sh->sum[h][3][r]);
+          const bool dead = !((alive >> lane) & 1) || sum == 0.f;
+          const float l2 = dead ? -INFINITY : sh->m[lane] - P_LOG2 + log2f(sum);
+          float inv = dead ? 0.f : 1.f / sum, keep = 0.f, all = l2;
+          if (!done.first) {
+            const float old = sh->run_lse[lane], top = fmaxf(old, l2);
+            const float a = old == -INFINITY ? 0.f : exp2f(old - top), b = l2 == -INFINITY ? 0.f : exp2f(l2 - top);
+            keep = a + b == 0.f ? 0.f : a / (a + b);
+            inv = dead ? 0.f : inv * (b / (a + b));
+            all = a + b == 0.f ? -INFINITY : top + log2f(a + b);
+          }
+          sh->run_lse[lane] = all;
+          sh->inv[lane] = inv;
+          sh->keep[lane] = keep;
+          if (done.last) {
+            if (!direct) P.part_lse[slot * NR + lane] = all;
+            else if (P.lse && row0 + lane < live)
+              P.lse[(long)done.b * live + row0 + lane] = all == -INFINITY ? all : all * 0.6931471805599453f;
+          }
+        }
+        softmax_sync();
+        wait_bar(B, &B->o_seg, kseg & 1, status);
+        tc_fence_after();
+        float inv[HALF];
+        lds16(sh->inv + r0, inv);
+        const uint64_t stay = l2_policy_evict_last();
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float o[HALF], e[HALF];
+          const uint32_t at = tmem + TM_O + 2 * NR * q + r0 + lanes;
+          tmem_ld16_nowait(at, o);
+          tmem_ld16_nowait(at + NR, e);
+          tmem_ld_wait();
+          tmem_reg_fence16(o);
+          tmem_reg_fence16(e);
+          float* part = P.part + (slot * NR + r0) * RANK + 128 * q + key;
+#pragma unroll
+          for (int r = 0; r < HALF; ++r) {
+            const float v = fmaf(e[r], 1.f / LO_UP, o[r]);
+            o[r] = inv[r] == 0.f ? 0.f : v * inv[r];
+          }
+          if (!done.first) {
+#pragma unroll
+            for (int r = 0; r < HALF; ++r) {
+              const float k = sh->keep[r0 + r];
+              if (k != 0.f) o[r] = fmaf(part[r * RANK], k, o[r]);
+            }
+          }
+          if (done.last && direct) {
+#pragma unroll
+            for (int r = 0; r < HALF; ++r)
+              if (row0 + r0 + r < live)
+                P.o_lat[((long)done.b * live + row0 + r0 + r) * RANK + 128 * q + key] = __float2half_rn(o[r]);
+          } else {
+            // (kept in L2 for the join: the cache's stream would push them out)
+#pragma unroll
+            for (int r = 0; r < HALF; ++r) st_global_hint(part + r * RANK, o[r], stay);
+          }
+        }
+        tc_fence_before();
+        u_seg += done.n;
+        g += done.n;
+        ++kseg;
+      }
+      if (!have) break;
       const int k_begin = s.k.j_lo + s.t0 * KT;
       float ks = scale_at(0);
       softmax_sync();                      // the segment before is done with the rows' state
@@ -539,27 +609,29 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         }
         sh->lo[lane] = lo;
         sh->hi[lane] = hi;
-        sh->m[lane] = -INFINITY;
         if (s.first) sh->run_lse[lane] = -INFINITY;
         const int fl = __reduce_max_sync(0xffffffffu, see ? lo : 0);
         const int fh = __reduce_min_sync(0xffffffffu, see ? hi : 0x7fffffff);
         const int al = __reduce_min_sync(0xffffffffu, see ? lo : 0x7fffffff);
         const int ah = __reduce_max_sync(0xffffffffu, see ? hi : 0);
-        const uint32_t alive = __ballot_sync(0xffffffffu, see);
+        const uint32_t sees = __ballot_sync(0xffffffffu, see);
         if (lane == 0) {
           sh->fast_lo = fl;
-          sh->fast_hi = alive ? fh : 0;
+          sh->fast_hi = sees ? fh : 0;
           sh->any_lo = al;
           sh->any_hi = ah;
-          sh->alive = alive;
+          sh->alive = sees;
         }
       }
       softmax_sync();
-      const uint32_t alive = sh->alive;
+      alive = sh->alive;
       const int fast_lo = sh->fast_lo, fast_hi = sh->fast_hi, any_lo = sh->any_lo, any_hi = sh->any_hi;
-      float l[HALF];
 #pragma unroll
-      for (int r = 0; r < HALF; ++r) l[r] = 0.f;
+      for (int r = 0; r < HALF; ++r) {
+        l[r] = 0.f;
+        m[r] = -INFINITY;
+      }
+      float m_lane = -INFINITY;            // the reference of row lane % 16
       for (int t = 0; t < s.n; ++t) {
         const uint32_t gg = g + t, buf = gg & 1;
         const int j0 = k_begin + t * KT, j = j0 + key;
@@ -593,7 +665,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
           tmem_reg_fence16(y);
           tmem_reg_fence16(z);
           float qs[HALF];
-          lds16(sh->q_scale[kseg & 1] + r0, qs);
+          lds16(sh->q_scale + r0, qs);
           const float kexp = (float)((int)(__float_as_uint(ks) >> 23) - 127);    // log2 of a power of two
 #pragma unroll
           for (int r = 0; r < HALF; ++r) x[r] = fmaf(x[r] + y[r], qs[r] * ks, fmaf(z[r], c2, kexp));
@@ -621,43 +693,25 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
               for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(row + q * CH_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
           }
         }
-        float m[HALF];
         {
           float y[HALF];
 #pragma unroll
           for (int r = 0; r < HALF; ++r) y[r] = x[r];
-          const float top = transpose_reduce16<true>(y, lane);
+          float top = transpose_reduce16<true>(y, lane);
           if (lane < HALF) sh->wpart[buf][grp][wq][lane] = top;
           group_sync(grp);
-          lds16(sh->m + r0, m);
-          bool grow = false;
-#pragma unroll
-          for (int r = 0; r < HALF; r += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(&sh->wpart[buf][grp][0][r]);
-            const float4 b = *reinterpret_cast<const float4*>(&sh->wpart[buf][grp][1][r]);
-            const float4 d = *reinterpret_cast<const float4*>(&sh->wpart[buf][grp][2][r]);
-            const float4 e = *reinterpret_cast<const float4*>(&sh->wpart[buf][grp][3][r]);
-            y[r] = fmaxf(fmaxf(a.x, b.x), fmaxf(d.x, e.x));
-            y[r + 1] = fmaxf(fmaxf(a.y, b.y), fmaxf(d.y, e.y));
-            y[r + 2] = fmaxf(fmaxf(a.z, b.z), fmaxf(d.z, e.z));
-            y[r + 3] = fmaxf(fmaxf(a.w, b.w), fmaxf(d.w, e.w));
-          }
-#pragma unroll
-          for (int r = 0; r < HALF; ++r) grow |= y[r] > m[r] + SLACK_LOG2;
-          if (grow) {                      // (the same for every thread of the group)
-            group_sync(grp);               // everyone has read the references
+          const float* part = &sh->wpart[buf][grp][0][lane % HALF];
+          top = fmaxf(fmaxf(part[0], part[HALF]), fmaxf(part[2 * HALF], part[3 * HALF]));
+          const bool up = top > m_lane + SLACK_LOG2;
+          if (__any_sync(0xffffffffu, up)) {               // (the same for every warp of the group)
+            const float m_new = up ? ceilf(top) : m_lane;
+            const float f = m_lane == -INFINITY ? 1.f : fast_exp2(m_lane - m_new);
+            m_lane = m_new;
 #pragma unroll
             for (int r = 0; r < HALF; ++r) {
-              const float m_new = y[r] > m[r] + SLACK_LOG2 ? ceilf(y[r]) : m[r];
-              y[r] = m[r] == -INFINITY ? 1.f : fast_exp2(m[r] - m_new);
-              m[r] = m_new;
+              m[r] = __shfl_sync(0xffffffffu, m_new, r);
+              y[r] = __shfl_sync(0xffffffffu, f, r);
               l[r] *= y[r];
-            }
-            if (key < HALF) {
-              float own = m[0];
-#pragma unroll
-              for (int r = 1; r < HALF; ++r) own = key == r ? m[r] : own;
-              sh->m[r0 + key] = own;
             }
             if (t > 0) {
               // O(g - 1) is issued behind S(g), and O(g) only behind this tile's P
@@ -708,80 +762,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         mbar_arrive(&B->p_full[buf]);
         ks = ks_next;
       }
-      // ---- end of the segment: its sums, then the output or the piece's slot
-      const long long unit0 = u_seg - s.t0;              // the unit's first tile
-      const bool direct = cta_of(unit0, U, G) == cta_of(unit0 + s.k.nt - 1, U, G);
-      const long slot = (long)s.unit + c;
-      {
-        const float sum = transpose_reduce16<false>(l, lane);
-        if (lane < HALF) sh->sum[grp][wq][lane] = sum;
-      }
-      softmax_sync();
-      if (warp == 0) {
-        const int h = lane / HALF, r = lane % HALF;
-        const float sum = (sh->sum[h][0][r] + sh->sum[h][1][r]) + (sh->sum[h][2][r] + sh->sum[h][3][r]);
-        const bool dead = !((alive >> lane) & 1) || sum == 0.f;
-        const float l2 = dead ? -INFINITY : sh->m[lane] - P_LOG2 + log2f(sum);
-        float inv = dead ? 0.f : 1.f / sum, keep = 0.f, all = l2;
-        if (!s.first) {
-          const float old = sh->run_lse[lane], top = fmaxf(old, l2);
-          const float a = old == -INFINITY ? 0.f : exp2f(old - top), b = l2 == -INFINITY ? 0.f : exp2f(l2 - top);
-          keep = a + b == 0.f ? 0.f : a / (a + b);
-          inv = dead ? 0.f : inv * (b / (a + b));
-          all = a + b == 0.f ? -INFINITY : top + log2f(a + b);
-        }
-        sh->run_lse[lane] = all;
-        sh->inv[lane] = inv;
-        sh->keep[lane] = keep;
-        if (s.last) {
-          if (!direct) P.part_lse[slot * NR + lane] = all;
-          else if (P.lse && grp0 + lane < live)
-            P.lse[(long)s.b * live + grp0 + lane] = all == -INFINITY ? all : all * 0.6931471805599453f;
-        }
-      }
-      softmax_sync();
-      wait_bar(B, &B->o_seg, kseg & 1, status);
-      tc_fence_after();
-      float inv[HALF];
-      lds16(sh->inv + r0, inv);
-      const uint64_t stay = l2_policy_evict_last();
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        float o[HALF], e[HALF];
-        const uint32_t at = tmem + TM_O + 2 * NR * q + r0 + lanes;
-        tmem_ld16_nowait(at, o);
-        tmem_ld16_nowait(at + NR, e);
-        tmem_ld_wait();
-        tmem_reg_fence16(o);
-        tmem_reg_fence16(e);
-        float* part = P.part + (slot * NR + r0) * RANK + 128 * q + key;
-#pragma unroll
-        for (int r = 0; r < HALF; ++r) {
-          const float v = fmaf(e[r], 1.f / LO_UP, o[r]);
-          o[r] = inv[r] == 0.f ? 0.f : v * inv[r];
-        }
-        if (!s.first) {
-#pragma unroll
-          for (int r = 0; r < HALF; ++r) {
-            const float k = sh->keep[r0 + r];
-            if (k != 0.f) o[r] = fmaf(part[r * RANK], k, o[r]);
-          }
-        }
-        if (s.last && direct) {
-#pragma unroll
-          for (int r = 0; r < HALF; ++r)
-            if (grp0 + r0 + r < live)
-              P.o_lat[((long)s.b * live + grp0 + r0 + r) * RANK + 128 * q + key] = __float2half_rn(o[r]);
-        } else {
-          // (kept in L2 for the join: the cache's stream would push them out)
-#pragma unroll
-          for (int r = 0; r < HALF; ++r) st_global_hint(part + r * RANK, o[r], stay);
-        }
-      }
-      tc_fence_before();
-      u_seg += s.n;
-      g += s.n;
-      ++kseg;
+      if (wq == 0 && lane < HALF) sh->m[r0 + lane] = m_lane;
+      done = s;
+      ended = true;
+      have = next_seg(P, it, s);
     }
   }
   pdl_wait();        // (a no-op for the threads that waited already)
