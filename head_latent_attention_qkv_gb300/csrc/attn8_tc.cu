@@ -24,7 +24,7 @@
 //   warps 0-7  : softmax, two groups of 128 threads, thread = key, 16 rows each; between
 //                segments the next one's queries are split before the last one's output is
 //                stored, so that its first S runs meanwhile
-//   warp 8     : tensor-memory allocation, MMA issue: S(0) S(1) O(0) S(2) O(1) ...
+//   warp 8     : tensor-memory allocation, MMA issue
 //   warps 9-11 : copies; a tile is five 16 KB chunks, each refilled once its product is done
 #include "cache8.cuh"
 #include "gemm_tc.cuh"
@@ -67,7 +67,7 @@ struct Params {
   const __nv_bfloat16* q;
   __half* o_lat;      // [rows, 512]
   float* lse;         // [rows] or NULL
-  float* part;        // [slots, 32, 512] normalised partial outputs
+  float* part;        // [slots][4 quarters][8 x 4 rows][128 dims][4 rows] normalised partial outputs
   float* part_lse;    // [slots, 32]
   long long* first_tile;   // [blocks + 1] tiles of a group's worth of keys before each block
   int num_blocks, groups, seg_rows;
@@ -136,6 +136,12 @@ __device__ __forceinline__ uint64_t smem_desc_sw64_mn(const void* tile) {
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)4 << 61;
   return d;
+}
+
+// 16-byte global store with an L2 eviction policy.
+__device__ __forceinline__ void st_global_hint4(float4* p, float4 v, uint64_t policy) {
+  asm volatile("st.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;"
+               ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "l"(policy) : "memory");
 }
 
 // 16 consecutive fp32 columns of this thread's TMEM lane, no wait.
@@ -350,12 +356,30 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       while (ok && next_seg(P, it, s)) {
         if (!(ok = wait_bar(B, &B->q_full, kseg & 1, status))) break;
         tc_fence_after();
-        for (int t = 0; t <= s.n && ok; ++t) {
-          if (t < s.n) {
-            const uint32_t gg = g + t, st = gg % STAGES;
-            if (!(ok = wait_bar(B, &B->full[st], (gg / STAGES) & 1, status))) break;
+        // S of the next tile and O of the one before it, whichever can start: a tile that is
+        // still on its way does not hold up the product that frees the place of the next
+        int ns = 0, no = 0;
+        uint32_t spins = 0;
+        while (no < s.n) {
+          const uint32_t gs = g + ns, go = g + no;
+          if (no < ns && mbar_test_wait(&B->p_full[go & 1], (go >> 1) & 1)) {
             tc_fence_after();
-            const uint32_t d = tmem + 128 * (gg & 1);
+            const uint32_t st = go % STAGES;
+            const uint64_t a = dV + st * U_STAGE, p = dP + (go & 1) * U_P;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_f8(tmem + TM_O + 64 * q, a + q * U_CH + i * U_VSTEP, p + i * U_PSTEP, id_o, no > 0 || i > 0);
+              mma_commit(&B->empty[st][q]);
+            }
+            mma_commit(&B->o_done);
+            if (++no == s.n) mma_commit(&B->o_seg);
+            spins = 0;
+          } else if (ns < s.n && ns <= no + 1 && mbar_test_wait(&B->full[gs % STAGES], (gs / STAGES) & 1)) {
+            // (the place of S(ns) was read before O(ns - 2) could start)
+            tc_fence_after();
+            const uint32_t st = gs % STAGES, d = tmem + 128 * (gs & 1);
             const uint64_t a = dK + st * U_STAGE;
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma_f16(d + 64, a + 4 * U_CH + 2 * i, dR + 2 * i, id_r, i > 0);
@@ -364,22 +388,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
             for (int q = 0; q < 4; ++q)
 #pragma unroll
               for (int i = 0; i < 4; ++i) mma_f8(d, a + q * U_CH + 2 * i, dQ + q * U_Q + 2 * i, id_s, q + i > 0);
-            mma_commit(&B->s_full[gg & 1]);
-          }
-          if (t >= 1) {
-            const uint32_t gg = g + t - 1, st = gg % STAGES;
-            if (!(ok = wait_bar(B, &B->p_full[gg & 1], (gg >> 1) & 1, status))) break;
-            tc_fence_after();
-            const uint64_t a = dV + st * U_STAGE, p = dP + (gg & 1) * U_P;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma_f8(tmem + TM_O + 64 * q, a + q * U_CH + i * U_VSTEP, p + i * U_PSTEP, id_o, t > 1 || i > 0);
-              mma_commit(&B->empty[st][q]);
-            }
-            mma_commit(&B->o_done);
-            if (t == s.n) mma_commit(&B->o_seg);
+            mma_commit(&B->s_full[gs & 1]);
+            ++ns;
+            spins = 0;
+          } else if (*(volatile int*)&B->abort || ++spins > kWaitBudget) {
+            if (!*(volatile int*)&B->abort) set_status(status, MLA_DEV_TIMEOUT);
+            B->abort = 1;
+            ok = false;
+            break;
           }
         }
         g += s.n;
@@ -561,7 +577,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
           tmem_ld_wait();
           tmem_reg_fence16(o);
           tmem_reg_fence16(e);
-          float* part = P.part + (slot * NR + r0) * RANK + 128 * q + key;
+          // partials lie [quarter][four rows][dim][row]: a thread's four rows of a dim are one store
+          float4* part = reinterpret_cast<float4*>(P.part + slot * NR * RANK) + (q * (NR / 4) + r0 / 4) * 128 + key;
 #pragma unroll
           for (int r = 0; r < HALF; ++r) {
             const float v = fmaf(e[r], 1.f / LO_UP, o[r]);
@@ -569,20 +586,31 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
           }
           if (!done.first) {
 #pragma unroll
-            for (int r = 0; r < HALF; ++r) {
-              const float k = sh->keep[r0 + r];
-              if (k != 0.f) o[r] = fmaf(part[r * RANK], k, o[r]);
+            for (int r = 0; r < HALF; r += 4) {
+              const float4 old = part[r / 4 * 128], k = *reinterpret_cast<const float4*>(sh->keep + r0 + r);
+              if (k.x != 0.f) o[r] = fmaf(old.x, k.x, o[r]);
+              if (k.y != 0.f) o[r + 1] = fmaf(old.y, k.y, o[r + 1]);
+              if (k.z != 0.f) o[r + 2] = fmaf(old.z, k.z, o[r + 2]);
+              if (k.w != 0.f) o[r + 3] = fmaf(old.w, k.w, o[r + 3]);
             }
           }
           if (done.last && direct) {
+            // neighbouring lanes' dims in one store: the even lane takes the first 8 rows
+            const bool odd = lane & 1;
+            __half* out = P.o_lat + ((long)done.b * live + row0 + r0 + (odd ? HALF / 2 : 0)) * RANK + 128 * q + (key & ~1);
 #pragma unroll
-            for (int r = 0; r < HALF; ++r)
-              if (row0 + r0 + r < live)
-                P.o_lat[((long)done.b * live + row0 + r0 + r) * RANK + 128 * q + key] = __float2half_rn(o[r]);
+            for (int r = 0; r < HALF / 2; ++r) {
+              const float mine = odd ? o[r + HALF / 2] : o[r], give = odd ? o[r] : o[r + HALF / 2];
+              const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+              if (row0 + r0 + (odd ? HALF / 2 : 0) + r < live)
+                *reinterpret_cast<__half2*>(out + (long)r * RANK) =
+                    odd ? __floats2half2_rn(got, mine) : __floats2half2_rn(mine, got);
+            }
           } else {
             // (kept in L2 for the join: the cache's stream would push them out)
 #pragma unroll
-            for (int r = 0; r < HALF; ++r) st_global_hint(part + r * RANK, o[r], stay);
+            for (int r = 0; r < HALF; r += 4)
+              st_global_hint4(part + r / 4 * 128, make_float4(o[r], o[r + 1], o[r + 2], o[r + 3]), stay);
           }
         }
         tc_fence_before();
@@ -777,8 +805,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
 }
 
 // Grid (unit, quarter of the value dims): the pieces of each row added by log-sum-exp in CTA
-// order.  Thread i: dims 128 quarter + 4 (i % 32) .. + 3 of rows i / 32 + 8 j; JOIN_LOADS
-// pieces' rows are in flight at once.
+// order.  Thread i: rows 4 (i / 32) .. + 3 of dims i % 32 + 32 j; JOIN_LOADS pieces' numbers are
+// in flight at once.
 constexpr int JOIN_THREADS = 256, JOIN_LOADS = 4;
 __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_constant__ Params P, int ctas) {
   extern __shared__ float w_s[];           // [pieces][32]
@@ -786,14 +814,13 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_con
   const int unit = blockIdx.x, part = blockIdx.y, tid = threadIdx.x;
   const int b = unit / P.groups, grp0 = (unit % P.groups) * NR, live = P.rule.T * P.rule.H;
   const long long t0 = P.first_tile[b], nt = P.first_tile[b + 1] - t0, U = P.first_tile[P.num_blocks] * P.groups;
-  const long row0 = (long)b * live + grp0;
-  const int d = 128 * part + 4 * (tid % 32);
-  float acc[4][4];
+  const long first_row = (long)b * live + grp0;
+  const int ra = 4 * (tid / 32), da = tid % 32;
+  float acc[4][4];                         // [j][row]
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-  const int ra = tid / 32;
   if (nt > 0) {
     const int G = (int)min((long long)ctas, U);
     const long long u = t0 * P.groups + (unit % P.groups) * nt;
@@ -831,20 +858,21 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_con
 #pragma unroll
       for (int i = 0; i < JOIN_LOADS; ++i)
         if (s0 + i < cnt) {
-          const float* src = P.part + ((slot0 + s0 + i) * NR + ra) * RANK + d;
+          const float4* src = reinterpret_cast<const float4*>(P.part + (slot0 + s0 + i) * NR * RANK) +
+                              (part * (NR / 4) + ra / 4) * 128 + da;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[i][j] = *reinterpret_cast<const float4*>(src + 8 * j * RANK);
+          for (int j = 0; j < 4; ++j) v[i][j] = src[32 * j];
         }
 #pragma unroll
       for (int i = 0; i < JOIN_LOADS; ++i)
         if (s0 + i < cnt) {
+          const float4 w = *reinterpret_cast<const float4*>(w_s + (s0 + i) * NR + ra);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float w = w_s[(s0 + i) * NR + ra + 8 * j];
-            acc[j][0] = fmaf(w, v[i][j].x, acc[j][0]);
-            acc[j][1] = fmaf(w, v[i][j].y, acc[j][1]);
-            acc[j][2] = fmaf(w, v[i][j].z, acc[j][2]);
-            acc[j][3] = fmaf(w, v[i][j].w, acc[j][3]);
+            acc[j][0] = fmaf(w.x, v[i][j].x, acc[j][0]);
+            acc[j][1] = fmaf(w.y, v[i][j].y, acc[j][1]);
+            acc[j][2] = fmaf(w.z, v[i][j].z, acc[j][2]);
+            acc[j][3] = fmaf(w.w, v[i][j].w, acc[j][3]);
           }
         }
     }
@@ -853,19 +881,15 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_con
   }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = ra + 8 * j;
-    if (grp0 + r < live) {
-      const __half2 lo = __floats2half2_rn(acc[j][0], acc[j][1]), hi = __floats2half2_rn(acc[j][2], acc[j][3]);
-      uint2 u;
-      u.x = *reinterpret_cast<const uint32_t*>(&lo);
-      u.y = *reinterpret_cast<const uint32_t*>(&hi);
-      *reinterpret_cast<uint2*>(P.o_lat + (row0 + r) * RANK + d) = u;
+  for (int r = 0; r < 4; ++r)
+    if (grp0 + ra + r < live) {
+      __half* out = P.o_lat + (first_row + ra + r) * RANK + 128 * part + da;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) out[32 * j] = __float2half_rn(acc[j][r]);
     }
-  }
   if (part == 0 && tid < NR && grp0 + tid < live && P.lse) {
     const float l2 = lse_s[tid];
-    P.lse[row0 + tid] = l2 == -INFINITY ? l2 : l2 * 0.6931471805599453f;
+    P.lse[first_row + tid] = l2 == -INFINITY ? l2 : l2 * 0.6931471805599453f;
   }
 }
 
