@@ -8,7 +8,6 @@ layer's dtype (weights, hidden, cache, out) or int32/int64/uint8 for indices.
 from __future__ import annotations
 
 import ctypes as C
-from typing import NamedTuple
 
 import torch
 
@@ -418,30 +417,45 @@ def mla_cache_compact_workspace_bytes(h: Handle, num_seqs: int, ldk: int) -> int
     return int(lib.mla_cache_compact_workspace_bytes(h.h, num_seqs, ldk))
 
 
-class Cache8(NamedTuple):
-    """The latent cache in 8 bits (mla_cache8_t): an entry stands for latent *
-    scale and rope."""
-    latent: torch.Tensor      # float8_e4m3fn [num_pages, page_size, 512]
-    rope: torch.Tensor        # bfloat16 [num_pages, page_size, 64]
-    scale: torch.Tensor       # float32 [num_pages, page_size]
+class Cache8:
+    """The latent cache in 8 bits (mla_cache8_t), of the caller's tensors: ``latent`` float8_e4m3fn
+    [num_pages, page_size, 512], ``rope`` bfloat16 [num_pages, page_size, 64], ``scale``
+    float32 [num_pages, page_size]; an entry stands for latent * scale and rope.  They are
+    looked at here, once, like a descriptor's; a call checks the page size and the device."""
+    __slots__ = ("latent", "rope", "scale", "num_pages", "page_size", "device_index", "_c", "_ref")
+
+    def __init__(self, latent, rope, scale):
+        n, page = scale.shape if scale.dim() == 2 else (-1, -1)
+        device = scale.get_device()
+        for name, t, dtype, shape in (("latent", latent, torch.float8_e4m3fn, (n, page, 512)),
+                                      ("rope", rope, torch.bfloat16, (n, page, 64)),
+                                      ("scale", scale, torch.float32, (n, page))):
+            if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+                raise ValueError(f"cache {name}: expected a contiguous {dtype} tensor of shape {shape} on the "
+                                 f"scale's device, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        self.latent, self.rope, self.scale = latent, rope, scale
+        self.num_pages, self.page_size, self.device_index = n, page, device
+        self._c = _lib.mla_cache8_t(latent.data_ptr(), rope.data_ptr(), scale.data_ptr())
+        self._ref = C.byref(self._c)
+
+    def __iter__(self):
+        return iter((self.latent, self.rope, self.scale))
 
 
 def make_cache8(h: Handle, num_pages: int) -> Cache8:
     """An 8-bit cache of ``num_pages`` pages whose entries are all zero."""
     def zeros(*width, dtype):
         return torch.zeros(num_pages, h.page_size, *width, dtype=dtype, device=h.device)
-    return Cache8(zeros(h.dims.kv_lora_rank, dtype=torch.uint8).view(torch.float8_e4m3fn),
-                  zeros(h.dims.qk_rope_head_dim, dtype=torch.bfloat16), zeros(dtype=torch.float32) + 1)
+    return Cache8(zeros(512, dtype=torch.uint8).view(torch.float8_e4m3fn), zeros(64, dtype=torch.bfloat16),
+                  zeros(dtype=torch.float32) + 1)
 
 
 def _take_cache8(h: Handle, c: Cache8):
     """The cache's C form, by reference, and its pages."""
-    n, d = c.scale.shape[0], h.dims
-    s = _lib.mla_cache8_t(
-        _take("cache latent", c.latent, torch.float8_e4m3fn, (n, h.page_size, d.kv_lora_rank), h),
-        _take("cache rope", c.rope, torch.bfloat16, (n, h.page_size, d.qk_rope_head_dim), h),
-        _take("cache scale", c.scale, torch.float32, (n, h.page_size), h))
-    return C.byref(s), n
+    if c.page_size != h.page_size or c.device_index != h.device_index:
+        raise ValueError(f"cache: expected pages of {h.page_size} on cuda:{h.device_index}, got pages of "
+                         f"{c.page_size} on {c.scale.device}")
+    return c._ref, c.num_pages
 
 
 def mla_cache8_store(h: Handle, entries, slot_mapping, cache: Cache8, stream=None):

@@ -27,9 +27,11 @@ namespace mla {
 namespace verify {
 namespace {
 
-constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int MAX_NODES = tree::MAX_NODES;
-constexpr int GROUP = 8;                   // elements a lane has in flight in a pass
+constexpr int STAGED = 5 * MAX_NODES / 2;  // elements (pairs) in the place of the five numbers a node has
+constexpr int GROUP = 16;                  // elements a lane has in flight in a pass
+constexpr int LOOK = 5;                    // and of a staged run
 
 struct Args {
   const void* target;
@@ -43,6 +45,7 @@ struct Args {
   int32_t* next_token;
   long ldt, ldd;
   int T, V;
+  bool wide;                               // rows start at 16-byte boundaries
   uint32_t* status;
 };
 
@@ -129,16 +132,65 @@ struct Rest {
     }
     return left_of(pv, qv, mass, MODE == DIFF ? 1 : k);
   }
-  template <int MODE>
-  __device__ __forceinline__ Pair at(int x) const {
-    return of<MODE>(prob(to_f32(p[x])), MODE == DIFF || MODE == DIFFS ? prob(to_f32(q[x])) : 0.f, x);
+  // What is left of element x, from its numbers in the rows.
+  __device__ __forceinline__ Pair left(float pv, float qv, int x) const {
+    return !k ? Pair{pv, 0.f} : q ? left_of(pv, qv, mass, k) : of<WITHOUT>(pv, 0.f, x);
   }
-  // A lane's share of the elements lo .. hi - 1.
+  // One more element into a running sum; the roundings gather in `tail`.  CLEAN: as left(); else an
+  // infinity makes the sum no finite number.
+  template <int MODE, bool CLEAN>
+  __device__ __forceinline__ void take(Pair& acc, float& tail, float pv, float qv, int x) const {
+    const Pair w = CLEAN ? of<MODE>(prob(pv), prob(qv), x) : of<MODE>(fmaxf(pv, 0.f), fmaxf(qv, 0.f), x);
+    const Pair s = two_sum(acc.hi, w.hi);
+    acc.hi = s.hi;
+    tail = __fadd_rn(tail, __fadd_rn(s.lo, w.lo));
+  }
+  // A lane's share of the elements lo .. hi - 1 (lo a multiple of 32); `wide`: rows are 16-byte aligned.
   template <int MODE>
-  __device__ __forceinline__ Pair sum(int lo, int hi, int lane) const {
+  __device__ __forceinline__ Pair sum(int lo, int hi, int lane, bool wide) const {
+    const Pair s = sum_of<MODE, false>(lo, hi, lane, wide);
+    return s.hi < INFINITY ? s : sum_of<MODE, true>(lo, hi, lane, false);
+  }
+  template <int MODE, bool CLEAN>
+  __device__ __forceinline__ Pair sum_of(int lo, int hi, int lane, bool wide) const {
     constexpr bool TWO = MODE == DIFF || MODE == DIFFS;
+    constexpr int NV = 16 / sizeof(T), LOADS = GROUP / NV;
     Pair acc{0.f, 0.f};
-    for (int x0 = lo + lane; x0 < hi; x0 += 32 * GROUP) {
+    int x0 = lo;
+    if (wide)
+      for (; x0 + 32 * GROUP <= hi; x0 += 32 * GROUP) {
+        uint4 pv[LOADS], qv[LOADS];
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+          pv[i] = *reinterpret_cast<const uint4*>(p + x0 + (32 * i + lane) * NV);
+          if (TWO) qv[i] = *reinterpret_cast<const uint4*>(q + x0 + (32 * i + lane) * NV);
+        }
+        if (MODE == WITHOUT) {             // (a refused token is in few of these)
+          for (int j = 0; j < k; ++j) {
+            const int x = banned[j] - x0, at = x / NV;
+            if ((unsigned)x < 32u * GROUP && at % 32 == lane) {
+#pragma unroll
+              for (int i = 0; i < LOADS; ++i)
+                if (i == at / 32) {
+                  uint32_t* word = reinterpret_cast<uint32_t*>(&pv[i]);
+                  const int e = x % NV, bits = 8 * sizeof(T), per = 32 / bits;
+#pragma unroll
+                  for (int w = 0; w < 4; ++w)
+                    if (w == e / per) word[w] &= per == 1 ? 0u : e % per ? 0xffffu : 0xffff0000u;
+                }
+            }
+          }
+        }
+        float tail = 0.f;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+#pragma unroll
+          for (int e = 0; e < NV; ++e)
+            take<MODE == WITHOUT ? ROW : MODE, CLEAN>(acc, tail, to_f32(reinterpret_cast<const T*>(&pv[i])[e]),
+                TWO ? to_f32(reinterpret_cast<const T*>(&qv[i])[e]) : 0.f, 0);
+        acc = quick_sum(acc.hi, __fadd_rn(acc.lo, tail));
+      }
+    for (x0 += lane; x0 < hi; x0 += 32 * GROUP) {
       float pv[GROUP], qv[GROUP];
 #pragma unroll
       for (int i = 0; i < GROUP; ++i) {
@@ -148,11 +200,7 @@ struct Rest {
       }
       float tail = 0.f;
 #pragma unroll
-      for (int i = 0; i < GROUP; ++i) {
-        const Pair w = of<MODE>(prob(pv[i]), prob(qv[i]), x0 + 32 * i), s = two_sum(acc.hi, w.hi);
-        acc.hi = s.hi;
-        tail = __fadd_rn(tail, __fadd_rn(s.lo, w.lo));
-      }
+      for (int i = 0; i < GROUP; ++i) take<MODE, CLEAN>(acc, tail, pv[i], qv[i], x0 + 32 * i);
       acc = quick_sum(acc.hi, __fadd_rn(acc.lo, tail));
     }
     return acc;
@@ -162,11 +210,16 @@ struct Rest {
 template <typename T, int CL>
 __global__ void __launch_bounds__(THREADS) verify_kernel(const Args a) {
   constexpr int SUMS = CL * WARPS, PER_LANE = (SUMS + 31) / 32;
-  __shared__ float px[MAX_NODES], qx[MAX_NODES], u[MAX_NODES];
-  __shared__ int par[MAX_NODES], path[MAX_NODES], tok[MAX_NODES];
+  __shared__ __align__(8) uint32_t pool[5 * MAX_NODES];
+  float *px = reinterpret_cast<float*>(pool), *qx = px + MAX_NODES, *u = qx + MAX_NODES;
+  int *par = reinterpret_cast<int*>(u + MAX_NODES), *tok = par + MAX_NODES;
+  __shared__ int path[MAX_NODES];
+  __shared__ bool takes[MAX_NODES];
   __shared__ Pair mass[MAX_NODES + 1];     // s after j refusals here
   __shared__ int banned[MAX_NODES];        // draft NULL: tokens refused here
   __shared__ State st;
+  __shared__ Pair parts[WARPS];
+  __shared__ int found, fallback;
   __shared__ Pair sums[2][WARPS];          // of this CTA's warps, by pass parity
   __shared__ Pair runs[SUMS], before[SUMS + 1];   // sums of the warps' runs, of those in front of each, of all
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -187,20 +240,21 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const Args a) {
     const bool read = in && known;
     px[i] = read ? prob(to_f32(target[(p + 1) * a.ldt + x])) : 0.f;
     qx[i] = read && draft ? prob(to_f32(draft[(p + 1) * a.ldd + x])) : 1.f;
+    takes[i] = above(Pair{px[i], 0.f}, times(Pair{qx[i], 0.f}, u[i]));    // with nothing refused before it
   }
   if (tid == 0) {
     st = State{-1, 0, 0, 0, false};
+    found = fallback = -1;
     mass[0] = Pair{1.f, 0.f};
   }
   __syncthreads();
 
   const int slice = ((V + SUMS - 1) / SUMS + 31) & ~31;
-  const int gw = rank * WARPS + warp;
-  const int lo = (int)min((long)gw * slice, (long)V), hi = min(lo + slice, V);
+  const int lo = (int)min((long)(rank * WARPS + warp) * slice, (long)V), hi = min(lo + slice, V);
   int parity = 0;
   bool whole = false;                      // nothing was left: the target's row itself
   Rest<T> rest{nullptr, nullptr, mass, banned, 0};
-  int mode = ROW, summed_node = -2, summed_k = 0;
+  int summed_node = -2, summed_k = 0;
   while (true) {
     if (tid == 0 && !st.over) {
       State s = st;
@@ -209,14 +263,18 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const Args a) {
         const int i = s.next;
         if (par[i] != s.node || tok[i] < 0) continue;
         Pair w{px[i], 0.f};
-        if (draft) {
-          if (s.refused) w = left_of(px[i], qx[i], mass, s.refused);
-        } else {
-          for (int j = 0; j < s.refused; ++j)
-            if (banned[j] == tok[i]) w.hi = 0.f;
-        }
         const Pair m = mass[s.refused];
-        if (above(w, times(times(m, qx[i]), u[i]))) {
+        bool take = takes[i];
+        if (s.refused) {
+          if (draft) {
+            w = left_of(px[i], qx[i], mass, s.refused);
+          } else {
+            for (int j = 0; j < s.refused; ++j)
+              if (banned[j] == tok[i]) w.hi = 0.f;
+          }
+          take = above(w, times(times(m, qx[i]), u[i]));
+        }
+        if (take) {
           path[s.kept++] = i;
           s.node = i;
           s.refused = 0;
@@ -240,11 +298,11 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const Args a) {
     if (s.node != summed_node || rest.k != summed_k || whole) {
       rest.p = target + (long)(s.node + 1) * a.ldt;
       rest.q = rest.k && draft ? draft + (long)(s.node + 1) * a.ldd : nullptr;
-      mode = rest.k == 0 ? ROW : !draft ? WITHOUT : rest.k == 1 ? DIFF : DIFFS;
-      Pair x = mode == ROW ? rest.template sum<ROW>(lo, hi, lane)
-               : mode == DIFF ? rest.template sum<DIFF>(lo, hi, lane)
-               : mode == DIFFS ? rest.template sum<DIFFS>(lo, hi, lane)
-                               : rest.template sum<WITHOUT>(lo, hi, lane);
+      const Mode mode = rest.k == 0 ? ROW : !draft ? WITHOUT : rest.k == 1 ? DIFF : DIFFS;
+      Pair x = mode == ROW ? rest.template sum<ROW>(lo, hi, lane, a.wide)
+               : mode == DIFF ? rest.template sum<DIFF>(lo, hi, lane, a.wide)
+               : mode == DIFFS ? rest.template sum<DIFFS>(lo, hi, lane, a.wide)
+                               : rest.template sum<WITHOUT>(lo, hi, lane, a.wide);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) x = add(x, shfl_xor(x, o));
       if (lane == 0) sums[parity][warp] = x;
@@ -288,8 +346,7 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const Args a) {
   }
 
   // The token: the least x whose sum is above the goal lies in the run of the last warp
-  // whose sum in front is not above it and that has anything (an earlier one, if
-  // rounding leaves nothing behind it).
+  // that has anything and whose sum in front is not above it.
   const Pair total = before[SUMS];
   const Pair goal = times(total, fmaxf(a.uniforms[b * (nodes + 1) + nodes], 0.f));
   int owner = -1;
@@ -299,23 +356,60 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const Args a) {
     const uint32_t some = __ballot_sync(0xffffffffu, mine);
     if (some) owner = i0 + 31 - __clz(some);
   }
-  if (owner == gw) {
-    int found = -1, last = -1;
-    Pair cum = before[owner];
-    for (int x0 = lo; x0 < hi && found < 0; x0 += 32) {
-      const int x = x0 + lane;
-      Pair w{0.f, 0.f};
-      if (x < hi)
-        w = mode == ROW ? rest.template at<ROW>(x) : mode == DIFF ? rest.template at<DIFF>(x)
-            : mode == DIFFS ? rest.template at<DIFFS>(x) : rest.template at<WITHOUT>(x);
-      const Pair c = add(cum, lane_sums(w, lane));
-      const uint32_t some = __ballot_sync(0xffffffffu, w.hi > 0.f);
-      const uint32_t over = __ballot_sync(0xffffffffu, w.hi > 0.f && above(c, goal));
-      if (over) found = x0 + __ffs(over) - 1;
-      if (some) last = x0 + 31 - __clz(some);
-      cum = Pair{__shfl_sync(0xffffffffu, c.hi, 31), __shfl_sync(0xffffffffu, c.lo, 31)};
+  if (owner >= 0 && owner / WARPS == rank) {
+    // Its CTA takes that run STAGED elements at a time: into shared memory, a contiguous part to
+    // each thread, and the thread whose part the goal falls into looks it up.
+    const int run_lo = (int)min((long)owner * slice, (long)V), run_hi = min(run_lo + slice, V);
+    Pair* el = reinterpret_cast<Pair*>(pool);
+    const T* row2 = rest.q ? rest.q : rest.p;
+    Pair front = before[owner];
+    int top = -1;                          // (where rounding leaves nothing above the goal)
+    for (int x0 = run_lo; x0 < run_hi; x0 += STAGED) {
+      const int n = min(STAGED, run_hi - x0), part = (n + THREADS - 1) / THREADS;
+      __syncthreads();                     // (the buffer is free; the last part's answer is known)
+      if (found >= 0) break;
+      for (int i = tid; i < n; i += THREADS * LOOK) {
+        float pv[LOOK], qv[LOOK];
+#pragma unroll
+        for (int e = 0; e < LOOK; ++e) {
+          const int x = x0 + min(i + e * THREADS, n - 1);
+          pv[e] = to_f32(rest.p[x]);
+          qv[e] = to_f32(row2[x]);
+        }
+#pragma unroll
+        for (int e = 0; e < LOOK; ++e)
+          if (i + e * THREADS < n) el[i + e * THREADS] = rest.left(prob(pv[e]), prob(qv[e]), x0 + i + e * THREADS);
+      }
+      __syncthreads();
+      const int i0 = min(tid * part, n), i1 = min(i0 + part, n);
+      Pair own{0.f, 0.f};
+      for (int i = i0; i < i1; ++i) own = add(own, el[i]);
+      const Pair incl = lane_sums(own, lane);
+      if (lane == 31) parts[warp] = incl;
+      const Pair lower{__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+      __syncthreads();
+      Pair cum = front;
+      for (int w = 0; w < WARPS; ++w) {
+        if (w == warp) cum = front;
+        front = add(front, parts[w]);
+      }
+      if (lane > 0) cum = add(cum, lower);
+      if (own.hi > 0.f && !above(cum, goal)) {
+        int last = -1, hit = -1;
+        for (int i = i0; i < i1 && hit < 0; ++i) {
+          cum = add(cum, el[i]);
+          if (el[i].hi > 0.f) {
+            last = x0 + i;
+            if (above(cum, goal)) hit = last;
+          }
+        }
+        if (hit >= 0) atomicMin(reinterpret_cast<unsigned*>(&found), (unsigned)hit);   // (-1: none yet)
+        top = last;
+      }
+      if (top >= 0) atomicMax(&fallback, top);
     }
-    if (lane == 0) a.next_token[b] = found >= 0 ? found : last;
+    __syncthreads();
+    if (tid == 0) a.next_token[b] = found >= 0 ? found : fallback;
   }
   if (rank == 0) {
     if (owner < 0 && tid == 0) {
@@ -332,8 +426,18 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const Args a) {
 template <typename T>
 cudaError_t launch(const Args& a, int num_seqs, int cl, cudaStream_t st) {
   Launch L(dim3((unsigned)(num_seqs * cl)), dim3(THREADS), 0, st, false, dim3((unsigned)cl, 1, 1));
-  return cl == 1 ? cudaLaunchKernelEx(&L.cfg, verify_kernel<T, 1>, a)
-                 : cudaLaunchKernelEx(&L.cfg, verify_kernel<T, 8>, a);
+  return cudaLaunchKernelEx(&L.cfg, cl == 1   ? verify_kernel<T, 1>
+                                    : cl == 2 ? verify_kernel<T, 2>
+                                    : cl == 4 ? verify_kernel<T, 4>
+                                              : verify_kernel<T, 8>, a);
+}
+
+// CTAs that share a sequence: 8, fewer where the sequences fill the GPU (four CTAs an SM) without
+// them, so that all of a batch's clusters run at once, and fewer for a small vocabulary.
+int cluster_size(int num_seqs, int vocab, int num_sms) {
+  int cl = 8;
+  while (cl > 1 && ((long)num_seqs * cl > 4L * num_sms || vocab <= 512 * cl)) cl /= 2;
+  return cl;
 }
 
 }  // namespace
@@ -362,9 +466,10 @@ extern "C" mla_status_t mla_verify_drafts(mla_handle_t* h, const void* target, i
   const size_t e = dtype == MLA_FP32 ? 4 : 2;
   if ((uintptr_t)target % e || (uintptr_t)draft % e)
     return fail(MLA_ERR_INVALID_ARG, "verify: target and draft must be aligned to their elements");
+  const bool wide = ((uintptr_t)target | (uintptr_t)draft | (size_t)ldt * e | (draft ? (size_t)ldd * e : 0)) % 16 == 0;
   const verify::Args a{target, num_nodes ? draft : nullptr, tokens, parent, uniforms, first, accepted,
-                       num_accepted, next_token, (long)ldt, (long)ldd, num_nodes, vocab, h->status};
-  const int cl = vocab > 4096 ? 8 : 1;
+                       num_accepted, next_token, (long)ldt, (long)ldd, num_nodes, vocab, wide, h->status};
+  const int cl = verify::cluster_size(num_seqs, vocab, h->num_sms);
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t err = dtype == MLA_FP32   ? verify::launch<float>(a, num_seqs, cl, st)
                           : dtype == MLA_BF16 ? verify::launch<__nv_bfloat16>(a, num_seqs, cl, st)
