@@ -24,8 +24,8 @@
 //   warps 0-7  : softmax, two groups of 128 threads, thread = key, 16 rows each; between
 //                segments the next one's queries are split before the last one's output is
 //                stored, so that its first S runs meanwhile
-//   warp 8     : tensor-memory allocation, MMA issue
-//   warps 9-11 : copies; a tile is five 16 KB chunks, each refilled once its product is done
+//   warps 8, 9 : the scores' and the outputs' MMAs (warp 8 holds the tensor memory)
+//   warps 10-11: copies; a tile is five 16 KB chunks, each refilled once its product is done
 #include "cache8.cuh"
 #include "gemm_tc.cuh"
 #include "tc_ptx.cuh"
@@ -53,7 +53,7 @@ constexpr int OFF_Q = STAGES * STAGE_BYTES;
 constexpr int OFF_QR = OFF_Q + 4 * Q_CH_BYTES;
 constexpr int OFF_P = OFF_QR + QR_BYTES;
 constexpr int OFF_RED = OFF_P + 2 * P_BYTES;
-constexpr int COPY_WARPS = 3, Q_ROWS = NR / (SM_THREADS / 32), Q_BATCH = 2;
+constexpr int Q_ROWS = NR / (SM_THREADS / 32), Q_BATCH = 2;
 // TMEM: S of tile g at column 128 (g % 2): hi 0-31, lo 32-63, rotary 64-95; O at 256: 4 x (hi | lo)
 constexpr uint32_t TMEM_COLS = 512, TM_O = 256;
 constexpr float SLACK_LOG2 = 1.75f;                  // 2^7 2^1.75 < 448
@@ -69,7 +69,7 @@ struct Params {
   float* lse;         // [rows] or NULL
   float* part;        // [slots][4 quarters][8 x 4 rows][128 dims][4 rows] normalised partial outputs
   float* part_lse;    // [slots, 32]
-  long long* first_tile;   // [blocks + 1] tiles of a group's worth of keys before each block
+  int* first_tile;    // [blocks + 1] tiles of a group's worth of keys before each block
   int num_blocks, groups, seg_rows;
   float scale_log2;
 };
@@ -82,34 +82,21 @@ struct Bars {
   uint64_t p_full[2];               // P(g) in shared memory
   uint64_t o_done;                  // O(g) done (waited on for a rescale only)
   uint64_t o_seg;                   // the segment's last O done
-  uint64_t drain;
+  uint64_t drain, drain_o;
   uint32_t tmem_slot;
   int abort;
 };
 
-struct __align__(16) Shared {
-  float wpart[2][2][4][HALF];       // by tile parity, group, warp: row maxima
-  float m[NR];                      // reference of each row (log2), at a segment's end
-  float inv[NR], keep[NR];          // factors of a segment's O and of what its piece has put away
-  float q_scale[NR];                // c 2^k of each row
-  int lo[NR], hi[NR];               // context keys that each row sees
-  float sum[2][4][HALF];
-  float run_lse[NR];                // log2-sum-exp of what a piece has put away
-  uint32_t seen[2][NR][4];          // by group: which keys of a tile each row sees
-  int fast_lo, fast_hi, any_lo, any_hi;
-  uint32_t alive;
-  int first_unit, first_tile;
-  long long scan[THREADS / 32];
-  Bars bars;
-};
-constexpr int SMEM_BYTES = 1024 + OFF_RED + (int)sizeof(Shared);
-static_assert(SMEM_BYTES <= 232448, "shared memory");
-
+// A bounded wait in few instructions: a CTA's code competes for the instruction cache.
 __device__ __forceinline__ bool wait_bar(Bars* B, uint64_t* bar, uint32_t parity, uint32_t* st) {
-  if (*(volatile int*)&B->abort) return false;
-  if (mbar_wait(bar, parity, st)) return true;
-  B->abort = 1;
-  return false;
+  if (mbar_test_wait(bar, parity)) return true;
+  uint32_t rounds = 0;
+  while (!mbar_try_wait(bar, parity))
+    if (++rounds > kWaitBudget || *(volatile int*)&B->abort) {
+      if (!atomicExch(&B->abort, 1)) set_status(st, MLA_DEV_TIMEOUT);
+      return false;
+    }
+  return true;
 }
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
@@ -138,6 +125,11 @@ __device__ __forceinline__ uint64_t smem_desc_sw64_mn(const void* tile) {
   return d;
 }
 
+// An untiled copy (addresses and size multiples of 16 bytes) that completes on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
 // 16-byte global store with an L2 eviction policy.
 __device__ __forceinline__ void st_global_hint4(float4* p, float4 v, uint64_t policy) {
   asm volatile("st.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;"
@@ -208,46 +200,91 @@ __device__ __forceinline__ Keys keys_of(const Params& P, int b, bool report) {
   return k;
 }
 
-// The CTA whose range [c U / G, (c + 1) U / G) holds tile u (G <= U).
-__device__ __forceinline__ int cta_of(long long u, long long U, int G) { return (int)(((u + 1) * G - 1) / U); }
+// The U tiles in G ranges (G <= U), the first U % G of them one tile longer.  (In 32 bits: the host
+// refuses more tiles.)
+struct Ranges {
+  int len, longer;                         // U / G, U % G
+  __device__ __forceinline__ int begin(int c) const { return c * len + min(c, longer); }
+  __device__ __forceinline__ int cta_of(int u) const {
+    const int head = longer * (len + 1);
+    return u < head ? u / (len + 1) : longer + (u - head) / len;
+  }
+};
 
-// Segments of a CTA's range, in order: tiles [t0, t0 + n) of unit u; a (unit, CTA) piece is one or
-// more of them.
+// A CTA's pieces, in order: tiles [t0, t0 + n) of a unit, its keys.  The first MAX_PIECES are worked
+// out once, before the copies start: what a role reads from memory later comes behind 160 KB of tiles.
+constexpr int MAX_PIECES = 32;
+struct Piece {
+  int unit, b, t0, n;
+  Keys k;
+};
+// Where a role stands in its CTA's range: a segment is at most SEG_TILES of a piece.
 struct Seg {
   int unit, b, t0, n;
   bool first, last;                        // of the piece
   Keys k;
 };
 struct SegIter {
-  int unit, t;
-  long long left;
-  bool cont;
+  int piece;                               // next one
+  int unit, left;                          // behind the listed pieces: the next unit, tiles to hand out
+  int rest;                                // tiles of the current piece not yet handed out
 };
-__device__ __forceinline__ bool next_seg(const Params& P, SegIter& it, Seg& s) {
-  const int units = P.num_blocks * P.groups;
-  while (it.left > 0 && it.unit < units) {
-    s.b = it.unit / P.groups;
-    s.k = keys_of(P, s.b, false);
-    if (it.t < s.k.nt) {
-      s.unit = it.unit;
-      s.t0 = it.t;
-      const int rest = (int)min((long long)(s.k.nt - it.t), it.left);
-      s.n = min(rest, SEG_TILES);
-      s.first = !it.cont;
-      s.last = s.n == rest;
-      it.cont = !s.last;
-      it.left -= s.n;
-      it.t += s.n;
-      if (it.t == s.k.nt) {
-        ++it.unit;
-        it.t = 0;
-      }
-      return true;
+
+struct __align__(128) Shared {
+  float scale[STAGES][KT];          // the keys' scales of a tile
+  float wpart[2][2][4][HALF];       // by tile parity, group, warp: row maxima
+  float m[NR];                      // reference of each row (log2), at a segment's end
+  float inv[NR], keep[NR];          // factors of a segment's O and of what its piece has put away
+  float q_scale[NR];                // c 2^k of each row
+  int lo[NR], hi[NR];               // context keys that each row sees
+  float sum[2][4][HALF];
+  float run_lse[NR];                // log2-sum-exp of what a piece has put away
+  uint32_t seen[2][NR][4];          // by group: which keys of a tile each row sees
+  int fast_lo, fast_hi, any_lo, any_hi;
+  uint32_t alive;
+  int first_unit, first_tile, pieces, more_unit, more_left;
+  Piece piece[MAX_PIECES];
+  int scan[THREADS / 32];
+  Bars bars;
+};
+
+constexpr int SMEM_BYTES = 1024 + OFF_RED + (int)sizeof(Shared);
+static_assert(SMEM_BYTES <= 232448, "shared memory");
+
+// The next segment of a CTA's range.
+__device__ __forceinline__ bool next_seg(const Params& P, const Shared* sh, SegIter& it, Seg& s) {
+  if (it.rest > 0) {                       // goes on with the piece
+    s.t0 += s.n;
+    s.first = false;
+  } else if (it.piece < sh->pieces) {
+    const Piece p = sh->piece[it.piece++];
+    s.unit = p.unit;
+    s.b = p.b;
+    s.t0 = p.t0;
+    s.k = p.k;
+    s.first = true;
+    it.rest = p.n;
+  } else {
+    if (it.piece++ == sh->pieces) {
+      it.unit = sh->more_unit;
+      it.left = sh->more_left;
     }
-    it.unit = s.k.nt == 0 ? (s.b + 1) * P.groups : it.unit + 1;
-    it.t = 0;
+    while (true) {                         // (small blocks: more of them than the list holds)
+      if (it.left <= 0) return false;
+      s.unit = it.unit++;
+      s.b = s.unit / P.groups;
+      s.k = keys_of(P, s.b, false);
+      if (s.k.nt > 0) break;
+    }
+    s.t0 = 0;
+    s.first = true;
+    it.rest = min(s.k.nt, it.left);
+    it.left -= it.rest;
   }
-  return false;
+  s.n = min(it.rest, SEG_TILES);
+  it.rest -= s.n;
+  s.last = it.rest == 0;
+  return true;
 }
 
 __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant__ Params P) {
@@ -272,6 +309,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
     mbar_init(&B->o_done, 1);
     mbar_init(&B->o_seg, 1);
     mbar_init(&B->drain, 1);
+    mbar_init(&B->drain_o, 1);
     B->abort = 0;
     sh->first_unit = nb * P.groups;
     sh->first_tile = 0;
@@ -281,10 +319,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
 
   // ---- schedule: the tiles of one group before each block, then this CTA's first unit and tile
   // (from the same numbers when every block has a thread)
-  long long U = 0, u0 = 0, u1 = 0;
-  int G = 1, nt = 0;
-  long long excl = 0;
-  auto count = [&](int base, long long run, bool report) {
+  int nt = 0, excl = 0;
+  auto count = [&](int base, int run, bool report) {
     const int b = base + tid;
     nt = b < nb ? keys_of(P, b, report).nt : 0;
     int x = nt;
@@ -295,7 +331,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
     }
     if (lane == 31) sh->scan[warp] = x;
     __syncthreads();
-    long long before = run, all = run;
+    int before = run, all = run;
     for (int w = 0; w < THREADS / 32; ++w) {
       before += w < warp ? sh->scan[w] : 0;
       all += sh->scan[w];
@@ -304,22 +340,21 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
     excl = before + x - nt;
     return all;
   };
-  long long run = 0;
+  int run = 0;
   for (int base = 0; base < nb; base += THREADS) run = count(base, run, c == 0);
-  U = run * P.groups;
   // the first min(gridDim, U) CTAs take one range each, so none is empty
-  G = (int)min((long long)gridDim.x, max(U, 1LL));
-  u0 = c < G ? U * c / G : U;
-  u1 = c < G ? U * (c + 1) / G : U;
+  const int U = run * P.groups, G = min((int)gridDim.x, max(U, 1));
+  const Ranges ranges{U / G, U % G};
+  const int u0 = c < G ? ranges.begin(c) : U, u1 = c < G ? ranges.begin(c + 1) : U;
   run = 0;
   for (int base = 0; base < nb; base += THREADS) {
     if (nb > THREADS) run = count(base, run, false);
     const int b = base + tid;
     if (b < nb) {
       if (nt > 0 && u1 > u0 && u0 >= excl * P.groups && u0 < (excl + nt) * P.groups) {
-        const long long in = u0 - excl * P.groups;
-        sh->first_unit = b * P.groups + (int)(in / nt);
-        sh->first_tile = (int)(in % nt);
+        const int in = u0 - excl * P.groups;
+        sh->first_unit = b * P.groups + in / nt;
+        sh->first_tile = in % nt;
       }
       if (c == 0) {
         pdl_wait();                        // the workspace may still be read by the kernel before
@@ -328,129 +363,191 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       }
     }
   }
+  __syncthreads();
+  if (warp == 11 && u1 > u0) {
+    // lane i: the i-th unit from the first one on
+    const int first = sh->first_unit, units = nb * P.groups, unit = first + lane;
+    Piece p{};
+    if (unit < units) {
+      p.unit = unit;
+      p.b = unit / P.groups;
+      p.k = keys_of(P, p.b, false);
+      p.t0 = lane ? 0 : sh->first_tile;
+    }
+    const int have = p.k.nt - p.t0;
+    int upto = have;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    p.n = max(min(have, u1 - u0 - (upto - have)), 0);
+    const uint32_t mine = __ballot_sync(0xffffffffu, p.n > 0);
+    if (p.n > 0) sh->piece[__popc(mine & ((1u << lane) - 1u))] = p;
+    if (lane == 31) {
+      sh->pieces = __popc(mine);
+      sh->more_unit = first + 32;
+      sh->more_left = u1 - u0 - upto;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem_slot;
-  const SegIter start{sh->first_unit, sh->first_tile, u1 - u0, false};
+  const SegIter start{};
   const bool work = u1 > u0;
   if (tid == 0) pdl_trigger();
   // (lengths, windows, positions and page rows are inputs of the call; what the kernel
   // before wrote, queries and entries, is read behind pdl_wait only)
 
+  // Two threads issue: the scores, as soon as a tile is there, and the outputs, as soon as its weights
+  // are; a commit and the look at a barrier cost 40 and 200 cycles of a thread, which pass while the
+  // other's products run.  (S(g) comes behind O(g - 2), which frees its tile's place, and behind the
+  // reading of S(g - 2), which P(g - 2) follows.)
   if (warp == 8) {
     if (lane == 0 && work) {
-      // ---- MMA issue ----
       const uint32_t id_s = idesc_f8(KT, 2 * NR);                            // K-major A and B
       const uint32_t id_r = idesc_f16(KT, NR, false);
-      const uint32_t id_o = idesc_f8(KT, 2 * NR) | (1u << 15) | (1u << 16);  // A and B MN-major
-      const uint64_t dK = smem_desc_sw128(smem), dV = smem_desc_sw128_mn(smem, CH_BYTES);
+      const uint64_t dK = smem_desc_sw128(smem);
       const uint64_t dQ = smem_desc_sw128(smem + OFF_Q), dR = smem_desc_sw128(smem + OFF_QR);
-      const uint64_t dP = smem_desc_sw64_mn(smem + OFF_P);
       constexpr uint32_t U_STAGE = STAGE_BYTES / 16, U_CH = CH_BYTES / 16, U_Q = Q_CH_BYTES / 16;
-      constexpr uint32_t U_P = P_BYTES / 16, U_VSTEP = 32 * 128 / 16, U_PSTEP = 32 * 64 / 16;
       SegIter it = start;
-      Seg s;
+      Seg s{};
       uint32_t g = 0, kseg = 0;
       bool ok = true;
-      while (ok && next_seg(P, it, s)) {
+      while (ok && next_seg(P, sh, it, s)) {
         if (!(ok = wait_bar(B, &B->q_full, kseg & 1, status))) break;
-        tc_fence_after();
-        // S of the next tile and O of the one before it, whichever can start: a tile that is
-        // still on its way does not hold up the product that frees the place of the next
-        int ns = 0, no = 0;
-        uint32_t spins = 0;
-        while (no < s.n) {
-          const uint32_t gs = g + ns, go = g + no;
-          if (no < ns && mbar_test_wait(&B->p_full[go & 1], (go >> 1) & 1)) {
-            tc_fence_after();
-            const uint32_t st = go % STAGES;
-            const uint64_t a = dV + st * U_STAGE, p = dP + (go & 1) * U_P;
+        for (int t = 0; t < s.n; ++t, ++g) {
+          const uint32_t st = g % STAGES, d = tmem + 128 * (g & 1);
+          if (g >= 2 && !(ok = wait_bar(B, &B->p_full[g & 1], ((g >> 1) - 1) & 1, status))) break;
+          if (!(ok = wait_bar(B, &B->full[st], (g / STAGES) & 1, status))) break;
+          tc_fence_after();
+          const uint64_t a = dK + st * U_STAGE;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+          for (int i = 0; i < 4; ++i) mma_f16(d + 64, a + 4 * U_CH + 2 * i, dR + 2 * i, id_r, i > 0);
+          mma_commit(&B->empty[st][4]);
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma_f8(tmem + TM_O + 64 * q, a + q * U_CH + i * U_VSTEP, p + i * U_PSTEP, id_o, no > 0 || i > 0);
-              mma_commit(&B->empty[st][q]);
-            }
-            mma_commit(&B->o_done);
-            if (++no == s.n) mma_commit(&B->o_seg);
-            spins = 0;
-          } else if (ns < s.n && ns <= no + 1 && mbar_test_wait(&B->full[gs % STAGES], (gs / STAGES) & 1)) {
-            // (the place of S(ns) was read before O(ns - 2) could start)
-            tc_fence_after();
-            const uint32_t st = gs % STAGES, d = tmem + 128 * (gs & 1);
-            const uint64_t a = dK + st * U_STAGE;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mma_f16(d + 64, a + 4 * U_CH + 2 * i, dR + 2 * i, id_r, i > 0);
-            mma_commit(&B->empty[st][4]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) mma_f8(d, a + q * U_CH + 2 * i, dQ + q * U_Q + 2 * i, id_s, q + i > 0);
-            mma_commit(&B->s_full[gs & 1]);
-            ++ns;
-            spins = 0;
-          } else if (*(volatile int*)&B->abort || ++spins > kWaitBudget) {
-            if (!*(volatile int*)&B->abort) set_status(status, MLA_DEV_TIMEOUT);
-            B->abort = 1;
-            ok = false;
-            break;
+            for (int i = 0; i < 4; ++i) mma_f8(d, a + q * U_CH + 2 * i, dQ + q * U_Q + 2 * i, id_s, q + i > 0);
           }
+          mma_commit(&B->s_full[g & 1]);
         }
-        g += s.n;
         ++kseg;
       }
       mma_commit(&B->drain);
       mbar_wait(&B->drain, 0, status);
     }
-  } else if (warp >= 9) {
+  } else if (warp == 9) {
     if (lane == 0 && work) {
-      // ---- copies: this warp takes every third of a tile's (chunk, page segment) copies ----
-      const int me = warp - 9;
-      const int ps = P.rule.page_size, past_end = P.rule.num_pages * ps, segs = KT / P.seg_rows;
-      prefetch_tmap(&P.tmL);
-      prefetch_tmap(&P.tmR);
+      const uint32_t id_o = idesc_f8(KT, 2 * NR) | (1u << 15) | (1u << 16);  // A and B MN-major
+      const uint64_t dV = smem_desc_sw128_mn(smem, CH_BYTES), dP = smem_desc_sw64_mn(smem + OFF_P);
+      constexpr uint32_t U_STAGE = STAGE_BYTES / 16, U_CH = CH_BYTES / 16;
+      constexpr uint32_t U_P = P_BYTES / 16, U_VSTEP = 32 * 128 / 16, U_PSTEP = 32 * 64 / 16;
       SegIter it = start;
-      Seg s;
+      Seg s{};
       uint32_t g = 0;
-      bool ok = true, waited = false;
-      while (ok && next_seg(P, it, s)) {
-        const int32_t* table = P.rule.block_table + (long)s.b * P.rule.max_pages;
-        for (int t = 0; t < s.n && ok; ++t, ++g) {
+      bool ok = true;
+      while (ok && next_seg(P, sh, it, s)) {
+        for (int t = 0; t < s.n; ++t, ++g) {
+          const uint32_t st = g % STAGES;
+          if (!(ok = wait_bar(B, &B->p_full[g & 1], (g >> 1) & 1, status))) break;
+          // (the tile itself: S(g), behind which P(g) came, was issued by the other thread)
+          if (!(ok = wait_bar(B, &B->full[st], (g / STAGES) & 1, status))) break;
+          tc_fence_after();
+          const uint64_t a = dV + st * U_STAGE, p = dP + (g & 1) * U_P;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_f8(tmem + TM_O + 64 * q, a + q * U_CH + i * U_VSTEP, p + i * U_PSTEP, id_o, t > 0 || i > 0);
+            mma_commit(&B->empty[st][q]);
+          }
+          mma_commit(&B->o_done);
+          if (t == s.n - 1) mma_commit(&B->o_seg);
+        }
+      }
+      mma_commit(&B->drain_o);
+      mbar_wait(&B->drain_o, 0, status);
+    }
+  } else if (warp >= 10) {
+    if (work) {
+      uint32_t g = 0;
+      bool ok = true;
+      // ---- copies: the rotary chunk, chunks 0 and 2 here, 1, 3 and the scales in the other warp, each
+      // as its place comes free; lane i takes page segment i of a chunk, and holds the number of page
+      // `base + i` and of the 32 behind them ----
+      const int ps = P.rule.page_size, past_end = P.rule.num_pages * ps, segs = KT / P.seg_rows;
+      const uint32_t scale_bytes = P.seg_rows * 4;
+      if (lane == 0) {
+        prefetch_tmap(&P.tmL);
+        prefetch_tmap(&P.tmR);
+      }
+      SegIter it = start;
+      Seg s{};
+      bool have = next_seg(P, sh, it, s);
+      const int32_t* table = P.rule.block_table + (long)s.b * P.rule.max_pages;
+      auto pages = [&](const int32_t* t, int at) { return t[min(at + lane, P.rule.max_pages - 1)]; };
+      int base = (s.k.j_lo + s.t0 * KT) / ps;
+      int cur = pages(table, base), ahead = pages(table, base + 32);
+      pdl_wait();
+      while (ok && have) {
+        const Seg was = s;
+        for (int t = 0; t < was.n && ok; ++t, ++g) {
           const uint32_t st = g % STAGES, ph = (g / STAGES) & 1;
-          const int j0 = s.k.j_lo + (s.t0 + t) * KT;
+          const int j0 = was.k.j_lo + (was.t0 + t) * KT;
           uint8_t* dst = smem + st * STAGE_BYTES;
-          int y = 0, have = -1;
-          if (!waited) {
-            pdl_wait();
-            waited = true;
+          if (t == was.n - 1) {
+            // the next segment's pages are on their way while this one's last tile waits for its place
+            have = next_seg(P, sh, it, s);
           }
-          // copy i: segment i / 5, chunk i % 5 (the rotary chunk first: its place is free first)
-          for (int i = me; i < segs * CHUNKS; i += COPY_WARPS) {
-            const int sg = i / CHUNKS, q = (i % CHUNKS + 4) % CHUNKS;
-            if (sg != have) {
-              have = sg;
-              const int j = j0 + sg * P.seg_rows;
-              y = past_end;                        // (zeros)
-              if (j < s.k.n) {
-                const int pg = table[j / ps];
-                if (pg >= 0 && pg < P.rule.num_pages) y = pg * ps + j % ps;
-                else set_status(status, MLA_DEV_BAD_PAGE);
-              }
+          if (j0 / ps >= base + 32) {
+            base += 32;
+            cur = ahead;
+            ahead = pages(table, base + 32);
+          }
+          // (32 pages are whole tiles: a tile's segments lie in one lot)
+          const int j = j0 + min(lane, segs - 1) * P.seg_rows;
+          const int pg = __shfl_sync(0xffffffffu, cur, j / ps - base);
+          int y = past_end;                              // (zeros)
+          if (lane < segs && j < was.k.n) {
+            if (pg >= 0 && pg < P.rule.num_pages) y = pg * ps + j % ps;
+            else set_status(status, MLA_DEV_BAD_PAGE);
+          }
+          auto copy = [&](int chunk) {
+            if (lane == 0) ok = ok && wait_bar(B, &B->empty[st][chunk], ph ^ 1, status);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (lane == 0 && ok && chunk == 4) mbar_arrive_expect_tx(&B->full[st], STAGE_BYTES + KT * 4);
+            uint8_t* to = dst + chunk * CH_BYTES + lane * P.seg_rows * 128;
+            if (ok && lane < segs) {
+              if (chunk < 4) tma_load_3d(to, &P.tmL, &B->full[st], 0, y, chunk);
+              else tma_load_3d(to, &P.tmR, &B->full[st], 0, y, 0);
+              // the scales with a chunk that is freed behind their use (where there is no page some scale:
+              // no row sees the key, or it is reported)
+              if (chunk == 1)
+                bulk_load(&sh->scale[st][lane * P.seg_rows], P.scale + (y == past_end ? 0 : y), scale_bytes, &B->full[st]);
             }
-            if (!(ok = wait_bar(B, &B->empty[st][q], ph ^ 1, status))) break;
-            if (i == 0) mbar_arrive_expect_tx(&B->full[st], STAGE_BYTES);
-            uint8_t* to = dst + q * CH_BYTES + sg * P.seg_rows * 128;
-            if (q < 4) tma_load_3d(to, &P.tmL, &B->full[st], 0, y, q);
-            else tma_load_3d(to, &P.tmR, &B->full[st], 0, y, 0);
+          };
+          if (warp == 10) {
+            copy(4);
+            copy(0);
+            copy(2);
+          } else {
+            copy(1);
+            copy(3);
           }
+        }
+        if (have && s.first) {
+          table = P.rule.block_table + (long)s.b * P.rule.max_pages;
+          base = (s.k.j_lo + s.t0 * KT) / ps;
+          cur = pages(table, base);
+          ahead = pages(table, base + 32);
         }
       }
       // the copies in flight land before the CTA exits (after a wait that gave up, a part of
       // one tile more; that wait gives up, too)
       if (!ok) ++g;
-      for (uint32_t i = g > STAGES ? g - STAGES : 0; i < g; ++i)
+      for (uint32_t i = g > STAGES ? g - STAGES : 0; lane == 0 && i < g; ++i)
         mbar_wait(&B->full[i % STAGES], (i / STAGES) & 1, status);
     }
   } else if (work) {
@@ -458,25 +555,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
     // that gave up everything runs on to its end (the barriers below count every thread). ----
     const int grp = warp / 4, wq = warp % 4, key = tid % 128;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    const int r0 = grp * HALF, ps = P.rule.page_size, live = P.rule.T * P.rule.H;
+    const int r0 = grp * HALF, live = P.rule.T * P.rule.H;
     const float c2 = P.scale_log2;
     SegIter it = start;
     Seg s{};
     uint32_t g = 0, kseg = 0;
-    long long u_seg = u0;                  // global index of the segment's first tile
-    // the scale of a tile's key, 1 where there is none
-    auto scale_at = [&](int t) {
-      const int j = s.k.j_lo + (s.t0 + t) * KT + key;
-      if (t >= s.n || j >= s.k.n) return 1.f;
-      const int pg = P.rule.block_table[(long)s.b * P.rule.max_pages + j / ps];
-      if (pg < 0 || pg >= P.rule.num_pages) return 1.f;
-      return __ldg(P.scale + (long)pg * ps + j % ps);
-    };
+    int u_seg = u0;                  // global index of the segment's first tile
     pdl_wait();
     uint32_t alive = 0;
     float l[HALF], m[HALF];
     Seg done{};                            // the segment whose tiles are done
-    bool have = next_seg(P, it, s), ended = false;
+    bool have = next_seg(P, sh, it, s), ended = false;
     while (true) {
       const int grp0 = (s.unit % P.groups) * NR;         // the unit's first row in its block
       if (have) {
@@ -532,8 +621,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       if (ended) {
         // ---- end of a segment: its sums, then the output or the piece's slot ----
         const int row0 = (done.unit % P.groups) * NR;
-        const long long unit0 = u_seg - done.t0;              // the unit's first tile
-        const bool direct = cta_of(unit0, U, G) == cta_of(unit0 + done.k.nt - 1, U, G);
+        const int unit0 = u_seg - done.t0;              // the unit's first tile
+        const bool direct = ranges.cta_of(unit0) == ranges.cta_of(unit0 + done.k.nt - 1);
         const long slot = (long)done.unit + c;
         {
           const float sum = transpose_reduce16<false>(l, lane);
@@ -620,7 +709,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       }
       if (!have) break;
       const int k_begin = s.k.j_lo + s.t0 * KT;
-      float ks = scale_at(0);
       softmax_sync();                      // the segment before is done with the rows' state
       if (warp == 0) {
         const int row = grp0 + lane, i = row / P.rule.H;
@@ -657,16 +745,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
 #pragma unroll
       for (int r = 0; r < HALF; ++r) {
         l[r] = 0.f;
-        m[r] = -INFINITY;
+        m[r] = 0.f;                        // the references less P_LOG2 (0 before the first)
       }
       float m_lane = -INFINITY;            // the reference of row lane % 16
+#pragma unroll 1
       for (int t = 0; t < s.n; ++t) {
+        asm volatile("" : "+r"(t));        // (one copy of the loop's code, none peeled off)
         const uint32_t gg = g + t, buf = gg & 1;
         const int j0 = k_begin + t * KT, j = j0 + key;
-        const float ks_next = scale_at(t + 1);
         const bool fast = j0 >= fast_lo && j0 + KT <= fast_hi;
         const bool bits = !fast && P.rule.parent && j0 + KT > s.k.ctx;
-        if (bits) {
+        if (__builtin_expect(bits, 0)) {
           // which keys each row sees: the group's first 64 threads take half a tile of a row each
           group_sync(grp);                 // (the tile before is done with the words)
           if (key < 2 * NR) {
@@ -679,8 +768,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
           }
           group_sync(grp);
         }
+        wait_bar(B, &B->full[gg % STAGES], (gg / STAGES) & 1, status);       // (for the scales; long done)
         wait_bar(B, &B->s_full[buf], (gg >> 1) & 1, status);
         tc_fence_after();
+        const float ks = sh->scale[gg % STAGES][key];
         float x[HALF];
         {
           float y[HALF], z[HALF];
@@ -698,7 +789,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
 #pragma unroll
           for (int r = 0; r < HALF; ++r) x[r] = fmaf(x[r] + y[r], qs[r] * ks, fmaf(z[r], c2, kexp));
         }
-        if (!fast) {
+        if (__builtin_expect(!fast, 0)) {
           bool seen = false;
           if (bits) {
 #pragma unroll
@@ -715,9 +806,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
           // it meets its weights, which are zero (S is done with it, and O waits for P)
           if (!seen) {
             uint8_t* row = smem + (gg % STAGES) * STAGE_BYTES + 2 * grp * CH_BYTES + key * 128;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < 2; ++q)
-#pragma unroll
+#pragma unroll 1
               for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(row + q * CH_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
           }
         }
@@ -731,13 +822,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
           const float* part = &sh->wpart[buf][grp][0][lane % HALF];
           top = fmaxf(fmaxf(part[0], part[HALF]), fmaxf(part[2 * HALF], part[3 * HALF]));
           const bool up = top > m_lane + SLACK_LOG2;
-          if (__any_sync(0xffffffffu, up)) {               // (the same for every warp of the group)
+          if (__builtin_expect(__any_sync(0xffffffffu, up), 0)) {               // (the same for every warp of the group)
             const float m_new = up ? ceilf(top) : m_lane;
             const float f = m_lane == -INFINITY ? 1.f : fast_exp2(m_lane - m_new);
             m_lane = m_new;
 #pragma unroll
             for (int r = 0; r < HALF; ++r) {
-              m[r] = __shfl_sync(0xffffffffu, m_new, r);
+              m[r] = __shfl_sync(0xffffffffu, m_new == -INFINITY ? 0.f : m_new - P_LOG2, r);
               y[r] = __shfl_sync(0xffffffffu, f, r);
               l[r] *= y[r];
             }
@@ -766,8 +857,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         uint32_t hi[HALF / 4], lo[HALF / 4];
 #pragma unroll
         for (int r = 0; r < HALF; r += 2) {
-          const float w0 = fast_exp2(x[r] - (m[r] == -INFINITY ? 0.f : m[r] - P_LOG2));
-          const float w1 = fast_exp2(x[r + 1] - (m[r + 1] == -INFINITY ? 0.f : m[r + 1] - P_LOG2));
+          const float w0 = fast_exp2(x[r] - m[r]), w1 = fast_exp2(x[r + 1] - m[r + 1]);
           l[r] = fmaf(w0, inv_ks, l[r]);
           l[r + 1] = fmaf(w1, inv_ks, l[r + 1]);
           const uint32_t h = e4m3x2(w0, w1);
@@ -788,12 +878,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&B->p_full[buf]);
-        ks = ks_next;
       }
       if (wq == 0 && lane < HALF) sh->m[r0 + lane] = m_lane;
       done = s;
       ended = true;
-      have = next_seg(P, it, s);
+      have = next_seg(P, sh, it, s);
     }
   }
   pdl_wait();        // (a no-op for the threads that waited already)
@@ -813,7 +902,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_con
   __shared__ float lse_s[NR];
   const int unit = blockIdx.x, part = blockIdx.y, tid = threadIdx.x;
   const int b = unit / P.groups, grp0 = (unit % P.groups) * NR, live = P.rule.T * P.rule.H;
-  const long long t0 = P.first_tile[b], nt = P.first_tile[b + 1] - t0, U = P.first_tile[P.num_blocks] * P.groups;
+  const int t0 = P.first_tile[b], nt = P.first_tile[b + 1] - t0, U = P.first_tile[P.num_blocks] * P.groups;
   const long first_row = (long)b * live + grp0;
   const int ra = 4 * (tid / 32), da = tid % 32;
   float acc[4][4];                         // [j][row]
@@ -822,9 +911,9 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_con
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
   if (nt > 0) {
-    const int G = (int)min((long long)ctas, U);
-    const long long u = t0 * P.groups + (unit % P.groups) * nt;
-    const int f = cta_of(u, U, G), cnt = cta_of(u + nt - 1, U, G) - f + 1;
+    const int G = min(ctas, U), u = t0 * P.groups + (unit % P.groups) * nt;
+    const Ranges ranges{U / G, U % G};
+    const int f = ranges.cta_of(u), cnt = ranges.cta_of(u + nt - 1) - f + 1;
     if (cnt == 1) return;
     const long slot0 = (long)unit + f;
     for (int i = tid; i < cnt * NR; i += JOIN_THREADS) w_s[i] = P.part_lse[slot0 * NR + i];
@@ -928,7 +1017,7 @@ size_t ws_layout(const mla_handle* h, const mla_attn_desc_t& d, size_t* off_lse,
   *off_lse = o;
   o += align256((size_t)slots * NR * 4);
   *off_first = o;
-  return o + align256((size_t)(d.num_blocks + 1) * 8);
+  return o + align256((size_t)(d.num_blocks + 1) * 4);
 }
 
 }  // namespace
@@ -957,11 +1046,12 @@ mla_status_t attention(cudaStream_t st, mla_handle* h, const tree::Rule& r, cons
   P.lse = lse;
   P.part = (float*)ws;
   P.part_lse = (float*)((char*)ws + off_lse);
-  P.first_tile = (long long*)((char*)ws + off_first);
+  P.first_tile = (int*)((char*)ws + off_first);
   P.num_blocks = d.num_blocks;
   P.groups = (int)(((long)d.block_len * h->lay.H + NR - 1) / NR);
   P.scale_log2 = h->scale * 1.4426950408889634f;
-  if ((long)P.num_blocks * P.groups > 0x3fffffffL) return fail(MLA_ERR_INVALID_ARG, "attention8: too many rows");
+  if ((double)P.num_blocks * P.groups * (((long)d.max_pages * ps + KT - 1) / KT) > 2147483647.0)
+    return fail(MLA_ERR_INVALID_ARG, "attention8: too many rows and keys (2^31 tiles of 32 x 128)");
   const size_t join_smem = (size_t)h->num_sms * NR * 4;
   static std::once_flag once;
   std::call_once(once, [] {

@@ -194,8 +194,8 @@ mla_status_t check_cache(const mla_handle* h, const mla_cache8_t* c, int num_pag
   if (!h || !c) return fail(MLA_ERR_INVALID_ARG, w + ": null handle or cache");
   if (h->cfg.dtype != MLA_BF16) return fail(MLA_ERR_UNSUPPORTED, w + ": the 8-bit cache is for bf16 layers");
   if (!c->latent || !c->rope || !c->scale) return fail(MLA_ERR_INVALID_ARG, w + ": null cache pointer");
-  if ((uintptr_t)c->latent % 16 || (uintptr_t)c->rope % 16 || (uintptr_t)c->scale % 4)
-    return fail(MLA_ERR_INVALID_ARG, w + ": latent and rope must be 16-byte aligned, scale 4-byte");
+  if ((uintptr_t)c->latent % 16 || (uintptr_t)c->rope % 16 || (uintptr_t)c->scale % 16)
+    return fail(MLA_ERR_INVALID_ARG, w + ": latent, rope and scale must be 16-byte aligned");
   if (num_pages <= 0) return fail(MLA_ERR_INVALID_ARG, w + ": num_pages <= 0");
   return MLA_OK;
 }

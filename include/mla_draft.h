@@ -524,7 +524,7 @@ mla_status_t mla_cache_compact(mla_handle_t *h, void *cache, int32_t num_pages,
  * in bf16 as they are.  Three arrays, page by page like the bf16 cache:
  *   latent: device e4m3 [num_pages, page_size, 512], 16-byte aligned
  *   rope:   device bf16 [num_pages, page_size, 64], 16-byte aligned
- *   scale:  device fp32 [num_pages, page_size], 4-byte aligned
+ *   scale:  device fp32 [num_pages, page_size], 16-byte aligned
  * and the entry stands for latent * scale and rope.  scale is the least power of two
  * that brings the latent's largest magnitude to 448 or below, 2^-64 at least; the
  * elements are rounded to nearest, ties to even (off by 2^-4 of their value at
