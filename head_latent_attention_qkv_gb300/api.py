@@ -267,7 +267,9 @@ def _take_workspace(workspace, h):
 def _run(fn, h: Handle, *args):
     """The entry point `fn` on the current stream (a caller's stream argument is
     made the current one, so that what the call allocates belongs to it)."""
-    check(fn(h.h, *args, torch._C._cuda_getCurrentRawStream(h.device_index)), fn.__name__)
+    status = fn(h.h, *args, torch._C._cuda_getCurrentRawStream(h.device_index))
+    if status:
+        check(status, fn.__name__)
 
 
 def _tree_args(h: Handle, q_abs, positions, cache, desc, parent):
@@ -519,8 +521,10 @@ def mla_latent_attention8(h: Handle, q_abs, positions, cache: Cache8, desc, pare
     par = None if parent is None else _take("parent", parent, torch.int32, (tokens,), h)
     lse_p = None if lse is None else _take("lse", lse, torch.float32, (rows,), h)
     if o_lat is None:
-        o_lat = _new(h, (rows, d.kv_lora_rank), torch.float16)
-    out = _take("o_lat", o_lat, torch.float16, (rows, d.kv_lora_rank), h)
+        o_lat = _new(h, (rows, 512), torch.float16)
+        out = o_lat.data_ptr()
+    else:
+        out = _take("o_lat", o_lat, torch.float16, (rows, 512), h)
     ref = C.byref(desc)
     if workspace is None:
         workspace = _new_workspace(h, lib.mla_latent_attention8_workspace_bytes(h.h, ref))
@@ -563,15 +567,22 @@ def mla_forward8_workspace_bytes(h: Handle, desc) -> int:
 _PROBABILITIES = {torch.float32: _lib.MLA_FP32, torch.bfloat16: _lib.MLA_BF16, torch.float16: _lib.MLA_FP16}
 
 
-def _take_probabilities(name, t, n, rows, vocab, dtype, h):
+def _take_probabilities(name, t, shape, dtype, h):
     """The pointer and row stride of probabilities [n, rows, vocab], whose rows may be
     parts of longer ones."""
-    if (t.shape != (n, rows, vocab) or t.dtype is not dtype or t.get_device() != h.device_index or
-            t.stride(2) != 1 or t.stride(1) < vocab or t.stride(0) != rows * t.stride(1)):
-        raise ValueError(f"{name}: expected {dtype} {(n, rows, vocab)} on cuda:{h.device_index}, rows evenly "
-                         f"spaced and contiguous, got {t.dtype} {tuple(t.shape)} of strides {t.stride()} on "
-                         f"{t.device}")
-    return t.data_ptr(), t.stride(1)
+    n, rows, vocab = shape
+    seq, row, one = t.stride()
+    if not n * rows:                                   # (nothing to read, whatever the strides)
+        seq, row, one = rows * vocab, vocab, 1
+    elif n < 2:
+        seq = rows * row
+    if rows < 2:                                       # (a stride of no second row says nothing)
+        row = seq // rows if n > 1 and rows else vocab
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != h.device_index or (one != 1 and vocab > 1) or
+            row < vocab or seq != rows * row):
+        raise ValueError(f"{name}: expected {dtype} {shape} on cuda:{h.device_index}, rows evenly spaced and "
+                         f"contiguous, got {t.dtype} {tuple(t.shape)} of strides {t.stride()} on {t.device}")
+    return t.data_ptr(), row
 
 
 def mla_verify_drafts(h: Handle, target, draft, tokens, uniforms, parent=None, first=None, stream=None):
@@ -586,11 +597,8 @@ def mla_verify_drafts(h: Handle, target, draft, tokens, uniforms, parent=None, f
     (n, T), vocab, i32 = tokens.shape, target.shape[-1], torch.int32
     if target.dtype not in _PROBABILITIES:
         raise ValueError(f"target: expected fp32, bf16 or fp16 probabilities, got {target.dtype}")
-    if n == 0 or T == 0:                               # (a stride of no rows says nothing)
-        draft = None
-    p, ldt = ((target.data_ptr(), vocab) if n == 0 else
-              _take_probabilities("target", target, n, T + 1, vocab, target.dtype, h))
-    q, ldd = (None, 0) if draft is None else _take_probabilities("draft", draft, n, T, vocab, target.dtype, h)
+    p, ldt = _take_probabilities("target", target, (n, T + 1, vocab), target.dtype, h)
+    q, ldd = (None, 0) if draft is None else _take_probabilities("draft", draft, (n, T, vocab), target.dtype, h)
     tok, u = _take("tokens", tokens, i32, (n, T), h), _take("uniforms", uniforms, torch.float32, (n, T + 1), h)
     par = None if parent is None else _take("parent", parent, i32, (n, T), h)
     fst = None if first is None else _take("first", first, i32, (n,), h)

@@ -32,6 +32,7 @@
 
 #include <math.h>
 
+#include <algorithm>
 #include <mutex>
 
 namespace mla {
@@ -42,6 +43,7 @@ using namespace tc;
 
 constexpr int KT = 128, NR = 32, HALF = 16;          // keys a tile, rows a unit, rows a softmax thread
 constexpr int SEG_TILES = 64;                        // tiles after which a piece is put away
+constexpr int JOIN_TILES = 3;                        // what cutting units costs, in tiles
 constexpr int THREADS = 384, SM_THREADS = 256;
 constexpr int STAGES = 2, CHUNKS = 5;                // 4 chunks of 128 latent dims, one of 64 rotary ones
 constexpr int CH_BYTES = KT * 128;                   // 16 KB
@@ -71,6 +73,7 @@ struct Params {
   float* part_lse;    // [slots, 32]
   int* first_tile;    // [blocks + 1] tiles of a group's worth of keys before each block
   int num_blocks, groups, seg_rows;
+  bool whole;         // every unit in one CTA: nothing to join
   float scale_log2;
 };
 
@@ -243,6 +246,7 @@ struct __align__(128) Shared {
   int fast_lo, fast_hi, any_lo, any_hi;
   uint32_t alive;
   int first_unit, first_tile, pieces, more_unit, more_left;
+  uint32_t empty;                   // of whole units: those without a key
   Piece piece[MAX_PIECES];
   int scan[THREADS / 32];
   Bars bars;
@@ -318,7 +322,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
   if (warp == 8) tmem_alloc(&B->tmem_slot, TMEM_COLS);
 
   // ---- schedule: the tiles of one group before each block, then this CTA's first unit and tile
-  // (from the same numbers when every block has a thread)
+  // (from the same numbers when every block has a thread); of whole units their numbers will do
   int nt = 0, excl = 0;
   auto count = [&](int base, int run, bool report) {
     const int b = base + tid;
@@ -340,38 +344,42 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
     excl = before + x - nt;
     return all;
   };
+  const int units = nb * P.groups;
   int run = 0;
-  for (int base = 0; base < nb; base += THREADS) run = count(base, run, c == 0);
+  if (!P.whole)
+    for (int base = 0; base < nb; base += THREADS) run = count(base, run, c == 0);
   // the first min(gridDim, U) CTAs take one range each, so none is empty
-  const int U = run * P.groups, G = min((int)gridDim.x, max(U, 1));
+  const int U = P.whole ? units : run * P.groups, G = min((int)gridDim.x, max(U, 1));
   const Ranges ranges{U / G, U % G};
   const int u0 = c < G ? ranges.begin(c) : U, u1 = c < G ? ranges.begin(c + 1) : U;
-  run = 0;
-  for (int base = 0; base < nb; base += THREADS) {
-    if (nb > THREADS) run = count(base, run, false);
-    const int b = base + tid;
-    if (b < nb) {
-      if (nt > 0 && u1 > u0 && u0 >= excl * P.groups && u0 < (excl + nt) * P.groups) {
-        const int in = u0 - excl * P.groups;
-        sh->first_unit = b * P.groups + in / nt;
-        sh->first_tile = in % nt;
-      }
-      if (c == 0) {
-        pdl_wait();                        // the workspace may still be read by the kernel before
-        P.first_tile[b] = excl;
-        if (b == nb - 1) P.first_tile[nb] = excl + nt;
+  if (!P.whole) {
+    run = 0;
+    for (int base = 0; base < nb; base += THREADS) {
+      if (nb > THREADS) run = count(base, run, false);
+      const int b = base + tid;
+      if (b < nb) {
+        if (nt > 0 && u1 > u0 && u0 >= excl * P.groups && u0 < (excl + nt) * P.groups) {
+          const int in = u0 - excl * P.groups;
+          sh->first_unit = b * P.groups + in / nt;
+          sh->first_tile = in % nt;
+        }
+        if (c == 0) {
+          pdl_wait();                      // the workspace may still be read by the kernel before
+          P.first_tile[b] = excl;
+          if (b == nb - 1) P.first_tile[nb] = excl + nt;
+        }
       }
     }
   }
   __syncthreads();
-  if (warp == 11 && u1 > u0) {
+  if (warp == 11) {
     // lane i: the i-th unit from the first one on
-    const int first = sh->first_unit, units = nb * P.groups, unit = first + lane;
+    const int first = P.whole ? u0 : sh->first_unit, unit = first + lane;
     Piece p{};
-    if (unit < units) {
+    if (u1 > u0 && unit < (P.whole ? u1 : units)) {
       p.unit = unit;
       p.b = unit / P.groups;
-      p.k = keys_of(P, p.b, false);
+      p.k = keys_of(P, p.b, P.whole && unit % P.groups == 0);
       p.t0 = lane ? 0 : sh->first_tile;
     }
     const int have = p.k.nt - p.t0;
@@ -381,13 +389,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       const int y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
     }
-    p.n = max(min(have, u1 - u0 - (upto - have)), 0);
+    p.n = P.whole ? have : max(min(have, u1 - u0 - (upto - have)), 0);
     const uint32_t mine = __ballot_sync(0xffffffffu, p.n > 0);
     if (p.n > 0) sh->piece[__popc(mine & ((1u << lane) - 1u))] = p;
+    const uint32_t none = __ballot_sync(0xffffffffu, P.whole && unit < u1 && p.n == 0);
     if (lane == 31) {
       sh->pieces = __popc(mine);
       sh->more_unit = first + 32;
-      sh->more_left = u1 - u0 - upto;
+      sh->more_left = P.whole ? 0 : u1 - u0 - upto;
+      sh->empty = none;
     }
   }
   tc_fence_before();
@@ -395,8 +405,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
   tc_fence_after();
   const uint32_t tmem = B->tmem_slot;
   const SegIter start{};
-  const bool work = u1 > u0;
-  if (tid == 0) pdl_trigger();
+  const bool work = sh->pieces > 0;
   // (lengths, windows, positions and page rows are inputs of the call; what the kernel
   // before wrote, queries and entries, is read behind pdl_wait only)
 
@@ -622,7 +631,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         // ---- end of a segment: its sums, then the output or the piece's slot ----
         const int row0 = (done.unit % P.groups) * NR;
         const int unit0 = u_seg - done.t0;              // the unit's first tile
-        const bool direct = ranges.cta_of(unit0) == ranges.cta_of(unit0 + done.k.nt - 1);
+        const bool direct = P.whole || ranges.cta_of(unit0) == ranges.cta_of(unit0 + done.k.nt - 1);
         const long slot = (long)done.unit + c;
         {
           const float sum = transpose_reduce16<false>(l, lane);
@@ -885,7 +894,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       have = next_seg(P, sh, it, s);
     }
   }
+  // (here, not earlier: a join that waits on every SM from the start costs the long cases a tenth)
+  if (tid == 0) pdl_trigger();
   pdl_wait();        // (a no-op for the threads that waited already)
+  for (uint32_t none = sh->empty; none; none &= none - 1) {      // (other than of whole units: the join's)
+    const int unit = u0 + __ffs(none) - 1, rows = P.rule.T * P.rule.H;
+    const int n = min(NR, rows - unit % P.groups * NR);
+    const long row = (long)(unit / P.groups) * rows + unit % P.groups * NR;
+    for (int i = tid; i < n * (RANK / 8); i += THREADS)
+      reinterpret_cast<uint4*>(P.o_lat + row * RANK)[i] = make_uint4(0, 0, 0, 0);
+    if (P.lse && tid < n) P.lse[row + tid] = -INFINITY;
+  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -900,6 +919,8 @@ constexpr int JOIN_THREADS = 256, JOIN_LOADS = 4;
 __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_constant__ Params P, int ctas) {
   extern __shared__ float w_s[];           // [pieces][32]
   __shared__ float lse_s[NR];
+  pdl_trigger();
+  pdl_wait();
   const int unit = blockIdx.x, part = blockIdx.y, tid = threadIdx.x;
   const int b = unit / P.groups, grp0 = (unit % P.groups) * NR, live = P.rule.T * P.rule.H;
   const int t0 = P.first_tile[b], nt = P.first_tile[b + 1] - t0, U = P.first_tile[P.num_blocks] * P.groups;
@@ -1009,10 +1030,24 @@ __global__ void __launch_bounds__(128) seen8_kernel(const tree::Rule a, long tok
   }
 }
 
-// Workspace: a slot for every (unit, CTA) piece, units + CTAs at most.
+int groups_of(const mla_handle* h, const mla_attn_desc_t& d) {
+  return (int)(((long)d.block_len * h->lay.H + NR - 1) / NR);
+}
+// Whether no unit is cut.  By the table's width, since the lengths are on the device: the fullest CTA
+// then has `rounds` units of `tiles` tiles, and with cuts an even share of all, whose join (a launch,
+// about 4 us of the GPU and 3 of the host) and second segment a CTA cost as much as JOIN_TILES tiles (a call
+// from Python, 16 rows over 300 keys: 17 us whole, 20 cut; over 640: 23 and 20; 64 sequences of 500 keys, 4 x 32
+// rows: 33 and 46; 152 of 2000 keys, 32 rows: 49 and 54).
+bool whole_units(const mla_handle* h, const mla_attn_desc_t& d) {
+  const long units = (long)d.num_blocks * groups_of(h, d), sms = h->num_sms;
+  const long tiles = ((long)d.max_pages * h->cfg.page_size + KT - 1) / KT;
+  return units <= 32 * sms && (units + sms - 1) / sms * tiles <= (units * tiles + sms - 1) / sms + JOIN_TILES;
+}
+// Workspace: a slot for every (unit, CTA) piece, units + CTAs at most; none of whole units.
 size_t ws_layout(const mla_handle* h, const mla_attn_desc_t& d, size_t* off_lse, size_t* off_first) {
-  const long groups = ((long)d.block_len * h->lay.H + NR - 1) / NR;
-  const long slots = d.num_blocks * groups + h->num_sms;
+  *off_lse = *off_first = 0;
+  if (whole_units(h, d)) return 0;
+  const long slots = (long)d.num_blocks * groups_of(h, d) + h->num_sms;
   size_t o = align256((size_t)slots * NR * RANK * 4);
   *off_lse = o;
   o += align256((size_t)slots * NR * 4);
@@ -1048,20 +1083,24 @@ mla_status_t attention(cudaStream_t st, mla_handle* h, const tree::Rule& r, cons
   P.part_lse = (float*)((char*)ws + off_lse);
   P.first_tile = (int*)((char*)ws + off_first);
   P.num_blocks = d.num_blocks;
-  P.groups = (int)(((long)d.block_len * h->lay.H + NR - 1) / NR);
+  P.groups = groups_of(h, d);
+  P.whole = whole_units(h, d);
   P.scale_log2 = h->scale * 1.4426950408889634f;
   if ((double)P.num_blocks * P.groups * (((long)d.max_pages * ps + KT - 1) / KT) > 2147483647.0)
     return fail(MLA_ERR_INVALID_ARG, "attention8: too many rows and keys (2^31 tiles of 32 x 128)");
-  const size_t join_smem = (size_t)h->num_sms * NR * 4;
+  const long units = (long)P.num_blocks * P.groups;
   static std::once_flag once;
   std::call_once(once, [] {
     cudaFuncSetAttribute(attn8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   });
-  Launch L(dim3((unsigned)h->num_sms), dim3(THREADS), SMEM_BYTES, st, pdl);
+  Launch L(dim3((unsigned)std::min<long>(h->num_sms, P.whole ? units : h->num_sms)), dim3(THREADS), SMEM_BYTES, st, pdl);
   MLA_CUDA_TRY(cudaLaunchKernelEx(&L.cfg, attn8_kernel, P));
-  join8_kernel<<<dim3((unsigned)(P.num_blocks * P.groups), 4), JOIN_THREADS, join_smem, st>>>(P, h->num_sms);
-  MLA_CUDA_TRY(cudaGetLastError());
-  h->launches += 2;
+  h->launches += 1;
+  if (!P.whole) {
+    Launch J(dim3((unsigned)units, 4), dim3(JOIN_THREADS), (size_t)h->num_sms * NR * 4, st, true);
+    MLA_CUDA_TRY(cudaLaunchKernelEx(&J.cfg, join8_kernel, P, h->num_sms));
+    h->launches += 1;
+  }
   if (d.vis_stats) {
     const long tokens = (long)d.num_blocks * d.block_len;
     seen8_kernel<<<(unsigned)((tokens + 3) / 4), 128, 0, st>>>(r, tokens, d.vis_stats);
