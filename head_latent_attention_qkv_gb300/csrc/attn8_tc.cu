@@ -42,6 +42,8 @@ namespace {
 using namespace tc;
 
 constexpr int KT = 128, NR = 32, HALF = 16;          // keys a tile, rows a unit, rows a softmax thread
+constexpr int FEW_UNITS = 16;                        // units whose join is shared by more CTAs (128 heads over
+                                                     // 131 k keys: 78 -> 75 us; 64 sequences: 42 -> 47)
 constexpr int SEG_TILES = 64;                        // tiles after which a piece is put away
 constexpr int JOIN_TILES = 3;                        // what cutting units costs, in tiles
 constexpr int THREADS = 384, SM_THREADS = 256;
@@ -912,11 +914,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
   if (warp == 8) tmem_dealloc(tmem, TMEM_COLS);
 }
 
-// Grid (unit, quarter of the value dims): the pieces of each row added by log-sum-exp in CTA
-// order.  Thread i: rows 4 (i / 32) .. + 3 of dims i % 32 + 32 j; JOIN_LOADS pieces' numbers are
-// in flight at once.
-constexpr int JOIN_THREADS = 256, JOIN_LOADS = 4;
+// Grid (unit, 32 DIMS value dims): the pieces of each row added by log-sum-exp in CTA order.  Thread
+// i: rows 4 (i / 32) .. + 3 of dims i % 32 + 32 j; 16 / DIMS pieces' numbers are in flight at once.
+// Few units are shared by more CTAs (DIMS = 1), since each has many pieces then.
+constexpr int JOIN_THREADS = 256;
+template <int DIMS>
 __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_constant__ Params P, int ctas) {
+  constexpr int JOIN_LOADS = 16 / DIMS;
   extern __shared__ float w_s[];           // [pieces][32]
   __shared__ float lse_s[NR];
   pdl_trigger();
@@ -926,9 +930,9 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_con
   const int t0 = P.first_tile[b], nt = P.first_tile[b + 1] - t0, U = P.first_tile[P.num_blocks] * P.groups;
   const long first_row = (long)b * live + grp0;
   const int ra = 4 * (tid / 32), da = tid % 32;
-  float acc[4][4];                         // [j][row]
+  float acc[DIMS][4];                      // [j][row]
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < DIMS; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
   if (nt > 0) {
@@ -964,21 +968,21 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_con
     }
     __syncthreads();
     for (int s0 = 0; s0 < cnt; s0 += JOIN_LOADS) {
-      float4 v[JOIN_LOADS][4];
+      float4 v[JOIN_LOADS][DIMS];
 #pragma unroll
       for (int i = 0; i < JOIN_LOADS; ++i)
         if (s0 + i < cnt) {
           const float4* src = reinterpret_cast<const float4*>(P.part + (slot0 + s0 + i) * NR * RANK) +
-                              (part * (NR / 4) + ra / 4) * 128 + da;
+                              (part * DIMS / 4 * (NR / 4) + ra / 4) * 128 + part * DIMS % 4 * 32 + da;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[i][j] = src[32 * j];
+          for (int j = 0; j < DIMS; ++j) v[i][j] = src[32 * j];
         }
 #pragma unroll
       for (int i = 0; i < JOIN_LOADS; ++i)
         if (s0 + i < cnt) {
           const float4 w = *reinterpret_cast<const float4*>(w_s + (s0 + i) * NR + ra);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < DIMS; ++j) {
             acc[j][0] = fmaf(w.x, v[i][j].x, acc[j][0]);
             acc[j][1] = fmaf(w.y, v[i][j].y, acc[j][1]);
             acc[j][2] = fmaf(w.z, v[i][j].z, acc[j][2]);
@@ -993,9 +997,9 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_con
 #pragma unroll
   for (int r = 0; r < 4; ++r)
     if (grp0 + ra + r < live) {
-      __half* out = P.o_lat + (first_row + ra + r) * RANK + 128 * part + da;
+      __half* out = P.o_lat + (first_row + ra + r) * RANK + 32 * DIMS * part + da;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) out[32 * j] = __float2half_rn(acc[j][r]);
+      for (int j = 0; j < DIMS; ++j) out[32 * j] = __float2half_rn(acc[j][r]);
     }
   if (part == 0 && tid < NR && grp0 + tid < live && P.lse) {
     const float l2 = lse_s[tid];
@@ -1097,8 +1101,9 @@ mla_status_t attention(cudaStream_t st, mla_handle* h, const tree::Rule& r, cons
   MLA_CUDA_TRY(cudaLaunchKernelEx(&L.cfg, attn8_kernel, P));
   h->launches += 1;
   if (!P.whole) {
-    Launch J(dim3((unsigned)units, 4), dim3(JOIN_THREADS), (size_t)h->num_sms * NR * 4, st, true);
-    MLA_CUDA_TRY(cudaLaunchKernelEx(&J.cfg, join8_kernel, P, h->num_sms));
+    const bool few = units <= FEW_UNITS;
+    Launch J(dim3((unsigned)units, few ? 16 : 4), dim3(JOIN_THREADS), (size_t)h->num_sms * NR * 4, st, true);
+    MLA_CUDA_TRY(cudaLaunchKernelEx(&J.cfg, few ? join8_kernel<1> : join8_kernel<4>, P, h->num_sms));
     h->launches += 1;
   }
   if (d.vis_stats) {
