@@ -117,6 +117,9 @@ def _load():
         "mla_forward8_workspace_bytes": (SZ, [P, C.POINTER(mla_attn_desc_t)]),
         "mla_draft_forward8": (I32, [P, P, P, P, C.POINTER(mla_cache8_t), I32, C.POINTER(mla_attn_desc_t),
                                      P, P, P, SZ, P]),
+        "mla_cache8_compact_workspace_bytes": (SZ, [P, I32, C.c_int64]),
+        "mla_cache8_compact": (I32, [P, C.POINTER(mla_cache8_t), I32, P, I32, P, I32, P, C.c_int64, P, P, P, I32, P,
+                                     P, C.c_int64, P, SZ, P]),
         "mla_verify_drafts": (I32, [P, P, C.c_int64, P, C.c_int64, I32, P, P, P, P, I32, I32, I32, P, P, P,
                                     P]),
     }

@@ -398,6 +398,12 @@ def mla_cache_compact(h: Handle, cache, block_table, kv_len, keep, keep_len, fir
         with torch.cuda.stream(stream):
             return mla_cache_compact(h, cache, block_table, kv_len, keep, keep_len, first, dst_block_table,
                                      weights, weights_out, None, workspace)
+    _compact(h, lib.mla_cache_compact, lib.mla_cache_compact_workspace_bytes, _take_cache(h, cache), cache.shape[0],
+             block_table, kv_len, keep, keep_len, first, dst_block_table, weights, weights_out, workspace)
+
+
+def _compact(h, fn, workspace_bytes, cache, num_pages, block_table, kv_len, keep, keep_len, first, dst_block_table,
+             weights, weights_out, workspace):
     n, i32 = kv_len.shape[0], torch.int32
     in_place = dst_block_table is None
     if weights is not None and weights_out is None and in_place:
@@ -406,13 +412,13 @@ def mla_cache_compact(h: Handle, cache, block_table, kv_len, keep, keep_len, fir
     keep_p, ldk = _take_rows("keep", keep, i32, n, h)
     dst, dst_pages = (None, 0) if in_place else _take_rows("dst_block_table", dst_block_table, i32, n, h)
     w, ldw = (None, 0) if weights is None else _take_rows("weights", weights, torch.float32, n, h)
-    args = (_take_cache(h, cache), cache.shape[0], table, max_pages, _take("kv_len", kv_len, i32, (n,), h), n,
+    args = (cache, num_pages, table, max_pages, _take("kv_len", kv_len, i32, (n,), h), n,
             keep_p, ldk, _take("keep_len", keep_len, i32, (n,), h),
             None if first is None else _take("first", first, i32, (n,), h), dst, dst_pages, w,
             None if weights_out is None else _take("weights_out", weights_out, torch.float32, (n, ldw), h), ldw)
     if workspace is None and in_place:
-        workspace = _new_workspace(h, lib.mla_cache_compact_workspace_bytes(h.h, n, ldk))
-    _run(lib.mla_cache_compact, h, *args, *_take_workspace(workspace, h))
+        workspace = _new_workspace(h, workspace_bytes(h.h, n, ldk))
+    _run(fn, h, *args, *_take_workspace(workspace, h))
 
 
 def mla_cache_compact_workspace_bytes(h: Handle, num_seqs: int, ldk: int) -> int:
@@ -562,6 +568,21 @@ def mla_draft_forward8(h: Handle, hidden, positions, block_slot_mapping, cache: 
 
 def mla_forward8_workspace_bytes(h: Handle, desc) -> int:
     return int(lib.mla_forward8_workspace_bytes(h.h, C.byref(desc)))
+
+
+def mla_cache8_compact(h: Handle, cache: Cache8, block_table, kv_len, keep, keep_len, first=None,
+                       dst_block_table=None, weights=None, weights_out=None, stream=None, workspace=None):
+    """mla_cache_compact of an 8-bit cache."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mla_cache8_compact(h, cache, block_table, kv_len, keep, keep_len, first, dst_block_table, weights,
+                                      weights_out, None, workspace)
+    _compact(h, lib.mla_cache8_compact, lib.mla_cache8_compact_workspace_bytes, *_take_cache8(h, cache), block_table,
+             kv_len, keep, keep_len, first, dst_block_table, weights, weights_out, workspace)
+
+
+def mla_cache8_compact_workspace_bytes(h: Handle, num_seqs: int, ldk: int) -> int:
+    return int(lib.mla_cache8_compact_workspace_bytes(h.h, num_seqs, ldk))
 
 
 _PROBABILITIES = {torch.float32: _lib.MLA_FP32, torch.bfloat16: _lib.MLA_BF16, torch.float16: _lib.MLA_FP16}

@@ -28,6 +28,7 @@
 // left alone.  2 entry rows of traffic per moved row: HBM bound (64 sequences to 1024 entries of 1152 bytes, 151 MB: 31
 // us, 4.9 TB/s; 16 rows a CTA, 33 us with 32).  In place the same takes 53 us: the
 // lists' kernel, the tickets and the waits for earlier chunks' loads.
+#include "cache8.cuh"
 #include "common.cuh"
 #include "tc_ptx.cuh"
 
@@ -514,23 +515,23 @@ extern "C" mla_status_t mla_cache_select(mla_handle_t* h, const float* weights, 
   return MLA_OK;
 }
 
-extern "C" size_t mla_cache_compact_workspace_bytes(const mla_handle_t* h, int32_t num_seqs,
-                                                    int64_t ldk) {
-  if (!h || num_seqs < 0 || ldk < 0) return 0;
+namespace {
+
+// Workspace of a compaction of rows of `bytes` bytes in place.
+size_t compact_ws(size_t bytes, int num_seqs, int64_t ldk) {
   int units, rows;
-  evict::chunk_shape((size_t)h->lay.L * h->lay.elt, false, &units, &rows);   // the smaller chunks
+  evict::chunk_shape(bytes, false, &units, &rows);       // the smaller chunks
   const size_t parts = (size_t)((ldk + evict::LIST_PART - 1) / evict::LIST_PART);
   return align256(((size_t)num_seqs * ((ldk + rows - 1) / rows + parts) + 1) * sizeof(int));
 }
 
-extern "C" mla_status_t mla_cache_compact(mla_handle_t* h, void* cache, int32_t num_pages,
-                                          const int32_t* block_table, int32_t max_pages,
-                                          const int32_t* kv_len, int32_t num_seqs,
-                                          const int32_t* keep, int64_t ldk, const int32_t* keep_len,
-                                          const int32_t* first, const int32_t* dst_block_table,
-                                          int32_t dst_max_pages, const float* weights,
-                                          float* weights_out, int64_t ldw, void* workspace,
-                                          size_t workspace_bytes, void* stream) {
+// mla_cache_compact of an array of rows of `bytes` bytes, page by page.
+mla_status_t compact_rows(mla_handle_t* h, void* cache, size_t bytes, int32_t num_pages,
+                          const int32_t* block_table, int32_t max_pages, const int32_t* kv_len,
+                          int32_t num_seqs, const int32_t* keep, int64_t ldk, const int32_t* keep_len,
+                          const int32_t* first, const int32_t* dst_block_table, int32_t dst_max_pages,
+                          const float* weights, float* weights_out, int64_t ldw, void* workspace,
+                          size_t workspace_bytes, void* stream) {
   if (!h) return fail(MLA_ERR_INVALID_ARG, "compact: null handle");
   if (num_seqs < 0 || max_pages <= 0 || num_pages <= 0 || ldk < 0 || ldk > 0x3fffffffL)
     return fail(MLA_ERR_INVALID_ARG, "compact: num_seqs >= 0, max_pages and num_pages > 0, 0 <= ldk < 2^30");
@@ -548,7 +549,6 @@ extern "C" mla_status_t mla_cache_compact(mla_handle_t* h, void* cache, int32_t 
   if (weights && ldw <= 0) return fail(MLA_ERR_INVALID_ARG, "compact: ldw > 0");
   if (weights && (weights == weights_out) != in_place)
     return fail(MLA_ERR_INVALID_ARG, "compact: weights_out == weights exactly when the cache is compacted in place");
-  const size_t bytes = (size_t)h->lay.L * h->lay.elt;
   const bool wide = bytes % 16 == 0 && (uintptr_t)cache % 16 == 0;
   evict::CompactArgs a{};
   evict::chunk_shape(bytes, wide, &a.units, &a.rows);
@@ -566,7 +566,7 @@ extern "C" mla_status_t mla_cache_compact(mla_handle_t* h, void* cache, int32_t 
   cudaStream_t st = (cudaStream_t)stream;
   a.num_seqs = num_seqs;
   if (in_place && a.chunks > 1) {
-    const size_t need = mla_cache_compact_workspace_bytes(h, num_seqs, ldk);
+    const size_t need = compact_ws(bytes, num_seqs, ldk);
     if (!workspace || workspace_bytes < need || (uintptr_t)workspace % 256)
       return fail(MLA_ERR_INVALID_ARG,
                   "compact: workspace smaller than mla_cache_compact_workspace_bytes() or not 256-byte aligned");
@@ -582,4 +582,48 @@ extern "C" mla_status_t mla_cache_compact(mla_handle_t* h, void* cache, int32_t 
   MLA_CUDA_TRY(cudaLaunchKernelEx(&L.cfg, wide ? evict::compact_kernel<uint4> : evict::compact_kernel<uint32_t>, a));
   h->launches += 1;
   return MLA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t mla_cache_compact_workspace_bytes(const mla_handle_t* h, int32_t num_seqs,
+                                                    int64_t ldk) {
+  return h && num_seqs >= 0 && ldk >= 0 ? compact_ws((size_t)h->lay.L * h->lay.elt, num_seqs, ldk) : 0;
+}
+
+extern "C" mla_status_t mla_cache_compact(mla_handle_t* h, void* cache, int32_t num_pages,
+                                          const int32_t* block_table, int32_t max_pages,
+                                          const int32_t* kv_len, int32_t num_seqs,
+                                          const int32_t* keep, int64_t ldk, const int32_t* keep_len,
+                                          const int32_t* first, const int32_t* dst_block_table,
+                                          int32_t dst_max_pages, const float* weights,
+                                          float* weights_out, int64_t ldw, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  return compact_rows(h, cache, h ? (size_t)h->lay.L * h->lay.elt : 0, num_pages, block_table, max_pages, kv_len,
+                      num_seqs, keep, ldk, keep_len, first, dst_block_table, dst_max_pages, weights, weights_out,
+                      ldw, workspace, workspace_bytes, stream);
+}
+
+// The three arrays of an 8-bit cache one after the other; in place the calls share the workspace (each
+// clears its flags behind the one before).
+extern "C" size_t mla_cache8_compact_workspace_bytes(const mla_handle_t* h, int32_t num_seqs, int64_t ldk) {
+  return h && num_seqs >= 0 && ldk >= 0 ? compact_ws(cache8::RANK, num_seqs, ldk) : 0;
+}
+
+extern "C" mla_status_t mla_cache8_compact(mla_handle_t* h, const mla_cache8_t* cache, int32_t num_pages,
+                                           const int32_t* block_table, int32_t max_pages,
+                                           const int32_t* kv_len, int32_t num_seqs, const int32_t* keep,
+                                           int64_t ldk, const int32_t* keep_len, const int32_t* first,
+                                           const int32_t* dst_block_table, int32_t dst_max_pages,
+                                           const float* weights, float* weights_out, int64_t ldw,
+                                           void* workspace, size_t workspace_bytes, void* stream) {
+  mla_status_t s = cache8::check_cache(h, cache, num_pages, "cache8 compact");
+  if (s != MLA_OK) return s;
+  void* const array[3] = {cache->latent, cache->rope, cache->scale};
+  const size_t bytes[3] = {cache8::RANK, 2 * cache8::ROPE, sizeof(float)};
+  for (int i = 0; i < 3 && s == MLA_OK; ++i)
+    s = compact_rows(h, array[i], bytes[i], num_pages, block_table, max_pages, kv_len, num_seqs, keep, ldk, keep_len,
+                     first, dst_block_table, dst_max_pages, i ? nullptr : weights, i ? nullptr : weights_out, ldw,
+                     workspace, workspace_bytes, stream);
+  return s;
 }

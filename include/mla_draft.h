@@ -586,6 +586,18 @@ mla_status_t mla_draft_forward8(mla_handle_t *h, const void *hidden, const int32
                                 const int32_t *parent, void *out, void *workspace,
                                 size_t workspace_bytes, void *stream);
 
+/* mla_cache_compact of an 8-bit cache: the same arguments, results and checks on the device
+ * (entries move with their scales).  workspace: mla_cache8_compact_workspace_bytes() bytes,
+ * 256-byte aligned, needed in place only. */
+size_t mla_cache8_compact_workspace_bytes(const mla_handle_t *h, int32_t num_seqs, int64_t ldk);
+mla_status_t mla_cache8_compact(mla_handle_t *h, const mla_cache8_t *cache, int32_t num_pages,
+                                const int32_t *block_table, int32_t max_pages,
+                                const int32_t *kv_len, int32_t num_seqs, const int32_t *keep,
+                                int64_t ldk, const int32_t *keep_len, const int32_t *first,
+                                const int32_t *dst_block_table, int32_t dst_max_pages,
+                                const float *weights, float *weights_out, int64_t ldw,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- verification of drafted tokens ---------------------------------------
  * Which of a sequence's num_nodes drafted tokens (T) the target keeps, and the
  * token behind them, from given random numbers, so that what is kept is

@@ -427,3 +427,235 @@ def test_the_layer_is_its_steps(heads, T, n, tree):
     # hold for outputs of several rms)
     assert ((out.float() - want.float()).abs() <= 2e-2 * rms + 2.0 ** -8 * (out.float().abs() + want.float().abs())).all()
     assert (out.float() - want.float()).abs().mean() <= 2e-3 * rms
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("page,lens,n_keep", [(16, [40, 700, 3], [5, 300, 3]), (128, [1000, 129], [999, 1]),
+                                              (64, [5000], [2500]), (32, [64, 64], [0, 64])])
+def test_compaction_moves_what_the_entries_stand_for(page, lens, n_keep, in_place):
+    # the 8-bit cache compacted and read back is the bf16 cache read back and compacted
+    from head_latent_attention_qkv_gb300 import api
+    from tests.tree_cases import Paged, i32
+    h = handle("bf16", 4, page)
+    rng = np.random.default_rng(page)
+    p = Paged(rng, h.dims, page, lens, spare=60)
+    c8 = to_cache8(h, p.cache, junk=False)
+    every = torch.arange(p.num_pages * page, device="cuda")
+    bf = api.mla_cache8_load(h, c8, every).view(p.num_pages, page, 576).contiguous()
+    firsts = [n // 3 if k < n // 2 else 0 for n, k in zip(lens, n_keep)]
+    width = max(max(n_keep), 1)
+    keep = np.full((len(lens), width), -1)
+    for b, (n, k, f) in enumerate(zip(lens, n_keep, firsts)):
+        keep[b, :k] = np.sort(rng.choice(np.arange(f, n), size=k, replace=False))
+    dst = None
+    if not in_place:
+        need = [-(-(f + k) // page) for f, k in zip(firsts, n_keep)]
+        d = np.full((len(lens), max(max(need), 1)), -1)
+        at = 0
+        for b, x in enumerate(need):
+            d[b, :x] = p.spare[at:at + x]
+            at += x
+        dst = i32(d)
+    w = torch.from_numpy(rng.random((len(lens), max(lens) + 2)).astype(np.float32)).cuda()
+    ws = [w.clone(), w.clone()]
+    outs = [None, None] if in_place else [torch.full_like(w, -1.0) for _ in ws]
+    args = (i32(p.table), i32(lens), i32(keep), i32(n_keep))
+    api.mla_cache8_compact(h, c8, *args, first=i32(firsts), dst_block_table=dst, weights=ws[0], weights_out=outs[0])
+    api.mla_cache_compact(h, bf, *args, first=i32(firsts), dst_block_table=dst, weights=ws[1], weights_out=outs[1])
+    torch.cuda.synchronize()
+    assert api.mla_get_device_status(h) == 0
+    got = api.mla_cache8_load(h, c8, every).view_as(bf)
+    assert torch.equal(got.nan_to_num(7.0), bf.nan_to_num(7.0))
+    pair = ws if in_place else outs
+    assert torch.equal(pair[0], pair[1])
+
+
+def test_compaction_leaves_a_list_that_does_not_ascend_alone():
+    from head_latent_attention_qkv_gb300 import _lib, api
+    from tests.tree_cases import Paged, i32
+    h = handle("bf16", 4, 16)
+    p = Paged(np.random.default_rng(1), h.dims, 16, [90, 80])
+    c8 = to_cache8(h, p.cache)
+    before = [x.clone() for x in c8]
+    keep = i32([[3, 9, 9, 20], [1, 2, 30, 40]])
+    api.mla_cache8_compact(h, c8, i32(p.table), i32([90, 80]), keep, i32([4, 4]))
+    assert api.mla_get_device_status(h) == _lib.MLA_DEV_BAD_KEEP
+    slots, other = p.slots(0, 90).cuda(), p.slots(1, 80).cuda()
+    for x, y in zip(c8, before):
+        x, y = (t.view(torch.uint8).reshape(p.num_pages * 16, -1) for t in (x, y))
+        assert torch.equal(x[slots], y[slots])
+        assert torch.equal(x[other[:4]], y[other[[1, 2, 30, 40]]])
+
+
+@pytest.mark.parametrize("heads,T,kind", [(16, 8, "tree"), (32, 5, "chain")])
+def test_serving_steps(heads, T, kind):
+    """Three steps as a serving program takes them: the drafted tokens' entries written in 8 bits, their
+    attention, verification, the accepted path compacted; then one token over what is left, against
+    the oracle on the entries that stayed."""
+    from head_latent_attention_qkv_gb300 import api
+    from oracle import cache8 as O8, tree as O
+    from tests.tree_cases import bushy, depths, i32
+    rng = np.random.default_rng(T)
+    page, n, V, pages = 16, 3, 5000, 90
+    h = handle("bf16", heads, page)
+    scale = 1.0 / np.sqrt(h.dims.qk_head_dim)
+    table = rng.permutation(pages)[:n * 20].reshape(n, 20)
+    c8 = api.make_cache8(h, pages)
+    length, kept = [150, 61, 0], [np.zeros((0, 576)) for _ in range(n)]
+
+    def slots(b, keys):
+        return torch.from_numpy(table[b][keys // page] * page + keys % page).cuda()
+
+    def store(b, keys):
+        e = torch.from_numpy(rng.normal(size=(len(keys), 576)).astype(np.float32)).bfloat16()
+        api.mla_cache8_store(h, e.cuda(), slots(b, keys), c8)
+        return O8.dequantise(*O8.quantise(e.double().numpy()))
+
+    for b in range(n):
+        kept[b] = store(b, np.arange(length[b]))
+    for step in range(3):
+        parents = [bushy(rng, T) if kind == "tree" else list(range(-1, T - 1)) for _ in range(n)]
+        own = [store(b, length[b] + np.arange(T)) for b in range(n)]
+        kv, first, par = i32([x + T for x in length]), i32(length), i32(parents)
+        pos = i32([x + d for x, q in zip(length, parents) for d in depths(q)])
+        q = torch.from_numpy(rng.normal(size=(n * T * heads, 576)).astype(np.float32)).bfloat16().cuda()
+        desc = api.make_desc(i32(table), kv, block_len=T)
+        o = api.mla_latent_attention8(h, q, pos, c8, desc, parent=par.flatten())
+        # (the layers above and the vocabulary's projection would follow)
+        z = rng.normal(size=(n, T + 1, V)) * 2
+        p = np.exp(z) / np.exp(z).sum(axis=-1, keepdims=True)
+        d = 0.7 * p[:, :T] + 0.3 / V
+        tokens = np.array([[rng.choice(V, p=d[b, parents[b][i] + 1]) for i in range(T)] for b in range(n)])
+        u = rng.random((n, T + 1)).astype(np.float32)
+        dev = [torch.from_numpy(x.astype(np.float32)).cuda() for x in (p, d)]
+        accepted, count, token = api.mla_verify_drafts(h, *dev, i32(tokens), torch.from_numpy(u).cuda(), parent=par,
+                                                       first=first)
+        api.mla_cache8_compact(h, c8, i32(table), kv, accepted, count, first=first)
+        torch.cuda.synchronize()
+        assert api.mla_get_device_status(h) == 0 and torch.isfinite(o).all()
+        for b in range(n):
+            path, want = O8.verify(dev[0][b].double().cpu().numpy(), dev[1][b].double().cpu().numpy(),
+                                   tokens[b].tolist(), u[b], parents[b])
+            assert (accepted[b, :count[b]].cpu().numpy() - length[b]).tolist() == path and token[b] == want
+            kept[b] = np.concatenate([kept[b], own[b][path]])
+            length[b] += len(path)
+    q = torch.from_numpy(rng.normal(size=(n * heads, 576)).astype(np.float32)).bfloat16().cuda()
+    o = api.mla_latent_attention8(h, q, i32(length), c8, api.make_desc(i32(table), i32(length), block_len=1))
+    assert api.mla_get_device_status(h) == 0
+    for b in range(n):
+        q64 = q.double().cpu().numpy().reshape(n, 1, heads, 576)[b]
+        vis = np.ones((1, length[b]), dtype=bool)
+        ref = O.attention(q64, kept[b], vis, 512, scale)[0][0]
+        mass = O.weight_mass(q64, kept[b], vis, 512, scale)[0]
+        got = o.double().cpu().numpy().reshape(n, heads, 512)[b]
+        # as above, the scores' error taken at 2^-12 and the least weights at 2^-12 of the mass
+        assert (np.abs(got - ref) <= (2.0 ** -8 + 2.0 ** -10) * mass + 2.0 ** -11 * np.abs(ref) + 1e-6).all()
+
+
+def test_short_blocks_whole_and_cut():
+    # tables that hold few tiles and wide ones, blocks without a key among them: equal results
+    from head_latent_attention_qkv_gb300 import api
+    from tests.tree_cases import i32
+    for heads, T, ctx in ((16, 3, [0, 5, 200, 90]), (64, 2, [300, 0, 128]), (4, 1, [0])):
+        c = Case8(heads, 32, ctx, T, seed=len(ctx), masked=T > 2)
+        before = api.mla_kernel_launches(c.h)
+        whole = c.attention()
+        assert api.mla_kernel_launches(c.h) == before + 2             # no join, and the counts
+        c.check_attention(*whole)
+        wide = np.full((c.n, 900), -1)
+        wide[:, :c.paged.max_pages] = c.paged.table
+        c.keep[0] = i32(wide)
+        c.desc = api.make_desc(c.keep[0], c.keep[1], None, c.keep[3], T, c.stats)
+        c.check_attention(*c.attention())
+        assert api.mla_kernel_launches(c.h) == before + 5
+        c.keep[1].zero_()                                              # no keys at all
+        c.desc.q_visible, c.parent = None, None
+        for table in (c.keep[0], i32(c.paged.table)):
+            desc = api.make_desc(table, c.keep[1], None, None, T)
+            lse = torch.full((c.q.shape[0],), 3.0, device="cuda")
+            o = api.mla_latent_attention8(c.h, c.q, c.positions, c.c8, desc, lse=lse)
+            assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+def test_pieces_longer_than_what_one_sum_holds():
+    # more than 64 tiles in a CTA: its parts are put away and joined (152 SMs, 1.3 M keys)
+    from head_latent_attention_qkv_gb300 import api
+    from tests.tree_cases import i32
+    h = handle("bf16", 32, 128)
+    n, kv = 12, 110000
+    pages = -(-kv // 128)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    c = api.make_cache8(h, pages)
+    api.mla_cache8_store(h, torch.randn(pages * 128, 576, generator=g, device="cuda").bfloat16(),
+                         torch.arange(pages * 128, device="cuda"), c)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(n, 1)
+    q = torch.randn(n * 32, 576, generator=g, device="cuda").bfloat16()
+    lens = i32([kv - 1000 * b for b in range(n)])
+    lse = torch.empty(n * 32, device="cuda")
+    o = api.mla_latent_attention8(h, q, lens, c, api.make_desc(table, lens, block_len=1), lse=lse)
+    assert api.mla_get_device_status(h) == 0
+    e = api.mla_cache8_load(h, c, torch.arange(kv, device="cuda")).double()
+    scale = 1.0 / np.sqrt(h.dims.qk_head_dim)
+    for b in range(0, n, 5):
+        k = kv - 1000 * b
+        s = q[32 * b:32 * b + 32].double() @ e[:k].T * scale
+        p = torch.softmax(s, 1)
+        ref, mass = p @ e[:k, :512], p @ e[:k, :512].abs()
+        # a weight is off by 2^-8, and by 2^-20 of the largest; scores (std 1.7) by 2^-16 here
+        tol = (2.0 ** -8 + 2.0 ** -14) * mass + 2.0 ** -20 * p.amax(1, keepdim=True) * e[:k, :512].abs().sum(0) + 2.0 ** -11 * ref.abs()
+        assert ((o[32 * b:32 * b + 32].double() - ref).abs() <= tol).all()
+        assert ((lse[32 * b:32 * b + 32].double() - torch.logsumexp(s, 1)).abs() <= 1e-4).all()
+
+
+def test_refusals_on_the_host():
+    import ctypes as C
+    from head_latent_attention_qkv_gb300 import _lib, api
+    lib, BAD, NO = _lib.lib, _lib.MLA_ERR_INVALID_ARG, _lib.MLA_ERR_UNSUPPORTED
+    c = Case8(16, 16, [60], 4)
+    h, ref, s = c.h.h, c.c8._ref, torch.cuda.current_stream().cuda_stream
+    before = api.mla_kernel_launches(c.h)
+    x = torch.zeros(4 * 16, 576, dtype=torch.bfloat16, device="cuda")
+    slots = torch.zeros(4, dtype=torch.int64, device="cuda")
+    assert lib.mla_cache8_store(h, x.data_ptr() + 2, slots.data_ptr(), 4, ref, 1, s) == BAD
+    assert lib.mla_cache8_store(h, x.data_ptr(), None, 4, ref, 1, s) == BAD
+    assert lib.mla_cache8_store(h, x.data_ptr(), slots.data_ptr(), -1, ref, 1, s) == BAD
+    assert lib.mla_cache8_load(h, ref, 0, slots.data_ptr(), 4, x.data_ptr(), s) == BAD
+    assert lib.mla_cache8_load(h, None, 1, slots.data_ptr(), 4, x.data_ptr(), s) == BAD
+    for field in ("latent", "rope", "scale"):
+        bad = _lib.mla_cache8_t(c.c8._c.latent, c.c8._c.rope, c.c8._c.scale)
+        setattr(bad, field, getattr(bad, field) + 8)
+        assert lib.mla_cache8_store(h, x.data_ptr(), slots.data_ptr(), 4, C.byref(bad), 1, s) == BAD
+        setattr(bad, field, None)
+        assert lib.mla_cache8_store(h, x.data_ptr(), slots.data_ptr(), 4, C.byref(bad), 1, s) == BAD
+    d, q, pos = C.byref(c.desc), c.q.data_ptr(), c.positions.data_ptr()
+    par, n = c.parent.data_ptr(), c.c8.num_pages
+    o = torch.zeros(c.q.shape[0], 512, dtype=torch.float16, device="cuda").data_ptr()
+
+    def attend(cache=ref, num_pages=n, desc=d, qp=q, op=o, ws=None, nws=0):
+        return lib.mla_latent_attention8(h, qp, pos, cache, num_pages, desc, par, op, None, ws, nws, s)
+    assert attend(cache=None) == BAD and attend(num_pages=0) == BAD and attend(num_pages=2 ** 27) == BAD
+    assert attend(qp=None) == BAD and attend(qp=q + 2) == BAD and attend(op=o + 2) == BAD and attend(desc=None) == BAD
+    wide = api.make_desc(torch.zeros(1, 900, dtype=torch.int32, device="cuda"), c.keep[1], block_len=4)
+    need = api.mla_latent_attention8_workspace_bytes(c.h, wide)
+    ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+    assert need > 0 and attend(desc=C.byref(wide)) == BAD
+    assert attend(desc=C.byref(wide), ws=ws.data_ptr(), nws=need - 1) == BAD
+    assert attend(desc=C.byref(wide), ws=ws.data_ptr() + 128, nws=need) == BAD
+    long = api.make_desc(c.keep[0], c.keep[1], block_len=1025)
+    assert attend(desc=C.byref(long)) == NO
+    fp32 = handle("fp32", 4, 16)
+    assert lib.mla_cache8_store(fp32.h, x.data_ptr(), slots.data_ptr(), 4, ref, 1, s) == NO
+    assert lib.mla_latent_attention8(fp32.h, q, pos, ref, n, d, par, o, None, None, 0, s) == NO
+    hidden = torch.zeros(4, c.h.dims.hidden_size, dtype=torch.bfloat16, device="cuda")
+    need = api.mla_append8_workspace_bytes(c.h, 4)
+    assert lib.mla_latent_cache_append8(h, hidden.data_ptr(), pos, slots.data_ptr(), 4, ref, n, ws.data_ptr(), need - 1, s) == BAD
+    need = api.mla_forward8_workspace_bytes(c.h, c.desc)
+    assert lib.mla_draft_forward8(h, hidden.data_ptr(), pos, None, ref, n, d, par, hidden.data_ptr(), ws.data_ptr(),
+                                  min(need - 1, ws.numel()), s) == BAD
+    assert api.mla_kernel_launches(c.h) == before
+    with pytest.raises(ValueError):
+        api.Cache8(c.c8.latent, c.c8.rope, c.c8.scale[:-1])
+    with pytest.raises(ValueError):
+        api.Cache8(c.c8.latent.view(torch.uint8), c.c8.rope, c.c8.scale)
+    with pytest.raises(ValueError):
+        api.mla_cache8_load(handle("bf16", 16, 32), c.c8, slots)

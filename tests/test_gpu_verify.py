@@ -102,6 +102,10 @@ CASES = [
     (4, 9, 333, dict(certain=True, kind="tree")), (2, 4, 9999, dict(certain=True, dtype="bf16")),
     (2, 300, 50, dict(kind="tree", noise=1.0)), (1, 1024, 64, dict(kind="tree", noise=0.1)),
     (1, 1024, 40, dict(certain=True, kind="chain", noise=0.0)), (70, 4, 600, dict(kind="tree")),
+    # whole lots of 16-byte loads: each type, refused siblings in them
+    (2, 6, 70016, dict(certain=True, kind="star")), (2, 5, 81920, dict(certain=True, kind="star", dtype="bf16")),
+    (1, 5, 90112, dict(certain=True, kind="star", dtype="fp16")), (2, 5, 40000, dict(kind="star", noise=3.0, dtype="bf16")),
+    (40, 2, 33000, dict(noise=1.0)), (160, 1, 9000, dict(noise=1.0)), (320, 1, 2600, dict(noise=2.0)),
 ]
 
 
@@ -142,14 +146,15 @@ def test_rows_may_be_parts_of_longer_ones():
     assert all((x.cpu().numpy() == y).all() for x, y in zip(got, want))
 
 
-def test_masses_at_the_edges():
+@pytest.mark.parametrize("V", [6000, 60000])
+def test_masses_at_the_edges(V):
     from head_latent_attention_qkv_gb300 import _lib, api
-    b = Batch(6, 3, 6000, seed=8, kind="star")
+    b = Batch(6, 3, V, seed=8, kind="star")
     b.target[0, 0] = b.draft[0, 0]                   # the draft's own law: kept for every u < 1
     b.u[0, 0] = 1 - 2.0 ** -24
     b.target[1, 0] = 0.0                             # no mass at all
     b.target[2, 0] = 0.0
-    b.target[2, 0, 5999] = 1.0                       # one token, the last
+    b.target[2, 0, V - 1] = 1.0                      # one token, the last
     b.u[2] = 1 - 2.0 ** -24
     b.target[3, 0, ::7] = float("nan")
     b.target[3, 0, 1::7] = -1.0
@@ -160,7 +165,7 @@ def test_masses_at_the_edges():
     b.u[5, :3] = 0.75
     got = b.run()
     b.check(got, status=_lib.MLA_DEV_BAD_DRAFT)
-    assert got[1][0] == 1 and got[2][1] == -1 and got[2][2] == 5999 and got[1][5] == 0
+    assert got[1][0] == 1 and got[2][1] == -1 and got[2][2] == V - 1 and got[1][5] == 0
     assert api.mla_get_device_status(the_handle()) == 0
 
 
@@ -198,3 +203,36 @@ def test_equal_bits_replays_and_streams():
         g.replay()
     torch.cuda.synchronize()
     assert all((p.cpu().numpy() == q).all() for p, q in zip(got, want))
+
+
+def test_a_long_run_is_staged_in_parts():
+    # one CTA a sequence (many of them): its warps' runs are longer than what is staged at once
+    b = Batch(640, 1, 25000, seed=3, noise=0.3)
+    b.check(b.run())
+
+
+def test_refusals():
+    from head_latent_attention_qkv_gb300 import _lib, api
+    lib, h = _lib.lib, the_handle()
+    b = Batch(2, 3, 50)
+    t, d = b.target.cuda(), b.draft.cuda()
+    tok = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    u, out = torch.zeros(2, 4, device="cuda"), torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    s, BAD = torch.cuda.current_stream().cuda_stream, _lib.MLA_ERR_INVALID_ARG
+    before = api.mla_kernel_launches(h)
+
+    def call(target=t.data_ptr(), ldt=50, draft=d.data_ptr(), ldd=50, dtype=1, tokens=tok.data_ptr(), un=u.data_ptr(),
+             n=2, T=3, V=50, acc=out.data_ptr(), cnt=out.data_ptr(), nxt=out.data_ptr()):
+        return lib.mla_verify_drafts(h.h, target, ldt, draft, ldd, dtype, tokens, None, un, None, n, T, V, acc, cnt, nxt, s)
+    for kw in (dict(target=None), dict(ldt=49), dict(ldd=49), dict(dtype=3), dict(dtype=-1), dict(tokens=None),
+               dict(un=None), dict(n=-1), dict(T=-1), dict(V=0), dict(acc=None), dict(cnt=None), dict(nxt=None),
+               dict(target=t.data_ptr() + 2), dict(draft=d.data_ptr() + 1)):
+        assert call(**kw) == BAD, kw
+    assert call(T=1025) == _lib.MLA_ERR_UNSUPPORTED and call(n=0) == _lib.MLA_OK
+    assert lib.mla_verify_drafts(None, None, 1, None, 1, 1, None, None, None, None, 1, 1, 1, None, None, None, s) == BAD
+    assert api.mla_kernel_launches(h) == before
+    for bad in (t[:, :, :49], t[:, :3], t.double(), t.cpu(), t.transpose(1, 2).contiguous().transpose(1, 2)):
+        with pytest.raises(ValueError):
+            api.mla_verify_drafts(h, bad, d, tok, u)
+    with pytest.raises(ValueError):
+        api.mla_verify_drafts(h, t, d.half(), tok, u)
