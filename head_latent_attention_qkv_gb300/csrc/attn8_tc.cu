@@ -26,6 +26,16 @@
 //                stored, so that its first S runs meanwhile
 //   warps 8, 9 : the scores' and the outputs' MMAs (warp 8 holds the tensor memory)
 //   warps 10-11: copies; a tile is five 16 KB chunks, each refilled once its product is done
+//
+// What bounds it.  Two tiles of 80 KB are all that fits beside the queries, so a tile's place goes
+// round in copy (1.2 k cycles from L2, up to 4 k from HBM) - scores (1.5-2.0 k) - softmax (1.3 k)
+// - output (1.5 k) and the hand-overs between them, 7.2 k: one tile in 3.6 k cycles, where the products'
+// operands alone pass shared memory in 1.7 k (an MMA of N = 64 takes 48 cycles, the time of
+// its 6 KB).  Widened to bf16 the same tile would not fit twice.  Code is the other bound: with the MMA
+// loops unrolled the roles' loops do not fit the instruction cache together (10% misses) and
+// 128 heads x 16 tokens over 4 x 8 k keys take 250-440 us instead of 214.  128 heads x 1 token
+// over 131 k keys 75 us, 64 sequences x 32 heads over 1-4 k keys 42 us (2.6 TB/s: first tiles
+// of a cold SM at 6 us, nine tiles, two stores, the join).
 #include "cache8.cuh"
 #include "gemm_tc.cuh"
 #include "tc_ptx.cuh"

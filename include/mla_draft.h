@@ -624,7 +624,7 @@ mla_status_t mla_cache8_compact(mla_handle_t *h, const mla_cache8_t *cache, int3
  * keep, keep_len and first.  uniforms: device fp32 [num_seqs, T + 1] in [0, 1).
  * A token outside the vocabulary is reported as MLA_DEV_BAD_DRAFT, its node
  * refused and w left as it was; a parent >= the node as MLA_DEV_BAD_TREE, its
- * node never reached.  Sums and differences are carried to 2^-44 or better.  T at most
+ * node never reached.  Sums and differences are carried to 2^-40 or better.  T at most
  * 1024 (MLA_ERR_UNSUPPORTED beyond); T == 0 draws from row 0. */
 mla_status_t mla_verify_drafts(mla_handle_t *h, const void *target, int64_t ldt, const void *draft,
                                int64_t ldd, int32_t dtype, const int32_t *tokens,

@@ -1,7 +1,7 @@
 """Verification of drafted tokens against the fp64 oracle (needs a GB300): whole
 numbers, equal to the oracle's.
 
-The oracle's sums are exact to 2^-53 and the library's to 2^-44; a draw of the tests
+The oracle's sums are exact to 2^-53 and the library's to 2^-40; a draw of the tests
 would have to fall within 2^-40 of a border to differ, which the oracle is asked
 about before the comparison.
 """
