@@ -29,13 +29,14 @@
 //
 // What bounds it.  Two tiles of 80 KB are all that fits beside the queries, so a tile's place goes
 // round in copy (1.2 k cycles from L2, up to 4 k from HBM) - scores (1.5-2.0 k) - softmax (1.3 k)
-// - output (1.5 k) and the hand-overs between them, 7.2 k: one tile in 3.6 k cycles, where the products'
+// - output (1.5 k) and the hand-overs between them, 7.0 k: one tile in 3.5 k cycles, where the products'
 // operands alone pass shared memory in 1.7 k (an MMA of N = 64 takes 48 cycles, the time of
 // its 6 KB).  Widened to bf16 the same tile would not fit twice.  Code is the other bound: with the MMA
 // loops unrolled the roles' loops do not fit the instruction cache together (10% misses) and
-// 128 heads x 16 tokens over 4 x 8 k keys take 250-440 us instead of 214.  128 heads x 1 token
-// over 131 k keys 75 us, 64 sequences x 32 heads over 1-4 k keys 42 us (2.6 TB/s: first tiles
-// of a cold SM at 6 us, nine tiles, two stores, the join).
+// 128 heads x 16 tokens over 4 x 8 k keys take 250-440 us instead of 207.  128 heads x 1 token
+// over 131 k keys 73 us, 64 sequences x 32 heads over 1-4 k keys 41 us (2.6 TB/s: first tiles
+// of a cold SM at 6 us, nine tiles, two stores, the join).  The softmax's arithmetic is in pairs of
+// fp32 (FFMA2) and its maxima are warp reductions of one instruction: 75 -> 73, 214 -> 207 us.
 #include "cache8.cuh"
 #include "gemm_tc.cuh"
 #include "tc_ptx.cuh"
@@ -118,6 +119,12 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 1 / x, off by one unit in the last place (the sums and their parts lie in 2^-120 .. 2^100).
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(2 + g) : "memory"); }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 4, 256;" ::: "memory"); }
 
@@ -180,21 +187,29 @@ __device__ __forceinline__ void lds16(const float* p, float* v) {
   for (int i = 0; i < HALF; i += 4) *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(p + i);
 }
 
-// Lane l ends with op over the warp's lanes of x[l % 16] (x[0 .. 15] per lane).
-template <bool kMax>
-__device__ __forceinline__ float transpose_reduce16(float* x, int lane) {
+// Two fp32 operations at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+// The largest over the warp's lanes (a NaN is left out).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Lane l ends with the sum over the warp's lanes of x[l % 16] (x[0 .. 15] per lane).
+__device__ __forceinline__ float transpose_sum16(float* x, int lane) {
 #pragma unroll
   for (int s = 8; s >= 1; s >>= 1) {
     const bool upper = (lane & s) != 0;
 #pragma unroll
     for (int i = 0; i < s; ++i) {
       const float send = upper ? x[i] : x[i + s], keep = upper ? x[i + s] : x[i];
-      const float recv = __shfl_xor_sync(0xffffffffu, send, s);
-      x[i] = kMax ? fmaxf(keep, recv) : keep + recv;
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
     }
   }
-  const float y = __shfl_xor_sync(0xffffffffu, x[0], 16);
-  return kMax ? fmaxf(x[0], y) : x[0] + y;
+  return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
 }
 
 // Keys of block b: [j_lo, n) in nt tiles, j_lo the first key that any row's window reaches,
@@ -646,7 +661,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         const bool direct = P.whole || ranges.cta_of(unit0) == ranges.cta_of(unit0 + done.k.nt - 1);
         const long slot = (long)done.unit + c;
         {
-          const float sum = transpose_reduce16<false>(l, lane);
+          const float sum = transpose_sum16(l, lane);
           if (lane < HALF) sh->sum[grp][wq][lane] = sum;
         }
         softmax_sync();
@@ -654,14 +669,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
           const int h = lane / HALF, r = lane % HALF;
           const float sum = (sh->sum[h][0][r] + sh->sum[h][1][r]) + (sh->sum[h][2][r] + sh->sum[h][3][r]);
           const bool dead = !((alive >> lane) & 1) || sum == 0.f;
-          const float l2 = dead ? -INFINITY : sh->m[lane] - P_LOG2 + log2f(sum);
-          float inv = dead ? 0.f : 1.f / sum, keep = 0.f, all = l2;
+          const float l2 = dead ? -INFINITY : sh->m[lane] - P_LOG2 + __log2f(sum);
+          float inv = dead ? 0.f : fast_rcp(sum), keep = 0.f, all = l2;
           if (!done.first) {
             const float old = sh->run_lse[lane], top = fmaxf(old, l2);
-            const float a = old == -INFINITY ? 0.f : exp2f(old - top), b = l2 == -INFINITY ? 0.f : exp2f(l2 - top);
-            keep = a + b == 0.f ? 0.f : a / (a + b);
-            inv = dead ? 0.f : inv * (b / (a + b));
-            all = a + b == 0.f ? -INFINITY : top + log2f(a + b);
+            const float a = old == -INFINITY ? 0.f : fast_exp2(old - top), b = l2 == -INFINITY ? 0.f : fast_exp2(l2 - top);
+            const float part = a + b == 0.f ? 0.f : fast_rcp(a + b);
+            keep = a * part;
+            inv = dead ? 0.f : inv * b * part;
+            all = a + b == 0.f ? -INFINITY : top + __log2f(a + b);
           }
           sh->run_lse[lane] = all;
           sh->inv[lane] = inv;
@@ -766,7 +782,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
 #pragma unroll
       for (int r = 0; r < HALF; ++r) {
         l[r] = 0.f;
-        m[r] = 0.f;                        // the references less P_LOG2 (0 before the first)
+        m[r] = 0.f;                        // P_LOG2 less the references (0 before the first)
       }
       float m_lane = -INFINITY;            // the reference of row lane % 16
 #pragma unroll 1
@@ -807,8 +823,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
           float qs[HALF];
           lds16(sh->q_scale + r0, qs);
           const float kexp = (float)((int)(__float_as_uint(ks) >> 23) - 127);    // log2 of a power of two
+          const float2 ks2 = make_float2(ks, ks), c22 = make_float2(c2, c2), kexp2 = make_float2(kexp, kexp);
 #pragma unroll
-          for (int r = 0; r < HALF; ++r) x[r] = fmaf(x[r] + y[r], qs[r] * ks, fmaf(z[r], c2, kexp));
+          for (int r = 0; r < HALF; r += 2) {
+            const float2 v = fma2(add2(make_float2(x[r], x[r + 1]), make_float2(y[r], y[r + 1])),
+                                  mul2(make_float2(qs[r], qs[r + 1]), ks2),
+                                  fma2(make_float2(z[r], z[r + 1]), c22, kexp2));
+            x[r] = v.x;
+            x[r + 1] = v.y;
+          }
         }
         if (__builtin_expect(!fast, 0)) {
           bool seen = false;
@@ -836,12 +859,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         {
           float y[HALF];
 #pragma unroll
-          for (int r = 0; r < HALF; ++r) y[r] = x[r];
-          float top = transpose_reduce16<true>(y, lane);
-          if (lane < HALF) sh->wpart[buf][grp][wq][lane] = top;
+          for (int r = 0; r < HALF; ++r) y[r] = warp_max(x[r]);
+          if (lane == 0) {
+#pragma unroll
+            for (int r = 0; r < HALF; r += 4)
+              *reinterpret_cast<float4*>(&sh->wpart[buf][grp][wq][r]) = make_float4(y[r], y[r + 1], y[r + 2], y[r + 3]);
+          }
           group_sync(grp);
           const float* part = &sh->wpart[buf][grp][0][lane % HALF];
-          top = fmaxf(fmaxf(part[0], part[HALF]), fmaxf(part[2 * HALF], part[3 * HALF]));
+          const float top = fmaxf(fmaxf(part[0], part[HALF]), fmaxf(part[2 * HALF], part[3 * HALF]));
           const bool up = top > m_lane + SLACK_LOG2;
           if (__builtin_expect(__any_sync(0xffffffffu, up), 0)) {               // (the same for every warp of the group)
             const float m_new = up ? ceilf(top) : m_lane;
@@ -849,7 +875,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
             m_lane = m_new;
 #pragma unroll
             for (int r = 0; r < HALF; ++r) {
-              m[r] = __shfl_sync(0xffffffffu, m_new == -INFINITY ? 0.f : m_new - P_LOG2, r);
+              m[r] = __shfl_sync(0xffffffffu, m_new == -INFINITY ? 0.f : P_LOG2 - m_new, r);
               y[r] = __shfl_sync(0xffffffffu, f, r);
               l[r] *= y[r];
             }
@@ -878,12 +904,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         uint32_t hi[HALF / 4], lo[HALF / 4];
 #pragma unroll
         for (int r = 0; r < HALF; r += 2) {
-          const float w0 = fast_exp2(x[r] - m[r]), w1 = fast_exp2(x[r + 1] - m[r + 1]);
-          l[r] = fmaf(w0, inv_ks, l[r]);
-          l[r + 1] = fmaf(w1, inv_ks, l[r + 1]);
-          const uint32_t h = e4m3x2(w0, w1);
+          const float2 d = add2(make_float2(x[r], x[r + 1]), make_float2(m[r], m[r + 1]));
+          const float2 w = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+          const float2 sum = fma2(w, make_float2(inv_ks, inv_ks), make_float2(l[r], l[r + 1]));
+          l[r] = sum.x;
+          l[r + 1] = sum.y;
+          const uint32_t h = e4m3x2(w.x, w.y);
           const float2 f = from_e4m3x2(h);
-          const uint32_t e = e4m3x2((w0 - f.x) * LO_UP, (w1 - f.y) * LO_UP);
+          // (exact: the difference, and a power of two times it)
+          const float2 rest = mul2(fma2(f, make_float2(-1.f, -1.f), w), make_float2(LO_UP, LO_UP));
+          const uint32_t e = e4m3x2(rest.x, rest.y);
           if (r % 4 == 0) {
             hi[r / 4] = h;
             lo[r / 4] = e;
