@@ -20,7 +20,7 @@
 // up by the CTA whose warp's run holds it, a run at a time in shared memory.
 //
 // Bound by the two rows of the node at which a sequence stops (64 chains of 15 over 152 k
-// tokens, fp32: 78 MB, 19.3 us in a graph of calls, 4.0 TB/s: 1 us until the first probabilities are
+// tokens, fp32: 78 MB, 19.8 us in a graph of calls, 3.9 TB/s: 1 us until the first probabilities are
 // there, 11 for the pass, 3 for its sums and 3.5 for the token).  A refusal costs a pass of
 // 2.5 us (8 trees of 32 nodes over 129 k, bf16: 26 us); one chain of 5 over 32 k takes 7.
 #include "common.cuh"
@@ -143,13 +143,14 @@ struct Rest {
     return !k ? Pair{pv, 0.f} : q ? left_of(pv, qv, mass, k) : of<WITHOUT>(pv, 0.f, x);
   }
   // One more element into a running sum; the roundings gather in `tail`.  CLEAN: as left(); else an
-  // infinity makes the sum no finite number.
+  // infinity makes the sum no finite number (the draft's by way of tail: 0 times it).
   template <int MODE, bool CLEAN>
   __device__ __forceinline__ void take(Pair& acc, float& tail, float pv, float qv, int x) const {
     const Pair w = CLEAN ? of<MODE>(prob(pv), prob(qv), x) : of<MODE>(fmaxf(pv, 0.f), fmaxf(qv, 0.f), x);
     const Pair s = two_sum(acc.hi, w.hi);
     acc.hi = s.hi;
     tail = __fadd_rn(tail, __fadd_rn(s.lo, w.lo));
+    if (!CLEAN && (MODE == DIFF || MODE == DIFFS)) tail = __fmaf_rn(fmaxf(qv, 0.f), 0.f, tail);
   }
   // A lane's share of the elements lo .. hi - 1 (lo a multiple of 32); `wide`: rows are 16-byte aligned.
   template <int MODE>

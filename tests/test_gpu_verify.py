@@ -169,6 +169,22 @@ def test_masses_at_the_edges(V):
     assert api.mla_get_device_status(the_handle()) == 0
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V", [500, 6000, 60000])
+def test_draft_numbers_that_do_not_count(V, dtype):
+    # one, two and three refusals at the context: what the draft's bad numbers leave of the
+    # target's mass decides about the next sibling and the token
+    b = Batch(12, 3, V, dtype=dtype, seed=21, kind="star", noise=3.0)
+    rng = np.random.default_rng(3)
+    for i, bad in enumerate((float("inf"), float("nan"), -1.0, float("-inf"))):
+        at = torch.from_numpy(rng.choice(V, size=V // 6, replace=False))
+        b.draft[3 * i:3 * i + 3, 0, at] = bad
+    b.draft[0, 0, :] = float("inf")                  # nothing that counts
+    b.u[:, :3] = 0.999
+    b.tokens[1::2, 0] = b.target[1::2, 0].float().argmin(dim=1).numpy()
+    b.check(b.run())
+
+
 def test_bad_tokens_and_parents_are_reported():
     from head_latent_attention_qkv_gb300 import _lib
     b = Batch(3, 4, 500, seed=1, kind="star")
