@@ -287,6 +287,24 @@ def test_a_poisoned_entry_reaches_the_rows_that_see_it():
     assert torch.isfinite(lse[T * 16:]).all() and torch.isfinite(o[T * 16:]).all()
 
 
+@pytest.mark.parametrize("ctx", [[60, 20], [3000, 700]])
+def test_a_query_that_is_no_number_spoils_its_row_only(ctx):
+    # (in units that lie in one CTA and in cut ones)
+    c = Case8(16, 16, ctx, 3, parents=[[-1] * 3, [-1] * 3])
+    want = c.attention()
+    c.q[5, 100] = float("nan")
+    c.q[21, 570] = float("nan")
+    c.q[40, 511] = float("inf")
+    c.q[70, 0] = float("-inf")
+    got = c.attention()
+    rows = torch.ones(len(c.q), dtype=torch.bool, device="cuda")
+    rows[[5, 21, 40, 70]] = False
+    for x, y in zip(got, want):
+        assert torch.equal(x[rows], y[rows])
+        assert torch.isnan(x[5]).all() and torch.isnan(x[21]).all()
+        assert not torch.isfinite(x[40]).any() and not torch.isfinite(x[70]).any()
+
+
 def test_device_checks():
     from head_latent_attention_qkv_gb300 import _lib, api
     c = Case8(16, 64, [300, 200, 150], 4)
