@@ -241,6 +241,17 @@ struct Ranges {
   }
 };
 
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p;
+}
+__device__ __forceinline__ int warp_same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint64_t desc(uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; }
+__device__ __forceinline__ bool warp_wait(Bars* B, uint64_t* bar, uint32_t parity, uint32_t* st) {
+  return __all_sync(0xffffffffu, wait_bar(B, bar, parity, st));
+}
+
 // A CTA's pieces, in order: tiles [t0, t0 + n) of a unit, its keys.  The first MAX_PIECES are worked
 // out once, before the copies start: what a role reads from memory later comes behind 160 KB of tiles.
 constexpr int MAX_PIECES = 32;
@@ -441,70 +452,86 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
   // other's products run.  (S(g) comes behind O(g - 2), which frees its tile's place, and behind the
   // reading of S(g - 2), which P(g - 2) follows.)
   if (warp == 8) {
-    if (lane == 0 && work) {
+    if (work) {
+      const uint32_t one = elect_one();
       const uint32_t id_s = idesc_f8(KT, 2 * NR);                            // K-major A and B
       const uint32_t id_r = idesc_f16(KT, NR, false);
-      const uint64_t dK = smem_desc_sw128(smem);
-      const uint64_t dQ = smem_desc_sw128(smem + OFF_Q), dR = smem_desc_sw128(smem + OFF_QR);
+      const uint32_t hi = (uint32_t)(smem_desc_sw128(smem) >> 32);
+      const uint32_t dK = (uint32_t)smem_desc_sw128(smem);
+      const uint32_t dQ = (uint32_t)smem_desc_sw128(smem + OFF_Q), dR = (uint32_t)smem_desc_sw128(smem + OFF_QR);
       constexpr uint32_t U_STAGE = STAGE_BYTES / 16, U_CH = CH_BYTES / 16, U_Q = Q_CH_BYTES / 16;
       SegIter it = start;
       Seg s{};
       uint32_t g = 0, kseg = 0;
       bool ok = true;
-      while (ok && next_seg(P, sh, it, s)) {
-        if (!(ok = wait_bar(B, &B->q_full, kseg & 1, status))) break;
-        for (int t = 0; t < s.n; ++t, ++g) {
+      while (ok && warp_same(next_seg(P, sh, it, s))) {
+        const int n = warp_same(s.n);
+        ok = warp_wait(B, &B->q_full, kseg & 1, status);
+        for (int t = 0; ok && t < n; ++t, ++g) {
           const uint32_t st = g % STAGES, d = tmem + 128 * (g & 1);
-          if (g >= 2 && !(ok = wait_bar(B, &B->p_full[g & 1], ((g >> 1) - 1) & 1, status))) break;
-          if (!(ok = wait_bar(B, &B->full[st], (g / STAGES) & 1, status))) break;
+          if (g >= 2 && !(ok = warp_wait(B, &B->p_full[g & 1], ((g >> 1) - 1) & 1, status))) break;
+          if (!(ok = warp_wait(B, &B->full[st], (g / STAGES) & 1, status))) break;
           tc_fence_after();
-          const uint64_t a = dK + st * U_STAGE;
+          const uint32_t a = dK + st * U_STAGE;
+          if (one) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma_f16(d + 64, a + 4 * U_CH + 2 * i, dR + 2 * i, id_r, i > 0);
-          mma_commit(&B->empty[st][4]);
+            for (int i = 0; i < 4; ++i) mma_f16(d + 64, desc(hi, a + 4 * U_CH + 2 * i), desc(hi, dR + 2 * i), id_r, i > 0);
+            mma_commit(&B->empty[st][4]);
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 4; ++q) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma_f8(d, a + q * U_CH + 2 * i, dQ + q * U_Q + 2 * i, id_s, q + i > 0);
+              for (int i = 0; i < 4; ++i) mma_f8(d, desc(hi, a + q * U_CH + 2 * i), desc(hi, dQ + q * U_Q + 2 * i), id_s, q + i > 0);
+            }
+            mma_commit(&B->s_full[g & 1]);
           }
-          mma_commit(&B->s_full[g & 1]);
+          __syncwarp();
         }
         ++kseg;
       }
-      mma_commit(&B->drain);
-      mbar_wait(&B->drain, 0, status);
+      if (one) {
+        mma_commit(&B->drain);
+        mbar_wait(&B->drain, 0, status);
+      }
     }
   } else if (warp == 9) {
-    if (lane == 0 && work) {
+    if (work) {
+      const uint32_t one = elect_one();
       const uint32_t id_o = idesc_f8(KT, 2 * NR) | (1u << 15) | (1u << 16);  // A and B MN-major
-      const uint64_t dV = smem_desc_sw128_mn(smem, CH_BYTES), dP = smem_desc_sw64_mn(smem + OFF_P);
+      const uint32_t hv = (uint32_t)(smem_desc_sw128_mn(smem, CH_BYTES) >> 32), dV = (uint32_t)smem_desc_sw128_mn(smem, CH_BYTES);
+      const uint32_t hp = (uint32_t)(smem_desc_sw64_mn(smem + OFF_P) >> 32), dP = (uint32_t)smem_desc_sw64_mn(smem + OFF_P);
       constexpr uint32_t U_STAGE = STAGE_BYTES / 16, U_CH = CH_BYTES / 16;
       constexpr uint32_t U_P = P_BYTES / 16, U_VSTEP = 32 * 128 / 16, U_PSTEP = 32 * 64 / 16;
       SegIter it = start;
       Seg s{};
       uint32_t g = 0;
       bool ok = true;
-      while (ok && next_seg(P, sh, it, s)) {
-        for (int t = 0; t < s.n; ++t, ++g) {
+      while (ok && warp_same(next_seg(P, sh, it, s))) {
+        const int n = warp_same(s.n);
+        for (int t = 0; t < n; ++t, ++g) {
           const uint32_t st = g % STAGES;
-          if (!(ok = wait_bar(B, &B->p_full[g & 1], (g >> 1) & 1, status))) break;
-          // (the tile itself: S(g), behind which P(g) came, was issued by the other thread)
-          if (!(ok = wait_bar(B, &B->full[st], (g / STAGES) & 1, status))) break;
+          // (the tile itself, whose scores the other thread issued, and its weights)
+          if (!(ok = warp_wait(B, &B->full[st], (g / STAGES) & 1, status))) break;
+          if (!(ok = warp_wait(B, &B->p_full[g & 1], (g >> 1) & 1, status))) break;
           tc_fence_after();
-          const uint64_t a = dV + st * U_STAGE, p = dP + (g & 1) * U_P;
+          const uint32_t a = dV + st * U_STAGE, p = dP + (g & 1) * U_P;
+          if (one) {
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 4; ++q) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_f8(tmem + TM_O + 64 * q, a + q * U_CH + i * U_VSTEP, p + i * U_PSTEP, id_o, t > 0 || i > 0);
-            mma_commit(&B->empty[st][q]);
+              for (int i = 0; i < 4; ++i)
+                mma_f8(tmem + TM_O + 64 * q, desc(hv, a + q * U_CH + i * U_VSTEP), desc(hp, p + i * U_PSTEP), id_o, t > 0 || i > 0);
+              mma_commit(&B->empty[st][q]);
+            }
+            mma_commit(&B->o_done);
+            if (t == n - 1) mma_commit(&B->o_seg);
           }
-          mma_commit(&B->o_done);
-          if (t == s.n - 1) mma_commit(&B->o_seg);
+          __syncwarp();
         }
       }
-      mma_commit(&B->drain_o);
-      mbar_wait(&B->drain_o, 0, status);
+      if (one) {
+        mma_commit(&B->drain_o);
+        mbar_wait(&B->drain_o, 0, status);
+      }
     }
   } else if (warp >= 10) {
     if (work) {
@@ -515,7 +542,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       // `base + i` and of the 32 behind them ----
       const int ps = P.rule.page_size, past_end = P.rule.num_pages * ps, segs = KT / P.seg_rows;
       const uint32_t scale_bytes = P.seg_rows * 4;
-      if (lane == 0) {
+      const uint32_t one = elect_one();
+      if (one) {
         prefetch_tmap(&P.tmL);
         prefetch_tmap(&P.tmR);
       }
@@ -524,8 +552,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       bool have = next_seg(P, sh, it, s);
       const int32_t* table = P.rule.block_table + (long)s.b * P.rule.max_pages;
       auto pages = [&](const int32_t* t, int at) { return t[min(at + lane, P.rule.max_pages - 1)]; };
-      int base = (s.k.j_lo + s.t0 * KT) / ps;
-      int cur = pages(table, base), ahead = pages(table, base + 32);
+      // page and row of a tile's first key
+      int page = (s.k.j_lo + s.t0 * KT) / ps, row = s.k.j_lo + s.t0 * KT - page * ps;
+      int base = page, cur = pages(table, base), ahead = pages(table, base + 32);
       pdl_wait();
       while (ok && have) {
         const Seg was = s;
@@ -537,31 +566,40 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
             // the next segment's pages are on their way while this one's last tile waits for its place
             have = next_seg(P, sh, it, s);
           }
-          if (j0 / ps >= base + 32) {
+          if (page >= base + 32) {
             base += 32;
             cur = ahead;
             ahead = pages(table, base + 32);
           }
           // (32 pages are whole tiles: a tile's segments lie in one lot)
-          const int j = j0 + min(lane, segs - 1) * P.seg_rows;
-          const int pg = __shfl_sync(0xffffffffu, cur, j / ps - base);
+          const int pg = __shfl_sync(0xffffffffu, cur, page - base + min(lane, segs - 1));
           int y = past_end;                              // (zeros)
-          if (lane < segs && j < was.k.n) {
-            if (pg >= 0 && pg < P.rule.num_pages) y = pg * ps + j % ps;
+          if (lane < segs && j0 + lane * P.seg_rows < was.k.n) {
+            if (pg >= 0 && pg < P.rule.num_pages) y = pg * ps + row;
             else set_status(status, MLA_DEV_BAD_PAGE);
           }
+          if (segs > 1) {
+            page += segs;
+          } else if ((row += KT) == ps) {
+            row = 0;
+            ++page;
+          }
           auto copy = [&](int chunk) {
-            if (lane == 0) ok = ok && wait_bar(B, &B->empty[st][chunk], ph ^ 1, status);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (lane == 0 && ok && chunk == 4) mbar_arrive_expect_tx(&B->full[st], STAGE_BYTES + KT * 4);
-            uint8_t* to = dst + chunk * CH_BYTES + lane * P.seg_rows * 128;
-            if (ok && lane < segs) {
-              if (chunk < 4) tma_load_3d(to, &P.tmL, &B->full[st], 0, y, chunk);
-              else tma_load_3d(to, &P.tmR, &B->full[st], 0, y, 0);
-              // the scales with a chunk that is freed behind their use (where there is no page some scale:
-              // no row sees the key, or it is reported)
-              if (chunk == 1)
-                bulk_load(&sh->scale[st][lane * P.seg_rows], P.scale + (y == past_end ? 0 : y), scale_bytes, &B->full[st]);
+            ok = ok && warp_wait(B, &B->empty[st][chunk], ph ^ 1, status);
+            if (!ok) return;
+            if (one && chunk == 4) mbar_arrive_expect_tx(&B->full[st], STAGE_BYTES + KT * 4);
+#pragma unroll 1
+            for (int i = 0; i < segs; ++i) {
+              const int yi = __shfl_sync(0xffffffffu, y, i);
+              uint8_t* to = dst + chunk * CH_BYTES + i * P.seg_rows * 128;
+              if (one) {
+                if (chunk < 4) tma_load_3d(to, &P.tmL, &B->full[st], 0, yi, chunk);
+                else tma_load_3d(to, &P.tmR, &B->full[st], 0, yi, 0);
+                // the scales with a chunk that is freed behind their use (where there is no page some scale:
+                // no row sees the key, or it is reported)
+                if (chunk == 1)
+                  bulk_load(&sh->scale[st][i * P.seg_rows], P.scale + (yi == past_end ? 0 : yi), scale_bytes, &B->full[st]);
+              }
             }
           };
           if (warp == 10) {
@@ -575,7 +613,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         }
         if (have && s.first) {
           table = P.rule.block_table + (long)s.b * P.rule.max_pages;
-          base = (s.k.j_lo + s.t0 * KT) / ps;
+          page = (s.k.j_lo + s.t0 * KT) / ps;
+          row = s.k.j_lo + s.t0 * KT - page * ps;
+          base = page;
           cur = pages(table, base);
           ahead = pages(table, base + 32);
         }
