@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         l[r] = 0.f;
         m[r] = 0.f;                        // P_LOG2 less the references (0 before the first)
       }
-      float m_lane = -INFINITY;            // the reference of row lane % 16
+      float m_lane = -INFINITY, top = -INFINITY;   // row lane % 16: its reference, its largest so far
 #pragma unroll 1
       for (int t = 0; t < s.n; ++t) {
         asm volatile("" : "+r"(t));        // (one copy of the loop's code, none peeled off)
@@ -893,7 +893,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
 #pragma unroll 1
             for (int q = 0; q < 2; ++q)
 #pragma unroll 1
-              for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(row + q * CH_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
+              for (int i = 0; i < 8; ++i)      // (neighbouring lanes' rows in different banks)
+                *reinterpret_cast<uint4*>(row + q * CH_BYTES + ((i ^ lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
         }
         {
@@ -907,10 +908,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
           }
           group_sync(grp);
           const float* part = &sh->wpart[buf][grp][0][lane % HALF];
-          const float top = fmaxf(fmaxf(part[0], part[HALF]), fmaxf(part[2 * HALF], part[3 * HALF]));
+          top = fmaxf(top, fmaxf(fmaxf(part[0], part[HALF]), fmaxf(part[2 * HALF], part[3 * HALF])));
           const bool up = top > m_lane + SLACK_LOG2;
           if (__builtin_expect(__any_sync(0xffffffffu, up), 0)) {               // (the same for every warp of the group)
-            const float m_new = up ? ceilf(top) : m_lane;
+            const float m_new = fmaxf(m_lane, ceilf(top));
             const float f = m_lane == -INFINITY ? 1.f : fast_exp2(m_lane - m_new);
             m_lane = m_new;
 #pragma unroll
