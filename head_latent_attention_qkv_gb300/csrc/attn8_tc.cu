@@ -1126,7 +1126,9 @@ int groups_of(const mla_handle* h, const mla_attn_desc_t& d) {
 bool whole_units(const mla_handle* h, const mla_attn_desc_t& d) {
   const long units = (long)d.num_blocks * groups_of(h, d), sms = h->num_sms;
   const long tiles = ((long)d.max_pages * h->cfg.page_size + KT - 1) / KT;
-  return units <= 32 * sms && (units + sms - 1) / sms * tiles <= (units * tiles + sms - 1) / sms + JOIN_TILES;
+  // (what a piece of several segments puts away needs a slot)
+  return tiles <= SEG_TILES && units <= 32 * sms &&
+         (units + sms - 1) / sms * tiles <= (units * tiles + sms - 1) / sms + JOIN_TILES;
 }
 // Workspace: a slot for every (unit, CTA) piece, units + CTAs at most; none of whole units.
 size_t ws_layout(const mla_handle* h, const mla_attn_desc_t& d, size_t* off_lse, size_t* off_first) {

@@ -220,6 +220,20 @@ def test_many_blocks():
     c.check_attention(*c.attention())
 
 
+@pytest.mark.parametrize("heads,ctx,opt", [
+    (32, [(97 * b * b) % 5000 for b in range(40)], dict(tree=False)),       # pieces that start with their unit
+    (96, [(331 * b) % 3001 for b in range(50)], dict(tree=False)),          # the same, three units a sequence
+    (32, [20000] + [30 * b for b in range(149)], {}),                       # one long sequence among short ones
+    (32, [8193] + [40] * 149, dict(tree=False)),                            # the first that needs two segments
+    (32, [8191] + [40] * 149, dict(tree=False)),
+    (32, [300] * 151 + [9000], dict(tree=False)),                           # as many units as SMs
+    (128, [19999, 0], dict(window=15000)),
+])
+def test_few_units_of_unequal_lengths(heads, ctx, opt):
+    c = Case8(heads, 64, ctx, 1, seed=len(ctx), **opt)
+    c.check_attention(*c.attention())
+
+
 def test_deep_trees():
     from tests.tree_cases import bushy
     for T, window in ((1024, 0), (90, 17)):
