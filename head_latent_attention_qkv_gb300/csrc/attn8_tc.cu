@@ -17,7 +17,8 @@
 // put away and joined by its log-sum-exp.  The sum of the softmax, l = sum w_j / s_j, is fp32.
 //
 // Work split.  One persistent CTA per SM.  The 128-key tiles of all units (a block's groups
-// of 32 rows), in order, are cut into equal ranges; a (unit, CTA) piece writes its
+// of 32 rows), in order, are cut into equal ranges, or, where there are fewer units than CTAs,
+// into equal pieces that start with their unit; a (unit, CTA) piece writes its
 // normalised partial to slot unit + CTA (unique: neither ever falls along the order and
 // one of them grows), or the output itself where the unit lies in one CTA; the join
 // kernel adds the pieces by log-sum-exp in order.
@@ -26,17 +27,22 @@
 //                stored, so that its first S runs meanwhile
 //   warps 8, 9 : the scores' and the outputs' MMAs (warp 8 holds the tensor memory)
 //   warps 10-11: copies; a tile is five 16 KB chunks, each refilled once its product is done
+// Warps 8 to 11 run converged with one elected thread that issues: operands of MMAs and copies lie in
+// uniform registers, and what a loop of one thread would move there for each MMA took 80-100 cycles of
+// issue for 48 of work (128 heads x 16 tokens: 207 -> 171 us).
 //
 // What bounds it.  Two tiles of 80 KB are all that fits beside the queries, so a tile's place goes
-// round in copy (1.2 k cycles from L2, up to 4 k from HBM) - scores (1.5-2.0 k) - softmax (1.3 k)
-// - output (1.5 k) and the hand-overs between them, 7.0 k: one tile in 3.5 k cycles, where the products'
-// operands alone pass shared memory in 1.7 k (an MMA of N = 64 takes 48 cycles, the time of
-// its 6 KB).  Widened to bf16 the same tile would not fit twice.  Code is the other bound: with the MMA
-// loops unrolled the roles' loops do not fit the instruction cache together (10% misses) and
-// 128 heads x 16 tokens over 4 x 8 k keys take 250-440 us instead of 207.  128 heads x 1 token
-// over 131 k keys 73 us, 64 sequences x 32 heads over 1-4 k keys 41 us (2.6 TB/s: first tiles
-// of a cold SM at 6 us, nine tiles, two stores, the join).  The softmax's arithmetic is in pairs of
-// fp32 (FFMA2) and its maxima are warp reductions of one instruction: 75 -> 73, 214 -> 207 us.
+// round in copy (1.0 k cycles from L2, up to 4 k from HBM) - scores (1.2 k) - softmax (0.8 k) - output
+// (0.8-1.0 k) and the hand-overs between them, 5.6 k: one tile in 2.8 k cycles, where the products'
+// operands alone pass shared memory in 1.75 k (an MMA of N = 64 takes 48 cycles, the time of
+// its 6 KB).  A raised reference waits for the output before it and costs 1.2 k: all rows' are raised to
+// their largest score so far when one has to be, which halves how often.  Widened to bf16 the same tile would not
+// fit twice.  Code is the other bound: with the MMA loops unrolled, or more of it elsewhere, the roles' loops
+// do not fit the instruction cache together (14% misses as it is), and what runs once in a segment runs cold: the step
+// from a unit to the next (queries, sums, output) takes 10 k cycles.  128 heads x 16 tokens over 4 x 8 k
+// keys 166 us (815 TFLOP/s of the bf16 operation), 128 heads x 1 token over 131 k keys 56 us, 64 sequences x 32
+// heads over 1-4 k keys 36 us (3.0 TB/s: first tiles of a cold SM at 6 us, eleven tiles, a store, the
+// join).  The softmax's arithmetic is in pairs of fp32 and its maxima are warp reductions of one instruction.
 #include "cache8.cuh"
 #include "gemm_tc.cuh"
 #include "tc_ptx.cuh"
@@ -54,7 +60,7 @@ using namespace tc;
 
 constexpr int KT = 128, NR = 32, HALF = 16;          // keys a tile, rows a unit, rows a softmax thread
 constexpr int FEW_UNITS = 16;                        // units whose join is shared by more CTAs (128 heads over
-                                                     // 131 k keys: 78 -> 75 us; 64 sequences: 42 -> 47)
+                                                     // 131 k keys: 59 -> 55.5 us; 64 sequences: 36 -> 40.5)
 constexpr int SEG_TILES = 64;                        // tiles after which a piece is put away
 constexpr int JOIN_TILES = 3;                        // what cutting units costs, in tiles
 constexpr int THREADS = 384, SM_THREADS = 256;
@@ -69,6 +75,7 @@ constexpr int OFF_QR = OFF_Q + 4 * Q_CH_BYTES;
 constexpr int OFF_P = OFF_QR + QR_BYTES;
 constexpr int OFF_RED = OFF_P + 2 * P_BYTES;
 constexpr int Q_ROWS = NR / (SM_THREADS / 32), Q_BATCH = 2;
+static_assert(Q_ROWS == 2 * Q_BATCH, "two rounds of a warp's rows");
 // TMEM: S of tile g at column 128 (g % 2): hi 0-31, lo 32-63, rotary 64-95; O at 256: 4 x (hi | lo)
 constexpr uint32_t TMEM_COLS = 512, TM_O = 256;
 constexpr float SLACK_LOG2 = 1.75f;                  // 2^7 2^1.75 < 448
@@ -84,7 +91,7 @@ struct Params {
   float* lse;         // [rows] or NULL
   float* part;        // [slots][4 quarters][8 x 4 rows][128 dims][4 rows] normalised partial outputs
   float* part_lse;    // [slots, 32]
-  int* first_tile;    // [blocks + 1] tiles of a group's worth of keys before each block
+  int* first_tile;    // [blocks + 1] tiles of a group's worth of keys before each block, [1] tiles of a piece or 0
   int num_blocks, groups, seg_rows;
   bool whole;         // every unit in one CTA: nothing to join
   float scale_log2;
@@ -362,9 +369,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
   // ---- schedule: the tiles of one group before each block, then this CTA's first unit and tile
   // (from the same numbers when every block has a thread); of whole units their numbers will do
   int nt = 0, excl = 0;
-  auto count = [&](int base, int run, bool report) {
-    const int b = base + tid;
-    nt = b < nb ? keys_of(P, b, report).nt : 0;
+  auto total = [&](int x) {                // over the CTA's threads
+    x = __reduce_add_sync(0xffffffffu, x);
+    if (lane == 0) sh->scan[warp] = x;
+    __syncthreads();
+    x = __reduce_add_sync(0xffffffffu, lane < THREADS / 32 ? sh->scan[lane] : 0);
+    __syncthreads();
+    return x;
+  };
+  auto scan = [&](int run) {
     int x = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -373,27 +386,46 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
     }
     if (lane == 31) sh->scan[warp] = x;
     __syncthreads();
-    int before = run, all = run;
-    for (int w = 0; w < THREADS / 32; ++w) {
-      before += w < warp ? sh->scan[w] : 0;
-      all += sh->scan[w];
-    }
+    const int of = lane < THREADS / 32 ? sh->scan[lane] : 0;
+    const int before = run + __reduce_add_sync(0xffffffffu, lane < warp ? of : 0);
+    const int all = run + __reduce_add_sync(0xffffffffu, of);
     __syncthreads();
     excl = before + x - nt;
     return all;
   };
+  auto keys = [&](int base, bool report) { nt = base + tid < nb ? keys_of(P, base + tid, report).nt : 0; };
   const int units = nb * P.groups;
-  int run = 0;
+  int run = 0, piece_tiles = 0;
   if (!P.whole)
-    for (int base = 0; base < nb; base += THREADS) run = count(base, run, c == 0);
+    for (int base = 0; base < nb; base += THREADS) {
+      keys(base, c == 0);
+      // Where there are fewer units than CTAs, pieces of L tiles that start with their unit, one a CTA, if an
+      // L of the even share to three tiles more gives few enough of them: a CTA's second unit costs it as
+      // much as four tiles (5 x 25 units behind a window 29.7 -> 25.7 us, 128 heads over 131 k keys 60 -> 56, 64
+      // sequences 36.4 -> 35.8).  The units count as padded to whole pieces.
+      if (units <= (int)gridDim.x) {
+        const int even = (total(nt) * P.groups + gridDim.x - 1) / gridDim.x;
+        if (even > 1) {
+#pragma unroll 1
+          for (int L = even; L <= even + 3 && !piece_tiles; ++L)
+            if (total(nt > 0 ? (nt - 1) / L + 1 : 0) * P.groups <= (int)gridDim.x) piece_tiles = L;
+          if (piece_tiles && nt > 0) nt = ((nt - 1) / piece_tiles + 1) * piece_tiles;
+        }
+      }
+      run = scan(run);
+    }
   // the first min(gridDim, U) CTAs take one range each, so none is empty
-  const int U = P.whole ? units : run * P.groups, G = min((int)gridDim.x, max(U, 1));
-  const Ranges ranges{U / G, U % G};
+  const int U = P.whole ? units : run * P.groups;
+  const int G = piece_tiles ? U / piece_tiles : min((int)gridDim.x, max(U, 1));
+  const Ranges ranges = piece_tiles ? Ranges{piece_tiles, 0} : Ranges{U / G, U % G};
   const int u0 = c < G ? ranges.begin(c) : U, u1 = c < G ? ranges.begin(c + 1) : U;
   if (!P.whole) {
     run = 0;
     for (int base = 0; base < nb; base += THREADS) {
-      if (nb > THREADS) run = count(base, run, false);
+      if (nb > THREADS) {
+        keys(base, false);
+        run = scan(run);
+      }
       const int b = base + tid;
       if (b < nb) {
         if (nt > 0 && u1 > u0 && u0 >= excl * P.groups && u0 < (excl + nt) * P.groups) {
@@ -404,7 +436,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         if (c == 0) {
           pdl_wait();                      // the workspace may still be read by the kernel before
           P.first_tile[b] = excl;
-          if (b == nb - 1) P.first_tile[nb] = excl + nt;
+          if (b == nb - 1) {
+            P.first_tile[nb] = excl + nt;
+            P.first_tile[nb + 1] = piece_tiles;
+          }
         }
       }
     }
@@ -428,13 +463,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       if (lane >= o) upto += y;
     }
     p.n = P.whole ? have : max(min(have, u1 - u0 - (upto - have)), 0);
+    if (piece_tiles && lane > 0) p.n = 0;
     const uint32_t mine = __ballot_sync(0xffffffffu, p.n > 0);
     if (p.n > 0) sh->piece[__popc(mine & ((1u << lane) - 1u))] = p;
     const uint32_t none = __ballot_sync(0xffffffffu, P.whole && unit < u1 && p.n == 0);
     if (lane == 31) {
       sh->pieces = __popc(mine);
       sh->more_unit = first + 32;
-      sh->more_left = P.whole ? 0 : u1 - u0 - upto;
+      sh->more_left = P.whole || piece_tiles ? 0 : u1 - u0 - upto;
       sh->empty = none;
     }
   }
@@ -646,20 +682,28 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       const int grp0 = (s.unit % P.groups) * NR;         // the unit's first row in its block
       if (have) {
         // ---- queries: four rows a warp, each split in two e4m3 numbers over a power of two (the
-        // S of the segment before are done: its last tile's weights have been made) ----
+        // S of the segment before are done: its last tile's weights have been made); all four are on their way
+        // at once, since what comes later waits behind the tiles' copies ----
+        uint4 v[Q_ROWS][2];
+        uint32_t vr[Q_ROWS];
+#pragma unroll
+        for (int i = 0; i < Q_ROWS; ++i) {
+          const int r = warp * Q_ROWS + i;
+          const bool in = grp0 + r < live;
+          const uint4* src = reinterpret_cast<const uint4*>(P.q + ((long)s.b * live + (in ? grp0 + r : 0)) * ENTRY);
+          v[i][0] = in ? src[2 * lane] : make_uint4(0, 0, 0, 0);
+          v[i][1] = in ? src[2 * lane + 1] : make_uint4(0, 0, 0, 0);
+          vr[i] = in ? reinterpret_cast<const uint32_t*>(src + RANK / 8)[lane] : 0u;
+        }
 #pragma unroll 1
         for (int i0 = 0; i0 < Q_ROWS; i0 += Q_BATCH) {
-          uint4 v[Q_BATCH][2];
-          uint32_t vr[Q_BATCH];
+          if (i0 > 0) {
 #pragma unroll
-          for (int i = 0; i < Q_BATCH; ++i) {
-            const int r = warp * Q_ROWS + i0 + i;
-            const bool in = grp0 + r < live;
-            const uint4* src =
-                reinterpret_cast<const uint4*>(P.q + ((long)s.b * live + (in ? grp0 + r : 0)) * ENTRY);
-            v[i][0] = in ? src[2 * lane] : make_uint4(0, 0, 0, 0);
-            v[i][1] = in ? src[2 * lane + 1] : make_uint4(0, 0, 0, 0);
-            vr[i] = in ? reinterpret_cast<const uint32_t*>(src + RANK / 8)[lane] : 0u;
+            for (int i = 0; i < Q_BATCH; ++i) {
+              v[i][0] = v[Q_BATCH + i][0];
+              v[i][1] = v[Q_BATCH + i][1];
+              vr[i] = vr[Q_BATCH + i];
+            }
           }
 #pragma unroll
           for (int i = 0; i < Q_BATCH; ++i) {
@@ -1018,7 +1062,8 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_con
     for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
   if (nt > 0) {
     const int G = min(ctas, U), u = t0 * P.groups + (unit % P.groups) * nt;
-    const Ranges ranges{U / G, U % G};
+    const int piece_tiles = P.first_tile[P.num_blocks + 1];
+    const Ranges ranges = piece_tiles ? Ranges{piece_tiles, 0} : Ranges{U / G, U % G};
     const int f = ranges.cta_of(u), cnt = ranges.cta_of(u + nt - 1) - f + 1;
     if (cnt == 1) return;
     const long slot0 = (long)unit + f;
@@ -1121,8 +1166,8 @@ int groups_of(const mla_handle* h, const mla_attn_desc_t& d) {
 // Whether no unit is cut.  By the table's width, since the lengths are on the device: the fullest CTA
 // then has `rounds` units of `tiles` tiles, and with cuts an even share of all, whose join (a launch,
 // about 4 us of the GPU and 3 of the host) and second segment a CTA cost as much as JOIN_TILES tiles (a call
-// from Python, 16 rows over 300 keys: 17 us whole, 20 cut; over 640: 23 and 20; 64 sequences of 500 keys, 4 x 32
-// rows: 33 and 46; 152 of 2000 keys, 32 rows: 49 and 54).
+// from Python, 16 rows over 300 keys: 15 us whole, 20 cut; over 640: 18.5 and 19.5, of the GPU 16.4 and 12.7;
+// 64 sequences of 500 keys, 4 x 32 rows: 29 and 39; 152 of 2000 keys, 32 rows: 44 and 49).
 bool whole_units(const mla_handle* h, const mla_attn_desc_t& d) {
   const long units = (long)d.num_blocks * groups_of(h, d), sms = h->num_sms;
   const long tiles = ((long)d.max_pages * h->cfg.page_size + KT - 1) / KT;
@@ -1139,7 +1184,7 @@ size_t ws_layout(const mla_handle* h, const mla_attn_desc_t& d, size_t* off_lse,
   *off_lse = o;
   o += align256((size_t)slots * NR * 4);
   *off_first = o;
-  return o + align256((size_t)(d.num_blocks + 1) * 4);
+  return o + align256((size_t)(d.num_blocks + 2) * 4);
 }
 
 }  // namespace
