@@ -248,13 +248,16 @@ struct Ranges {
   }
 };
 
+// One lane of a converged warp, always the same.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(p));
   return p;
 }
+// Lane 0's number: the compiler then knows that the warp's lanes agree.
 __device__ __forceinline__ int warp_same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ uint64_t desc(uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; }
+// wait_bar() of a whole warp.
 __device__ __forceinline__ bool warp_wait(Bars* B, uint64_t* bar, uint32_t parity, uint32_t* st) {
   return __all_sync(0xffffffffu, wait_bar(B, bar, parity, st));
 }
@@ -483,8 +486,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
   // (lengths, windows, positions and page rows are inputs of the call; what the kernel
   // before wrote, queries and entries, is read behind pdl_wait only)
 
-  // Two threads issue: the scores, as soon as a tile is there, and the outputs, as soon as its weights
-  // are; a commit and the look at a barrier cost 40 and 200 cycles of a thread, which pass while the
+  // Two warps issue: the scores, as soon as a tile is there, and the outputs, as soon as its weights
+  // are; a commit and the look at a barrier cost 40 and 200 cycles, which pass while the
   // other's products run.  (S(g) comes behind O(g - 2), which frees its tile's place, and behind the
   // reading of S(g - 2), which P(g - 2) follows.)
   if (warp == 8) {
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         const int n = warp_same(s.n);
         for (int t = 0; t < n; ++t, ++g) {
           const uint32_t st = g % STAGES;
-          // (the tile itself, whose scores the other thread issued, and its weights)
+          // (the tile itself, whose scores the other warp issued, and its weights)
           if (!(ok = warp_wait(B, &B->full[st], (g / STAGES) & 1, status))) break;
           if (!(ok = warp_wait(B, &B->p_full[g & 1], (g >> 1) & 1, status))) break;
           tc_fence_after();
