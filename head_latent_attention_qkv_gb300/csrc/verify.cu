@@ -22,12 +22,14 @@
 // Bound by the two rows of the node at which a sequence stops (64 chains of 15 over 152 k
 // tokens, fp32: 78 MB, 19.8 us in a graph of calls, 3.9 TB/s: 1 us until the first probabilities are
 // there, 11 for the pass, 3 for its sums and 3.5 for the token).  A refusal costs a pass of
-// 2.5 us (8 trees of 32 nodes over 129 k, bf16: 26 us); one chain of 5 over 32 k takes 7.
+// 1.8 us (8 trees of 32 nodes over 129 k, bf16: 19 us); one chain of 5 over 32 k takes 7.
 #include "common.cuh"
 #include "tc_ptx.cuh"
 #include "tree.cuh"
 
 #include <math.h>
+
+#include <mutex>
 
 namespace mla {
 namespace verify {
@@ -432,18 +434,27 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const Args a) {
 
 template <typename T>
 cudaError_t launch(const Args& a, int num_seqs, int cl, cudaStream_t st) {
+  static std::once_flag once;
+  static cudaError_t wide = cudaSuccess;   // clusters of 16 have to be asked for
+  std::call_once(once, [] {
+    wide = cudaFuncSetAttribute(verify_kernel<T, 16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  if (cl == 16 && wide != cudaSuccess) return wide;
   Launch L(dim3((unsigned)(num_seqs * cl)), dim3(THREADS), 0, st, false, dim3((unsigned)cl, 1, 1));
   return cudaLaunchKernelEx(&L.cfg, cl == 1   ? verify_kernel<T, 1>
                                     : cl == 2 ? verify_kernel<T, 2>
                                     : cl == 4 ? verify_kernel<T, 4>
-                                              : verify_kernel<T, 8>, a);
+                                    : cl == 8 ? verify_kernel<T, 8>
+                                              : verify_kernel<T, 16>, a);
 }
 
-// CTAs that share a sequence: 8, fewer where the sequences fill the GPU (four CTAs an SM) without
-// them, so that all of a batch's clusters run at once, and fewer for a small vocabulary.
+// CTAs that share a sequence: 16, fewer where the sequences fill the GPU (four CTAs an SM) without
+// them, so that all of a batch's clusters run at once, and fewer for a small vocabulary, whose passes are
+// shorter than what a wider cluster's barriers cost (16 for 8: 20 trees of 8 over 129 k tokens 42 -> 27 us,
+// one chain over 152 k 11.0 -> 9.2; 30 chains over 32 k 8.1 -> 10.3).
 int cluster_size(int num_seqs, int vocab, int num_sms) {
-  int cl = 8;
-  while (cl > 1 && ((long)num_seqs * cl > 4L * num_sms || vocab <= 512 * cl)) cl /= 2;
+  int cl = 16;
+  while (cl > 1 && ((long)num_seqs * cl > 4L * num_sms || vocab <= 2048 * cl)) cl /= 2;
   return cl;
 }
 
