@@ -234,6 +234,20 @@ def test_few_units_of_unequal_lengths(heads, ctx, opt):
     c.check_attention(*c.attention())
 
 
+@pytest.mark.parametrize("n,heads,wide", [(5500, 2, 0), (700, 33, 600), (4864, 1, 0)])
+def test_more_blocks_than_threads_and_more_units_than_a_list(n, heads, wide):
+    # (of 152 SMs: a CTA's units beyond its list of 32, blocks in two lots; the last ones whole, 32 a CTA)
+    from head_latent_attention_qkv_gb300 import api
+    from tests.tree_cases import i32
+    c = Case8(heads, 16, [(b * b) % 19 for b in range(n)], 1, tree=False)
+    if wide:
+        table = np.full((n, wide), -1)
+        table[:, :c.paged.max_pages] = c.paged.table
+        c.keep[0] = i32(table)
+        c.desc = api.make_desc(c.keep[0], c.keep[1], None, None, 1, c.stats)
+    c.check_attention(*c.attention())
+
+
 def test_deep_trees():
     from tests.tree_cases import bushy
     for T, window in ((1024, 0), (90, 17)):
