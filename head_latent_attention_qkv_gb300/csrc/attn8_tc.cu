@@ -928,10 +928,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
               if (!((sh->seen[grp][r0 + r][wq] >> lane) & 1)) x[r] = -INFINITY;
             for (int r = 0; r < NR; ++r) seen |= (sh->seen[grp][r][wq] >> lane) & 1;
           } else {
-#pragma unroll
-            for (int r = 0; r < HALF; ++r)
-              if (j < sh->lo[r0 + r] || j >= sh->hi[r0 + r]) x[r] = -INFINITY;
             seen = j >= any_lo && j < any_hi;
+            if (fast_lo == any_lo && fast_hi == any_hi) {      // (the rows that see anything see the same: little code)
+              if (!seen)
+#pragma unroll
+                for (int r = 0; r < HALF; ++r) x[r] = -INFINITY;
+            } else {
+#pragma unroll
+              for (int r = 0; r < HALF; ++r)
+                if (j < sh->lo[r0 + r] || j >= sh->hi[r0 + r]) x[r] = -INFINITY;
+            }
           }
           // a key that no row of the unit sees may hold any bytes: its latent becomes zero before
           // it meets its weights, which are zero (S is done with it, and O waits for P)
