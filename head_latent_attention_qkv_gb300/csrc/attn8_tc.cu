@@ -19,9 +19,8 @@
 // Work split.  One persistent CTA per SM.  The 128-key tiles of all units (a block's groups
 // of 32 rows), in order, are cut into equal ranges, or, where there are fewer units than CTAs,
 // into equal pieces that start with their unit; a (unit, CTA) piece writes its
-// normalised partial to slot unit + CTA (unique: neither ever falls along the order and
-// one of them grows), or the output itself where the unit lies in one CTA; the join
-// kernel adds the pieces by log-sum-exp in order.
+// normalised partial to one of the CTA's two slots, or the output itself where the unit lies in one CTA; the
+// join kernel adds the pieces by log-sum-exp in order.
 //   warps 0-7  : softmax, two groups of 128 threads, thread = key, 16 rows each; between
 //                segments the next one's queries are split before the last one's output is
 //                stored, so that its first S runs meanwhile
@@ -40,7 +39,7 @@
 // fit twice.  Code is the other bound: with the MMA loops unrolled, or more of it elsewhere, the roles' loops
 // do not fit the instruction cache together (7% misses as it is), and what runs once in a segment runs cold: the step
 // from a unit to the next (queries, sums, output) takes 10 k cycles.  128 heads x 16 tokens over 4 x 8 k
-// keys 166 us (815 TFLOP/s of the bf16 operation), 128 heads x 1 token over 131 k keys 56 us, 64 sequences x 32
+// keys 166 us (815 TFLOP/s of the bf16 operation), 128 heads x 1 token over 131 k keys 56.5 us, 64 sequences x 32
 // heads over 1-4 k keys 36 us (3.0 TB/s: first tiles of a cold SM at 6 us, eleven tiles, a store, the
 // join).  The softmax's arithmetic is in pairs of fp32 and its maxima are warp reductions of one instruction.
 #include "cache8.cuh"
@@ -261,6 +260,10 @@ __device__ __forceinline__ uint64_t desc(uint32_t hi, uint32_t lo) { return (uin
 __device__ __forceinline__ bool warp_wait(Bars* B, uint64_t* bar, uint32_t parity, uint32_t* st) {
   return __all_sync(0xffffffffu, wait_bar(B, bar, parity, st));
 }
+
+// Where CTA c leaves what it has of a unit that others share: of one begun before its range, or of the
+// last one of its range (which also puts away the segments of units of its own, before).
+__device__ __forceinline__ long slot_of(int c, bool begun, int ctas) { return begun ? c : ctas + c; }
 
 // A CTA's pieces, in order: tiles [t0, t0 + n) of a unit, its keys.  The first MAX_PIECES are worked
 // out once, before the copies start: what a role reads from memory later comes behind 160 KB of tiles.
@@ -746,7 +749,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         const int row0 = (done.unit % P.groups) * NR;
         const int unit0 = u_seg - done.t0;              // the unit's first tile
         const bool direct = P.whole || ranges.cta_of(unit0) == ranges.cta_of(unit0 + done.k.nt - 1);
-        const long slot = (long)done.unit + c;
+        const long slot = slot_of(c, unit0 < u0, gridDim.x);
         {
           const float sum = transpose_sum16(l, lane);
           if (lane < HALF) sh->sum[grp][wq][lane] = sum;
@@ -1075,8 +1078,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_con
     const Ranges ranges = piece_tiles ? Ranges{piece_tiles, 0} : Ranges{U / G, U % G};
     const int f = ranges.cta_of(u), cnt = ranges.cta_of(u + nt - 1) - f + 1;
     if (cnt == 1) return;
-    const long slot0 = (long)unit + f;
-    for (int i = tid; i < cnt * NR; i += JOIN_THREADS) w_s[i] = P.part_lse[slot0 * NR + i];
+    for (int i = tid; i < cnt * NR; i += JOIN_THREADS) w_s[i] = P.part_lse[slot_of(f + i / NR, i >= NR, ctas) * NR + i % NR];
     __syncthreads();
     {
       const int r = tid / 8, sl = tid % 8;
@@ -1107,7 +1109,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 2) join8_kernel(const __grid_con
 #pragma unroll
       for (int i = 0; i < JOIN_LOADS; ++i)
         if (s0 + i < cnt) {
-          const float4* src = reinterpret_cast<const float4*>(P.part + (slot0 + s0 + i) * NR * RANK) +
+          const float4* src = reinterpret_cast<const float4*>(P.part + slot_of(f + s0 + i, s0 + i > 0, ctas) * NR * RANK) +
                               (part * DIMS / 4 * (NR / 4) + ra / 4) * 128 + part * DIMS % 4 * 32 + da;
 #pragma unroll
           for (int j = 0; j < DIMS; ++j) v[i][j] = src[32 * j];
@@ -1184,11 +1186,12 @@ bool whole_units(const mla_handle* h, const mla_attn_desc_t& d) {
   return tiles <= SEG_TILES && units <= 32 * sms &&
          (units + sms - 1) / sms * tiles <= (units * tiles + sms - 1) / sms + JOIN_TILES;
 }
-// Workspace: a slot for every (unit, CTA) piece, units + CTAs at most; none of whole units.
+// Workspace: two slots a CTA, whatever the number of units (20 MB; a slot for each unit and CTA made 128 heads x 1
+// over 131 k keys 0.5 us faster and took 64 KB a unit); none of whole units.
 size_t ws_layout(const mla_handle* h, const mla_attn_desc_t& d, size_t* off_lse, size_t* off_first) {
   *off_lse = *off_first = 0;
   if (whole_units(h, d)) return 0;
-  const long slots = (long)d.num_blocks * groups_of(h, d) + h->num_sms;
+  const long slots = 2L * h->num_sms;
   size_t o = align256((size_t)slots * NR * RANK * 4);
   *off_lse = o;
   o += align256((size_t)slots * NR * 4);

@@ -623,6 +623,15 @@ def test_short_blocks_whole_and_cut():
             assert (o == 0).all() and torch.isneginf(lse).all()
 
 
+def test_the_workspace_does_not_grow_with_the_rows():
+    from head_latent_attention_qkv_gb300 import api
+    from tests.tree_cases import i32
+    h = handle("bf16", 128, 64)
+    sizes = [api.mla_latent_attention8_workspace_bytes(h, api.make_desc(i32(np.zeros((n, 400))), i32([9] * n), block_len=T))
+             for n, T in ((2, 1), (50, 16), (50, 700), (3000, 1))]
+    assert 0 < sizes[0] <= sizes[-1] <= 21 << 20 and max(sizes) - min(sizes) <= 4 * 3100
+
+
 def test_pieces_longer_than_what_one_sum_holds():
     # more than 64 tiles in a CTA: its parts are put away and joined (152 SMs, 1.3 M keys)
     from head_latent_attention_qkv_gb300 import api
