@@ -219,7 +219,8 @@ __device__ __forceinline__ float transpose_sum16(float* x, int lane) {
 }
 
 // Keys of block b: [j_lo, n) in nt tiles, j_lo the first key that any row's window reaches,
-// rounded down to a tile.
+// rounded down to a tile.  Not behind the context: a window counts the nodes' own positions, which
+// may lie anywhere ahead of their keys' indices.
 struct Keys {
   int n, W, ctx, j_lo, nt;
 };
@@ -230,7 +231,7 @@ __device__ __forceinline__ Keys keys_of(const Params& P, int b, bool report) {
   if (k.W > 0 && k.n > 0) {
     int p = 0x7fffffff;
     for (int t = 0; t < P.rule.T; ++t) p = min(p, P.rule.positions[(long)b * P.rule.T + t]);
-    k.j_lo = min(tree::window_start(p, k.W), k.n) / KT * KT;
+    k.j_lo = min(tree::window_start(p, k.W), k.ctx) / KT * KT;
   }
   k.nt = k.n > k.j_lo ? (k.n - k.j_lo + KT - 1) / KT : 0;
   return k;
