@@ -271,6 +271,7 @@ struct CompactArgs {
   const float* weights;
   float* weights_out;
   long ldk, ldw;
+  long row_cap;               // longest sequence that the caller's weights have room for
   int num_pages, page_size, max_pages, dst_pages;
   int units, rows;            // 16- or 4-byte units of an entry; rows of a chunk
   int data_chunks, chunks;    // per sequence: chunks that may move rows; with those that clear weights
@@ -343,8 +344,7 @@ __global__ void __launch_bounds__(MV_THREADS) compact_kernel(const CompactArgs a
   }
   __syncthreads();
   const int seq = s_ticket / a.chunks, c = s_ticket % a.chunks;
-  const long row_cap = a.weights_out ? a.ldw : 0x7fffffffL;
-  const int cap = (int)min((long)a.max_pages * a.page_size, row_cap);
+  const int cap = (int)min((long)a.max_pages * a.page_size, a.row_cap);
   const int n = a.kv_len[seq];
   if (n < 0 || n > cap) {
     if (tid == 0 && c == 0) set_status(a.status, MLA_DEV_BAD_LENGTH);
@@ -525,12 +525,15 @@ size_t compact_ws(size_t bytes, int num_seqs, int64_t ldk) {
   return align256(((size_t)num_seqs * ((ldk + rows - 1) / rows + parts) + 1) * sizeof(int));
 }
 
-// mla_cache_compact of an array of rows of `bytes` bytes, page by page.
+// Longest sequence that weights [num_seqs, ldw] (or none) have room for.
+long weights_cap(const float* weights, int64_t ldw) { return weights ? (long)ldw : 0x7fffffffL; }
+
+// mla_cache_compact of an array of rows of `bytes` bytes, page by page, of sequences of at most row_cap rows.
 mla_status_t compact_rows(mla_handle_t* h, void* cache, size_t bytes, int32_t num_pages,
                           const int32_t* block_table, int32_t max_pages, const int32_t* kv_len,
                           int32_t num_seqs, const int32_t* keep, int64_t ldk, const int32_t* keep_len,
                           const int32_t* first, const int32_t* dst_block_table, int32_t dst_max_pages,
-                          const float* weights, float* weights_out, int64_t ldw, void* workspace,
+                          const float* weights, float* weights_out, int64_t ldw, long row_cap, void* workspace,
                           size_t workspace_bytes, void* stream) {
   if (!h) return fail(MLA_ERR_INVALID_ARG, "compact: null handle");
   if (num_seqs < 0 || max_pages <= 0 || num_pages <= 0 || ldk < 0 || ldk > 0x3fffffffL)
@@ -560,7 +563,7 @@ mla_status_t compact_rows(mla_handle_t* h, void* cache, size_t bytes, int32_t nu
   if ((dc + zc) * num_seqs > 0x7fffffffL) return fail(MLA_ERR_INVALID_ARG, "compact: too many rows");
   a.cache = (char*)cache; a.block_table = block_table; a.kv_len = kv_len; a.keep = keep;
   a.keep_len = keep_len; a.first = first; a.dst_table = dst_block_table; a.weights = weights;
-  a.weights_out = weights_out; a.ldk = ldk; a.ldw = ldw; a.num_pages = num_pages;
+  a.weights_out = weights_out; a.ldk = ldk; a.ldw = ldw; a.row_cap = row_cap; a.num_pages = num_pages;
   a.page_size = h->cfg.page_size; a.max_pages = max_pages; a.dst_pages = dst_max_pages;
   a.data_chunks = (int)dc; a.chunks = (int)(dc + zc); a.in_place = in_place; a.status = h->status;
   cudaStream_t st = (cudaStream_t)stream;
@@ -601,11 +604,12 @@ extern "C" mla_status_t mla_cache_compact(mla_handle_t* h, void* cache, int32_t 
                                           size_t workspace_bytes, void* stream) {
   return compact_rows(h, cache, h ? (size_t)h->lay.L * h->lay.elt : 0, num_pages, block_table, max_pages, kv_len,
                       num_seqs, keep, ldk, keep_len, first, dst_block_table, dst_max_pages, weights, weights_out,
-                      ldw, workspace, workspace_bytes, stream);
+                      ldw, weights_cap(weights, ldw), workspace, workspace_bytes, stream);
 }
 
 // The three arrays of an 8-bit cache one after the other; in place the calls share the workspace (each
-// clears its flags behind the one before).
+// clears its flags behind the one before).  The weights move with the first; all three take the same sequences:
+// an entry is worth nothing without its scale.
 extern "C" size_t mla_cache8_compact_workspace_bytes(const mla_handle_t* h, int32_t num_seqs, int64_t ldk) {
   return h && num_seqs >= 0 && ldk >= 0 ? compact_ws(cache8::RANK, num_seqs, ldk) : 0;
 }
@@ -624,6 +628,6 @@ extern "C" mla_status_t mla_cache8_compact(mla_handle_t* h, const mla_cache8_t* 
   for (int i = 0; i < 3 && s == MLA_OK; ++i)
     s = compact_rows(h, array[i], bytes[i], num_pages, block_table, max_pages, kv_len, num_seqs, keep, ldk, keep_len,
                      first, dst_block_table, dst_max_pages, i ? nullptr : weights, i ? nullptr : weights_out, ldw,
-                     workspace, workspace_bytes, stream);
+                     weights_cap(weights, ldw), workspace, workspace_bytes, stream);
   return s;
 }
