@@ -96,6 +96,16 @@ struct Params {
   float scale_log2;
 };
 
+// The scales of entries that are no page's (their dims are copied as zeros): such a key counts as zeros whatever
+// the cache holds.
+struct Ones {
+  float of[KT];
+  constexpr Ones() : of() {
+    for (int i = 0; i < KT; ++i) of[i] = 1.f;
+  }
+};
+__device__ __align__(16) const Ones no_page_scales;
+
 struct Bars {
   uint64_t full[STAGES];            // a tile landed
   uint64_t empty[STAGES][CHUNKS];   // the products of a chunk are done
@@ -638,10 +648,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
               if (one) {
                 if (chunk < 4) tma_load_3d(to, &P.tmL, &B->full[st], 0, yi, chunk);
                 else tma_load_3d(to, &P.tmR, &B->full[st], 0, yi, 0);
-                // the scales with a chunk that is freed behind their use (where there is no page some scale:
-                // no row sees the key, or it is reported)
+                // the scales with a chunk that is freed behind their use
                 if (chunk == 1)
-                  bulk_load(&sh->scale[st][i * P.seg_rows], P.scale + (yi == past_end ? 0 : yi), scale_bytes, &B->full[st]);
+                  bulk_load(&sh->scale[st][i * P.seg_rows], yi == past_end ? no_page_scales.of : P.scale + yi, scale_bytes,
+                            &B->full[st]);
               }
             }
           };
