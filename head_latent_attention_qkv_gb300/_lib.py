@@ -17,7 +17,7 @@ MLA_BF16, MLA_FP32, MLA_FP16 = 0, 1, 2
 MLA_ROPE_NEOX, MLA_ROPE_INTERLEAVED = 0, 1
 MLA_DEV_BAD_SLOT, MLA_DEV_BAD_POSITION, MLA_DEV_BAD_PAGE, MLA_DEV_TIMEOUT, MLA_DEV_BAD_LENGTH = 1, 2, 4, 8, 16
 MLA_DEV_BAD_WINDOW = 32
-MLA_DEV_BAD_TREE, MLA_DEV_BAD_KEEP, MLA_DEV_BAD_DRAFT = 64, 128, 256
+MLA_DEV_BAD_TREE, MLA_DEV_BAD_KEEP, MLA_DEV_BAD_DRAFT, MLA_DEV_BAD_SCALE = 64, 128, 256, 512
 MLA_WS_Q_ABS, MLA_WS_O_LAT, MLA_WS_O, MLA_WS_LSE = 0, 1, 2, 3
 
 

@@ -428,7 +428,8 @@ def mla_cache_compact_workspace_bytes(h: Handle, num_seqs: int, ldk: int) -> int
 class Cache8:
     """The latent cache in 8 bits (mla_cache8_t), of the caller's tensors: ``latent`` float8_e4m3fn
     [num_pages, page_size, 512], ``rope`` bfloat16 [num_pages, page_size, 64], ``scale``
-    float32 [num_pages, page_size]; an entry stands for latent * scale and rope.  They are
+    float32 [num_pages, page_size]; an entry stands for latent * scale and rope, its scale a power
+    of two (or NaN: the attention reports another number).  They are
     looked at here, once, like a descriptor's; a call checks the page size and the device."""
     __slots__ = ("latent", "rope", "scale", "num_pages", "page_size", "device_index", "_c", "_ref")
 

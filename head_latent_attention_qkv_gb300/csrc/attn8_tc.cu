@@ -909,7 +909,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
         wait_bar(B, &B->full[gg % STAGES], (gg / STAGES) & 1, status);       // (for the scales; long done)
         wait_bar(B, &B->s_full[buf], (gg >> 1) & 1, status);
         tc_fence_after();
-        const float ks = sh->scale[gg % STAGES][key];
+        float ks = sh->scale[gg % STAGES][key];
+        // what is below takes a scale by its exponent: another number is as NaN, and reported where a row sees the key
+        bool odd = false;
+        if (__builtin_expect(!sound_scale(ks), 0)) {
+          odd = !isnan(ks);
+          ks = __uint_as_float(0x7fc00000u);
+        }
         float x[HALF];
         {
           float y[HALF], z[HALF];
@@ -956,6 +962,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
           // a key that no row of the unit sees may hold any bytes: its latent becomes zero before
           // it meets its weights, which are zero (S is done with it, and O waits for P)
           if (!seen) {
+            odd = false;
             uint8_t* row = smem + (gg % STAGES) * STAGE_BYTES + 2 * grp * CH_BYTES + key * 128;
 #pragma unroll 1
             for (int q = 0; q < 2; ++q)
@@ -964,6 +971,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
                 *reinterpret_cast<uint4*>(row + q * CH_BYTES + ((i ^ lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
         }
+        if (__builtin_expect(odd, 0)) set_status(status, MLA_DEV_BAD_SCALE);
         {
           float y[HALF];
 #pragma unroll

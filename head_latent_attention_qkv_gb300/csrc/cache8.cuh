@@ -18,7 +18,7 @@ namespace mla {
 namespace cache8 {
 
 constexpr int RANK = 512, ROPE = 64, ENTRY = RANK + ROPE;
-constexpr int K_MIN = -64;                 // least exponent of a scale
+constexpr int K_MIN = -64, K_MAX = 119;    // least exponent of a scale, and that of a latent just below 2^127
 
 // Exponent of an entry's scale from the largest |bits| of its latent's bf16 numbers: the
 // least k >= K_MIN with amax <= 448 2^k (448 = 1.75 2^8).
@@ -26,6 +26,12 @@ __device__ __forceinline__ int scale_exponent(uint32_t amax_bits) {
   return max((int)(amax_bits >> 7) - 127 - 8 + ((amax_bits & 0x7fu) > 96u ? 1 : 0), K_MIN);
 }
 __device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+// Whether a scale is one that a store writes for an entry that it holds: 2^K_MIN .. 2^K_MAX.  (The bits above those
+// of 2^K_MIN, turned so that a power of two is its exponent and every other number large.)
+__device__ __forceinline__ bool sound_scale(float s) {
+  const uint32_t above = __float_as_uint(s) - ((uint32_t)(K_MIN + 127) << 23);
+  return __funnelshift_l(above, above, 9) <= (uint32_t)(K_MAX - K_MIN);
+}
 // An entry that 8 bits do not hold: something NaN or infinite, or a latent of 2^127 or more.
 __device__ __forceinline__ bool poisoned(uint32_t amax_latent_bits, uint32_t amax_rope_bits) {
   return amax_latent_bits >= 0x7f00u || amax_rope_bits >= 0x7f80u;

@@ -78,8 +78,10 @@ enum {
   MLA_DEV_BAD_TREE = 64,     /* a node's parent is not an earlier node        */
   MLA_DEV_BAD_KEEP = 128,    /* a list of kept keys that is not ascending in
                                 [0, kv_len), or longer than its sequence      */
-  MLA_DEV_BAD_DRAFT = 256    /* a drafted token outside the vocabulary, or a
+  MLA_DEV_BAD_DRAFT = 256,   /* a drafted token outside the vocabulary, or a
                                 row of the target without any mass            */
+  MLA_DEV_BAD_SCALE = 512    /* a scale of an 8-bit cache that is no power of
+                                two (its readers become NaN)                  */
 };
 
 /* Intermediate tensors the forward leaves in its workspace
@@ -532,7 +534,10 @@ mla_status_t mla_cache_compact(mla_handle_t *h, void *cache, int32_t num_pages,
  * was read back and is stored again stands for the same numbers.  An entry with an
  * element that is NaN, infinite, or a latent of 2^127 or more has scale NaN and
  * latent 0: its latent reads back as NaN, a row that sees it becomes NaN, and
- * rows that do not see it are as without it. */
+ * rows that do not see it are as without it.
+ *   The attention takes a scale by its exponent: of entries written by other means, too,
+ * every scale that a row sees must be a power of two, 2^-64 .. 2^119 (or NaN).  Another
+ * number is reported as MLA_DEV_BAD_SCALE and counts as NaN. */
 typedef struct {
   void *latent, *rope;
   float *scale;

@@ -1,4 +1,5 @@
-"""Pages outside an 8-bit cache (needs a GB300)."""
+"""Pages outside an 8-bit cache, and scales that are no powers of two (needs a GB300)."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -42,3 +43,53 @@ def test_a_page_outside_the_cache_reads_as_zeros(page, ctx, first):
         assert api.mla_get_device_status(c.h) == _lib.MLA_DEV_BAD_PAGE
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     c.keep[0].copy_(table)
+
+
+@pytest.mark.parametrize("scale", [0.0, 3.0, -1.0, 1.0 + 2.0 ** -23, 2.0 ** -65, 2.0 ** 120, 1e-40, float("inf"), -float("inf")])
+@pytest.mark.parametrize("ctx", [[60, 20], [3000, 700]])
+def test_a_scale_that_is_no_power_of_two_is_reported(ctx, scale):
+    # (in units that lie in one CTA and in cut ones); it counts as NaN: its readers become NaN, others stay
+    from head_latent_attention_qkv_gb300 import _lib, api
+    T, H = 9, 16
+    c = Case8(H, 16, ctx, T, parents=[[-1] * T, [-1] * T])
+    want = c.attention()
+    slot = c.paged.slots(0, c.kv[0])
+    flat = c.c8.scale.view(-1)
+
+    def rows(lo, hi):
+        r = torch.zeros(2 * T * H, dtype=torch.bool, device="cuda")
+        r[lo * H:hi * H] = True
+        return r
+    for key, (lo, hi) in ((ctx[0] + 4, (4, 5)), (30, (0, T))):         # a node's own key, one of the context
+        was = flat[slot[key]].item()
+        flat[slot[key]] = scale
+        o, lse = c.attention()
+        assert api.mla_get_device_status(c.h) == _lib.MLA_DEV_BAD_SCALE
+        bad = rows(lo, hi)
+        assert torch.isnan(o[bad]).all() and torch.isnan(lse[bad]).all()
+        assert torch.equal(o[~bad], want[0][~bad]) and torch.equal(lse[~bad], want[1][~bad])
+        flat[slot[key]] = was
+
+
+def test_scales_at_the_ends_of_their_range_and_of_unseen_entries():
+    from head_latent_attention_qkv_gb300 import api
+    c = Case8(16, 16, [600, 20], 5, padded=True)     # (entries that nobody sees, and pages' ends, hold anything)
+    want = c.attention()
+    seen = torch.zeros(c.c8.scale.numel(), dtype=torch.bool)
+    for b in range(c.n):
+        seen[c.paged.slots(b, c.kv[b])[torch.from_numpy(c.vis[b].any(axis=0))]] = True
+    for junk in (0.0, 3.0, -2.0, float("inf"), float("nan"), 1e-42):
+        c.c8.scale.view(-1)[~seen.cuda()] = junk
+        o, lse = c.attention()
+        assert api.mla_get_device_status(c.h) == 0
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    for k in (-64, 119):                             # zeros of the least scale, and of the largest
+        c = Case8(16, 16, [40], 1, tree=False)
+        c.c8.latent.view(torch.uint8).zero_()
+        c.c8.rope.zero_()
+        c.c8.scale.fill_(2.0 ** k)
+        o, lse = c.attention()
+        assert api.mla_get_device_status(c.h) == 0
+        # (the log-sum-exp is the difference of two numbers below 2^7, one of them an fp32 logarithm good to
+        # 2^-22 of itself)
+        assert (o == 0).all() and ((lse - np.log(41)).abs() <= 2.0 ** -14).all()
