@@ -430,7 +430,8 @@ class Cache8:
     [num_pages, page_size, 512], ``rope`` bfloat16 [num_pages, page_size, 64], ``scale``
     float32 [num_pages, page_size]; an entry stands for latent * scale and rope, its scale a power
     of two (or NaN: the attention reports another number).  They are
-    looked at here, once, like a descriptor's; a call checks the page size and the device."""
+    looked at here, once, like a descriptor's, and cannot be replaced; a call checks the page size and
+    the device."""
     __slots__ = ("latent", "rope", "scale", "num_pages", "page_size", "device_index", "_c", "_ref")
 
     def __init__(self, latent, rope, scale):
@@ -442,10 +443,16 @@ class Cache8:
             if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
                 raise ValueError(f"cache {name}: expected a contiguous {dtype} tensor of shape {shape} on the "
                                  f"scale's device, got {t.dtype} {tuple(t.shape)} on {t.device}")
-        self.latent, self.rope, self.scale = latent, rope, scale
-        self.num_pages, self.page_size, self.device_index = n, page, device
-        self._c = _lib.mla_cache8_t(latent.data_ptr(), rope.data_ptr(), scale.data_ptr())
-        self._ref = C.byref(self._c)
+        c = _lib.mla_cache8_t(latent.data_ptr(), rope.data_ptr(), scale.data_ptr())
+        for name, value in zip(self.__slots__, (latent, rope, scale, n, page, device, c, C.byref(c))):
+            object.__setattr__(self, name, value)
+
+    # (the C form holds the tensors' addresses, and these attributes what keeps the tensors alive)
+    def __setattr__(self, name, value):
+        raise AttributeError(f"Cache8.{name} is fixed: make another Cache8 for other tensors")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"Cache8.{name} is fixed")
 
     def __iter__(self):
         return iter((self.latent, self.rope, self.scale))
