@@ -1253,9 +1253,11 @@ mla_status_t attention(cudaStream_t st, mla_handle* h, const tree::Rule& r, cons
     return fail(MLA_ERR_INVALID_ARG, "attention8: too many rows and keys (2^31 tiles of 32 x 128)");
   const long units = (long)P.num_blocks * P.groups;
   static std::once_flag once;
+  static cudaError_t room = cudaSuccess;
   std::call_once(once, [] {
-    cudaFuncSetAttribute(attn8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    room = cudaFuncSetAttribute(attn8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   });
+  if (room != cudaSuccess) return cuda_fail(room, "attention8: shared memory");
   Launch L(dim3((unsigned)std::min<long>(h->num_sms, P.whole ? units : h->num_sms)), dim3(THREADS), SMEM_BYTES, st, pdl);
   MLA_CUDA_TRY(cudaLaunchKernelEx(&L.cfg, attn8_kernel, P));
   h->launches += 1;

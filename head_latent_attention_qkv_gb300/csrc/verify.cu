@@ -432,14 +432,25 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const Args a) {
   if (CL > 1) tc::cluster_sync_all();      // a peer may still read this CTA's sums
 }
 
+// Whether the GPU runs clusters of 16 (more than 8 have to be asked for, and may be refused: a part of a GPU may have
+// no 16 SMs that can form one).
+template <typename T>
+bool wide_clusters() {
+  static std::once_flag once;
+  static bool wide = false;
+  std::call_once(once, [] {
+    Launch L(dim3(16), dim3(THREADS), 0, nullptr, false, dim3(16, 1, 1));
+    int clusters = 0;
+    wide = cudaFuncSetAttribute(verify_kernel<T, 16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+           cudaOccupancyMaxActiveClusters(&clusters, verify_kernel<T, 16>, &L.cfg) == cudaSuccess && clusters > 0;
+    if (!wide) cudaGetLastError();         // (the refusal is dealt with)
+  });
+  return wide;
+}
+
 template <typename T>
 cudaError_t launch(const Args& a, int num_seqs, int cl, cudaStream_t st) {
-  static std::once_flag once;
-  static cudaError_t wide = cudaSuccess;   // clusters of 16 have to be asked for
-  std::call_once(once, [] {
-    wide = cudaFuncSetAttribute(verify_kernel<T, 16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  });
-  if (cl == 16 && wide != cudaSuccess) return wide;
+  if (cl == 16 && !wide_clusters<T>()) cl = 8;
   Launch L(dim3((unsigned)(num_seqs * cl)), dim3(THREADS), 0, st, false, dim3((unsigned)cl, 1, 1));
   return cudaLaunchKernelEx(&L.cfg, cl == 1   ? verify_kernel<T, 1>
                                     : cl == 2 ? verify_kernel<T, 2>
