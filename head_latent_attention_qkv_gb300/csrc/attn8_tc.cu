@@ -39,7 +39,7 @@
 // fit twice.  Code is the other bound: with the MMA loops unrolled, or more of it elsewhere, the roles' loops
 // do not fit the instruction cache together (7% misses as it is), and what runs once in a segment runs cold: the step
 // from a unit to the next (queries, sums, output) takes 10 k cycles.  128 heads x 16 tokens over 4 x 8 k
-// keys 166 us (815 TFLOP/s of the bf16 operation), 128 heads x 1 token over 131 k keys 56.5 us, 64 sequences x 32
+// keys 166 us (816 TFLOP/s of the bf16 operation), 128 heads x 1 token over 131 k keys 57 us, 64 sequences x 32
 // heads over 1-4 k keys 36 us (3.0 TB/s: first tiles of a cold SM at 6 us, eleven tiles, a store, the
 // join).  The softmax's arithmetic is in pairs of fp32 and its maxima are warp reductions of one instruction.
 #include "cache8.cuh"
@@ -58,8 +58,10 @@ namespace {
 using namespace tc;
 
 constexpr int KT = 128, NR = 32, HALF = 16;          // keys a tile, rows a unit, rows a softmax thread
-constexpr int FEW_UNITS = 16;                        // units whose join is shared by more CTAs (128 heads over
-                                                     // 131 k keys: 59 -> 55.5 us; 64 sequences: 36 -> 40.5)
+// Units whose join is shared by 16 CTAs, not 4 (32 heads x 1 over 1-2 k and 8-16 k keys, with 16 and with 4: 8 units
+// 15.6 and 17.0 us, 24.0 and 25.9; 16 units 16.4 and 17.0, 36.3 and 37.6; 20 units 18.3 and 16.8, 35.0 and 33.8;
+// 24 units 18.7 and 17.0, 47.3 and 44.7; 64 units 30.8 and 24.4, 100 and 92).
+constexpr int FEW_UNITS = 16;
 constexpr int SEG_TILES = 64;                        // tiles after which a piece is put away
 constexpr int JOIN_TILES = 3;                        // what cutting units costs, in tiles
 constexpr int THREADS = 384, SM_THREADS = 256;
@@ -418,8 +420,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn8_kernel(const __grid_constant
       keys(base, c == 0);
       // Where there are fewer units than CTAs, pieces of L tiles that start with their unit, one a CTA, if an
       // L of the even share to three tiles more gives few enough of them: a CTA's second unit costs it as
-      // much as four tiles (5 x 25 units behind a window 29.7 -> 25.7 us, 128 heads over 131 k keys 60 -> 56, 64
-      // sequences 36.4 -> 35.8).  The units count as padded to whole pieces.
+      // much as four tiles (5 x 25 units behind a window 29.7 -> 25.7 us, 128 heads over 131 k keys 60 -> 56; 32 heads
+      // over 1-2 k and 8-16 k keys, even ranges and pieces: 2 units 14.0 and 14.2, 23.0 and 21.1; 8 units 15.2 and 15.6,
+      // 26.4 and 24.0; 16 units 20.3 and 16.4, 38.2 and 36.3; 32 units 22.2 and 18.3, 56.1 and 55.8; 48 units 23.6 and
+      // 20.8, 74.4 and 75.2; 64 units 26.7 and 24.4, 92.2 and 92.5).  The units count as padded to whole pieces.
       if (units <= (int)gridDim.x) {
         const int even = (total(nt) * P.groups + gridDim.x - 1) / gridDim.x;
         if (even > 1) {

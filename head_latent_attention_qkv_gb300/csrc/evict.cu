@@ -609,7 +609,8 @@ extern "C" mla_status_t mla_cache_compact(mla_handle_t* h, void* cache, int32_t 
 
 // The three arrays of an 8-bit cache one after the other; in place the calls share the workspace (each
 // clears its flags behind the one before).  The weights move with the first; all three take the same sequences:
-// an entry is worth nothing without its scale.
+// an entry is worth nothing without its scale.  64 sequences of 4 k entries to 1024: 23.7 us into other pages (29.3 for
+// the bf16 cache, 1.8 times the bytes), 48.6 in place (54.3); 5 of 16 nodes of each: 10.9 us in place (3.9), three launches.
 extern "C" size_t mla_cache8_compact_workspace_bytes(const mla_handle_t* h, int32_t num_seqs, int64_t ldk) {
   return h && num_seqs >= 0 && ldk >= 0 ? compact_ws(cache8::RANK, num_seqs, ldk) : 0;
 }

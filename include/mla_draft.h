@@ -537,7 +537,8 @@ mla_status_t mla_cache_compact(mla_handle_t *h, void *cache, int32_t num_pages,
  * rows that do not see it are as without it.
  *   The attention takes a scale by its exponent: of entries written by other means, too,
  * every scale that a row sees must be a power of two, 2^-64 .. 2^119 (or NaN).  Another
- * number is reported as MLA_DEV_BAD_SCALE and counts as NaN. */
+ * number is reported as MLA_DEV_BAD_SCALE and counts as NaN.  (mla_cache8_load multiplies by whatever
+ * number it finds and rounds to bf16.) */
 typedef struct {
   void *latent, *rope;
   float *scale;
@@ -570,7 +571,13 @@ mla_status_t mla_latent_cache_append8(mla_handle_t *h, const void *hidden,
  * entries that the cache stands for; same q_abs, positions, desc, o_lat, lse,
  * same checks on the device, any block_len.  Entries that no row sees may hold
  * anything.  num_pages * page_size < 2^31.  Every block's keys are split over the SMs and joined by
- * log-sum-exp.  workspace: mla_latent_attention8_workspace_bytes() bytes,
+ * log-sum-exp.
+ *   Rounding: a softmax weight is held to 2^-8 of itself, and weight times scale to 2^-20 of the row's
+ * largest such product; a query's elements exactly down to 2^-10 of the row's largest, and to 2^-17 of it
+ * below; scores, sums and log-sum-exps in fp32; o_lat in fp16.  (Outputs are half as far from the exact ones
+ * as those of mla_latent_attention and mla_tree_attention over the same entries in bf16.)  A key whose weight times
+ * scale is below 2^-120 of the row's largest adds nothing to the sums; zeros have scale 2^-64.
+ *   workspace: mla_latent_attention8_workspace_bytes() bytes,
  * 256-byte aligned; two calls that may overlap on the GPU need two. */
 size_t mla_latent_attention8_workspace_bytes(const mla_handle_t *h, const mla_attn_desc_t *desc);
 mla_status_t mla_latent_attention8(mla_handle_t *h, const void *q_abs, const int32_t *positions,

@@ -93,3 +93,29 @@ def test_scales_at_the_ends_of_their_range_and_of_unseen_entries():
         # (the log-sum-exp is the difference of two numbers below 2^7, one of them an fp32 logarithm good to
         # 2^-22 of itself)
         assert (o == 0).all() and ((lse - np.log(41)).abs() <= 2.0 ** -14).all()
+
+
+def test_latents_of_zeros_keep_their_weight():
+    # their scale is the least one, 2^-64, beside others of up to 2^13; every other key has such a latent
+    from oracle import tree as O
+    from tests.test_gpu_cache8 import rebuilt
+    for q_scale, spread in ((1e-6, 21), (0.3, 1), (3.0, 1)):
+        c = Case8(8, 64, [700, 90], 3, seed=4, q_scale=q_scale)
+        for b, e in enumerate(c.paged.entries):
+            e[:, :512] *= 2.0 ** np.random.default_rng(b).integers(1 - spread, spread, size=len(e))[:, None]
+            e[::2, :512] = np.where(np.isnan(e[::2, :512]), np.nan, 0.0)
+        rebuilt(c)
+        o, lse = c.attention()
+        # latents of 2^22 leave fp16: what rounds to 65536 or more is infinite there, so that an infinity is right
+        # where the exact number, with the weights' 2^-8 and as much again, reaches 65520
+        o, count = o.double().view(c.n, c.T, c.H, 512), 0
+        for b, e in enumerate(c.paged.entries):
+            ref = O.attention(c.q64[b], e, c.vis[b], 512, c.scale)[0]
+            mass = O.weight_mass(c.q64[b], e, c.vis[b], 512, c.scale)
+            inf = o[b].isinf().cpu().numpy()
+            assert (np.abs(ref[inf]) + 2.0 ** -7 * mass[inf] >= 65520).all()
+            assert (np.sign(ref[inf]) == np.sign(o[b].cpu().numpy()[inf])).all()
+            o[b] = torch.where(o[b].isinf(), torch.from_numpy(ref).cuda(), o[b])
+            count += inf.sum()
+        assert (count > 0) == (spread > 1)
+        c.check_attention(o, lse)
