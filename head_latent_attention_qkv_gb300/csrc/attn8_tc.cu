@@ -37,7 +37,7 @@
 // its 6 KB).  A raised reference waits for the output before it and costs 1.2 k: all rows' are raised to
 // their largest score so far when one has to be, which halves how often.  Widened to bf16 the same tile would not
 // fit twice.  Code is the other bound: with the MMA loops unrolled, or more of it elsewhere, the roles' loops
-// do not fit the instruction cache together (7% misses as it is), and what runs once in a segment runs cold: the step
+// do not fit the instruction cache together (8% misses as it is), and what runs once in a segment runs cold: the step
 // from a unit to the next (queries, sums, output) takes 10 k cycles.  128 heads x 16 tokens over 4 x 8 k
 // keys 166 us (816 TFLOP/s of the bf16 operation), 128 heads x 1 token over 131 k keys 57 us, 64 sequences x 32
 // heads over 1-4 k keys 36 us (3.0 TB/s: first tiles of a cold SM at 6 us, eleven tiles, a store, the
